@@ -30,6 +30,9 @@ GDN_MAX_NODES = 32
 GDN_MAX_TREE_DEPTH = 16
 GDN_PREFILL_CHUNK = 64
 GDN_MAX_CONV_WIDTH = 8
+GDN_MAX_POOLS = 8
+GDN_POOL_MAX_ROWS = 65536
+GDN_POOL_MAX_SEQS = 8192
 GDN_F16_MAX = 65504.0
 GDN_PREFILL_SCRATCH_BYTES = 32 << 20
 
@@ -60,6 +63,11 @@ class GdnShape(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class GdnPool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64), ("layer_bytes", ctypes.c_int64),
+                ("n_layers", ctypes.c_int32), ("n_slots", ctypes.c_int32)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _SIGS = {
@@ -80,9 +88,15 @@ _SIGS = {
     "gdn_prefill_boundary_states": [_vp, _i32, _i32],
     "gdn_prefill_varlen": [ctypes.POINTER(GdnShape)] + [_vp] * 10 + [_i32, _vp, ctypes.c_size_t, _vp, _vp],
     "gdn_prefill_chunked_noalloc": [ctypes.POINTER(GdnShape)] + [_vp] * 10,
+    "gdn_pool_copy": [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp],
+    "gdn_pool_fork_workspace_bytes": [_i32],
+    "gdn_pool_fork": [_vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp],
+    "gdn_pool_compact_workspace_bytes": [_i32],
+    "gdn_pool_compact": [_vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp],
 }
 _RESTYPES = {"gdn_status_string": ctypes.c_char_p, "gdn_prefill_workspace_bytes": ctypes.c_size_t,
-             "gdn_prefill_varlen_workspace_bytes": ctypes.c_size_t, "gdn_prefill_boundary_states": ctypes.c_int64}
+             "gdn_prefill_varlen_workspace_bytes": ctypes.c_size_t, "gdn_prefill_boundary_states": ctypes.c_int64,
+             "gdn_pool_fork_workspace_bytes": ctypes.c_size_t, "gdn_pool_compact_workspace_bytes": ctypes.c_size_t}
 
 
 def lib() -> ctypes.CDLL:
@@ -553,3 +567,137 @@ def gdn_prefill_varlen(cu_seqlens, q, k, v, alpha, beta, state, out, *, chunk_st
             _dev_ptr(status, "status"), _stream(stream))
     return _invoke("gdn_prefill_varlen", args, (sh, cu, q, k, v, alpha, beta, state, state_slot, out, chunk_states,
                                                 workspace, status), prepare)
+
+
+# ---------------------------------------------------------------------------
+# rows of a state pool
+# ---------------------------------------------------------------------------
+def _pool_structs(pools, name="pools"):
+    """gdn_pool structs of pool tensors [layers][slots][...]; rows are contiguous, layers may be apart."""
+    if isinstance(pools, torch.Tensor):
+        pools = (pools,)
+    if not 1 <= len(pools) <= GDN_MAX_POOLS:
+        raise ValueError(f"{name}: 1 to {GDN_MAX_POOLS} pools, got {len(pools)}")
+    structs = (GdnPool * len(pools))()
+    for p, t in zip(structs, pools):
+        if not isinstance(t, torch.Tensor) or t.dim() < 3:
+            raise ValueError(f"{name} must be tensors [layers][slots][...]")
+        size, strides, row = t.shape, t.stride(), 1
+        for i in range(t.dim() - 1, 0, -1):  # the rows of a layer, and what a row holds, are dense
+            if size[i] != 1 and strides[i] != row:
+                raise ValueError(f"the rows of {name} must be contiguous within a layer")
+            row *= size[i]
+        slots, e = size[1], t.element_size()
+        if slots < 1 or row == 0:
+            raise ValueError(f"{name} must hold at least one row")
+        p.data, p.row_bytes, p.n_layers, p.n_slots = t.data_ptr(), row // slots * e, size[0], slots
+        p.layer_bytes = (strides[0] if size[0] > 1 else row) * e
+        if slots != structs[0].n_slots:
+            raise ValueError(f"the {name} must have the same number of rows")
+    return structs, tuple(pools)
+
+
+def _int_array(t, name, n=None):
+    """The length of an int32 vector (0 where it is not given)."""
+    if t is None:
+        return 0
+    _expect(t, name, (n,), torch.int32)
+    return t.shape[0]
+
+
+def _on_current_device(name, *tensors):
+    """Every tensor is on the current device, where the call launches."""
+    if not torch.cuda.is_available():  # no device at all: refused with the tensor's name below
+        return
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != device:
+            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{device}")
+
+
+def _pool_ptrs(pools, name="pools"):
+    for t in pools:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be device tensors")
+
+
+def gdn_pool_copy(pools, src_rows, dst_rows, *, src_pools=None, status=None, stream=None, prepare: bool = False):
+    """Copy rows src_rows[i] -> dst_rows[i] (int32 device arrays) in every pool; see include/gdn.h.
+
+    ``pools``: one tensor or up to 8, each [layers][slots][...].  ``src_pools``: the pools the rows
+    come from, in the same order, where they are not ``pools`` themselves.
+    """
+    dst, keep = _pool_structs(pools)
+    src, keep_src = (None, ()) if src_pools is None else _pool_structs(src_pools, "src_pools")
+    if src is not None and [(p.row_bytes, p.n_layers) for p in src] != [(p.row_bytes, p.n_layers) for p in dst]:
+        raise ValueError("src_pools must have the layers and row sizes of pools")
+    n = _int_array(src_rows, "src_rows")
+    _expect(dst_rows, "dst_rows", (n,), torch.int32)
+    _check_status(status)
+    _pool_ptrs(keep)
+    _pool_ptrs(keep_src, "src_pools")
+    _on_current_device("gdn_pool_copy", *keep, *keep_src, src_rows, dst_rows, status)
+    args = (dst, src if src is not None else _vp(None), _i32(len(keep)), _dev_ptr(src_rows, "src_rows"),
+            _dev_ptr(dst_rows, "dst_rows"), _i32(n), _dev_ptr(status, "status"), _stream(stream))
+    return _invoke("gdn_pool_copy", args, (keep, keep_src, src_rows, dst_rows, status), prepare)
+
+
+def _pool_table(pools, table, n_rows, released, table_out, status):
+    structs, keep = _pool_structs(pools)
+    m = _int_array(table, "table")
+    _expect(table_out, "table_out", (m,), torch.int32)
+    n_rel = _int_array(released, "released")
+    _check_status(status)
+    slots = structs[0].n_slots
+    n_rows = min(slots, GDN_POOL_MAX_ROWS) if n_rows is None else int(n_rows)
+    if not 1 <= n_rows <= min(slots, GDN_POOL_MAX_ROWS):
+        raise ValueError(f"n_rows must be between 1 and the pools' rows ({slots}, at most {GDN_POOL_MAX_ROWS})")
+    if m > GDN_POOL_MAX_SEQS:
+        raise ValueError(f"table holds {m} sequences, at most {GDN_POOL_MAX_SEQS}")
+    return structs, keep, m, n_rel, n_rows, table if table_out is None else table_out
+
+
+def _workspace(need, device, stream):
+    """A workspace of this call's own, not handed out again before `stream` is done with it."""
+    workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        workspace.record_stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
+    return workspace
+
+
+def gdn_pool_fork(pools, table, parent, child, *, released=None, table_out=None, n_rows=None, workspace=None,
+                  status=None, stream=None, prepare: bool = False):
+    """Release sequences and give each child[i] a free row that holds sequence parent[i]'s (-1: zeros); see
+    include/gdn.h.  All index arrays are int32 device tensors; ``table_out`` defaults to ``table`` itself, ``n_rows``
+    to all rows of the pools.  ``workspace`` is allocated here with torch when omitted."""
+    structs, keep, m, n_rel, n_rows, table_out = _pool_table(pools, table, n_rows, released, table_out, status)
+    n = _int_array(parent, "parent")
+    if n != _int_array(child, "child"):
+        raise ValueError("parent and child must have the same length")
+    if n > GDN_POOL_MAX_SEQS:
+        raise ValueError(f"{n} children, at most {GDN_POOL_MAX_SEQS}")
+    _pool_ptrs(keep)
+    _on_current_device("gdn_pool_fork", *keep, table, table_out, released, parent, child, workspace, status)
+    if workspace is None:
+        workspace = _workspace(8 * n, keep[0].device, stream)
+    args = (structs, _i32(len(keep)), _dev_ptr(table, "table"), _i32(m), _i32(n_rows), _dev_ptr(released, "released"),
+            _i32(n_rel), _dev_ptr(parent, "parent"), _dev_ptr(child, "child"), _i32(n), _dev_ptr(table_out, "table_out"),
+            _dev_ptr(workspace, "workspace"), ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"),
+            _stream(stream))
+    return _invoke("gdn_pool_fork", args, (keep, table, released, parent, child, table_out, workspace, status), prepare)
+
+
+def gdn_pool_compact(pools, table, *, released=None, table_out=None, count=None, n_rows=None, workspace=None,
+                     status=None, stream=None, prepare: bool = False):
+    """Release sequences and move the rows still in use to the lowest rows; ``count`` (int32, one element) receives
+    how many there are.  See include/gdn.h; the other arguments as :func:`gdn_pool_fork`."""
+    structs, keep, m, n_rel, n_rows, table_out = _pool_table(pools, table, n_rows, released, table_out, status)
+    _expect(count, "count", (1,), torch.int32)
+    _pool_ptrs(keep)
+    _on_current_device("gdn_pool_compact", *keep, table, table_out, released, count, workspace, status)
+    if workspace is None:
+        workspace = _workspace(16 + 8 * n_rows, keep[0].device, stream)
+    args = (structs, _i32(len(keep)), _dev_ptr(table, "table"), _i32(m), _i32(n_rows), _dev_ptr(released, "released"),
+            _i32(n_rel), _dev_ptr(table_out, "table_out"), _dev_ptr(count, "count"), _dev_ptr(workspace, "workspace"),
+            ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"), _stream(stream))
+    return _invoke("gdn_pool_compact", args, (keep, table, released, table_out, count, workspace, status), prepare)

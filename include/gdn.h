@@ -62,6 +62,9 @@ extern "C" {
 #define GDN_MAX_TREE_DEPTH 16 /* nodes on a root-to-leaf path, root included */
 #define GDN_PREFILL_CHUNK 64  /* tokens per chunk of gdn_prefill_chunked */
 #define GDN_MAX_CONV_WIDTH 8  /* taps of the causal convolution whose history gdn_conv_commit keeps */
+#define GDN_MAX_POOLS 8       /* pools of one gdn_pool_copy, gdn_pool_fork or gdn_pool_compact call */
+#define GDN_POOL_MAX_ROWS 65536 /* rows gdn_pool_fork hands out and gdn_pool_compact moves */
+#define GDN_POOL_MAX_SEQS 8192  /* entries of their index table */
 
 typedef enum gdn_status {
     GDN_OK = 0,
@@ -271,6 +274,88 @@ int gdn_replay_verify_chain(const gdn_shape* shape, const int32_t* accepted_prev
  */
 int gdn_commit_index(const int32_t* accepted_node, int32_t* state_slot, int32_t batch, int32_t n_nodes,
                      int32_t draft_row0, int32_t n_slots, int32_t* status, void* stream);
+
+/*
+ * Rows of a state pool.  A sequence of a hybrid model owns one row: its
+ * recurrent state in every layer, and its convolution history.  Page
+ * "LightSeek's TokenSpeed Hits 580 Tokens per Second on Qwen3.5's 400B Model",
+ * section "How they actually got there": states live in the rows of a buffer,
+ * an index table records which row holds each sequence's state, and cached
+ * prefixes are states that other sequences continue from.
+ *
+ * A gdn_pool is one array of rows for several layers: row r of layer l starts
+ * at data + l layer_bytes + r row_bytes.  The pools of one call have the same
+ * n_slots, do not overlap, and row r means row r of every layer of each of
+ * them.  Rows hold anything (bytes are moved).
+ */
+typedef struct gdn_pool {
+    void* data;          /* 16-byte aligned (not read where n_layers is 0) */
+    int64_t row_bytes;   /* bytes of a row, a multiple of 16, at least 16 */
+    int64_t layer_bytes; /* from one layer to the next, a multiple of 16, at least n_slots * row_bytes */
+    int32_t n_layers;    /* >= 0 */
+    int32_t n_slots;     /* rows of a layer, >= 1 */
+} gdn_pool;
+
+/*
+ * Copy rows: row dst_row[i] of every dst pool <- row src_row[i] of the src pool
+ * of the same place, for i < n (restoring a cached prefix into a sequence's
+ * row, keeping a row as a checkpoint).  src NULL copies within dst; otherwise
+ * src[p] has dst[p]'s row_bytes and n_layers, rows of its own number, and does
+ * not overlap any dst pool.  src_row and dst_row are DEVICE arrays [n].  A
+ * source row of -1 zero-fills the destination row (a fresh sequence); a pair
+ * whose destination row is -1 is passed over.  One source may be named by any
+ * number of pairs.  A pair with a row outside the pools, and every pair whose
+ * destination is also another pair's destination or (within dst) another
+ * pair's source, is not copied and sets *status to GDN_ERR_SLOT; rows that no
+ * copied pair names are left as they were.
+ */
+int gdn_pool_copy(const gdn_pool* dst, const gdn_pool* src, int32_t n_pools, const int32_t* src_row,
+                  const int32_t* dst_row, int32_t n, int32_t* status, void* stream);
+
+/*
+ * Release sequences and fork others.  `table` (DEVICE, [n_seqs]) is the index
+ * table: the row of each sequence, -1 where it has none.  The rows this call
+ * may hand out are rows 0 .. n_rows - 1 (n_rows <= n_slots: the rest, such as
+ * the draft region of gdn_commit_index, is not touched) that no entry of
+ * `table` names.  In this order:
+ *   - child i (i < n_children) gets the i-th lowest free row; the row of
+ *     sequence parent[i] is copied there in all pools (a parent of -1: zeroed);
+ *   - table_out is `table` with -1 for the sequences in released[n_released],
+ *     then the new row for each sequence child[i].
+ * A parent may be released by the same call (its row is not handed out by it),
+ * and a child may be a released sequence, but no child may hold a row that is
+ * not released.  A child that does, one outside [0, n_seqs), one that an
+ * earlier child names too, one whose parent is outside [-1, n_seqs) or holds
+ * no row, and one for which no free row is left gets nothing and sets *status
+ * to GDN_ERR_SLOT, as do a released sequence outside [0, n_seqs) and a table
+ * entry outside [-1, n_slots) (both are otherwise passed over).
+ * released, parent and child are DEVICE arrays; table_out is `table` itself or
+ * does not overlap it.  With n_children = 0 the call only releases.
+ * `workspace`: device memory of gdn_pool_fork_workspace_bytes(n_children)
+ * bytes, 16-byte aligned; calls that share one are ordered on one stream.
+ */
+size_t gdn_pool_fork_workspace_bytes(int32_t n_children);
+int gdn_pool_fork(const gdn_pool* pools, int32_t n_pools, const int32_t* table, int32_t n_seqs, int32_t n_rows,
+                  const int32_t* released, int32_t n_released, const int32_t* parent, const int32_t* child,
+                  int32_t n_children, int32_t* table_out, void* workspace, size_t workspace_bytes, int32_t* status,
+                  void* stream);
+
+/*
+ * Release sequences and move the rows still in use together.  With L the
+ * number of rows below n_rows that the entries of `table` name once the
+ * sequences in released[n_released] have none, the rows in use end up in rows
+ * 0 .. L - 1: the m-th row in use at or above L (in row order) moves to the
+ * m-th free row below L, all others stay.  table_out is the table with the
+ * moved rows' new places and -1 for the released sequences; sequences that
+ * share a row still share it.  Entries at or above n_rows stay as they are.
+ * *count (nullable, DEVICE) receives L.  Vacated rows keep their contents.
+ * Other arguments and device errors as gdn_pool_fork; `workspace` holds
+ * gdn_pool_compact_workspace_bytes(n_rows) bytes.
+ */
+size_t gdn_pool_compact_workspace_bytes(int32_t n_rows);
+int gdn_pool_compact(const gdn_pool* pools, int32_t n_pools, const int32_t* table, int32_t n_seqs, int32_t n_rows,
+                     const int32_t* released, int32_t n_released, int32_t* table_out, int32_t* count, void* workspace,
+                     size_t workspace_bytes, int32_t* status, void* stream);
 
 /* Shape of a causal-convolution history commit. */
 typedef struct gdn_conv_shape {
