@@ -88,6 +88,11 @@ _SIGS = {
     "gdn_prefill_boundary_states": [_vp, _i32, _i32],
     "gdn_prefill_varlen": [ctypes.POINTER(GdnShape)] + [_vp] * 10 + [_i32, _vp, ctypes.c_size_t, _vp, _vp],
     "gdn_prefill_chunked_noalloc": [ctypes.POINTER(GdnShape)] + [_vp] * 10,
+    "gdn_scan_tape_bytes": [ctypes.POINTER(GdnShape), _vp],
+    "gdn_scan_forward_workspace_bytes": [ctypes.POINTER(GdnShape), _vp, _i32],
+    "gdn_scan_forward": [ctypes.POINTER(GdnShape)] + [_vp] * 11 + [ctypes.c_size_t, _vp, ctypes.c_size_t, _vp, _vp],
+    "gdn_scan_backward_workspace_bytes": [ctypes.POINTER(GdnShape), _vp],
+    "gdn_scan_backward": [ctypes.POINTER(GdnShape)] + [_vp] * 7 + [ctypes.c_size_t] + [_vp] * 9 + [ctypes.c_size_t, _vp],
     "gdn_pool_copy": [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp],
     "gdn_pool_fork_workspace_bytes": [_i32],
     "gdn_pool_fork": [_vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp],
@@ -96,6 +101,8 @@ _SIGS = {
 }
 _RESTYPES = {"gdn_status_string": ctypes.c_char_p, "gdn_prefill_workspace_bytes": ctypes.c_size_t,
              "gdn_prefill_varlen_workspace_bytes": ctypes.c_size_t, "gdn_prefill_boundary_states": ctypes.c_int64,
+             "gdn_scan_tape_bytes": ctypes.c_size_t, "gdn_scan_forward_workspace_bytes": ctypes.c_size_t,
+             "gdn_scan_backward_workspace_bytes": ctypes.c_size_t,
              "gdn_pool_fork_workspace_bytes": ctypes.c_size_t, "gdn_pool_compact_workspace_bytes": ctypes.c_size_t}
 
 
@@ -567,6 +574,93 @@ def gdn_prefill_varlen(cu_seqlens, q, k, v, alpha, beta, state, out, *, chunk_st
             _dev_ptr(status, "status"), _stream(stream))
     return _invoke("gdn_prefill_varlen", args, (sh, cu, q, k, v, alpha, beta, state, state_slot, out, chunk_states,
                                                 workspace, status), prepare)
+
+
+# ---------------------------------------------------------------------------
+# the training scan
+# ---------------------------------------------------------------------------
+def _scan_shape(cu, q, k, v, alpha, beta, out, n_slots, scale, out_name="out") -> GdnShape:
+    total, Hqk, dk = _shape_of(q, "q", 3)
+    _expect(k, "k", (total, Hqk, dk), q.dtype)
+    _expect(v, "v", (total, None, None), q.dtype)
+    if q.dtype not in _QKV:
+        raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
+    Hv, dv = v.shape[1], v.shape[2]
+    _expect(alpha, "alpha", (total, Hv), torch.float32)
+    _expect(beta, "beta", (total, Hv), torch.float32)
+    if out is None:
+        raise ValueError(f"{out_name} is required")
+    _expect(out, out_name, (total, Hv, dv), _OUT)
+    if int(cu[-1]) != total:
+        raise ValueError(f"cu_seqlens ends at {int(cu[-1])}, the inputs hold {total} tokens")
+    return GdnShape(cu.size - 1, total, Hqk, Hv, dk, dv, n_slots, _dtype_code(q), _dtype_code(out), GDN_F16,
+                    float(scale))
+
+
+def gdn_scan_tape_bytes(cu_seqlens, q, v) -> int:
+    """Bytes of the tape gdn_scan_forward writes for gdn_scan_backward (0: the shapes are refused)."""
+    cu = _host_cu(cu_seqlens)
+    total, Hqk, dk = _shape_of(q, "q", 3)
+    sh = GdnShape(cu.size - 1, total, Hqk, v.shape[1], dk, v.shape[2], 0, _dtype_code(q), GDN_F32, GDN_F16, 1.0)
+    return int(lib().gdn_scan_tape_bytes(ctypes.byref(sh), cu.ctypes.data))
+
+
+def gdn_scan_forward(cu_seqlens, q, k, v, alpha, beta, out, *, tape=None, state=None, state_slot=None,
+                     final_state=None, workspace=None, status=None, scale: float = 1.0, stream=None,
+                     prepare: bool = False):
+    """The recurrence over packed sequences at fp32 accuracy (q [total][h_qk][d_k], ...; ``cu_seqlens`` a host
+    array [B + 1]); see include/gdn.h.  ``tape``: uint8 device tensor of gdn_scan_tape_bytes bytes, for
+    :func:`gdn_scan_backward`.  ``workspace`` is allocated here with torch when omitted."""
+    cu = _host_cu(cu_seqlens)
+    sh = _scan_shape(cu, q, k, v, alpha, beta, out, state.shape[0] if state is not None else 0, scale)
+    if state is not None:
+        _check_state(state, state_slot, sh.batch, sh.h_v, sh.d_v, sh.d_k)
+    elif state_slot is not None:
+        raise ValueError("state_slot needs a state")
+    _expect(final_state, "final_state", (sh.batch, sh.h_v, sh.d_v, sh.d_k), torch.float32)
+    _expect(tape, "tape", (None,), torch.uint8)
+    _check_status(status)
+    _on_current_device("gdn_scan_forward", q, k, v, alpha, beta, out, tape, state, state_slot, final_state, workspace,
+                       status)
+    if workspace is None:
+        need = lib().gdn_scan_forward_workspace_bytes(ctypes.byref(sh), cu.ctypes.data, int(tape is not None))
+        workspace = _workspace(int(need), q.device, stream)
+    args = (ctypes.byref(sh), _vp(cu.ctypes.data), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+            _dev_ptr(alpha, "alpha"), _dev_ptr(beta, "beta"), _dev_ptr(state, "state"),
+            _dev_ptr(state_slot, "state_slot"), _dev_ptr(out, "out"), _dev_ptr(final_state, "final_state"),
+            _dev_ptr(tape, "tape"), ctypes.c_size_t(0 if tape is None else _bytes_of(tape)),
+            _dev_ptr(workspace, "workspace"), ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"),
+            _stream(stream))
+    return _invoke("gdn_scan_forward", args, (sh, cu, q, k, v, alpha, beta, state, state_slot, out, final_state, tape,
+                                              workspace, status), prepare)
+
+
+def gdn_scan_backward(cu_seqlens, q, k, v, alpha, beta, tape, dout, dq, dk, dv, dalpha, dbeta, *, dfinal=None,
+                      dstate=None, workspace=None, scale: float = 1.0, stream=None, prepare: bool = False):
+    """The gradients of :func:`gdn_scan_forward` from its tape, written to dq, dk, dv (q's dtype), dalpha, dbeta and
+    ``dstate`` (fp32); ``dfinal``: the gradient of the final states (zeros when omitted).  See include/gdn.h."""
+    cu = _host_cu(cu_seqlens)
+    sh = _scan_shape(cu, q, k, v, alpha, beta, dout, 0, scale, "dout")
+    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v), (dalpha, "dalpha", alpha), (dbeta, "dbeta", beta)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _expect(t, name, tuple(like.shape), like.dtype)
+    for t, name in ((dfinal, "dfinal"), (dstate, "dstate")):
+        _expect(t, name, (sh.batch, sh.h_v, sh.d_v, sh.d_k), torch.float32)
+    _expect(tape, "tape", (None,), torch.uint8)
+    _on_current_device("gdn_scan_backward", q, k, v, alpha, beta, tape, dout, dq, dk, dv, dalpha, dbeta, dfinal, dstate,
+                       workspace)
+    if workspace is None:
+        need = lib().gdn_scan_backward_workspace_bytes(ctypes.byref(sh), cu.ctypes.data)
+        workspace = _workspace(int(need), q.device, stream)
+    args = (ctypes.byref(sh), _vp(cu.ctypes.data), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+            _dev_ptr(alpha, "alpha"), _dev_ptr(beta, "beta"), _dev_ptr(tape, "tape"),
+            ctypes.c_size_t(0 if tape is None else _bytes_of(tape)), _dev_ptr(dout, "dout"), _dev_ptr(dfinal, "dfinal"),
+            _dev_ptr(dq, "dq"), _dev_ptr(dk, "dk"), _dev_ptr(dv, "dv"), _dev_ptr(dalpha, "dalpha"),
+            _dev_ptr(dbeta, "dbeta"), _dev_ptr(dstate, "dstate"), _dev_ptr(workspace, "workspace"),
+            ctypes.c_size_t(_bytes_of(workspace)), _stream(stream))
+    return _invoke("gdn_scan_backward", args, (sh, cu, q, k, v, alpha, beta, tape, dout, dfinal, dq, dk, dv, dalpha,
+                                               dbeta, dstate, workspace), prepare)
 
 
 # ---------------------------------------------------------------------------

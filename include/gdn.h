@@ -479,6 +479,58 @@ int gdn_prefill_varlen(const gdn_shape* shape, const int32_t* cu_seqlens, const 
                        void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
 /*
+ * The training scan: the recurrence over packed sequences at fp32 accuracy,
+ * with its gradients.  gdn_prefill_varlen evaluates the same rule for serving,
+ * with f16 matrix operands; here every product is fp32 (over the whole fp32
+ * range), so the gradients, those of the gates included, are accurate to fp32.
+ *
+ * cu_seqlens is a HOST array [batch + 1] as for gdn_prefill_varlen (batch
+ * equal sequences [B][T] are the offsets 0, T, 2 T, ...), and q, k [total]
+ * [h_qk][d_k], v, out [total][h_v][d_v], alpha, beta [total][h_v] are packed
+ * alike (total = shape.n_nodes).  q, k, v are F32 or BF16, out F32, F16 or
+ * BF16; d_k is 32, 64 or 128, d_v a multiple of 16 up to 256.  alpha is at
+ * least 0; below 2^-60 it counts as 2^-60 (a state carried over with that
+ * factor leaves no trace in fp32).
+ *
+ * gdn_scan_forward starts sequence b from state[slot(b)] (only read), or from
+ * zeros where `state` is NULL, and writes `out` and the fp32 state after the
+ * last token to final_state[b] (nullable; may be `state` itself when state_slot
+ * is NULL).  A sequence without tokens has its initial state as its final one.
+ * A slot outside [0, n_slots) skips the sequence (its outputs are left as they
+ * were, and so are its gradients in the backward pass) and sets *status.
+ *
+ * `tape` (gdn_scan_tape_bytes bytes) receives what the backward pass needs
+ * besides the inputs: the state before every 64-token chunk, the delta rule's
+ * errors, the chunks' triangular inverses and the gates, about 8.1 MB per 64
+ * tokens at 48 value heads and d_k = d_v = 128.  Without one (NULL) the
+ * workspace holds it during the call.
+ *
+ * gdn_scan_backward takes the same shape, cu_seqlens and inputs, the tape as
+ * gdn_scan_forward left it, the gradients dout (out_dtype) of the outputs and
+ * dfinal (nullable: zeros) of the final states, and writes the gradients dq,
+ * dk, dv (qkv_dtype; those of a q/k head are summed over its value heads in
+ * fp32), dalpha, dbeta (fp32) and dstate [B][h_v][d_v][d_k] (nullable) of the
+ * inputs and the initial states.  The tape is only read: a second backward pass
+ * over it gives the same result.  Nothing is accumulated with atomics; results
+ * repeat bit for bit.
+ *
+ * tape, workspaces, dout, dfinal and dstate are 16-byte aligned, the other
+ * outputs 4-byte.  The workspaces' contents on entry are ignored; calls that
+ * share one are ordered on one stream.
+ */
+size_t gdn_scan_tape_bytes(const gdn_shape* shape, const int32_t* cu_seqlens);
+size_t gdn_scan_forward_workspace_bytes(const gdn_shape* shape, const int32_t* cu_seqlens, int32_t with_tape);
+int gdn_scan_forward(const gdn_shape* shape, const int32_t* cu_seqlens, const void* q, const void* k, const void* v,
+                     const float* alpha, const float* beta, const float* state, const int32_t* state_slot, void* out,
+                     float* final_state, void* tape, size_t tape_bytes, void* workspace, size_t workspace_bytes,
+                     int32_t* status, void* stream);
+size_t gdn_scan_backward_workspace_bytes(const gdn_shape* shape, const int32_t* cu_seqlens);
+int gdn_scan_backward(const gdn_shape* shape, const int32_t* cu_seqlens, const void* q, const void* k, const void* v,
+                      const float* alpha, const float* beta, const void* tape, size_t tape_bytes, const void* dout,
+                      const float* dfinal, void* dq, void* dk, void* dv, float* dalpha, float* dbeta, float* dstate,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Plan (and validate) the walk gdn_verify_tree takes through one tree.
  * Host-only; enqueues nothing.  Writes n_nodes steps to `walk` (host,
  * uint16 each): bits 0-4 the node, bit 5 "restore the parent's state from
