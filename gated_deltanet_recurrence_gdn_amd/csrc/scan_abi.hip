@@ -61,18 +61,20 @@ size_t carve_tape(const gdn_shape* sh, int64_t units, void* base, ScanArgs* a) {
 
 size_t carve_forward(const gdn_shape* sh, int64_t units, bool tape_inside, void* base, ScanArgs* a) {
     Carver c{static_cast<unsigned char*>(base)};
-    a->W = c.take<float>((size_t)units * sh->h_v * kScanChunk * sh->d_k);
-    a->Kt = c.take<float>((size_t)units * sh->h_qk * kScanChunk * sh->d_k);
+    const size_t chunk = (size_t)kScanChunk * sh->d_k, parts = sh->qkv_dtype == GDN_BF16 ? 1 : 3;
+    a->W = c.take<uint16_t>((size_t)units * sh->h_v * 3 * chunk);
+    a->Kt = c.take<uint16_t>((size_t)units * sh->h_qk * parts * chunk);
     if (tape_inside) c.used += carve_tape(sh, units, base == nullptr ? nullptr : c.base + c.used, a);
     return c.used;
 }
 
 size_t carve_backward(const gdn_shape* sh, int64_t units, void* base, ScanArgs* a) {
     Carver c{static_cast<unsigned char*>(base)};
-    const size_t heads = (size_t)units * sh->h_v, qk = (size_t)units * sh->h_qk * kScanChunk * sh->d_k;
-    a->W = c.take<float>(heads * kScanChunk * sh->d_k);
-    a->Kt = c.take<float>(qk);
-    a->Qt = c.take<float>(qk);
+    const size_t heads = (size_t)units * sh->h_v, chunk = (size_t)kScanChunk * sh->d_k;
+    const size_t qk = (size_t)units * sh->h_qk * (sh->qkv_dtype == GDN_BF16 ? 1 : 3) * chunk;
+    a->W = c.take<uint16_t>(heads * 3 * chunk);
+    a->Kt = c.take<uint16_t>(qk);
+    a->Qt = c.take<uint16_t>(qk);
     a->dR = c.take<float>(heads * kScanChunk * sh->d_v);
     a->G = c.take<float>(heads * sh->d_v * sh->d_k);
     return c.used;
@@ -181,7 +183,7 @@ int gdn_scan_backward(const gdn_shape* shape, const int32_t* cu_seqlens, const v
     if ((rc = check_inputs(sh, q, k, v, alpha, beta)) != GDN_OK) return rc;
     if (sh->n_nodes > 0 && (!dout || !dq || !dk || !dv || !dalpha || !dbeta)) return GDN_ERR_NULL;
     if (!aligned(dout, 16) || !aligned(dfinal, 16) || !aligned(dstate, 16) || !aligned(dq, 4) || !aligned(dk, 4) ||
-        !aligned(dv, 4) || !aligned(dalpha, 4) || !aligned(dbeta, 4))
+        !aligned(dv, 16) || !aligned(dalpha, 4) || !aligned(dbeta, 4))
         return GDN_ERR_ALIGN;
     ScanArgs a;
     std::memset(&a, 0, sizeof(a));

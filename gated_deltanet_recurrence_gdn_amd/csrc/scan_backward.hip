@@ -3,7 +3,7 @@
 // Three launches (notation in scan_internal.h).  scan_back_prepare, one
 // workgroup per chunk and value head, forms what does not depend on the state's
 // gradient: Wb and dR0.  scan_back_state, one workgroup per sequence, value head
-// and 16 value columns, walks the chunks backwards: dR = dR0 + Wb G^T, dv, then
+// and 16 value columns, walks the chunks backwards: dR = dR0 + Wb G^T, then
 // the gradient G of the state before the chunk.  scan_grad, one workgroup per
 // chunk and q/k head, forms the other gradients from the stored states, errors
 // and their gradients, its value heads one after the other: the gradients of a
@@ -22,7 +22,7 @@
 namespace gdn {
 namespace {
 
-template <int DK>
+template <int DK, int TK>
 __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a, const PrefillSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY, kQZ = kScanChunk * (LDK > LDY ? LDK : LDY);
     extern __shared__ __align__(16) float lds[];
@@ -51,11 +51,11 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
     __syncthreads();
     const float *be = gt + 128, *er = gt + 320;
     if (h % a.group == 0) {  // K and Q laid out for the state kernel
-        const size_t at = ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (DK * kScanChunk);
+        const size_t at = ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk);
         for (int p = tid; p < DK * (kScanChunk / 4); p += 512) {
             const int c = p / (kScanChunk / 4), i = p % (kScanChunk / 4) * 4;
-            st4(a.Kt + at + c * kScanChunk + i, ld_col4(Kl + i * LDK + c, LDK));
-            st4(a.Qt + at + c * kScanChunk + i, ld_col4(QZ + i * LDK + c, LDK));
+            store_parts<TK>(a.Kt + at + c * kScanChunk + i, DK * kScanChunk, ld_col4(Kl + i * LDK + c, LDK));
+            store_parts<TK>(a.Qt + at + c * kScanChunk + i, DK * kScanChunk, ld_col4(QZ + i * LDK + c, LDK));
         }
     }
     // P, lower tiles
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
     {
         constexpr int NT = DK / 16, MW = NT / 2;  // waves share the key columns' tiles, 4 / (8 / NT) row tiles each
         const int n = wave % NT, m0 = wave / NT * MW;
-        float* w = a.W + uh * (kScanChunk * DK);
+        uint16_t* w = a.W + uh * (3 * kScanChunk * DK);
         f32x4 c[MW] = {};
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -129,15 +129,13 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
             for (int s = 0; s < 4; ++s) x[s] *= be[i + s] * er[i + s];
 #pragma unroll
             for (int m = 0; m < MW; ++m)
-                if (m0 + m <= kk) c[m] = mma16(ld_col4(Yl + i * LDY + 16 * (m0 + m) + col, LDY), x, c[m]);
+                if (m0 + m <= kk) c[m] = mma16(x, ld_col4(Yl + i * LDY + 16 * (m0 + m) + col, LDY), c[m]);
         }
 #pragma unroll
-        for (int m = 0; m < MW; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = 16 * (m0 + m) + 4 * g + r;
-                w[j * DK + 16 * n + col] = er[j] * Kl[j * LDK + 16 * n + col] - c[m][r];
-            }
+        for (int m = 0; m < MW; ++m) {  // transposed: a lane has four neighbours of a token's row
+            const int j = 16 * (m0 + m) + col;
+            store_parts<3>(w + j * DK + 16 * n + 4 * g, kScanChunk * DK, er[j] * ld4(Kl + j * LDK + 16 * n + 4 * g) - c[m]);
+        }
     }
     // dR0_j = scale sum_{i >= j} Z_ij dO_i
     for (int c0 = 16 * wave; c0 < a.d_v; c0 += 128) {
@@ -162,105 +160,146 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
 }
 
 // The gradient's walk, the mirror image of scan_state: G^T in accumulators, two
-// matrix operands (K and Q) and two exchanged right sides.
-template <int DK>
+// matrix operands (K and Q) and two exchanged right sides, the same two operand
+// sets that take turns.  OT: the type of dout, whose values stay as loaded until
+// they are used.
+template <int DK, int TK, typename OT>
 struct BackOperands {
     static constexpr int kTiles = DK / 16 >= 4 ? DK / 64 : 1;
-    f32x4 w[DK / 16], kt[kTiles][4], qt[kTiles][4], e, o, be, eb;
+    bf16x8 w[DK / 32][3], kt[kTiles][2][TK], qt[kTiles][2][TK];
+    f32x4 e, be, eb;
+    OT o[4];
     float decay;
 };
 
-template <int DK>
-__device__ __forceinline__ void load_back_operands(const ScanArgs& a, int unit, int tok, int len, int h, int c0, int wave,
-                                                   int col, int g, BackOperands<DK>& o) {
-    const size_t uh = (size_t)unit * a.h_v + h;
-    const float* w = a.W + uh * (kScanChunk * DK) + (16 * wave + col) * DK + 4 * g;
-#pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) o.w[kk] = ld4(w + 16 * kk);
-    if (wave < DK / 16) {
-        const size_t at = ((size_t)unit * a.h_qk + h / a.group) * (DK * kScanChunk) + (16 * wave * o.kTiles + col) * kScanChunk + 4 * g;
-#pragma unroll
-        for (int i = 0; i < o.kTiles; ++i)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                o.kt[i][kk] = ld4(a.Kt + at + 16 * i * kScanChunk + 16 * kk);
-                o.qt[i][kk] = ld4(a.Qt + at + 16 * i * kScanChunk + 16 * kk);
-            }
-    }
-    const int i0 = 16 * wave + 4 * g;
-    const float* e = a.dR + uh * ((size_t)kScanChunk * a.d_v) + (size_t)i0 * a.d_v + c0 + col;
-    o.e = f32x4{e[0], e[a.d_v], e[2 * a.d_v], e[3 * a.d_v]};
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        o.o[r] = i0 + r < len ? load_out(a.dout, ((size_t)(tok + i0 + r) * a.h_v + h) * a.d_v + c0 + col, a.out_dtype) : 0.f;
-    const float* gt = a.gates + uh * (kGateRows * kScanChunk);
-    o.be = ld4(gt + 128 + i0);
-    o.eb = ld4(gt + 256 + i0);
-    o.decay = gt[256 + 63];
-}
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(_Float16 x) { return (float)x; }
+__device__ __forceinline__ float to_f32(uint16_t x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }  // bf16
 
-template <int DK>
-__global__ __launch_bounds__(256) void scan_back_state_kernel(const ScanArgs a, const PrefillSeqs seqs) {
-    constexpr int LDK = DK + 4, LDU = kScanLdY, TPW = BackOperands<DK>::kTiles;
-    __shared__ __align__(16) float Gl[16 * LDK];
-    __shared__ __align__(16) float Ul[16 * LDU];
-    __shared__ __align__(16) float Ol[16 * LDU];
+template <int DK, int TK, typename OT>
+__global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+    using Ops = BackOperands<DK, TK, OT>;
+    constexpr int LDK = DK + 8, LDU = kScanChunk + 8, TPW = Ops::kTiles;
+    constexpr int PG = 16 * LDK, PU = 16 * LDU;  // a part's plane
+    __shared__ __align__(16) uint16_t Gl[3 * PG];
+    __shared__ __align__(16) uint16_t Ul[3 * PU];
+    __shared__ __align__(16) uint16_t Ol[3 * PU];
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int c0 = lb % a.slices * 16, h = lb / a.slices % a.h_v, s = lb / a.slices / a.h_v;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
     const int b = a.seq0 + s, T = seqs.len[s], t0 = seqs.tok0[s], u0 = a.unit_base + seqs.unit0[s];
     const int n_units = (T + kScanChunk - 1) / kScanChunk;
     if (a.valid[b] == 0) return;
-    const bool owns = wave < DK / 16;
-    const int k0 = 16 * wave * TPW + 4 * g;
+    const bool owns = DK >= 64 || wave < DK / 16;
+    const int k0 = 16 * wave * TPW + 4 * g, i0 = 16 * wave + 4 * g;
+    const size_t head = (size_t)a.d_v * DK, e_unit = (size_t)kScanChunk * a.d_v;
     f32x4 G[TPW] = {};
-    const size_t seq_at = ((size_t)b * a.h_v + h) * ((size_t)a.d_v * DK) + (size_t)(c0 + col) * DK + k0;
+    const size_t seq_at = ((size_t)b * a.h_v + h) * head + (size_t)(c0 + col) * DK + k0;
     if (owns && a.dfinal != nullptr)
 #pragma unroll
         for (int i = 0; i < TPW; ++i) G[i] = ld4(a.dfinal + seq_at + 16 * i);
-    BackOperands<DK> cur, next;
-    if (n_units > 0)
-        load_back_operands<DK>(a, u0 + n_units - 1, t0 + (n_units - 1) * kScanChunk, T - (n_units - 1) * kScanChunk, h, c0, wave, col, g, cur);
-    for (int c = n_units - 1; c >= 0; --c) {
+    const OT* dout = static_cast<const OT*>(a.dout) + (size_t)h * a.d_v + c0 + col;
+    auto load = [&](int c, Ops& o) {
+        c = c < 0 ? 0 : c;
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        const int tok = t0 + c * kScanChunk, len = T - c * kScanChunk < kScanChunk ? T - c * kScanChunk : kScanChunk;
-        if (c > 0) load_back_operands<DK>(a, u0 + c - 1, tok - kScanChunk, kScanChunk, h, c0, wave, col, g, next);
+        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (16 * wave + col) * DK + 8 * g;
+#pragma unroll
+        for (int kk = 0; kk < DK / 32; ++kk)
+#pragma unroll
+            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + t * (kScanChunk * DK) + 32 * kk);
         if (owns) {
-            float* st = a.G + uh * ((size_t)a.d_v * DK) + (size_t)(c0 + col) * DK + k0;
+            const size_t at = ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (16 * wave * TPW + col) * kScanChunk + 8 * g;
+#pragma unroll
+            for (int i = 0; i < TPW; ++i)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int t = 0; t < TK; ++t) {
+                        o.kt[i][kk][t] = ld_bf8(a.Kt + at + t * (DK * kScanChunk) + 16 * i * kScanChunk + 32 * kk);
+                        o.qt[i][kk][t] = ld_bf8(a.Qt + at + t * (DK * kScanChunk) + 16 * i * kScanChunk + 32 * kk);
+                    }
+        }
+        const float* e = a.dR + uh * e_unit + (size_t)i0 * a.d_v + c0 + col;
+        o.e = f32x4{e[0], e[a.d_v], e[2 * a.d_v], e[3 * a.d_v]};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // past the sequence's end: its last token's, used as zero
+            const int t = c * kScanChunk + i0 + r;
+            o.o[r] = dout[(size_t)(t0 + (t < T ? t : T - 1)) * a.h_v * a.d_v];
+        }
+        const float* gt = a.gates + uh * (kGateRows * kScanChunk);
+        o.be = ld4(gt + 128 + i0);
+        o.eb = ld4(gt + 256 + i0);
+        o.decay = gt[256 + 63];
+    };
+    auto step = [&](int c, const Ops& cur, Ops& next) {
+        const size_t uh = (size_t)(u0 + c) * a.h_v + h;
+        load(c - 1, next);
+        if (owns) {
+            float* st = a.G + uh * head + (size_t)(c0 + col) * DK + k0;
 #pragma unroll
             for (int i = 0; i < TPW; ++i) {
-                st4(Gl + col * LDK + k0 + 16 * i, G[i]);
+                store_parts<3>(Gl + col * LDK + k0 + 16 * i, PG, G[i]);
                 st4(st + 16 * i, G[i]);
             }
         }
-        __syncthreads();
-        f32x4 x = cur.e;
+        {
+            f32x4 o;
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) x = mma16(cur.w[kk], ld4(Gl + col * LDK + 16 * kk + 4 * g), x);
-        const int i0 = 16 * wave + 4 * g;
-        float* e = a.dR + uh * ((size_t)kScanChunk * a.d_v) + (size_t)i0 * a.d_v + c0 + col;
-        const f32x4 dv = cur.be * x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            e[(size_t)r * a.d_v] = x[r];
-            if (i0 + r < len) store_typed(a.dv, ((size_t)(tok + i0 + r) * a.h_v + h) * a.d_v + c0 + col, dv[r], a.qkv_bf16);
+            for (int r = 0; r < 4; ++r) o[r] = c * kScanChunk + i0 + r < T ? a.scale * to_f32(cur.o[r]) : 0.f;
+            store_parts<3>(Ol + col * LDU + i0, PU, cur.eb * o);
         }
-        st4(Ul + col * LDU + i0, -(cur.eb * dv));
-        st4(Ol + col * LDU + i0, a.scale * (cur.eb * cur.o));
+        __syncthreads();
+        f32x4 x[3] = {};
+        f32x4 y[TPW][3] = {};
+        {
+            bf16x8 f[DK / 32][3], fo[2][3];
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk)
+#pragma unroll
+                for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Gl + t * PG + col * LDK + 32 * kk + 8 * g);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int t = 0; t < 3; ++t) fo[kk][t] = ld_bf8(Ol + t * PU + col * LDU + 32 * kk + 8 * g);
+            __builtin_amdgcn_sched_barrier(0);  // every read is on its way before the products start
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk) mma_parts<3, 3>(cur.w[kk], f[kk], x);
+            // dout's part of the new gradient does not wait for dR
+#pragma unroll
+            for (int i = 0; i < TPW; ++i) y[i][0] = G[i] * cur.decay;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < TPW; ++i) mma_parts<TK, 3>(cur.qt[i][kk], fo[kk], y[i]);
+        }
+        const f32x4 dr = cur.e + sum_parts(x);
+        store_parts<3>(Ul + col * LDU + i0, PU, -(cur.eb * cur.be * dr));
+        float* e = a.dR + uh * e_unit + (size_t)i0 * a.d_v + c0 + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) e[(size_t)r * a.d_v] = dr[r];
         __syncthreads();
         if (owns) {
+            bf16x8 f[2][3];
 #pragma unroll
-            for (int i = 0; i < TPW; ++i) {
-                f32x4 y = G[i] * cur.decay;
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    y = mma16(cur.kt[i][kk], ld4(Ul + col * LDU + 16 * kk + 4 * g), y);
-                    y = mma16(cur.qt[i][kk], ld4(Ol + col * LDU + 16 * kk + 4 * g), y);
-                }
-                G[i] = y;
-            }
+                for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Ul + t * PU + col * LDU + 32 * kk + 8 * g);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < TPW; ++i) mma_parts<TK, 3>(cur.kt[i][kk], f[kk], y[i]);
+#pragma unroll
+            for (int i = 0; i < TPW; ++i) G[i] = sum_parts(y[i]);
         }
-        cur = next;
+    };
+    if (n_units > 0) {
+        Ops p, q;
+        load(n_units - 1, p);
+        for (int c = n_units - 1; c >= 0; c -= 2) {
+            step(c, p, q);
+            if (c > 0) step(c - 1, q, p);
+        }
     }
     if (owns && a.dstate != nullptr)
 #pragma unroll
@@ -355,7 +394,9 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
                     f32x4 x = {};
                     if (i < len) x = load4_out(a.dout, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, a.out_dtype);
                     st4(st + i * LDS + c, x);
-                    st4(st + (kScanChunk + i) * LDS + c, ld4(a.dR + at));
+                    const f32x4 dr = ld4(a.dR + at);
+                    st4(st + (kScanChunk + i) * LDS + c, dr);
+                    if (i < len) store4_typed(a.dv, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, gt[128 + i] * dr, a.qkv_bf16);
                     st4(st + (2 * kScanChunk + i) * LDS + c, ld4(a.E + at));
                 }
             }
@@ -508,7 +549,7 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
         }
 }
 
-template <int DK>
+template <int DK, int TK>
 hipError_t launch_backward(const ScanArgs& args, const PrefillSeqs& seqs, hipStream_t st) {
     ScanArgs a = args;
     hipError_t e;
@@ -516,12 +557,15 @@ hipError_t launch_backward(const ScanArgs& args, const PrefillSeqs& seqs, hipStr
         constexpr int LDK = DK + 4;
         constexpr size_t lds = sizeof(float) * (kScanChunk * LDK + kScanChunk * (LDK > kScanLdY ? LDK : kScanLdY) +
                                                 kScanChunk * kScanLdY + kGateRows * kScanChunk);
-        if ((e = allow_max_lds<scan_back_prepare_kernel<DK>>()) != hipSuccess) return e;
-        hipLaunchKernelGGL(scan_back_prepare_kernel<DK>, dim3((unsigned)(a.units * a.h_v)), dim3(512), lds, st, a, seqs);
+        if ((e = allow_max_lds<scan_back_prepare_kernel<DK, TK>>()) != hipSuccess) return e;
+        hipLaunchKernelGGL((scan_back_prepare_kernel<DK, TK>), dim3((unsigned)(a.units * a.h_v)), dim3(512), lds, st, a, seqs);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     a.slices = a.d_v / 16;
-    hipLaunchKernelGGL(scan_back_state_kernel<DK>, dim3((unsigned)(a.n_seq * a.h_v * a.slices)), dim3(256), 0, st, a, seqs);
+    const dim3 grid((unsigned)(a.n_seq * a.h_v * a.slices));
+    if (a.out_dtype == GDN_F32) hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, float>), grid, dim3(256), 0, st, a, seqs);
+    else if (a.out_dtype == GDN_F16) hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, _Float16>), grid, dim3(256), 0, st, a, seqs);
+    else hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, uint16_t>), grid, dim3(256), 0, st, a, seqs);
     if ((e = hipGetLastError()) != hipSuccess || a.units == 0) return e;
     if ((e = allow_max_lds<scan_grad_kernel<DK>>()) != hipSuccess) return e;
     hipLaunchKernelGGL(scan_grad_kernel<DK>, dim3((unsigned)(a.units * a.h_qk)), dim3(kGradThreads),
@@ -532,9 +576,13 @@ hipError_t launch_backward(const ScanArgs& args, const PrefillSeqs& seqs, hipStr
 }  // namespace
 
 hipError_t launch_scan_backward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream) {
-    return d_k == 128 ? launch_backward<128>(a, seqs, stream)
-         : d_k == 64  ? launch_backward<64>(a, seqs, stream)
-                      : launch_backward<32>(a, seqs, stream);
+    if (input_parts(a) == 1)
+        return d_k == 128 ? launch_backward<128, 1>(a, seqs, stream)
+             : d_k == 64  ? launch_backward<64, 1>(a, seqs, stream)
+                          : launch_backward<32, 1>(a, seqs, stream);
+    return d_k == 128 ? launch_backward<128, 3>(a, seqs, stream)
+         : d_k == 64  ? launch_backward<64, 3>(a, seqs, stream)
+                      : launch_backward<32, 3>(a, seqs, stream);
 }
 
 }  // namespace gdn

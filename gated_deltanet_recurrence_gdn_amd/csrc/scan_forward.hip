@@ -14,9 +14,12 @@
 namespace gdn {
 namespace {
 
+#ifndef SCAN_NS
+#define SCAN_NS 1
+#endif
 constexpr int kPrepThreads = 256;
 
-template <int DK>
+template <int DK, int TK>
 __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanArgs a, const PrefillSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY;
     __shared__ __align__(16) float Kl[kScanChunk * LDK];
@@ -98,10 +101,10 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
             Yl[i * LDY + lane] = y;
         }
     } else if (h % a.group == 0) {
-        float* kt = a.Kt + ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (DK * kScanChunk);
+        uint16_t* kt = a.Kt + ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk);
         for (int p = tid - 64; p < DK * (kScanChunk / 4); p += kPrepThreads - 64) {
             const int c = p / (kScanChunk / 4), i = p % (kScanChunk / 4) * 4;
-            st4(kt + c * kScanChunk + i, ld_col4(Kl + i * LDK + c, LDK));
+            store_parts<TK>(kt + c * kScanChunk + i, DK * kScanChunk, ld_col4(Kl + i * LDK + c, LDK));
         }
     }
     __syncthreads();
@@ -114,8 +117,8 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
         }
     }
 
-    // W = 2^b K - Y (beta 2^b K)
-    float* w = a.W + uh * (kScanChunk * DK);
+    // W^T = (2^b K)^T - (beta 2^b K)^T Y^T: a lane has four neighbours of a token's row
+    uint16_t* w = a.W + uh * (3 * kScanChunk * DK);
     for (int n = wave; n < DK / 16; n += 4) {
         f32x4 c[4] = {};
 #pragma unroll
@@ -125,15 +128,13 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 #pragma unroll
             for (int s = 0; s < 4; ++s) x[s] *= be[j + s] * eb[j + s];
 #pragma unroll
-            for (int m = kk; m < 4; ++m) c[m] = mma16(ld4(Yl + (16 * m + col) * LDY + j), x, c[m]);
+            for (int m = kk; m < 4; ++m) c[m] = mma16(x, ld4(Yl + (16 * m + col) * LDY + j), c[m]);
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * g + r;
-                w[i * DK + 16 * n + col] = eb[i] * Kl[i * LDK + 16 * n + col] - c[m][r];
-            }
+        for (int m = 0; m < 4; ++m) {
+            const int i = 16 * m + col;
+            store_parts<3>(w + i * DK + 16 * n + 4 * g, kScanChunk * DK, eb[i] * ld4(Kl + i * LDK + 16 * n + 4 * g) - c[m]);
+        }
     }
     // E0 = V - Y (beta V), 64 value columns at a time
     for (int c0 = 0; c0 < a.d_v; c0 += 64) {
@@ -173,42 +174,25 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 // d_k / 4 key rows of the state (as S^T, in accumulators); both are exchanged
 // through LDS, in an order that makes a lane's four values one 16-byte piece.
 // The matrix operands come straight from global memory into registers, one
-// chunk ahead.
-template <int DK, int NS>
+// chunk ahead: two sets that take turns (nothing is copied between them), loaded
+// without branches (the last chunk loads itself again) and used as loaded, so
+// that no step waits for its own loads or for its stores.
+template <int DK, int NS, int TK>
 struct StateOperands {
     static constexpr int kTiles = DK / 16 >= 4 ? DK / 64 : 1;
-    f32x4 w[DK / 16], kt[kTiles][4], e[NS], g;
+    bf16x8 w[DK / 32][3], kt[kTiles][2][TK];
+    f32x4 e[NS], be, er;
     float decay;
 };
 
-template <int DK, int NS>
-__device__ __forceinline__ void load_state_operands(const ScanArgs& a, int unit, int h, int c0, int wave, int col, int g,
-                                                    StateOperands<DK, NS>& o) {
-    const size_t uh = (size_t)unit * a.h_v + h;
-    const float* w = a.W + uh * (kScanChunk * DK) + (16 * wave + col) * DK + 4 * g;
-#pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) o.w[kk] = ld4(w + 16 * kk);
-    const float* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (DK * kScanChunk);
-    if (wave < DK / 16) {
-#pragma unroll
-        for (int i = 0; i < o.kTiles; ++i)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) o.kt[i][kk] = ld4(kt + (16 * (wave * o.kTiles + i) + col) * kScanChunk + 16 * kk + 4 * g);
-    }
-    const float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + (size_t)(16 * wave + 4 * g) * a.d_v + c0 + col;
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-        if (c0 + 16 * n < a.d_v) o.e[n] = f32x4{e[16 * n], e[16 * n + a.d_v], e[16 * n + 2 * a.d_v], e[16 * n + 3 * a.d_v]};
-    const float* gt = a.gates + uh * (kGateRows * kScanChunk);
-    o.g = ld4(gt + 128 + 16 * wave + 4 * g) * ld4(gt + 320 + 16 * wave + 4 * g);  // beta 2^(b_63 - b)
-    o.decay = gt[256 + 63];
-}
-
-template <int DK, int NS>
-__global__ __launch_bounds__(256) void scan_state_kernel(const ScanArgs a, const PrefillSeqs seqs) {
-    constexpr int LDK = DK + 4, LDU = kScanLdY, TPW = StateOperands<DK, NS>::kTiles;
-    __shared__ __align__(16) float Sl[16 * NS * LDK];
-    __shared__ __align__(16) float Ul[16 * NS * LDU];
+template <int DK, int NS, int TK>
+__global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+    using Ops = StateOperands<DK, NS, TK>;
+    // rows of bf16 in LDS, 16 bytes apart modulo the 64 banks: 16 lanes' 16-byte reads meet no bank twice
+    constexpr int LDK = DK + 8, LDU = kScanChunk + 8, TPW = Ops::kTiles;
+    constexpr int PS = 16 * NS * LDK, PU = 16 * NS * LDU;  // a part's plane
+    __shared__ __align__(16) uint16_t Sl[3 * PS];
+    __shared__ __align__(16) uint16_t Ul[3 * PU];
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int c0 = lb % a.slices * (16 * NS), h = lb / a.slices % a.h_v, s = lb / a.slices / a.h_v;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
@@ -227,80 +211,148 @@ __global__ __launch_bounds__(256) void scan_state_kernel(const ScanArgs a, const
     }
     if (lead) a.valid[b] = 1;
 
-    const bool owns = wave < DK / 16;  // of the state's key rows
+    const bool owns = DK >= 64 || wave < DK / 16;  // of the state's key rows
     const int k0 = 16 * wave * TPW + 4 * g;
+    // a slice past d_v (NS = 2, odd number of tiles) repeats the first tile and stores nothing
+    int cn[NS];
+    bool in[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        in[n] = n == 0 || c0 + 16 * n < a.d_v;
+        cn[n] = c0 + (in[n] ? 16 * n : 0) + col;
+    }
+    const size_t head = (size_t)a.d_v * DK, e_unit = (size_t)kScanChunk * a.d_v;
     f32x4 S[TPW][NS] = {};
     if (owns && a.state != nullptr) {
-        const float* st = a.state + ((size_t)row * a.h_v + h) * ((size_t)a.d_v * DK);
+        const float* st = a.state + ((size_t)row * a.h_v + h) * head + k0;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
-            if (c0 + 16 * n < a.d_v)
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) S[i][n] = ld4(st + (size_t)(c0 + 16 * n + col) * DK + k0 + 16 * i);
+            for (int i = 0; i < TPW; ++i) S[i][n] = ld4(st + (size_t)cn[n] * DK + 16 * i);
     }
-    StateOperands<DK, NS> cur, next;
-    if (n_units > 0) load_state_operands<DK, NS>(a, u0, h, c0, wave, col, g, cur);
-    for (int c = 0; c < n_units; ++c) {
-        const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        if (c + 1 < n_units) load_state_operands<DK, NS>(a, u0 + c + 1, h, c0, wave, col, g, next);
+    auto load = [&](int c, Ops& o) {
+        const int unit = u0 + (c < n_units ? c : n_units - 1);
+        const size_t uh = (size_t)unit * a.h_v + h;
+        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (16 * wave + col) * DK + 8 * g;
+#pragma unroll
+        for (int kk = 0; kk < DK / 32; ++kk)
+#pragma unroll
+            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + t * (kScanChunk * DK) + 32 * kk);
         if (owns) {
-            float* st = a.S + uh * ((size_t)a.d_v * DK);
+            const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (16 * wave * TPW + col) * kScanChunk + 8 * g;
+#pragma unroll
+            for (int i = 0; i < TPW; ++i)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + t * (DK * kScanChunk) + 16 * i * kScanChunk + 32 * kk);
+        }
+        const float* e = a.E + uh * e_unit + (size_t)(16 * wave + 4 * g) * a.d_v;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            const float* p = e + cn[n];
+            o.e[n] = f32x4{p[0], p[a.d_v], p[2 * a.d_v], p[3 * a.d_v]};
+        }
+        const float* gt = a.gates + uh * (kGateRows * kScanChunk);
+        o.be = ld4(gt + 128 + 16 * wave + 4 * g);
+        o.er = ld4(gt + 320 + 16 * wave + 4 * g);
+        o.decay = gt[256 + 63];
+    };
+    auto step = [&](int c, const Ops& cur, Ops& next) {
+        const size_t uh = (size_t)(u0 + c) * a.h_v + h;
+        load(c + 1, next);
+        if (owns) {
+            float* st = a.S + uh * head + k0;
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int i = 0; i < TPW; ++i) {
-                    st4(Sl + (16 * n + col) * LDK + k0 + 16 * i, S[i][n]);
-                    if (c0 + 16 * n < a.d_v) st4(st + (size_t)(c0 + 16 * n + col) * DK + k0 + 16 * i, S[i][n]);
+                    store_parts<3>(Sl + (16 * n + col) * LDK + k0 + 16 * i, PS, S[i][n]);
+                    if (in[n]) st4(st + (size_t)cn[n] * DK + 16 * i, S[i][n]);
                 }
         }
         __syncthreads();
-        f32x4 x[NS] = {};
+        f32x4 x[NS][3] = {};
+        {
+            bf16x8 f[DK / 32][NS][3];
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk)
+            for (int kk = 0; kk < DK / 32; ++kk)
 #pragma unroll
-            for (int n = 0; n < NS; ++n) x[n] = mma16(cur.w[kk], ld4(Sl + (16 * n + col) * LDK + 16 * kk + 4 * g), x[n]);
-        float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + (size_t)(16 * wave + 4 * g) * a.d_v + c0 + col;
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) f[kk][n][t] = ld_bf8(Sl + t * PS + (16 * n + col) * LDK + 32 * kk + 8 * g);
+            __builtin_amdgcn_sched_barrier(0);  // every read is on its way before the products start
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk)
+#pragma unroll
+                for (int n = 0; n < NS; ++n) mma_parts<3, 3>(cur.w[kk], f[kk][n], x[n]);
+        }
+        float* e = a.E + uh * e_unit + (size_t)(16 * wave + 4 * g) * a.d_v;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            if (c0 + 16 * n >= a.d_v) continue;
-            const f32x4 y = cur.e[n] - x[n];
+            const f32x4 y = cur.e[n] - sum_parts(x[n]);
+            store_parts<3>(Ul + (16 * n + col) * LDU + 16 * wave + 4 * g, PU, cur.be * cur.er * y);
+            if (in[n])
 #pragma unroll
-            for (int r = 0; r < 4; ++r) e[16 * n + (size_t)r * a.d_v] = y[r];
-            st4(Ul + (16 * n + col) * LDU + 16 * wave + 4 * g, cur.g * y);
+                for (int r = 0; r < 4; ++r) e[cn[n] + (size_t)r * a.d_v] = y[r];
         }
         __syncthreads();
         if (owns) {
+            bf16x8 f[2][NS][3];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) f[kk][n][t] = ld_bf8(Ul + t * PU + (16 * n + col) * LDU + 32 * kk + 8 * g);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 y[TPW][NS][3] = {};
 #pragma unroll
             for (int i = 0; i < TPW; ++i)
 #pragma unroll
-                for (int n = 0; n < NS; ++n) {
-                    f32x4 y = S[i][n] * cur.decay;
+                for (int n = 0; n < NS; ++n) y[i][n][0] = S[i][n] * cur.decay;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) y = mma16(cur.kt[i][kk], ld4(Ul + (16 * n + col) * LDU + 16 * kk + 4 * g), y);
-                    S[i][n] = y;
-                }
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int i = 0; i < TPW; ++i) mma_parts<TK, 3>(cur.kt[i][kk], f[kk][n], y[i][n]);
+#pragma unroll
+            for (int i = 0; i < TPW; ++i)
+#pragma unroll
+                for (int n = 0; n < NS; ++n) S[i][n] = sum_parts(y[i][n]);
         }
-        cur = next;
+    };
+    if (n_units > 0) {
+        Ops p, q;
+        load(0, p);
+        for (int c = 0; c < n_units; c += 2) {
+            step(c, p, q);
+            if (c + 1 < n_units) step(c + 1, q, p);
+        }
     }
     if (owns && a.final_state != nullptr) {
-        float* st = a.final_state + ((size_t)b * a.h_v + h) * ((size_t)a.d_v * DK);
+        float* st = a.final_state + ((size_t)b * a.h_v + h) * head + k0;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
-            if (c0 + 16 * n < a.d_v)
+            if (in[n])
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) st4(st + (size_t)(c0 + 16 * n + col) * DK + k0 + 16 * i, S[i][n]);
+                for (int i = 0; i < TPW; ++i) st4(st + (size_t)cn[n] * DK + 16 * i, S[i][n]);
     }
 }
 
 // O = scale (2^b Q S0^T + P beta E).  Q and K are staged in LDS, P replaces K;
 // a wave takes 16 value columns at a time, with their rows of S0 and their
-// columns of E straight from memory (each is used by one wave only).
+// columns of E straight from memory (each is used by one wave only), the first
+// of them on their way before the staging starts.
+constexpr int kOutThreads = 512;
+
 template <int DK>
-__global__ __launch_bounds__(256) void scan_output_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+__global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanArgs a, const PrefillSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY, kKP = kScanChunk * (LDK > LDY ? LDK : LDY);
     __shared__ __align__(16) float Ql[kScanChunk * LDK];
     __shared__ __align__(16) float KP[kKP];
-    __shared__ float gt[kGateRows * kScanChunk];
+    __shared__ __align__(16) float gt[kGateRows * kScanChunk];
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int unit = lb / a.h_v, h = lb % a.h_v, hq = h / a.group;
     int seq, tok, len;
@@ -308,14 +360,28 @@ __global__ __launch_bounds__(256) void scan_output_kernel(const ScanArgs a, cons
     if (a.valid[a.seq0 + seq] == 0) return;
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    for (int i = tid; i < kGateRows * kScanChunk; i += 256) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
-    stage_rows<DK, LDK, 256>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, Ql);
-    stage_rows<DK, LDK, 256>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, KP);
-    __syncthreads();
-    f32x4 p[3];
+    int c0 = 16 * wave;
+    const int c_first = c0 < a.d_v ? c0 : 0;
+    f32x4 sb[DK / 16], ee[4];
+    auto load = [&](int c) {
+        const float* st = a.S + uh * ((size_t)a.d_v * DK) + (size_t)(c + col) * DK + 4 * g;
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        const int t = wave + 4 * q;
+        for (int kk = 0; kk < DK / 16; ++kk) sb[kk] = ld4(st + 16 * kk);
+        const float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + c + col;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) ee[kk][s] = e[(size_t)(16 * kk + 4 * g + s) * a.d_v];
+    };
+    load(c_first);
+    if (tid < kGateRows * kScanChunk) gt[tid] = a.gates[uh * (kGateRows * kScanChunk) + tid];
+    stage_rows<DK, LDK, kOutThreads>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, Ql);
+    stage_rows<DK, LDK, kOutThreads>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, KP);
+    __syncthreads();
+    f32x4 p[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int t = wave + 8 * q;
         if (t >= 10) continue;
         int m, n;
         lower_tile(t, m, n);
@@ -326,37 +392,28 @@ __global__ __launch_bounds__(256) void scan_output_kernel(const ScanArgs a, cons
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        const int t = wave + 4 * q;
+    for (int q = 0; q < 2; ++q) {
+        const int t = wave + 8 * q;
         if (t >= 10) continue;
         int m, n;
         lower_tile(t, m, n);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = 16 * m + 4 * g + r, j = 16 * n + col;
-            KP[i * LDY + j] = j <= i ? p[q][r] * decay_between(gt, gt + 64, i, j) : 0.f;
+            KP[i * LDY + j] = j <= i ? gt[128 + j] * p[q][r] * decay_between(gt, gt + 64, i, j) : 0.f;
         }
     }
     __syncthreads();
-    for (int c0 = 16 * wave; c0 < a.d_v; c0 += 64) {
-        const float* st = a.S + uh * ((size_t)a.d_v * DK) + (size_t)(c0 + col) * DK + 4 * g;
-        f32x4 sb[DK / 16], ee[4];
-#pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) sb[kk] = ld4(st + 16 * kk);
-        const float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + c0 + col;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) ee[kk][s] = e[(size_t)(16 * kk + 4 * g + s) * a.d_v] * gt[128 + 16 * kk + 4 * g + s];
+    while (c0 < a.d_v) {
         f32x4 o[4] = {};
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk)
+        for (int kk = 0; kk < DK / 16; ++kk) {
+            __builtin_amdgcn_sched_barrier(0);  // not all reads at once: they would not fit the registers
 #pragma unroll
             for (int m = 0; m < 4; ++m) o[m] = mma16(ld4(Ql + (16 * m + col) * LDK + 16 * kk + 4 * g), sb[kk], o[m]);
+        }
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[m][r] *= gt[256 + 16 * m + 4 * g + r];
+        for (int m = 0; m < 4; ++m) o[m] *= ld4(gt + 256 + 16 * m + 4 * g);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -368,32 +425,39 @@ __global__ __launch_bounds__(256) void scan_output_kernel(const ScanArgs a, cons
                 const int i = 16 * m + 4 * g + r;
                 if (i < len) store_out(a.out, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + col, a.scale * o[m][r], a.out_dtype);
             }
+        c0 += 16 * (kOutThreads / 64);
+        if (c0 < a.d_v) load(c0);
     }
 }
 
-template <int DK>
+template <int DK, int TK>
 hipError_t launch_forward(const ScanArgs& args, const PrefillSeqs& seqs, hipStream_t st) {
     ScanArgs a = args;
     const unsigned heads = (unsigned)(a.units * a.h_v);
     if (heads > 0) {
-        hipLaunchKernelGGL(scan_prepare_kernel<DK>, dim3(heads), dim3(kPrepThreads), 0, st, a, seqs);
+        hipLaunchKernelGGL((scan_prepare_kernel<DK, TK>), dim3(heads), dim3(kPrepThreads), 0, st, a, seqs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    a.slices = (a.d_v + 15) / 16;
-    hipLaunchKernelGGL((scan_state_kernel<DK, 1>), dim3((unsigned)(a.n_seq * a.h_v * a.slices)), dim3(256), 0, st, a, seqs);
+    constexpr int NS = SCAN_NS;
+    a.slices = (a.d_v + 16 * NS - 1) / (16 * NS);
+    hipLaunchKernelGGL((scan_state_kernel<DK, NS, TK>), dim3((unsigned)(a.n_seq * a.h_v * a.slices)), dim3(256), 0, st, a, seqs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || heads == 0) return e;
-    hipLaunchKernelGGL(scan_output_kernel<DK>, dim3(heads), dim3(256), 0, st, a, seqs);
+    hipLaunchKernelGGL(scan_output_kernel<DK>, dim3(heads), dim3(kOutThreads), 0, st, a, seqs);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_scan_forward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream) {
-    return d_k == 128 ? launch_forward<128>(a, seqs, stream)
-         : d_k == 64  ? launch_forward<64>(a, seqs, stream)
-                      : launch_forward<32>(a, seqs, stream);
+    if (input_parts(a) == 1)
+        return d_k == 128 ? launch_forward<128, 1>(a, seqs, stream)
+             : d_k == 64  ? launch_forward<64, 1>(a, seqs, stream)
+                          : launch_forward<32, 1>(a, seqs, stream);
+    return d_k == 128 ? launch_forward<128, 3>(a, seqs, stream)
+         : d_k == 64  ? launch_forward<64, 3>(a, seqs, stream)
+                      : launch_forward<32, 3>(a, seqs, stream);
 }
 
 }  // namespace gdn

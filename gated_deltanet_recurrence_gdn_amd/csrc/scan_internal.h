@@ -52,9 +52,9 @@ struct ScanArgs {
     float* E;      // [64][d_v] (E0 between the prepare and the state kernel)
     float* S;      // [d_v][d_k] the state before the chunk
     // workspace
-    float* W;   // forward W, backward Wb: [64][d_k] per unit and value head
-    float* Kt;  // [d_k][64] per unit and q/k head
-    float* Qt;
+    uint16_t* W;   // forward W, backward Wb, in three parts: [3][64][d_k] per unit and value head
+    uint16_t* Kt;  // K and Q laid out [parts][d_k][64], per unit and q/k head
+    uint16_t* Qt;
     float* dR;  // [64][d_v] (dR0 between the prepare and the state kernel)
     float* G;   // [d_v][d_k] the gradient of the state after the chunk
     // backward
@@ -73,6 +73,8 @@ struct ScanArgs {
 };
 
 // Sequences of a launch: first token, tokens, first chunk unit (PrefillSeqs' tables).
+// Parts of the inputs q, k: one in bf16, three in fp32.
+inline int input_parts(const ScanArgs& a) { return a.qkv_bf16 ? 1 : 3; }
 hipError_t launch_scan_forward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream);
 hipError_t launch_scan_backward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream);
 
@@ -94,6 +96,61 @@ __device__ __forceinline__ void st4(float* p, f32x4 v) { *reinterpret_cast<f32x4
 
 // Four values down a column of a row-major matrix (the contraction runs over rows).
 __device__ __forceinline__ f32x4 ld_col4(const float* p, int ld) { return f32x4{p[0], p[ld], p[2 * ld], p[3 * ld]}; }
+
+// fp32 products on the bf16 matrix instructions.  A value is cut into three bf16
+// parts of 8 significant bits each, by truncation: x = h + m + l exactly.  The
+// product of two such values needs six of the nine partial products (the other
+// three are below 2^-23 of it), one of a bf16 input, which is its own only part,
+// three.  They are accumulated apart by size, h h, then h m + m h, then the rest,
+// and added once at the end: fewer roundings than one fp32 chain, and chains
+// that do not wait for each other.  Six partial products of v_mfma_f32_16x16x32_bf16
+// take 96 cycles where the fp32 instruction takes 256, three take 48.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// The three parts of four values, two to a word.
+__device__ __forceinline__ void split4(f32x4 x, u32x2 (&p)[3]) {
+    uint32_t w[4], v[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float y = x[i];  // a bit cast of the element itself compiles to one of element 0
+        w[i] = __builtin_bit_cast(uint32_t, y);
+        const float r = y - __builtin_bit_cast(float, w[i] & 0xffff0000u);
+        v[i] = __builtin_bit_cast(uint32_t, r);
+        u[i] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, v[i] & 0xffff0000u));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // the upper halves of two words
+        p[0][i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302);
+        p[1][i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07060302);
+        p[2][i] = __builtin_amdgcn_perm(u[2 * i + 1], u[2 * i], 0x07060302);
+    }
+}
+
+// v_mfma_f32_16x16x32_bf16: lane l holds A[l % 16][8 (l / 16) ..+7] and
+// B[8 (l / 16) ..+7][l % 16]; C as above.  TA, TB: parts of the operands.
+template <int TA, int TB>
+__device__ __forceinline__ void mma_parts(const bf16x8 (&a)[TA], const bf16x8 (&b)[TB], f32x4 (&c)[3]) {
+    auto go = [](bf16x8 x, bf16x8 y, f32x4 z) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, z, 0, 0, 0); };
+    c[0] = go(a[0], b[0], c[0]);
+    if constexpr (TB == 3) c[1] = go(a[0], b[1], c[1]);
+    if constexpr (TA == 3) c[1] = go(a[1], b[0], c[1]);
+    if constexpr (TA == 3 && TB == 3) c[2] = go(a[1], b[1], c[2]);
+    if constexpr (TB == 3) c[2] = go(a[0], b[2], c[2]);
+    if constexpr (TA == 3) c[2] = go(a[2], b[0], c[2]);
+}
+
+__device__ __forceinline__ f32x4 sum_parts(const f32x4 (&c)[3]) { return c[0] + (c[1] + c[2]); }
+
+__device__ __forceinline__ bf16x8 ld_bf8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// Writes the T parts of four neighbours, T arrays `plane` elements apart.
+template <int T>
+__device__ __forceinline__ void store_parts(uint16_t* p, size_t plane, f32x4 x) {
+    u32x2 w[3];
+    split4(x, w);
+#pragma unroll
+    for (int t = 0; t < T; ++t) *reinterpret_cast<u32x2*>(p + t * plane) = w[t];
+}
 
 // Tile t of the 10 on and below the diagonal of a 4 x 4 tiling.
 __device__ __forceinline__ void lower_tile(int t, int& m, int& n) {
@@ -134,6 +191,17 @@ __device__ __forceinline__ void stage_rows(const void* x, bool bf16, int tok, in
 __device__ __forceinline__ void store_typed(void* p, size_t i, float x, bool bf16) {
     if (bf16) static_cast<uint16_t*>(p)[i] = f32_to_bf16(x);
     else static_cast<float*>(p)[i] = x;
+}
+
+// Four neighbours; i is a multiple of 4.
+__device__ __forceinline__ void store4_typed(void* p, size_t i, f32x4 x, bool bf16) {
+    if (bf16) {
+        const u32x2 w = {(uint32_t)f32_to_bf16(x[0]) | (uint32_t)f32_to_bf16(x[1]) << 16,
+                         (uint32_t)f32_to_bf16(x[2]) | (uint32_t)f32_to_bf16(x[3]) << 16};
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + i) = w;
+    } else {
+        st4(static_cast<float*>(p) + i, x);
+    }
 }
 
 __device__ __forceinline__ float load_out(const void* p, size_t i, int dtype) {
