@@ -52,10 +52,11 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
     const float *be = gt + 128, *er = gt + 320;
     if (h % a.group == 0) {  // K and Q laid out for the state kernel
         const size_t at = ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk);
-        for (int p = tid; p < DK * (kScanChunk / 4); p += 512) {
-            const int c = p / (kScanChunk / 4), i = p % (kScanChunk / 4) * 4;
-            store_parts<TK>(a.Kt + at + c * kScanChunk + i, DK * kScanChunk, ld_col4(Kl + i * LDK + c, LDK));
-            store_parts<TK>(a.Qt + at + c * kScanChunk + i, DK * kScanChunk, ld_col4(QZ + i * LDK + c, LDK));
+        for (int p = wave; p < DK / 8; p += 8) {  // key tile p / 2, tokens 32 (p % 2) ..
+            const int x = (32 * (p % 2) + 8 * g) * LDK + 16 * (p / 2) + col;
+            const size_t to = at + (p * TK * 64 + lane) * 8;
+            store_operand<TK>(a.Kt + to, ld_col4(Kl + x, LDK), ld_col4(Kl + x + 4 * LDK, LDK));
+            store_operand<TK>(a.Qt + to, ld_col4(QZ + x, LDK), ld_col4(QZ + x + 4 * LDK, LDK));
         }
     }
     // P, lower tiles
@@ -133,8 +134,9 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
         }
 #pragma unroll
         for (int m = 0; m < MW; ++m) {  // transposed: a lane has four neighbours of a token's row
-            const int j = 16 * (m0 + m) + col;
-            store_parts<3>(w + j * DK + 16 * n + 4 * g, kScanChunk * DK, er[j] * ld4(Kl + j * LDK + 16 * n + 4 * g) - c[m]);
+            const int j = 16 * (m0 + m) + col, to = col + 16 * (n % 2 * 2 + g / 2);
+            store_parts<3>(w + (((m0 + m) * (DK / 32) + n / 2) * 3 * 64 + to) * 8 + g % 2 * 4, 512,
+                           er[j] * ld4(Kl + j * LDK + 16 * n + 4 * g) - c[m]);
         }
     }
     // dR0_j = scale sum_{i >= j} Z_ij dO_i
@@ -151,11 +153,9 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
 #pragma unroll
             for (int m = 0; m <= kk; ++m) c[m] = mma16(ld_col4(QZ + (16 * kk + 4 * g) * LDY + 16 * m + col, LDY), x, c[m]);
         }
-        float* e = a.dR + uh * ((size_t)kScanChunk * a.d_v) + c0 + col;
+        float* e = a.dR + uh * ((size_t)kScanChunk * a.d_v) + c0 * 16 + lane * 4;
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) e[(size_t)(16 * m + 4 * g + r) * a.d_v] = a.scale * c[m][r];
+        for (int m = 0; m < 4; ++m) st4(e + 16 * m * a.d_v, a.scale * c[m]);
     }
 }
 
@@ -202,25 +202,25 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     auto load = [&](int c, Ops& o) {
         c = c < 0 ? 0 : c;
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (16 * wave + col) * DK + 8 * g;
+        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)(wave * (DK / 32) * 3 * 512 + lane * 8);
 #pragma unroll
         for (int kk = 0; kk < DK / 32; ++kk)
 #pragma unroll
-            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + t * (kScanChunk * DK) + 32 * kk);
+            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + (kk * 3 + t) * 512);
         if (owns) {
-            const size_t at = ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (16 * wave * TPW + col) * kScanChunk + 8 * g;
+            const size_t at = ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk);
+            const uint16_t *kt = a.Kt + at + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8), *qt = a.Qt + at + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
 #pragma unroll
             for (int i = 0; i < TPW; ++i)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                     for (int t = 0; t < TK; ++t) {
-                        o.kt[i][kk][t] = ld_bf8(a.Kt + at + t * (DK * kScanChunk) + 16 * i * kScanChunk + 32 * kk);
-                        o.qt[i][kk][t] = ld_bf8(a.Qt + at + t * (DK * kScanChunk) + 16 * i * kScanChunk + 32 * kk);
+                        o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
+                        o.qt[i][kk][t] = ld_bf8(qt + ((i * 2 + kk) * TK + t) * 512);
                     }
         }
-        const float* e = a.dR + uh * e_unit + (size_t)i0 * a.d_v + c0 + col;
-        o.e = f32x4{e[0], e[a.d_v], e[2 * a.d_v], e[3 * a.d_v]};
+        o.e = ld4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {  // past the sequence's end: its last token's, used as zero
             const int t = c * kScanChunk + i0 + r;
@@ -235,11 +235,11 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
         load(c - 1, next);
         if (owns) {
-            float* st = a.G + uh * head + (size_t)(c0 + col) * DK + k0;
+            float* st = a.G + uh * head + (unsigned)(c0 * DK + wave * TPW * 256 + lane * 4);
 #pragma unroll
             for (int i = 0; i < TPW; ++i) {
                 store_parts<3>(Gl + col * LDK + k0 + 16 * i, PG, G[i]);
-                st4(st + 16 * i, G[i]);
+                st4(st + i * 256, G[i]);
             }
         }
         {
@@ -274,9 +274,7 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
         }
         const f32x4 dr = cur.e + sum_parts(x);
         store_parts<3>(Ul + col * LDU + i0, PU, -(cur.eb * cur.be * dr));
-        float* e = a.dR + uh * e_unit + (size_t)i0 * a.d_v + c0 + col;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) e[(size_t)r * a.d_v] = dr[r];
+        st4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4), dr);
         __syncthreads();
         if (owns) {
             bf16x8 f[2][3];
@@ -372,8 +370,8 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
     for (int hh = 0; hh < a.group; ++hh) {
         const int h = hq * a.group + hh;
         const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
-        const float* S0 = a.S + uh * ((size_t)a.d_v * DK) + 16 * nt + col;
-        const float* G0 = a.G + uh * ((size_t)a.d_v * DK) + 16 * nt + col;
+        const float* S0 = a.S + uh * ((size_t)a.d_v * DK) + nt * 256 + (4 * g + 16 * (col / 4)) * 4 + col % 4;
+        const float* G0 = a.G + uh * ((size_t)a.d_v * DK) + nt * 256 + (4 * g + 16 * (col / 4)) * 4 + col % 4;
         f32x4 os[MW] = {}, rs[MW] = {}, eg[MW] = {}, dp[2] = {}, da[2] = {};
         float gs = 0.f;
         for (int i = tid; i < kGateRows * kScanChunk; i += kGradThreads) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
@@ -383,24 +381,34 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if (16 * ks >= width) continue;
-                sb[ks] = ld_col4(S0 + (size_t)(c0 + 16 * ks + 4 * g) * DK, DK);
-                gb[ks] = ld_col4(G0 + (size_t)(c0 + 16 * ks + 4 * g) * DK, DK);
+                sb[ks] = ld_col4(S0 + (size_t)(c0 + 16 * ks) * DK, 4);
+                gb[ks] = ld_col4(G0 + (size_t)(c0 + 16 * ks) * DK, 4);
             }
             __syncthreads();
             {
                 const int i = tid / 8, c = tid % 8 * 4;
                 if (c < width) {
-                    const size_t at = uh * ((size_t)kScanChunk * a.d_v) + (size_t)i * a.d_v + c0 + c;
                     f32x4 x = {};
                     if (i < len) x = load4_out(a.dout, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, a.out_dtype);
                     st4(st + i * LDS + c, x);
-                    const f32x4 dr = ld4(a.dR + at);
-                    st4(st + (kScanChunk + i) * LDS + c, dr);
-                    if (i < len) store4_typed(a.dv, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, gt[128 + i] * dr, a.qkv_bf16);
-                    st4(st + (2 * kScanChunk + i) * LDS + c, ld4(a.E + at));
+                }
+                const int m = wave / 2, n = wave % 2;  // a tile of dR and E each
+                if (16 * n < width) {
+                    const size_t at = uh * ((size_t)kScanChunk * a.d_v) + 16 * m * a.d_v + (c0 / 16 + n) * 256 + lane * 4;
+                    const f32x4 x = ld4(a.dR + at), y = ld4(a.E + at);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        st[(kScanChunk + 16 * m + 4 * g + r) * LDS + 16 * n + col] = x[r];
+                        st[(2 * kScanChunk + 16 * m + 4 * g + r) * LDS + 16 * n + col] = y[r];
+                    }
                 }
             }
             __syncthreads();
+            {
+                const int i = tid / 8, c = tid % 8 * 4;
+                if (i < len && c < width)
+                    store4_typed(a.dv, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, gt[128 + i] * ld4(st + (kScanChunk + i) * LDS + c), a.qkv_bf16);
+            }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if (16 * ks >= width) continue;

@@ -102,9 +102,9 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
         }
     } else if (h % a.group == 0) {
         uint16_t* kt = a.Kt + ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk);
-        for (int p = tid - 64; p < DK * (kScanChunk / 4); p += kPrepThreads - 64) {
-            const int c = p / (kScanChunk / 4), i = p % (kScanChunk / 4) * 4;
-            store_parts<TK>(kt + c * kScanChunk + i, DK * kScanChunk, ld_col4(Kl + i * LDK + c, LDK));
+        for (int p = wave - 1; p < DK / 8; p += kPrepThreads / 64 - 1) {  // key tile p / 2, tokens 32 (p % 2) ..
+            const float* x = Kl + (32 * (p % 2) + 8 * g) * LDK + 16 * (p / 2) + col;
+            store_operand<TK>(kt + (p * TK * 64 + lane) * 8, ld_col4(x, LDK), ld_col4(x + 4 * LDK, LDK));
         }
     }
     __syncthreads();
@@ -132,8 +132,9 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const int i = 16 * m + col;
-            store_parts<3>(w + i * DK + 16 * n + 4 * g, kScanChunk * DK, eb[i] * ld4(Kl + i * LDK + 16 * n + 4 * g) - c[m]);
+            const int i = 16 * m + col, to = col + 16 * (n % 2 * 2 + g / 2);
+            store_parts<3>(w + ((m * (DK / 32) + n / 2) * 3 * 64 + to) * 8 + g % 2 * 4, 512,
+                           eb[i] * ld4(Kl + i * LDK + 16 * n + 4 * g) - c[m]);
         }
     }
     // E0 = V - Y (beta V), 64 value columns at a time
@@ -159,14 +160,14 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 #pragma unroll
             for (int m = kk; m < 4; ++m) c[m] = mma16(ld4(Yl + (16 * m + col) * LDY + j), x, c[m]);
         }
-        float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + c0 + 16 * wave + col;
+        float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + ((c0 / 16 + wave) * 64 + lane) * 4;
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < 4; ++m) {
+            f32x4 y;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * g + r;
-                e[(size_t)i * a.d_v] = Vl[i * LDY + 16 * wave + col] - c[m][r];
-            }
+            for (int r = 0; r < 4; ++r) y[r] = Vl[(16 * m + 4 * g + r) * LDY + 16 * wave + col] - c[m][r];
+            st4(e + m * 16 * a.d_v, y);
+        }
     }
 }
 
@@ -214,12 +215,13 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     const bool owns = DK >= 64 || wave < DK / 16;  // of the state's key rows
     const int k0 = 16 * wave * TPW + 4 * g;
     // a slice past d_v (NS = 2, odd number of tiles) repeats the first tile and stores nothing
-    int cn[NS];
+    int cn[NS], tn[NS];  // this lane's value column, the value tile
     bool in[NS];
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
         in[n] = n == 0 || c0 + 16 * n < a.d_v;
-        cn[n] = c0 + (in[n] ? 16 * n : 0) + col;
+        tn[n] = c0 / 16 + (in[n] ? n : 0);
+        cn[n] = 16 * tn[n] + col;
     }
     const size_t head = (size_t)a.d_v * DK, e_unit = (size_t)kScanChunk * a.d_v;
     f32x4 S[TPW][NS] = {};
@@ -233,26 +235,23 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     auto load = [&](int c, Ops& o) {
         const int unit = u0 + (c < n_units ? c : n_units - 1);
         const size_t uh = (size_t)unit * a.h_v + h;
-        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (16 * wave + col) * DK + 8 * g;
+        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)(wave * (DK / 32) * 3 * 512 + lane * 8);
 #pragma unroll
         for (int kk = 0; kk < DK / 32; ++kk)
 #pragma unroll
-            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + t * (kScanChunk * DK) + 32 * kk);
+            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + (kk * 3 + t) * 512);
         if (owns) {
-            const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (16 * wave * TPW + col) * kScanChunk + 8 * g;
+            const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
 #pragma unroll
             for (int i = 0; i < TPW; ++i)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                    for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + t * (DK * kScanChunk) + 16 * i * kScanChunk + 32 * kk);
+                    for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
         }
-        const float* e = a.E + uh * e_unit + (size_t)(16 * wave + 4 * g) * a.d_v;
+        const float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const float* p = e + cn[n];
-            o.e[n] = f32x4{p[0], p[a.d_v], p[2 * a.d_v], p[3 * a.d_v]};
-        }
+        for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
         const float* gt = a.gates + uh * (kGateRows * kScanChunk);
         o.be = ld4(gt + 128 + 16 * wave + 4 * g);
         o.er = ld4(gt + 320 + 16 * wave + 4 * g);
@@ -262,13 +261,13 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
         load(c + 1, next);
         if (owns) {
-            float* st = a.S + uh * head + k0;
+            float* st = a.S + uh * head + (unsigned)(wave * TPW * 256 + lane * 4);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int i = 0; i < TPW; ++i) {
                     store_parts<3>(Sl + (16 * n + col) * LDK + k0 + 16 * i, PS, S[i][n]);
-                    if (in[n]) st4(st + (size_t)cn[n] * DK + 16 * i, S[i][n]);
+                    if (in[n]) st4(st + tn[n] * (16 * DK) + i * 256, S[i][n]);
                 }
         }
         __syncthreads();
@@ -287,14 +286,12 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 #pragma unroll
                 for (int n = 0; n < NS; ++n) mma_parts<3, 3>(cur.w[kk], f[kk][n], x[n]);
         }
-        float* e = a.E + uh * e_unit + (size_t)(16 * wave + 4 * g) * a.d_v;
+        float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const f32x4 y = cur.e[n] - sum_parts(x[n]);
             store_parts<3>(Ul + (16 * n + col) * LDU + 16 * wave + 4 * g, PU, cur.be * cur.er * y);
-            if (in[n])
-#pragma unroll
-                for (int r = 0; r < 4; ++r) e[cn[n] + (size_t)r * a.d_v] = y[r];
+            if (in[n]) st4(e + tn[n] * 256, y);
         }
         __syncthreads();
         if (owns) {
@@ -364,14 +361,12 @@ __global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanA
     const int c_first = c0 < a.d_v ? c0 : 0;
     f32x4 sb[DK / 16], ee[4];
     auto load = [&](int c) {
-        const float* st = a.S + uh * ((size_t)a.d_v * DK) + (size_t)(c + col) * DK + 4 * g;
+        const float* st = a.S + uh * ((size_t)a.d_v * DK) + (size_t)c * DK + lane * 4;
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) sb[kk] = ld4(st + 16 * kk);
-        const float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + c + col;
+        for (int kk = 0; kk < DK / 16; ++kk) sb[kk] = ld4(st + 256 * kk);
+        const float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + c * 16 + lane * 4;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) ee[kk][s] = e[(size_t)(16 * kk + 4 * g + s) * a.d_v];
+        for (int kk = 0; kk < 4; ++kk) ee[kk] = ld4(e + 16 * kk * a.d_v);
     };
     load(c_first);
     if (tid < kGateRows * kScanChunk) gt[tid] = a.gates[uh * (kGateRows * kScanChunk) + tid];

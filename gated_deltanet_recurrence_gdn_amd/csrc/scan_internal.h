@@ -49,14 +49,14 @@ struct ScanArgs {
     int32_t* valid;
     float* gates;  // [kGateRows][64]
     float* Y;      // [64][64]
-    float* E;      // [64][d_v] (E0 between the prepare and the state kernel)
-    float* S;      // [d_v][d_k] the state before the chunk
+    float* E;      // the errors (E0 between the prepare and the state kernel), [token tile][value tile] accumulators
+    float* S;      // the state before the chunk, transposed, [value tile][key tile] accumulators
     // workspace
-    uint16_t* W;   // forward W, backward Wb, in three parts: [3][64][d_k] per unit and value head
-    uint16_t* Kt;  // K and Q laid out [parts][d_k][64], per unit and q/k head
+    uint16_t* W;   // forward W, backward Wb, in three parts, per unit and value head: row operands [token tile][key step][part]
+    uint16_t* Kt;  // K and Q transposed, per unit and q/k head: row operands [key tile][token step][part]
     uint16_t* Qt;
-    float* dR;  // [64][d_v] (dR0 between the prepare and the state kernel)
-    float* G;   // [d_v][d_k] the gradient of the state after the chunk
+    float* dR;  // gradients of the errors' system, as E (dR0 between the prepare and the state kernel)
+    float* G;   // the gradient of the state after the chunk, as S
     // backward
     const void* dout;
     const float* dfinal;  // nullable: zeros
@@ -71,6 +71,12 @@ struct ScanArgs {
     int32_t n_seq, seq0, units, unit_base;
     float scale;
 };
+
+// What one kernel hands to the next lies in memory in the order of the matrix
+// instructions' registers, so that a wave's load or store is one contiguous
+// kilobyte: accumulators as [tile][lane][4] floats (lane l: rows 4 (l / 16) ..+3,
+// column l % 16 of the 16 x 16 tile), row operands as [tile][step][part][lane][8]
+// bf16 (lane l: row l % 16, columns 8 (l / 16) ..+7 of the 16 x 32 tile).
 
 // Sequences of a launch: first token, tokens, first chunk unit (PrefillSeqs' tables).
 // Parts of the inputs q, k: one in bf16, three in fp32.
@@ -142,6 +148,16 @@ __device__ __forceinline__ void mma_parts(const bf16x8 (&a)[TA], const bf16x8 (&
 __device__ __forceinline__ f32x4 sum_parts(const f32x4 (&c)[3]) { return c[0] + (c[1] + c[2]); }
 
 __device__ __forceinline__ bf16x8 ld_bf8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// Writes the T parts of eight neighbours as a lane's piece of a row operand.
+template <int T>
+__device__ __forceinline__ void store_operand(uint16_t* p, f32x4 x, f32x4 y) {
+    u32x2 w[3], v[3];
+    split4(x, w);
+    split4(y, v);
+#pragma unroll
+    for (int t = 0; t < T; ++t) *reinterpret_cast<u32x4*>(p + t * 512) = u32x4{w[t][0], w[t][1], v[t][0], v[t][1]};
+}
 
 // Writes the T parts of four neighbours, T arrays `plane` elements apart.
 template <int T>
