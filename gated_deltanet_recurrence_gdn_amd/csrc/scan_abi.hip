@@ -1,6 +1,7 @@
 // scan_abi.hip -- the training scan's C entry points: host validation, the
 // layout of the tape and the workspaces, and the launches.  Every check runs
 // before anything is enqueued.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -32,7 +33,7 @@ int check_scan(const gdn_shape* sh, const int32_t* cu, int64_t* units) {
         *units += chunks_of((int64_t)cu[b + 1] - cu[b]);
     }
     // workgroups of a launch: one per chunk and head, and one per sequence, head and 16 value columns
-    if (*units * sh->h_v > 0x7fffffffLL || (int64_t)kMaxPrefillSeqs * sh->h_v * (sh->d_v / 16) > 0x7fffffffLL) return GDN_ERR_SHAPE;
+    if (*units * sh->h_v > 0x7fffffffLL || (int64_t)sh->h_v * (sh->d_v / 16) > 0x7fffffffLL) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
 
@@ -97,13 +98,13 @@ void fill(const gdn_shape* sh, const void* q, const void* k, const void* v, cons
     a->qkv_bf16 = sh->qkv_dtype == GDN_BF16; a->out_dtype = sh->out_dtype; a->scale = sh->scale;
 }
 
-// Launches of up to kMaxPrefillSeqs sequences each.
+// Launches of up to kScanSeqs sequences each.
 int launch_all(const gdn_shape* sh, const int32_t* cu, ScanArgs* a, hipStream_t stream,
-               hipError_t (*launch)(const ScanArgs&, const PrefillSeqs&, int, hipStream_t)) {
+               hipError_t (*launch)(const ScanArgs&, const ScanSeqs&, int, hipStream_t)) {
     int64_t unit_base = 0;
-    for (int s0 = 0; s0 < sh->batch; s0 += kMaxPrefillSeqs) {
-        const int ns = sh->batch - s0 < kMaxPrefillSeqs ? sh->batch - s0 : kMaxPrefillSeqs;
-        PrefillSeqs seqs;
+    for (int s0 = 0; s0 < sh->batch; s0 += kScanSeqs) {
+        const int ns = sh->batch - s0 < kScanSeqs ? sh->batch - s0 : kScanSeqs;
+        ScanSeqs seqs;
         std::memset(&seqs, 0, sizeof(seqs));
         int64_t units = 0;
         for (int i = 0; i <= ns; ++i) {
@@ -113,6 +114,8 @@ int launch_all(const gdn_shape* sh, const int32_t* cu, ScanArgs* a, hipStream_t 
             seqs.len[i] = cu[s0 + i + 1] - cu[s0 + i];
             units += chunks_of(seqs.len[i]);
         }
+        for (int i = 0; i < ns; ++i) seqs.order[i] = (uint8_t)i;
+        std::stable_sort(seqs.order, seqs.order + ns, [&](uint8_t x, uint8_t y) { return seqs.len[x] > seqs.len[y]; });
         a->n_seq = ns;
         a->seq0 = s0;
         a->units = (int32_t)units;

@@ -23,7 +23,7 @@ namespace gdn {
 namespace {
 
 template <int DK, int TK>
-__global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+__global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY, kQZ = kScanChunk * (LDK > LDY ? LDK : LDY);
     extern __shared__ __align__(16) float lds[];
     float* Kl = lds;                    // [64][LDK]
@@ -177,15 +177,16 @@ __device__ __forceinline__ float to_f32(_Float16 x) { return (float)x; }
 __device__ __forceinline__ float to_f32(uint16_t x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }  // bf16
 
 template <int DK, int TK, typename OT>
-__global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+__global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using Ops = BackOperands<DK, TK, OT>;
     constexpr int LDK = DK + 8, LDU = kScanChunk + 8, TPW = Ops::kTiles;
     constexpr int PG = 16 * LDK, PU = 16 * LDU;  // a part's plane
     __shared__ __align__(16) uint16_t Gl[3 * PG];
     __shared__ __align__(16) uint16_t Ul[3 * PU];
     __shared__ __align__(16) uint16_t Ol[3 * PU];
-    const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
-    const int c0 = lb % a.slices * 16, h = lb / a.slices % a.h_v, s = lb / a.slices / a.h_v;
+    int s, h, slice;
+    state_block(a, seqs, s, h, slice);
+    const int c0 = slice * 16;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
     const int b = a.seq0 + s, T = seqs.len[s], t0 = seqs.tok0[s], u0 = a.unit_base + seqs.unit0[s];
     const int n_units = (T + kScanChunk - 1) / kScanChunk;
@@ -199,7 +200,18 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
 #pragma unroll
         for (int i = 0; i < TPW; ++i) G[i] = ld4(a.dfinal + seq_at + 16 * i);
     const OT* dout = static_cast<const OT*>(a.dout) + (size_t)h * a.d_v + c0 + col;
-    auto load = [&](int c, Ops& o) {
+    auto load_o = [&](int c, Ops& o) {  // dout's part
+        c = c < 0 ? 0 : c;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // past the sequence's end: its last token's, used as zero
+            const int t = c * kScanChunk + i0 + r;
+            o.o[r] = dout[(size_t)(t0 + (t < T ? t : T - 1)) * a.h_v * a.d_v];
+        }
+        const float* gt = a.gates + ((size_t)(u0 + c) * a.h_v + h) * (kGateRows * kScanChunk);
+        o.be = ld4(gt + 128 + i0);
+        o.eb = ld4(gt + 256 + i0);
+    };
+    auto load_w = [&](int c, Ops& o) {  // what dR and dout's part of the gradient need
         c = c < 0 ? 0 : c;
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
         const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)(wave * (DK / 32) * 3 * 512 + lane * 8);
@@ -208,32 +220,31 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
 #pragma unroll
             for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + (kk * 3 + t) * 512);
         if (owns) {
-            const size_t at = ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk);
-            const uint16_t *kt = a.Kt + at + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8), *qt = a.Qt + at + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
+            const uint16_t* qt = a.Qt + ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
 #pragma unroll
             for (int i = 0; i < TPW; ++i)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                    for (int t = 0; t < TK; ++t) {
-                        o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
-                        o.qt[i][kk][t] = ld_bf8(qt + ((i * 2 + kk) * TK + t) * 512);
-                    }
+                    for (int t = 0; t < TK; ++t) o.qt[i][kk][t] = ld_bf8(qt + ((i * 2 + kk) * TK + t) * 512);
         }
         o.e = ld4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {  // past the sequence's end: its last token's, used as zero
-            const int t = c * kScanChunk + i0 + r;
-            o.o[r] = dout[(size_t)(t0 + (t < T ? t : T - 1)) * a.h_v * a.d_v];
-        }
-        const float* gt = a.gates + uh * (kGateRows * kScanChunk);
-        o.be = ld4(gt + 128 + i0);
-        o.eb = ld4(gt + 256 + i0);
-        o.decay = gt[256 + 63];
+        o.decay = a.gates[uh * (kGateRows * kScanChunk) + 256 + 63];
     };
-    auto step = [&](int c, const Ops& cur, Ops& next) {
+    auto load_k = [&](int c, Ops& o) {  // what dR's part of the gradient needs
+        c = c < 0 ? 0 : c;
+        if (owns) {
+            const uint16_t* kt = a.Kt + ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
+#pragma unroll
+            for (int i = 0; i < TPW; ++i)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
+        }
+    };
+    auto step = [&](int c, Ops& cur) {
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        load(c - 1, next);
         if (owns) {
             float* st = a.G + uh * head + (unsigned)(c0 * DK + wave * TPW * 256 + lane * 4);
 #pragma unroll
@@ -275,6 +286,8 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
         const f32x4 dr = cur.e + sum_parts(x);
         store_parts<3>(Ul + col * LDU + i0, PU, -(cur.eb * cur.be * dr));
         st4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4), dr);
+        load_w(c - 2, cur);
+        load_o(c - 2, cur);
         __syncthreads();
         if (owns) {
             bf16x8 f[2][3];
@@ -290,13 +303,19 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
 #pragma unroll
             for (int i = 0; i < TPW; ++i) G[i] = sum_parts(y[i]);
         }
+        load_k(c - 2, cur);
     };
     if (n_units > 0) {
         Ops p, q;
-        load(n_units - 1, p);
+        load_w(n_units - 1, p);
+        load_o(n_units - 1, p);
+        load_k(n_units - 1, p);
+        load_w(n_units - 2, q);
+        load_o(n_units - 2, q);
+        load_k(n_units - 2, q);
         for (int c = n_units - 1; c >= 0; c -= 2) {
-            step(c, p, q);
-            if (c > 0) step(c - 1, q, p);
+            step(c, p);
+            if (c > 0) step(c - 1, q);
         }
     }
     if (owns && a.dstate != nullptr)
@@ -325,7 +344,7 @@ constexpr int grad_lds_floats() {
 }
 
 template <int DK>
-__global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+__global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs a, const ScanSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY, LDS = kGradLdS;
     constexpr int NT = DK / 16, MW = NT / 2;
     static_assert(3 * kScanChunk * LDS <= 2 * kScanChunk * LDY, "the staged rows and the 64 x 64 sums share their place");
@@ -558,7 +577,7 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
 }
 
 template <int DK, int TK>
-hipError_t launch_backward(const ScanArgs& args, const PrefillSeqs& seqs, hipStream_t st) {
+hipError_t launch_backward(const ScanArgs& args, const ScanSeqs& seqs, hipStream_t st) {
     ScanArgs a = args;
     hipError_t e;
     if (a.units > 0) {
@@ -570,7 +589,7 @@ hipError_t launch_backward(const ScanArgs& args, const PrefillSeqs& seqs, hipStr
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     a.slices = a.d_v / 16;
-    const dim3 grid((unsigned)(a.n_seq * a.h_v * a.slices));
+    const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq);
     if (a.out_dtype == GDN_F32) hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, float>), grid, dim3(256), 0, st, a, seqs);
     else if (a.out_dtype == GDN_F16) hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, _Float16>), grid, dim3(256), 0, st, a, seqs);
     else hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, uint16_t>), grid, dim3(256), 0, st, a, seqs);
@@ -583,7 +602,7 @@ hipError_t launch_backward(const ScanArgs& args, const PrefillSeqs& seqs, hipStr
 
 }  // namespace
 
-hipError_t launch_scan_backward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream) {
+hipError_t launch_scan_backward(const ScanArgs& a, const ScanSeqs& seqs, int d_k, hipStream_t stream) {
     if (input_parts(a) == 1)
         return d_k == 128 ? launch_backward<128, 1>(a, seqs, stream)
              : d_k == 64  ? launch_backward<64, 1>(a, seqs, stream)

@@ -20,7 +20,7 @@ namespace {
 constexpr int kPrepThreads = 256;
 
 template <int DK, int TK>
-__global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+__global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY;
     __shared__ __align__(16) float Kl[kScanChunk * LDK];
     __shared__ __align__(16) float Yl[kScanChunk * LDY];
@@ -174,10 +174,11 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 // The state's walk.  A wave owns token rows 16 w .. 16 w + 15 of the errors and
 // d_k / 4 key rows of the state (as S^T, in accumulators); both are exchanged
 // through LDS, in an order that makes a lane's four values one 16-byte piece.
-// The matrix operands come straight from global memory into registers, one
-// chunk ahead: two sets that take turns (nothing is copied between them), loaded
-// without branches (the last chunk loads itself again) and used as loaded, so
-// that no step waits for its own loads or for its stores.
+// The matrix operands come straight from global memory into registers: two sets
+// that take turns (nothing is copied between them), each part of a set loaded
+// for the chunk after next as soon as its last use is issued, without branches
+// (past the end, the last chunk's again) and used as loaded, so that no step
+// waits for its own loads or for its stores.
 template <int DK, int NS, int TK>
 struct StateOperands {
     static constexpr int kTiles = DK / 16 >= 4 ? DK / 64 : 1;
@@ -187,15 +188,16 @@ struct StateOperands {
 };
 
 template <int DK, int NS, int TK>
-__global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+__global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using Ops = StateOperands<DK, NS, TK>;
     // rows of bf16 in LDS, 16 bytes apart modulo the 64 banks: 16 lanes' 16-byte reads meet no bank twice
     constexpr int LDK = DK + 8, LDU = kScanChunk + 8, TPW = Ops::kTiles;
     constexpr int PS = 16 * NS * LDK, PU = 16 * NS * LDU;  // a part's plane
     __shared__ __align__(16) uint16_t Sl[3 * PS];
     __shared__ __align__(16) uint16_t Ul[3 * PU];
-    const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
-    const int c0 = lb % a.slices * (16 * NS), h = lb / a.slices % a.h_v, s = lb / a.slices / a.h_v;
+    int s, h, slice;
+    state_block(a, seqs, s, h, slice);
+    const int c0 = slice * (16 * NS);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
     const int b = a.seq0 + s, n_units = (seqs.len[s] + kScanChunk - 1) / kScanChunk, u0 = a.unit_base + seqs.unit0[s];
     const bool lead = h == 0 && c0 == 0 && tid == 0;
@@ -232,14 +234,22 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 #pragma unroll
             for (int i = 0; i < TPW; ++i) S[i][n] = ld4(st + (size_t)cn[n] * DK + 16 * i);
     }
-    auto load = [&](int c, Ops& o) {
-        const int unit = u0 + (c < n_units ? c : n_units - 1);
-        const size_t uh = (size_t)unit * a.h_v + h;
+    auto load_w = [&](int c, Ops& o) {  // what the errors need
+        const size_t uh = (size_t)(u0 + (c < n_units ? c : n_units - 1)) * a.h_v + h;
         const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)(wave * (DK / 32) * 3 * 512 + lane * 8);
 #pragma unroll
         for (int kk = 0; kk < DK / 32; ++kk)
 #pragma unroll
             for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + (kk * 3 + t) * 512);
+        const float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
+        const float* gt = a.gates + uh * (kGateRows * kScanChunk);
+        o.be = ld4(gt + 128 + 16 * wave + 4 * g);
+        o.er = ld4(gt + 320 + 16 * wave + 4 * g);
+    };
+    auto load_k = [&](int c, Ops& o) {  // what the state needs
+        const int unit = u0 + (c < n_units ? c : n_units - 1);
         if (owns) {
             const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
 #pragma unroll
@@ -249,17 +259,10 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 #pragma unroll
                     for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
         }
-        const float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
-#pragma unroll
-        for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
-        const float* gt = a.gates + uh * (kGateRows * kScanChunk);
-        o.be = ld4(gt + 128 + 16 * wave + 4 * g);
-        o.er = ld4(gt + 320 + 16 * wave + 4 * g);
-        o.decay = gt[256 + 63];
+        o.decay = a.gates[((size_t)unit * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63];
     };
-    auto step = [&](int c, const Ops& cur, Ops& next) {
+    auto step = [&](int c, Ops& cur) {
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        load(c + 1, next);
         if (owns) {
             float* st = a.S + uh * head + (unsigned)(wave * TPW * 256 + lane * 4);
 #pragma unroll
@@ -293,6 +296,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
             store_parts<3>(Ul + (16 * n + col) * LDU + 16 * wave + 4 * g, PU, cur.be * cur.er * y);
             if (in[n]) st4(e + tn[n] * 256, y);
         }
+        load_w(c + 2, cur);
         __syncthreads();
         if (owns) {
             bf16x8 f[2][NS][3];
@@ -319,13 +323,17 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 #pragma unroll
                 for (int n = 0; n < NS; ++n) S[i][n] = sum_parts(y[i][n]);
         }
+        load_k(c + 2, cur);
     };
     if (n_units > 0) {
         Ops p, q;
-        load(0, p);
+        load_w(0, p);
+        load_k(0, p);
+        load_w(1, q);
+        load_k(1, q);
         for (int c = 0; c < n_units; c += 2) {
-            step(c, p, q);
-            if (c + 1 < n_units) step(c + 1, q, p);
+            step(c, p);
+            if (c + 1 < n_units) step(c + 1, q);
         }
     }
     if (owns && a.final_state != nullptr) {
@@ -345,7 +353,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 constexpr int kOutThreads = 512;
 
 template <int DK>
-__global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanArgs a, const PrefillSeqs seqs) {
+__global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanArgs a, const ScanSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY, kKP = kScanChunk * (LDK > LDY ? LDK : LDY);
     __shared__ __align__(16) float Ql[kScanChunk * LDK];
     __shared__ __align__(16) float KP[kKP];
@@ -426,7 +434,7 @@ __global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanA
 }
 
 template <int DK, int TK>
-hipError_t launch_forward(const ScanArgs& args, const PrefillSeqs& seqs, hipStream_t st) {
+hipError_t launch_forward(const ScanArgs& args, const ScanSeqs& seqs, hipStream_t st) {
     ScanArgs a = args;
     const unsigned heads = (unsigned)(a.units * a.h_v);
     if (heads > 0) {
@@ -436,7 +444,7 @@ hipError_t launch_forward(const ScanArgs& args, const PrefillSeqs& seqs, hipStre
     }
     constexpr int NS = SCAN_NS;
     a.slices = (a.d_v + 16 * NS - 1) / (16 * NS);
-    hipLaunchKernelGGL((scan_state_kernel<DK, NS, TK>), dim3((unsigned)(a.n_seq * a.h_v * a.slices)), dim3(256), 0, st, a, seqs);
+    hipLaunchKernelGGL((scan_state_kernel<DK, NS, TK>), dim3((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq), dim3(256), 0, st, a, seqs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || heads == 0) return e;
     hipLaunchKernelGGL(scan_output_kernel<DK>, dim3(heads), dim3(kOutThreads), 0, st, a, seqs);
@@ -445,7 +453,7 @@ hipError_t launch_forward(const ScanArgs& args, const PrefillSeqs& seqs, hipStre
 
 }  // namespace
 
-hipError_t launch_scan_forward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream) {
+hipError_t launch_scan_forward(const ScanArgs& a, const ScanSeqs& seqs, int d_k, hipStream_t stream) {
     if (input_parts(a) == 1)
         return d_k == 128 ? launch_forward<128, 1>(a, seqs, stream)
              : d_k == 64  ? launch_forward<64, 1>(a, seqs, stream)

@@ -78,11 +78,29 @@ struct ScanArgs {
 // column l % 16 of the 16 x 16 tile), row operands as [tile][step][part][lane][8]
 // bf16 (lane l: row l % 16, columns 8 (l / 16) ..+7 of the 16 x 32 tile).
 
-// Sequences of a launch: first token, tokens, first chunk unit (PrefillSeqs' tables).
+// The sequences of a launch: first token, tokens, first chunk unit (one entry
+// more), and their order by length, longest first (the state kernels' workgroups
+// are started in that order).
+constexpr int kScanSeqs = 64;
+struct ScanSeqs {
+    int32_t tok0[kScanSeqs], len[kScanSeqs], unit0[kScanSeqs + 1];
+    uint8_t order[kScanSeqs];
+};
+
+// Workgroups of a state kernel: blockIdx.x is one of h_v * slices, contiguous
+// runs of them on one XCD (the slices of a head read the same operands), the
+// same for every sequence, so that the XCDs have equal shares of each.
+__device__ __forceinline__ void state_block(const ScanArgs& a, const ScanSeqs& seqs, int& s, int& h, int& slice) {
+    const int x = xcd_logical_block(blockIdx.x, gridDim.x);
+    s = seqs.order[blockIdx.y];
+    h = x / a.slices;
+    slice = x % a.slices;
+}
+
 // Parts of the inputs q, k: one in bf16, three in fp32.
 inline int input_parts(const ScanArgs& a) { return a.qkv_bf16 ? 1 : 3; }
-hipError_t launch_scan_forward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream);
-hipError_t launch_scan_backward(const ScanArgs& a, const PrefillSeqs& seqs, int d_k, hipStream_t stream);
+hipError_t launch_scan_forward(const ScanArgs& a, const ScanSeqs& seqs, int d_k, hipStream_t stream);
+hipError_t launch_scan_backward(const ScanArgs& a, const ScanSeqs& seqs, int d_k, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
 // device pieces
@@ -175,7 +193,7 @@ __device__ __forceinline__ void lower_tile(int t, int& m, int& n) {
 }
 
 // A chunk unit's place: its sequence (in the launch), first token and tokens.
-__device__ __forceinline__ void find_unit(const PrefillSeqs& s, int n_seq, int unit, int& seq, int& tok, int& len) {
+__device__ __forceinline__ void find_unit(const ScanSeqs& s, int n_seq, int unit, int& seq, int& tok, int& len) {
     int lo = 0, hi = n_seq;  // unit0[lo] <= unit < unit0[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
