@@ -116,27 +116,35 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
         for (int r = 0; r < 4; ++r) QZ[(16 * m + 4 * g + r) * LDY + 16 * n + col] = p[q][r];
     }
     __syncthreads();
-    // Wb_j = 2^(b_63 - b_j) K_j - sum_{i > j} Y_ij beta_i 2^(b_63 - b_i) K_i
+    // Wb_j = 2^(b_63 - b_j) K_j - sum_{i > j} Y_ij beta_i 2^(b_63 - b_i) K_i, transposed
+    // and 32 key columns at a time: a lane has its piece of the state kernel's row operand
     {
-        constexpr int NT = DK / 16, MW = NT / 2;  // waves share the key columns' tiles, 4 / (8 / NT) row tiles each
-        const int n = wave % NT, m0 = wave / NT * MW;
-        uint16_t* w = a.W + uh * (3 * kScanChunk * DK);
-        f32x4 c[MW] = {};
+        constexpr int KS = DK / 32, MW = KS / 2 > 0 ? KS / 2 : 1;  // token tiles of a wave
+        uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + lane * 8;
+        const int n = wave % KS, m0 = wave / KS * MW;
+        if (m0 < 4) {
+            f32x4 c[MW][2] = {};
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const int i = 16 * kk + 4 * g;
-            f32x4 x = ld_col4(Kl + i * LDK + 16 * n + col, LDK);
+            for (int kk = 0; kk < 4; ++kk) {
+                const int i = 16 * kk + 4 * g;
+                f32x4 x = ld_col4(Kl + i * LDK + 32 * n + col, LDK), y = ld_col4(Kl + i * LDK + 32 * n + 16 + col, LDK);
+                const f32x4 f = ld4(be + i) * ld4(er + i);
+                x *= f;
+                y *= f;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) x[s] *= be[i + s] * er[i + s];
+                for (int m = 0; m < MW; ++m)
+                    if (m0 + m <= kk) {
+                        const f32x4 yl = ld_col4(Yl + i * LDY + 16 * (m0 + m) + col, LDY);
+                        c[m][0] = mma16(x, yl, c[m][0]);
+                        c[m][1] = mma16(y, yl, c[m][1]);
+                    }
+            }
 #pragma unroll
-            for (int m = 0; m < MW; ++m)
-                if (m0 + m <= kk) c[m] = mma16(x, ld_col4(Yl + i * LDY + 16 * (m0 + m) + col, LDY), c[m]);
-        }
-#pragma unroll
-        for (int m = 0; m < MW; ++m) {  // transposed: a lane has four neighbours of a token's row
-            const int j = 16 * (m0 + m) + col, to = col + 16 * (n % 2 * 2 + g / 2);
-            store_parts<3>(w + (((m0 + m) * (DK / 32) + n / 2) * 3 * 64 + to) * 8 + g % 2 * 4, 512,
-                           er[j] * ld4(Kl + j * LDK + 16 * n + 4 * g) - c[m]);
+            for (int m = 0; m < MW; ++m) {
+                const int j = 16 * (m0 + m) + col;
+                const float* kr = Kl + j * LDK + 32 * n + 4 * g;
+                store_operand<3>(w + ((m0 + m) * KS + n) * 3 * 512, er[j] * ld4(kr) - c[m][0], er[j] * ld4(kr + 16) - c[m][1]);
+            }
         }
     }
     // dR0_j = scale sum_{i >= j} Z_ij dO_i
@@ -165,8 +173,7 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
 // they are used.
 template <int DK, int TK, typename OT>
 struct BackOperands {
-    static constexpr int kTiles = DK / 16 >= 4 ? DK / 64 : 1;
-    bf16x8 w[DK / 32][3], kt[kTiles][2][TK], qt[kTiles][2][TK];
+    bf16x8 w[DK / 32][3], kt[2][2][TK], qt[2][2][TK];
     f32x4 e, be, eb;
     OT o[4];
     float decay;
@@ -179,28 +186,29 @@ __device__ __forceinline__ float to_f32(uint16_t x) { return __builtin_bit_cast(
 template <int DK, int TK, typename OT>
 __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using Ops = BackOperands<DK, TK, OT>;
-    constexpr int LDK = DK + 8, LDU = kScanChunk + 8, TPW = Ops::kTiles;
-    constexpr int PG = 16 * LDK, PU = 16 * LDU;  // a part's plane
-    __shared__ __align__(16) uint16_t Gl[3 * PG];
+    constexpr int KS = DK / 32;
+    constexpr int LDU = kScanChunk + 8, PU = 16 * LDU;  // a part's plane
+    __shared__ __align__(16) float Pl[KS * 4 * 256];  // partial products [key step][token tile][lane][4]
     __shared__ __align__(16) uint16_t Ul[3 * PU];
     __shared__ __align__(16) uint16_t Ol[3 * PU];
     int s, h, slice;
     state_block(a, seqs, s, h, slice);
     const int c0 = slice * 16;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int ks = wave % KS, m0 = wave / KS * KS;
     const int b = a.seq0 + s, T = seqs.len[s], t0 = seqs.tok0[s], u0 = a.unit_base + seqs.unit0[s];
     const int n_units = (T + kScanChunk - 1) / kScanChunk;
     if (a.valid[b] == 0) return;
-    const bool owns = DK >= 64 || wave < DK / 16;
-    const int k0 = 16 * wave * TPW + 4 * g, i0 = 16 * wave + 4 * g;
+    const bool owns = KS == 4 || m0 == 0;
+    const int k0 = 32 * ks + 4 * g, i0 = 16 * wave + 4 * g;
     const size_t head = (size_t)a.d_v * DK, e_unit = (size_t)kScanChunk * a.d_v;
-    f32x4 G[TPW] = {};
+    f32x4 G[2] = {};
     const size_t seq_at = ((size_t)b * a.h_v + h) * head + (size_t)(c0 + col) * DK + k0;
-    if (owns && a.dfinal != nullptr)
+    if (a.dfinal != nullptr)
 #pragma unroll
-        for (int i = 0; i < TPW; ++i) G[i] = ld4(a.dfinal + seq_at + 16 * i);
+        for (int i = 0; i < 2; ++i) G[i] = ld4(a.dfinal + seq_at + 16 * i);
     const OT* dout = static_cast<const OT*>(a.dout) + (size_t)h * a.d_v + c0 + col;
-    auto load_o = [&](int c, Ops& o) {  // dout's part
+    auto load_o = [&](int c, Ops& o) {  // dout
         c = c < 0 ? 0 : c;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {  // past the sequence's end: its last token's, used as zero
@@ -211,98 +219,89 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
         o.be = ld4(gt + 128 + i0);
         o.eb = ld4(gt + 256 + i0);
     };
-    auto load_w = [&](int c, Ops& o) {  // what dR and dout's part of the gradient need
+    auto load_w = [&](int c, Ops& o) {  // what dR needs
         c = c < 0 ? 0 : c;
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)(wave * (DK / 32) * 3 * 512 + lane * 8);
+        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
 #pragma unroll
-        for (int kk = 0; kk < DK / 32; ++kk)
+        for (int m = 0; m < KS; ++m)
 #pragma unroll
-            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + (kk * 3 + t) * 512);
-        if (owns) {
-            const uint16_t* qt = a.Qt + ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
-#pragma unroll
-            for (int i = 0; i < TPW; ++i)
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                    for (int t = 0; t < TK; ++t) o.qt[i][kk][t] = ld_bf8(qt + ((i * 2 + kk) * TK + t) * 512);
-        }
+            for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
         o.e = ld4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4));
-        o.decay = a.gates[uh * (kGateRows * kScanChunk) + 256 + 63];
     };
-    auto load_k = [&](int c, Ops& o) {  // what dR's part of the gradient needs
+    auto load_k = [&](int c, Ops& o) {  // what G needs
         c = c < 0 ? 0 : c;
-        if (owns) {
-            const uint16_t* kt = a.Kt + ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
+        const size_t at = ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk);
+        const uint16_t *kt = a.Kt + at + (unsigned)(ks * 4 * TK * 512 + lane * 8), *qt = a.Qt + at + (unsigned)(ks * 4 * TK * 512 + lane * 8);
 #pragma unroll
-            for (int i = 0; i < TPW; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                    for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
-        }
+                for (int t = 0; t < TK; ++t) {
+                    o.qt[i][kk][t] = ld_bf8(qt + ((i * 2 + kk) * TK + t) * 512);
+                    o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
+                }
+        o.decay = a.gates[((size_t)(u0 + c) * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63];
     };
     auto step = [&](int c, Ops& cur) {
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        if (owns) {
-            float* st = a.G + uh * head + (unsigned)(c0 * DK + wave * TPW * 256 + lane * 4);
-#pragma unroll
-            for (int i = 0; i < TPW; ++i) {
-                store_parts<3>(Gl + col * LDK + k0 + 16 * i, PG, G[i]);
-                st4(st + i * 256, G[i]);
-            }
-        }
         {
+            bf16x8 f[3];
+            operand_of(G[0], G[1], f);
+            f32x4 x[KS] = {};
+#pragma unroll
+            for (int m = 0; m < KS; ++m) x[m] = mma_parts<3, 3>(cur.w[m], f, x[m]);
             f32x4 o;
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = c * kScanChunk + i0 + r < T ? a.scale * to_f32(cur.o[r]) : 0.f;
             store_parts<3>(Ol + col * LDU + i0, PU, cur.eb * o);
+#pragma unroll
+            for (int m = 0; m < KS; ++m) st4(Pl + (ks * 4 + m0 + m) * 256 + lane * 4, x[m]);
+        }
+        if (owns) {
+            float* st = a.G + uh * head + (unsigned)(c0 * DK + ks * 512 + lane * 4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) st4(st + i * 256, G[i]);
         }
         __syncthreads();
-        f32x4 x[3] = {};
-        f32x4 y[TPW][3] = {};
+        f32x4 y[2] = {};
         {
-            bf16x8 f[DK / 32][3], fo[2][3];
+            f32x4 x[KS];
+            bf16x8 f[2][3];
 #pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk)
-#pragma unroll
-                for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Gl + t * PG + col * LDK + 32 * kk + 8 * g);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int t = 0; t < 3; ++t) fo[kk][t] = ld_bf8(Ol + t * PU + col * LDU + 32 * kk + 8 * g);
-            __builtin_amdgcn_sched_barrier(0);  // every read is on its way before the products start
-#pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk) mma_parts<3, 3>(cur.w[kk], f[kk], x);
-            // dout's part of the new gradient does not wait for dR
-#pragma unroll
-            for (int i = 0; i < TPW; ++i) y[i][0] = G[i] * cur.decay;
+            for (int q = 0; q < KS; ++q) x[q] = ld4(Pl + (q * 4 + wave) * 256 + lane * 4);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) mma_parts<TK, 3>(cur.qt[i][kk], fo[kk], y[i]);
+                for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Ol + t * PU + col * LDU + 32 * kk + 8 * g);
+            __builtin_amdgcn_sched_barrier(0);  // every read is on its way before anything waits
+#pragma unroll
+            for (int q = 1; q < KS; ++q) x[0] += x[q];
+            const f32x4 dr = cur.e + x[0];
+            store_parts<3>(Ul + col * LDU + i0, PU, -(cur.eb * cur.be * dr));
+            st4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4), dr);
+            // dout's part of the new gradient needs no dR: it is formed while the others' is on its way
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) y[i] = mma_parts<TK, 3>(cur.qt[i][kk], f[kk], y[i]);
         }
-        const f32x4 dr = cur.e + sum_parts(x);
-        store_parts<3>(Ul + col * LDU + i0, PU, -(cur.eb * cur.be * dr));
-        st4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4), dr);
         load_w(c - 2, cur);
         load_o(c - 2, cur);
         __syncthreads();
-        if (owns) {
-            bf16x8 f[2][3];
+        bf16x8 f[2][3];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Ul + t * PU + col * LDU + 32 * kk + 8 * g);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Ul + t * PU + col * LDU + 32 * kk + 8 * g);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) mma_parts<TK, 3>(cur.kt[i][kk], f[kk], y[i]);
+            for (int i = 0; i < 2; ++i) y[i] = mma_parts<TK, 3>(cur.kt[i][kk], f[kk], y[i]);
 #pragma unroll
-            for (int i = 0; i < TPW; ++i) G[i] = sum_parts(y[i]);
-        }
+        for (int i = 0; i < 2; ++i) G[i] = G[i] * cur.decay + y[i];
         load_k(c - 2, cur);
     };
     if (n_units > 0) {
@@ -320,7 +319,7 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     }
     if (owns && a.dstate != nullptr)
 #pragma unroll
-        for (int i = 0; i < TPW; ++i) st4(a.dstate + seq_at + 16 * i, G[i]);
+        for (int i = 0; i < 2; ++i) st4(a.dstate + seq_at + 16 * i, G[i]);
 }
 
 // Sum over 64 lanes.

@@ -117,24 +117,33 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
         }
     }
 
-    // W^T = (2^b K)^T - (beta 2^b K)^T Y^T: a lane has four neighbours of a token's row
-    uint16_t* w = a.W + uh * (3 * kScanChunk * DK);
-    for (int n = wave; n < DK / 16; n += 4) {
-        f32x4 c[4] = {};
+    // W^T = (2^b K)^T - (beta 2^b K)^T Y^T, 32 key columns at a time: a lane has
+    // its piece of the state kernel's row operand
+    uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + lane * 8;
+    constexpr int KS = DK / 32;
+    for (int q = wave; q < KS * (4 / KS); q += 4) {
+        const int n = q % KS, m0 = q / KS * KS;  // all waves have work where d_k is small
+        f32x4 c[KS][2] = {};
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
             const int j = 16 * kk + 4 * g;
-            f32x4 x = ld_col4(Kl + j * LDK + 16 * n + col, LDK);
+            f32x4 x = ld_col4(Kl + j * LDK + 32 * n + col, LDK), y = ld_col4(Kl + j * LDK + 32 * n + 16 + col, LDK);
+            const f32x4 f = {be[j] * eb[j], be[j + 1] * eb[j + 1], be[j + 2] * eb[j + 2], be[j + 3] * eb[j + 3]};
+            x *= f;
+            y *= f;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) x[s] *= be[j + s] * eb[j + s];
-#pragma unroll
-            for (int m = kk; m < 4; ++m) c[m] = mma16(x, ld4(Yl + (16 * m + col) * LDY + j), c[m]);
+            for (int m = 0; m < KS; ++m)
+                if (m0 + m >= kk) {
+                    const f32x4 yl = ld4(Yl + (16 * (m0 + m) + col) * LDY + j);
+                    c[m][0] = mma16(x, yl, c[m][0]);
+                    c[m][1] = mma16(y, yl, c[m][1]);
+                }
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int i = 16 * m + col, to = col + 16 * (n % 2 * 2 + g / 2);
-            store_parts<3>(w + ((m * (DK / 32) + n / 2) * 3 * 64 + to) * 8 + g % 2 * 4, 512,
-                           eb[i] * ld4(Kl + i * LDK + 16 * n + 4 * g) - c[m]);
+        for (int m = 0; m < KS; ++m) {
+            const int i = 16 * (m0 + m) + col;
+            const float* kr = Kl + i * LDK + 32 * n + 4 * g;
+            store_operand<3>(w + ((m0 + m) * KS + n) * 3 * 512, eb[i] * ld4(kr) - c[m][0], eb[i] * ld4(kr + 16) - c[m][1]);
         }
     }
     // E0 = V - Y (beta V), 64 value columns at a time
@@ -171,9 +180,12 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
     }
 }
 
-// The state's walk.  A wave owns token rows 16 w .. 16 w + 15 of the errors and
-// d_k / 4 key rows of the state (as S^T, in accumulators); both are exchanged
-// through LDS, in an order that makes a lane's four values one 16-byte piece.
+// The state's walk.  The state (as S^T, in accumulators) is spread over the waves
+// by its key rows, 32 to a wave (where d_k < 128, several waves hold the same
+// rows and share the token tiles).  A wave multiplies W's columns with its own
+// rows straight from its registers; the partial products of the 16-token tiles
+// are summed through LDS by one wave each, which forms the errors and hands
+// their scaled parts to all waves for the state's update: two exchanges a chunk.
 // The matrix operands come straight from global memory into registers: two sets
 // that take turns (nothing is copied between them), each part of a set loaded
 // for the chunk after next as soon as its last use is issued, without branches
@@ -181,8 +193,7 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 // waits for its own loads or for its stores.
 template <int DK, int NS, int TK>
 struct StateOperands {
-    static constexpr int kTiles = DK / 16 >= 4 ? DK / 64 : 1;
-    bf16x8 w[DK / 32][3], kt[kTiles][2][TK];
+    bf16x8 w[DK / 32][3], kt[2][2][TK];  // W of this wave's token tiles, K^T of its key tiles
     f32x4 e[NS], be, er;
     float decay;
 };
@@ -190,15 +201,16 @@ struct StateOperands {
 template <int DK, int NS, int TK>
 __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using Ops = StateOperands<DK, NS, TK>;
+    constexpr int KS = DK / 32;  // waves that share the key rows; also token tiles of a wave
     // rows of bf16 in LDS, 16 bytes apart modulo the 64 banks: 16 lanes' 16-byte reads meet no bank twice
-    constexpr int LDK = DK + 8, LDU = kScanChunk + 8, TPW = Ops::kTiles;
-    constexpr int PS = 16 * NS * LDK, PU = 16 * NS * LDU;  // a part's plane
-    __shared__ __align__(16) uint16_t Sl[3 * PS];
+    constexpr int LDU = kScanChunk + 8, PU = 16 * NS * LDU;  // a part's plane
+    __shared__ __align__(16) float Pl[KS * 4 * NS * 256];  // partial products [key step][token tile][value tile][lane][4]
     __shared__ __align__(16) uint16_t Ul[3 * PU];
     int s, h, slice;
     state_block(a, seqs, s, h, slice);
     const int c0 = slice * (16 * NS);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int ks = wave % KS, m0 = wave / KS * KS;
     const int b = a.seq0 + s, n_units = (seqs.len[s] + kScanChunk - 1) / kScanChunk, u0 = a.unit_base + seqs.unit0[s];
     const bool lead = h == 0 && c0 == 0 && tid == 0;
     int row = b;
@@ -214,8 +226,8 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     }
     if (lead) a.valid[b] = 1;
 
-    const bool owns = DK >= 64 || wave < DK / 16;  // of the state's key rows
-    const int k0 = 16 * wave * TPW + 4 * g;
+    const bool owns = KS == 4 || m0 == 0;  // of the waves with the same key rows, the one that stores them
+    const int k0 = 32 * ks + 4 * g;
     // a slice past d_v (NS = 2, odd number of tiles) repeats the first tile and stores nothing
     int cn[NS], tn[NS];  // this lane's value column, the value tile
     bool in[NS];
@@ -226,21 +238,21 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
         cn[n] = 16 * tn[n] + col;
     }
     const size_t head = (size_t)a.d_v * DK, e_unit = (size_t)kScanChunk * a.d_v;
-    f32x4 S[TPW][NS] = {};
-    if (owns && a.state != nullptr) {
+    f32x4 S[2][NS] = {};
+    if (a.state != nullptr) {
         const float* st = a.state + ((size_t)row * a.h_v + h) * head + k0;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int i = 0; i < TPW; ++i) S[i][n] = ld4(st + (size_t)cn[n] * DK + 16 * i);
+            for (int i = 0; i < 2; ++i) S[i][n] = ld4(st + (size_t)cn[n] * DK + 16 * i);
     }
     auto load_w = [&](int c, Ops& o) {  // what the errors need
         const size_t uh = (size_t)(u0 + (c < n_units ? c : n_units - 1)) * a.h_v + h;
-        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)(wave * (DK / 32) * 3 * 512 + lane * 8);
+        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
 #pragma unroll
-        for (int kk = 0; kk < DK / 32; ++kk)
+        for (int m = 0; m < KS; ++m)
 #pragma unroll
-            for (int t = 0; t < 3; ++t) o.w[kk][t] = ld_bf8(w + (kk * 3 + t) * 512);
+            for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
         const float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
 #pragma unroll
         for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
@@ -250,79 +262,73 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     };
     auto load_k = [&](int c, Ops& o) {  // what the state needs
         const int unit = u0 + (c < n_units ? c : n_units - 1);
-        if (owns) {
-            const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(wave * TPW * 2 * TK * 512 + lane * 8);
+        const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(ks * 4 * TK * 512 + lane * 8);
 #pragma unroll
-            for (int i = 0; i < TPW; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                    for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
-        }
+                for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
         o.decay = a.gates[((size_t)unit * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63];
     };
     auto step = [&](int c, Ops& cur) {
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
+        {
+            bf16x8 f[NS][3];
+#pragma unroll
+            for (int n = 0; n < NS; ++n) operand_of(S[0][n], S[1][n], f[n]);
+            f32x4 x[KS][NS] = {};
+#pragma unroll
+            for (int m = 0; m < KS; ++m)
+#pragma unroll
+                for (int n = 0; n < NS; ++n) x[m][n] = mma_parts<3, 3>(cur.w[m], f[n], x[m][n]);
+#pragma unroll
+            for (int m = 0; m < KS; ++m)
+#pragma unroll
+                for (int n = 0; n < NS; ++n) st4(Pl + ((ks * 4 + m0 + m) * NS + n) * 256 + lane * 4, x[m][n]);
+        }
         if (owns) {
-            float* st = a.S + uh * head + (unsigned)(wave * TPW * 256 + lane * 4);
+            float* st = a.S + uh * head + (unsigned)(ks * 512 + lane * 4);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) {
-                    store_parts<3>(Sl + (16 * n + col) * LDK + k0 + 16 * i, PS, S[i][n]);
+                for (int i = 0; i < 2; ++i)
                     if (in[n]) st4(st + tn[n] * (16 * DK) + i * 256, S[i][n]);
-                }
         }
         __syncthreads();
-        f32x4 x[NS][3] = {};
-        {
-            bf16x8 f[DK / 32][NS][3];
-#pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk)
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) f[kk][n][t] = ld_bf8(Sl + t * PS + (16 * n + col) * LDK + 32 * kk + 8 * g);
-            __builtin_amdgcn_sched_barrier(0);  // every read is on its way before the products start
-#pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk)
-#pragma unroll
-                for (int n = 0; n < NS; ++n) mma_parts<3, 3>(cur.w[kk], f[kk][n], x[n]);
-        }
         float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            const f32x4 y = cur.e[n] - sum_parts(x[n]);
+            f32x4 x[KS];
+#pragma unroll
+            for (int q = 0; q < KS; ++q) x[q] = ld4(Pl + ((q * 4 + wave) * NS + n) * 256 + lane * 4);
+#pragma unroll
+            for (int q = 1; q < KS; ++q) x[0] += x[q];
+            const f32x4 y = cur.e[n] - x[0];
             store_parts<3>(Ul + (16 * n + col) * LDU + 16 * wave + 4 * g, PU, cur.be * cur.er * y);
             if (in[n]) st4(e + tn[n] * 256, y);
         }
         load_w(c + 2, cur);
         __syncthreads();
-        if (owns) {
-            bf16x8 f[2][NS][3];
+        bf16x8 f[2][NS][3];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int n = 0; n < NS; ++n)
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
-                    for (int t = 0; t < 3; ++t) f[kk][n][t] = ld_bf8(Ul + t * PU + (16 * n + col) * LDU + 32 * kk + 8 * g);
-            __builtin_amdgcn_sched_barrier(0);
-            f32x4 y[TPW][NS][3] = {};
+                for (int t = 0; t < 3; ++t) f[kk][n][t] = ld_bf8(Ul + t * PU + (16 * n + col) * LDU + 32 * kk + 8 * g);
+        __builtin_amdgcn_sched_barrier(0);  // every read is on its way before the products start
+        f32x4 y[2][NS] = {};
 #pragma unroll
-            for (int i = 0; i < TPW; ++i)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int n = 0; n < NS; ++n) y[i][n][0] = S[i][n] * cur.decay;
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+                for (int i = 0; i < 2; ++i) y[i][n] = mma_parts<TK, 3>(cur.kt[i][kk], f[kk][n], y[i][n]);
 #pragma unroll
-                for (int n = 0; n < NS; ++n)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < TPW; ++i) mma_parts<TK, 3>(cur.kt[i][kk], f[kk][n], y[i][n]);
-#pragma unroll
-            for (int i = 0; i < TPW; ++i)
-#pragma unroll
-                for (int n = 0; n < NS; ++n) S[i][n] = sum_parts(y[i][n]);
-        }
+            for (int n = 0; n < NS; ++n) S[i][n] = S[i][n] * cur.decay + y[i][n];
         load_k(c + 2, cur);
     };
     if (n_units > 0) {
@@ -342,7 +348,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
         for (int n = 0; n < NS; ++n)
             if (in[n])
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) st4(st + (size_t)cn[n] * DK + 16 * i, S[i][n]);
+                for (int i = 0; i < 2; ++i) st4(st + (size_t)cn[n] * DK + 16 * i, S[i][n]);
     }
 }
 

@@ -76,7 +76,8 @@ struct ScanArgs {
 // instructions' registers, so that a wave's load or store is one contiguous
 // kilobyte: accumulators as [tile][lane][4] floats (lane l: rows 4 (l / 16) ..+3,
 // column l % 16 of the 16 x 16 tile), row operands as [tile][step][part][lane][8]
-// bf16 (lane l: row l % 16, columns 8 (l / 16) ..+7 of the 16 x 32 tile).
+// bf16 (lane l: row l % 16, columns 8 (l / 16) ..+7 of the 16 x 32 tile; W's
+// columns 4 (l / 16) ..+3 and 16 + 4 (l / 16) ..+3, as operand_of).
 
 // The sequences of a launch: first token, tokens, first chunk unit (one entry
 // more), and their order by length, longest first (the state kernels' workgroups
@@ -125,9 +126,7 @@ __device__ __forceinline__ f32x4 ld_col4(const float* p, int ld) { return f32x4{
 // parts of 8 significant bits each, by truncation: x = h + m + l exactly.  The
 // product of two such values needs six of the nine partial products (the other
 // three are below 2^-23 of it), one of a bf16 input, which is its own only part,
-// three.  They are accumulated apart by size, h h, then h m + m h, then the rest,
-// and added once at the end: fewer roundings than one fp32 chain, and chains
-// that do not wait for each other.  Six partial products of v_mfma_f32_16x16x32_bf16
+// three.  Six partial products of v_mfma_f32_16x16x32_bf16
 // take 96 cycles where the fp32 instruction takes 256, three take 48.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -151,19 +150,30 @@ __device__ __forceinline__ void split4(f32x4 x, u32x2 (&p)[3]) {
 }
 
 // v_mfma_f32_16x16x32_bf16: lane l holds A[l % 16][8 (l / 16) ..+7] and
-// B[8 (l / 16) ..+7][l % 16]; C as above.  TA, TB: parts of the operands.
+// B[8 (l / 16) ..+7][l % 16]; C as above.  TA, TB: parts of the operands.  The
+// small partial products come first, so that the sum is rounded at its own size
+// only when the large ones arrive.
 template <int TA, int TB>
-__device__ __forceinline__ void mma_parts(const bf16x8 (&a)[TA], const bf16x8 (&b)[TB], f32x4 (&c)[3]) {
+__device__ __forceinline__ f32x4 mma_parts(const bf16x8 (&a)[TA], const bf16x8 (&b)[TB], f32x4 c) {
     auto go = [](bf16x8 x, bf16x8 y, f32x4 z) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, z, 0, 0, 0); };
-    c[0] = go(a[0], b[0], c[0]);
-    if constexpr (TB == 3) c[1] = go(a[0], b[1], c[1]);
-    if constexpr (TA == 3) c[1] = go(a[1], b[0], c[1]);
-    if constexpr (TA == 3 && TB == 3) c[2] = go(a[1], b[1], c[2]);
-    if constexpr (TB == 3) c[2] = go(a[0], b[2], c[2]);
-    if constexpr (TA == 3) c[2] = go(a[2], b[0], c[2]);
+    if constexpr (TA == 3) c = go(a[2], b[0], c);
+    if constexpr (TB == 3) c = go(a[0], b[2], c);
+    if constexpr (TA == 3 && TB == 3) c = go(a[1], b[1], c);
+    if constexpr (TA == 3) c = go(a[1], b[0], c);
+    if constexpr (TB == 3) c = go(a[0], b[1], c);
+    return go(a[0], b[0], c);
 }
 
-__device__ __forceinline__ f32x4 sum_parts(const f32x4 (&c)[3]) { return c[0] + (c[1] + c[2]); }
+// The parts of two 16 x 16 accumulator tiles as one operand of 32 indices: lane
+// group g holds indices 4 g ..+3 of either tile.  The other operand has to be in
+// that order too.
+__device__ __forceinline__ void operand_of(f32x4 x, f32x4 y, bf16x8 (&p)[3]) {
+    u32x2 w[3], v[3];
+    split4(x, w);
+    split4(y, v);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) p[t] = __builtin_bit_cast(bf16x8, u32x4{w[t][0], w[t][1], v[t][0], v[t][1]});
+}
 
 __device__ __forceinline__ bf16x8 ld_bf8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
