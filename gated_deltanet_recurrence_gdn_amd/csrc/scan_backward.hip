@@ -25,7 +25,8 @@ namespace {
 template <int DK, int TK>
 __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
     constexpr int LDK = DK + 4, LDY = kScanLdY, kQZ = kScanChunk * (LDK > LDY ? LDK : LDY);
-    extern __shared__ __align__(16) float lds[];
+    extern __shared__ __align__(16) float lds_raw[];
+    float* lds = lds_raw;
     float* Kl = lds;                    // [64][LDK]
     float* QZ = Kl + kScanChunk * LDK;  // Q, then Z: [64][LDK] / [64][LDY]
     float* Yl = QZ + kQZ;               // [64][LDY]
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
     find_unit(seqs, a.n_seq, unit, seq, tok, len);
     if (a.valid[a.seq0 + seq] == 0) return;
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     for (int i = tid; i < kGateRows * kScanChunk; i += 512) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
     stage_rows<DK, LDK, 512>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, Kl);
     stage_rows<DK, LDK, 512>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, QZ);
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     int s, h, slice;
     state_block(a, seqs, s, h, slice);
     const int c0 = slice * 16;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     const int ks = wave % KS, m0 = wave / KS * KS;
     const int b = a.seq0 + s, T = seqs.len[s], t0 = seqs.tok0[s], u0 = a.unit_base + seqs.unit0[s];
     const int n_units = (T + kScanChunk - 1) / kScanChunk;
@@ -330,143 +331,224 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x;
 }
 
-// The products over d_v run 32 value columns at a time: dO, dR and E of the
-// chunk staged in LDS (row operands), S0 and G straight from memory (each wave
-// reads only its own 16 key columns).  A wave owns one 16-column tile of the
-// 64 x d_k sums and one or two of the ten lower tiles of the 64 x 64 ones.
+// The products over d_v run 32 value columns (one step of the matrix
+// instruction) at a time.  S0, G, dR and E arrive as accumulator tiles (a lane
+// holds four neighbours across d_v), are cut into parts and laid in LDS with d_v
+// as the row index; the transposing reads then give both operands of every
+// product.  A wave owns one 16-column tile of the 64 x d_k sums and one or two of
+// the ten lower tiles of the 64 x 64 ones.  The next step's tiles are loaded
+// while this one's products run.
 constexpr int kGradThreads = 512;
-constexpr int kGradStage = 32;
-constexpr int kGradLdS = kGradStage + 4;
-template <int DK>
-constexpr int grad_lds_floats() {
-    return 2 * kScanChunk * (DK + 4) + 2 * kScanChunk * kScanLdY + kGateRows * kScanChunk + 2 * 8 * kScanChunk + 3 * kScanChunk;
+constexpr int kGradWaves = kGradThreads / 64;
+constexpr int kLdR = kScanChunk + 16;  // LDS rows of dR, E (64 tokens) and, below, of S0, G (d_k) for the
+                                       // transposing reads: 4 rows of a 16-lane group fall on different banks
+constexpr int kLdO = 32 + 8;           // rows of dout (32 value columns), read 16 bytes a lane
+
+template <int DK, int TO>
+struct GradLds {
+    static constexpr int kLdS = DK + 16, kPlS = 32 * kLdS, kPlR = 32 * kLdR, kPlO = kScanChunk * kLdO;  // in bf16
+    static constexpr int S = 0, G = S + 3 * kPlS * 2, R = G + 3 * kPlS * 2, E = R + 3 * kPlR * 2, O = E + 3 * kPlR * 2;
+    static constexpr int kStaged = O + TO * kPlO * 2;
+    // in the staged tiles' place: K and Q (fp32) before and after the heads, M after a head's products
+    static constexpr int kLdK = DK + 4, K = 0, Q = kScanChunk * kLdK * 4, kInputs = 2 * Q, M = 0;
+    static constexpr int kShared = kStaged > kInputs ? kStaged : kInputs;
+    static constexpr int X = kShared, P = X + kScanChunk * kScanLdY * 4;  // sums over the heads
+    static constexpr int kGates = P + kScanChunk * kScanLdY * 4, kY = kGates + kGateRows * kScanChunk * 4;
+    static constexpr int kZ = kY + 8 * kScanChunk * 4, kB = kZ + 8 * kScanChunk * 4, kF = kB + kScanChunk * 4, kG = kF + kScanChunk * 4;
+    static constexpr int kBytes = kG + kGradWaves * 4;
+    static_assert(kScanChunk * kScanLdY * 4 <= R, "M lies in S0's and G's place");
+    static_assert(kBytes <= kMaxLdsBytes, "LDS of a compute unit");
+};
+
+// One operand step from rows of 16-bit values with the contraction as the row
+// index.  ds_read_b64_tr_b16 gives lane c of a 16-lane group the values c of the
+// four rows whose quarters the group's lanes address: lane 4 e + q row e,
+// columns 4 q ..+3.  Group g reads rows 8 g ..+7.
+__device__ __forceinline__ bf16x8 read_rows(const uint16_t* p, int ld) {
+    typedef short s4v __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4v lds_s4;
+    const int lane = threadIdx.x & 63;
+    const uint16_t* q = p + (8 * (lane >> 4) + ((lane >> 2) & 3)) * ld + 4 * (lane & 3);
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)q));
+    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + 4 * ld)));
+    return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
 }
 
-template <int DK>
-__global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs a, const ScanSeqs seqs) {
-    constexpr int LDK = DK + 4, LDY = kScanLdY, LDS = kGradLdS;
+template <int T>
+__device__ __forceinline__ void read_parts(const uint16_t* p, int plane, int ld, bf16x8 (&f)[T]) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) f[t] = read_rows(p + t * plane, ld);
+}
+
+// TK, TO: parts of q, k and of dout.
+template <int DK, int TK, int TO>
+__global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanArgs a, const ScanSeqs seqs) {
+    using L = GradLds<DK, TO>;
+    constexpr int LDK = L::kLdK, LDY = kScanLdY, LDS = L::kLdS;
     constexpr int NT = DK / 16, MW = NT / 2;
-    static_assert(3 * kScanChunk * LDS <= 2 * kScanChunk * LDY, "the staged rows and the 64 x 64 sums share their place");
-    extern __shared__ __align__(16) float lds[];
-    float* Kl = lds;
-    float* Ql = Kl + kScanChunk * LDK;
-    float* st = Ql + kScanChunk * LDK;           // dO, dR, E: [3][64][LDS]; M: [64][LDY]; at the end two [64][LDY]
-    float* gt = st + 2 * kScanChunk * LDY;       // the gates
-    float* ry = gt + kGateRows * kScanChunk;     // [8][64] y, by wave
-    float* rz = ry + 8 * kScanChunk;             // [8][64] z
-    float* rb = rz + 8 * kScanChunk;             // [64] dbeta
-    float* rf = rb + kScanChunk;                 // [64] the sums over M
-    float* rg = rf + kScanChunk;                 // [8] <G, S0>, by wave
+    constexpr int kSg = 2 * NT > kGradWaves ? 2 * NT / kGradWaves : 1;  // S0 (and G) tiles of a wave and step
+    extern __shared__ __align__(16) float lds_raw[];
+    unsigned char* lds = reinterpret_cast<unsigned char*>(lds_raw);
+    float *Kl = reinterpret_cast<float*>(lds + L::K), *Ql = reinterpret_cast<float*>(lds + L::Q), *Ml = reinterpret_cast<float*>(lds + L::M);
+    float *Xl = reinterpret_cast<float*>(lds + L::X), *Ps = reinterpret_cast<float*>(lds + L::P);
+    float *gt = reinterpret_cast<float*>(lds + L::kGates), *ry = reinterpret_cast<float*>(lds + L::kY), *rz = reinterpret_cast<float*>(lds + L::kZ);
+    float *rb = reinterpret_cast<float*>(lds + L::kB), *rf = reinterpret_cast<float*>(lds + L::kF), *rg = reinterpret_cast<float*>(lds + L::kG);
+    uint16_t *Sp = reinterpret_cast<uint16_t*>(lds + L::S), *Gp = reinterpret_cast<uint16_t*>(lds + L::G), *Rp = reinterpret_cast<uint16_t*>(lds + L::R);
+    uint16_t *Ep = reinterpret_cast<uint16_t*>(lds + L::E), *Op = reinterpret_cast<uint16_t*>(lds + L::O);
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int unit = lb / a.h_qk, hq = lb % a.h_qk;
     int seq, tok, len;
     find_unit(seqs, a.n_seq, unit, seq, tok, len);
     if (a.valid[a.seq0 + seq] == 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, col = lane & 15, g = lane >> 4;
     const int nt = wave % NT, m0 = wave / NT * MW;  // this wave's key columns and row tiles
+
+    // the next step's tiles, in registers
+    f32x4 sn[kSg], gn[kSg], rn, en, on;
+    auto load = [&](int hh, int c0) {
+        const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + hq * a.group + hh;
+        const int width = a.d_v - c0;  // 16: the second value tile is zero
+        const float *st = a.S + uh * ((size_t)a.d_v * DK) + (size_t)c0 * DK + lane * 4, *gd = a.G + uh * ((size_t)a.d_v * DK) + (size_t)c0 * DK + lane * 4;
+#pragma unroll
+        for (int q = 0; q < kSg; ++q) {
+            const int t = wave * kSg + q;  // value tile t / NT, key tile t % NT
+            sn[q] = gn[q] = f32x4{};
+            if (t < 2 * NT && 16 * (t / NT) < width) {
+                sn[q] = ld4(st + t * 256);
+                gn[q] = ld4(gd + t * 256);
+            }
+        }
+        rn = en = on = f32x4{};
+        if (16 * (wave % 2) < width) {  // token tile wave / 2, value tile wave % 2
+            const size_t at = uh * ((size_t)kScanChunk * a.d_v) + wave / 2 * 16 * a.d_v + (c0 / 16 + wave % 2) * 256 + lane * 4;
+            rn = ld4(a.dR + at);
+            en = ld4(a.E + at);
+        }
+        const int i = tid / 8, c = tid % 8 * 4;
+        if (i < len && c < width) on = load4_out(a.dout, ((size_t)(tok + i) * a.h_v + hq * a.group + hh) * a.d_v + c0 + c, a.out_dtype);
+    };
+    load(0, 0);
     stage_rows<DK, LDK, kGradThreads>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, Kl);
     stage_rows<DK, LDK, kGradThreads>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, Ql);
     __syncthreads();
-    f32x4 kk_[2], qk_[2], xs[2] = {}, ps[2] = {}, accq[MW] = {}, acck[MW] = {};
+    f32x4 kk_[2] = {}, qk_[2] = {}, accq[MW] = {}, acck[MW] = {};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const int t = wave + 8 * q;
+        const int t = wave + kGradWaves * q;
         if (t >= 10) continue;
         int m, n;
         lower_tile(t, m, n);
-        f32x4 c = {}, d = {};
 #pragma unroll
         for (int k = 0; k < DK; k += 16) {
             const f32x4 x = ld4(Kl + (16 * n + col) * LDK + k + 4 * g);
-            c = mma16(ld4(Kl + (16 * m + col) * LDK + k + 4 * g), x, c);
-            d = mma16(ld4(Ql + (16 * m + col) * LDK + k + 4 * g), x, d);
+            kk_[q] = mma16(ld4(Kl + (16 * m + col) * LDK + k + 4 * g), x, kk_[q]);
+            qk_[q] = mma16(ld4(Ql + (16 * m + col) * LDK + k + 4 * g), x, qk_[q]);
         }
-        kk_[q] = c;
-        qk_[q] = d;
     }
+    // this wave's elements of K and Q: a bf16 pair in a word, or two words
+    uint32_t kq[MW][4][TK == 1 ? 1 : 2];
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int at = (16 * (m0 + m) + 4 * g + r) * LDK + 16 * nt + col;
+            const uint32_t x = __builtin_bit_cast(uint32_t, Kl[at]), y = __builtin_bit_cast(uint32_t, Ql[at]);
+            if constexpr (TK == 1) {
+                kq[m][r][0] = __builtin_amdgcn_perm(y, x, 0x07060302);
+            } else {
+                kq[m][r][0] = x;
+                kq[m][r][1] = y;
+            }
+        }
 
     for (int hh = 0; hh < a.group; ++hh) {
+        // the lane's numbers are made opaque: hundreds of LDS addresses would otherwise be formed before the loop and kept
+        asm volatile("" : "+v"(lane), "+v"(col), "+v"(g));
         const int h = hq * a.group + hh;
         const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
-        const float* S0 = a.S + uh * ((size_t)a.d_v * DK) + nt * 256 + (4 * g + 16 * (col / 4)) * 4 + col % 4;
-        const float* G0 = a.G + uh * ((size_t)a.d_v * DK) + nt * 256 + (4 * g + 16 * (col / 4)) * 4 + col % 4;
         f32x4 os[MW] = {}, rs[MW] = {}, eg[MW] = {}, dp[2] = {}, da[2] = {};
         float gs = 0.f;
-        for (int i = tid; i < kGateRows * kScanChunk; i += kGradThreads) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
-        for (int c0 = 0; c0 < a.d_v; c0 += kGradStage) {
-            const int width = a.d_v - c0 < kGradStage ? a.d_v - c0 : kGradStage;  // 16 or 32
-            f32x4 sb[2], gb[2];
+        const float gate = tid < kGateRows * kScanChunk ? a.gates[uh * (kGateRows * kScanChunk) + tid] : 0.f;
+        for (int c0 = 0; c0 < a.d_v; c0 += 32) {
+            __syncthreads();  // the last step's reads (or K's, Q's and M's) are done
+            if (c0 == 0 && tid < kGateRows * kScanChunk) gt[tid] = gate;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                if (16 * ks >= width) continue;
-                sb[ks] = ld_col4(S0 + (size_t)(c0 + 16 * ks) * DK, 4);
-                gb[ks] = ld_col4(G0 + (size_t)(c0 + 16 * ks) * DK, 4);
-            }
-            __syncthreads();
-            {
-                const int i = tid / 8, c = tid % 8 * 4;
-                if (c < width) {
-                    f32x4 x = {};
-                    if (i < len) x = load4_out(a.dout, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, a.out_dtype);
-                    st4(st + i * LDS + c, x);
+            for (int q = 0; q < kSg; ++q) {
+                const int t = wave * kSg + q;
+                if (t < 2 * NT) {
+                    const int at = (16 * (t / NT) + col) * LDS + 16 * (t % NT) + 4 * g;
+                    store_parts<3>(Sp + at, L::kPlS, sn[q]);
+                    store_parts<3>(Gp + at, L::kPlS, gn[q]);
                 }
-                const int m = wave / 2, n = wave % 2;  // a tile of dR and E each
-                if (16 * n < width) {
-                    const size_t at = uh * ((size_t)kScanChunk * a.d_v) + 16 * m * a.d_v + (c0 / 16 + n) * 256 + lane * 4;
-                    const f32x4 x = ld4(a.dR + at), y = ld4(a.E + at);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        st[(kScanChunk + 16 * m + 4 * g + r) * LDS + 16 * n + col] = x[r];
-                        st[(2 * kScanChunk + 16 * m + 4 * g + r) * LDS + 16 * n + col] = y[r];
-                    }
-                }
+                for (int r = 0; r < 4; ++r) gs = __builtin_fmaf(sn[q][r], gn[q][r], gs);
             }
-            __syncthreads();
             {
-                const int i = tid / 8, c = tid % 8 * 4;
-                if (i < len && c < width)
-                    store4_typed(a.dv, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, gt[128 + i] * ld4(st + (kScanChunk + i) * LDS + c), a.qkv_bf16);
+                const int at = (16 * (wave % 2) + col) * kLdR + wave / 2 * 16 + 4 * g;
+                store_parts<3>(Rp + at, L::kPlR, rn);
+                store_parts<3>(Ep + at, L::kPlR, en);
+                store_parts<TO>(Op + tid / 8 * kLdO + tid % 8 * 4, L::kPlO, on);
             }
+            const f32x4 dr = rn;
+            if (c0 + 32 < a.d_v) load(hh, c0 + 32);
+            else if (hh + 1 < a.group) load(hh + 1, 0);
+            __syncthreads();
+            if (c0 + 16 * (wave % 2) < a.d_v)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                if (16 * ks >= width) continue;
-                const float* p = st + col * LDS + 16 * ks + 4 * g;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) gs = __builtin_fmaf(sb[ks][s], gb[ks][s], gs);
+                for (int r = 0; r < 4; ++r) {  // dv = beta dR
+                    const int i = wave / 2 * 16 + 4 * g + r;
+                    if (i < len) store_typed(a.dv, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + 16 * (wave % 2) + col, gt[128 + i] * dr[r], a.qkv_bf16);
+                }
+            {
+                bf16x8 sb[3], gb[3];
+                read_parts<3>(Sp + 16 * nt, L::kPlS, LDS, sb);
+                read_parts<3>(Gp + 16 * nt, L::kPlS, LDS, gb);
 #pragma unroll
                 for (int m = 0; m < MW; ++m) {
-                    os[m] = mma16(ld4(p + 16 * (m0 + m) * LDS), sb[ks], os[m]);
-                    rs[m] = mma16(ld4(p + (kScanChunk + 16 * (m0 + m)) * LDS), sb[ks], rs[m]);
-                    eg[m] = mma16(ld4(p + (2 * kScanChunk + 16 * (m0 + m)) * LDS), gb[ks], eg[m]);
-                }
+                    __builtin_amdgcn_sched_barrier(0);  // one row tile's operands at a time
+                    bf16x8 ao[TO], ar[3], ae[3];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int t = wave + 8 * q;
-                    if (t >= 10) continue;
-                    int m, n;
-                    lower_tile(t, m, n);
-                    const f32x4 x = ld4(p + (2 * kScanChunk + 16 * n) * LDS);
-                    dp[q] = mma16(ld4(p + 16 * m * LDS), x, dp[q]);
-                    da[q] = mma16(ld4(p + (kScanChunk + 16 * m) * LDS), x, da[q]);
+                    for (int t = 0; t < TO; ++t) ao[t] = ld_bf8(Op + t * L::kPlO + (16 * (m0 + m) + col) * kLdO + 8 * g);
+                    read_parts<3>(Rp + 16 * (m0 + m), L::kPlR, kLdR, ar);
+                    read_parts<3>(Ep + 16 * (m0 + m), L::kPlR, kLdR, ae);
+                    os[m] = mma_parts<TO, 3>(ao, sb, os[m]);
+                    rs[m] = mma_parts<3, 3>(ar, sb, rs[m]);
+                    eg[m] = mma_parts<3, 3>(ae, gb, eg[m]);
                 }
             }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t = wave + kGradWaves * q;
+                if (t >= 10) continue;
+                __builtin_amdgcn_sched_barrier(0);
+                int m, n;
+                lower_tile(t, m, n);
+                bf16x8 ao[TO], ar[3], be[3];
+#pragma unroll
+                for (int t2 = 0; t2 < TO; ++t2) ao[t2] = ld_bf8(Op + t2 * L::kPlO + (16 * m + col) * kLdO + 8 * g);
+                read_parts<3>(Rp + 16 * m, L::kPlR, kLdR, ar);
+                read_parts<3>(Ep + 16 * n, L::kPlR, kLdR, be);
+                dp[q] = mma_parts<TO, 3>(ao, be, dp[q]);
+                da[q] = mma_parts<3, 3>(ar, be, da[q]);
+            }
         }
-        __syncthreads();  // the staged rows have been read: M takes their place
+        __syncthreads();  // the staged tiles have been read: M takes their place
         const float *be = gt + 128, *al = gt + 192, *eb = gt + 256, *er = gt + 320;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int t = wave + 8 * q;
+            const int t = wave + kGradWaves * q;
             if (t >= 10) continue;
             int m, n;
             lower_tile(t, m, n);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * g + r, j = 16 * n + col;
+                const int i = 16 * m + 4 * g + r, j = 16 * n + col, at = i * LDY + j;
                 const float d = j <= i ? be[j] * decay_between(gt, gt + 64, i, j) : 0.f;
                 const float x = j < i ? -be[i] * d * da[q][r] : 0.f, p = a.scale * d * dp[q][r];
-                xs[q][r] += x;
-                ps[q][r] += p;
-                st[i * LDY + j] = j < i ? x * kk_[q][r] + p * qk_[q][r] : 0.f;
+                Xl[at] = hh == 0 ? x : Xl[at] + x;
+                Ps[at] = hh == 0 ? p : Ps[at] + p;
+                Ml[at] = j < i ? x * kk_[q][r] + p * qk_[q][r] : 0.f;
                 if (i == j) rb[i] = da[q][r];  // dbeta_i = dR_i . E_i
             }
         }
@@ -474,8 +556,16 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
         for (int m = 0; m < MW; ++m)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
+                __builtin_amdgcn_sched_barrier(0);
                 const int i = 16 * (m0 + m) + 4 * g + r;
-                const float qv = Ql[i * LDK + 16 * nt + col], kv = Kl[i * LDK + 16 * nt + col];
+                float kv, qv;
+                if constexpr (TK == 1) {
+                    kv = bf16_lo(kq[m][r][0]);
+                    qv = bf16_hi(kq[m][r][0]);
+                } else {
+                    kv = __builtin_bit_cast(float, kq[m][r][0]);
+                    qv = __builtin_bit_cast(float, kq[m][r][1]);
+                }
                 const float o = a.scale * eb[i] * os[m][r], x = be[i] * eb[i] * rs[m][r], e = er[i] * be[i] * eg[m][r];
                 accq[m][r] += o;
                 acck[m][r] += e - x;
@@ -486,18 +576,18 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
                     rz[nt * kScanChunk + i] = z;
                 }
             }
-        gs = wave_sum(m0 == 0 ? gs : 0.f);
+        gs = wave_sum(gs);
         if (lane == 0) rg[wave] = gs;
         __syncthreads();
         // F_t = sum_{j < t <= i} M_ij: wave w the eight t from 8 w on, one column j per lane
         {
             const int t1 = 8 * wave + 7;
             float run = 0.f;
-            for (int i = kScanChunk - 1; i > t1; --i) run += lane < i ? st[i * LDY + lane] : 0.f;
+            for (int i = kScanChunk - 1; i > t1; --i) run += lane < i ? Ml[i * LDY + lane] : 0.f;
 #pragma unroll
             for (int t = 7; t >= 0; --t) {
                 const int i = 8 * wave + t;
-                run += lane < i ? st[i * LDY + lane] : 0.f;
+                run += lane < i ? Ml[i * LDY + lane] : 0.f;
                 const float f = wave_sum(lane < i ? run : 0.f);
                 if (lane == 0) rf[i] = f;
             }
@@ -509,8 +599,9 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
             for (int n = 0; n < NT; ++n) {
                 y += ry[n * kScanChunk + lane];
                 z += rz[n * kScanChunk + lane];
-                gsum += rg[n];  // the waves that own row tile 0
             }
+#pragma unroll
+            for (int n = 0; n < kGradWaves; ++n) gsum += rg[n];
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {  // y: sum over i >= t; z: over j <= t
                 const float yo = __shfl_down(y, o), zo = __shfl_up(z, o);
@@ -525,29 +616,23 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
                 a.dbeta[at] = rb[lane];
             }
         }
-        __syncthreads();  // M and the gates are done with
     }
 
-    // dQ += Ps K, dK += (Xs + Xs^T) K + Ps^T Q
-    float* X = st;
-    float* P = st + kScanChunk * LDY;
+    // dQ += Ps K, dK += (Xs + Xs^T) K + Ps^T Q: Xs made symmetric, Ps' upper tiles cleared
+    __syncthreads();
+    stage_rows<DK, LDK, kGradThreads>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, Kl);
+    stage_rows<DK, LDK, kGradThreads>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, Ql);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const int t = wave + 8 * q;
+        const int t = wave + kGradWaves * q;
         if (t >= 10) continue;
         int m, n;
         lower_tile(t, m, n);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = 16 * m + 4 * g + r, j = 16 * n + col;
-            P[i * LDY + j] = ps[q][r];
-            if (m != n) P[(16 * n + 4 * g + r) * LDY + 16 * m + col] = 0.f;
-            if (j < i) {
-                X[i * LDY + j] = xs[q][r];
-                X[j * LDY + i] = xs[q][r];
-            } else if (i == j) {
-                X[i * LDY + j] = 0.f;
-            }
+            if (m != n) Ps[(16 * n + 4 * g + r) * LDY + 16 * m + col] = 0.f;
+            if (j < i) Xl[j * LDY + i] = Xl[i * LDY + j];
         }
     }
     __syncthreads();
@@ -557,9 +642,9 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
         const f32x4 kb = ld_col4(Kl + j * LDK + 16 * nt + col, LDK), qb = ld_col4(Ql + j * LDK + 16 * nt + col, LDK);
 #pragma unroll
         for (int m = 0; m < MW; ++m) {
-            accq[m] = mma16(ld4(P + (16 * (m0 + m) + col) * LDY + j), kb, accq[m]);
-            acck[m] = mma16(ld4(X + (16 * (m0 + m) + col) * LDY + j), kb, acck[m]);
-            acck[m] = mma16(ld_col4(P + j * LDY + 16 * (m0 + m) + col, LDY), qb, acck[m]);
+            accq[m] = mma16(ld4(Ps + (16 * (m0 + m) + col) * LDY + j), kb, accq[m]);
+            acck[m] = mma16(ld4(Xl + (16 * (m0 + m) + col) * LDY + j), kb, acck[m]);
+            acck[m] = mma16(ld_col4(Ps + j * LDY + 16 * (m0 + m) + col, LDY), qb, acck[m]);
         }
     }
 #pragma unroll
@@ -573,6 +658,14 @@ __global__ __launch_bounds__(kGradThreads) void scan_grad_kernel(const ScanArgs 
                 store_typed(a.dk, at, acck[m][r], a.qkv_bf16);
             }
         }
+}
+
+template <int DK, int TK, int TO>
+hipError_t launch_grad(const ScanArgs& a, const ScanSeqs& seqs, hipStream_t st) {
+    const hipError_t e = allow_max_lds<scan_grad_kernel<DK, TK, TO>>();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((scan_grad_kernel<DK, TK, TO>), dim3((unsigned)(a.units * a.h_qk)), dim3(kGradThreads), (GradLds<DK, TO>::kBytes), st, a, seqs);
+    return hipGetLastError();
 }
 
 template <int DK, int TK>
@@ -593,10 +686,7 @@ hipError_t launch_backward(const ScanArgs& args, const ScanSeqs& seqs, hipStream
     else if (a.out_dtype == GDN_F16) hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, _Float16>), grid, dim3(256), 0, st, a, seqs);
     else hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, uint16_t>), grid, dim3(256), 0, st, a, seqs);
     if ((e = hipGetLastError()) != hipSuccess || a.units == 0) return e;
-    if ((e = allow_max_lds<scan_grad_kernel<DK>>()) != hipSuccess) return e;
-    hipLaunchKernelGGL(scan_grad_kernel<DK>, dim3((unsigned)(a.units * a.h_qk)), dim3(kGradThreads),
-                       sizeof(float) * grad_lds_floats<DK>(), st, a, seqs);
-    return hipGetLastError();
+    return a.out_dtype == GDN_BF16 ? launch_grad<DK, TK, 1>(a, seqs, st) : launch_grad<DK, TK, 3>(a, seqs, st);
 }
 
 }  // namespace

@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
     int seq, tok, len;
     find_unit(seqs, a.n_seq, unit, seq, tok, len);
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
 
     if (wave == 0) {
         float al = 1.f, bt = 0.f;
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     int s, h, slice;
     state_block(a, seqs, s, h, slice);
     const int c0 = slice * (16 * NS);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     const int ks = wave % KS, m0 = wave / KS * KS;
     const int b = a.seq0 + s, n_units = (seqs.len[s] + kScanChunk - 1) / kScanChunk, u0 = a.unit_base + seqs.unit0[s];
     const bool lead = h == 0 && c0 == 0 && tid == 0;
@@ -370,7 +370,7 @@ __global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanA
     find_unit(seqs, a.n_seq, unit, seq, tok, len);
     if (a.valid[a.seq0 + seq] == 0) return;
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     int c0 = 16 * wave;
     const int c_first = c0 < a.d_v ? c0 : 0;
     f32x4 sb[DK / 16], ee[4];
