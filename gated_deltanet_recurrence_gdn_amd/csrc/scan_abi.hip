@@ -163,7 +163,7 @@ int gdn_scan_forward(const gdn_shape* shape, const int32_t* cu_seqlens, const vo
     if (sh->batch == 0) return GDN_OK;
     if ((rc = check_inputs(sh, q, k, v, alpha, beta)) != GDN_OK) return rc;
     if (sh->n_nodes > 0 && out == nullptr) return GDN_ERR_NULL;
-    if (!aligned(state, 16) || !aligned(final_state, 16) || !aligned(out, 4) || !aligned(state_slot, 4) || !aligned(status, 4))
+    if (!aligned(state, 16) || !aligned(final_state, 16) || !aligned(out, 16) || !aligned(state_slot, 4) || !aligned(status, 4))
         return GDN_ERR_ALIGN;
     ScanArgs a;
     std::memset(&a, 0, sizeof(a));

@@ -22,15 +22,27 @@
 namespace gdn {
 namespace {
 
+constexpr int kBackThreads = 256;
+
 template <int DK, int TK>
-__global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
-    constexpr int LDK = DK + 4, LDY = kScanLdY, kQZ = kScanChunk * (LDK > LDY ? LDK : LDY);
+struct BackPrepLds {
+    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, kPlZ = kScanChunk * kLdT;  // in bf16
+    static constexpr int K = 0, Q = TK * kPlK * 2, Z = Q;  // Z takes Q's place
+    static constexpr int kGates = Q + (TK * kPlK > 3 * kPlZ ? TK * kPlK : 3 * kPlZ) * 2;
+    static constexpr int kBytes = kGates + kGateRows * kScanChunk * 4;
+};
+
+// Wave c owns the tokens i of tile c as columns: P^T's tiles (rows j) stay in
+// accumulators, the right operand of Z^T = P^T - (beta Y)^T P^T as they are, with
+// Y's tiles straight from memory as the left one.  Z's parts go through LDS once.
+template <int DK, int TK>
+__global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
+    using L = BackPrepLds<DK, TK>;
+    constexpr int LDK = L::kLdK, KS = DK / 32;
     extern __shared__ __align__(16) float lds_raw[];
-    float* lds = lds_raw;
-    float* Kl = lds;                    // [64][LDK]
-    float* QZ = Kl + kScanChunk * LDK;  // Q, then Z: [64][LDK] / [64][LDY]
-    float* Yl = QZ + kQZ;               // [64][LDY]
-    float* gt = Yl + kScanChunk * LDY;  // the gates
+    unsigned char* lds = reinterpret_cast<unsigned char*>(lds_raw);
+    uint16_t *Kp = reinterpret_cast<uint16_t*>(lds + L::K), *Qp = reinterpret_cast<uint16_t*>(lds + L::Q), *Zp = reinterpret_cast<uint16_t*>(lds + L::Z);
+    float* gt = reinterpret_cast<float*>(lds + L::kGates);
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int unit = lb / a.h_v, h = lb % a.h_v, hq = h / a.group;
     int seq, tok, len;
@@ -38,133 +50,133 @@ __global__ __launch_bounds__(512) void scan_back_prepare_kernel(const ScanArgs a
     if (a.valid[a.seq0 + seq] == 0) return;
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
-    for (int i = tid; i < kGateRows * kScanChunk; i += 512) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
-    stage_rows<DK, LDK, 512>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, Kl);
-    stage_rows<DK, LDK, 512>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, QZ);
-    {
-        const float* y = a.Y + uh * (kScanChunk * kScanChunk);
+    // dout of this wave's first value tile: rows 16 m + 4 g + r of its column, on the way early
+    const size_t o_row = (size_t)a.h_v * a.d_v;
+    f32x4 o[4];
+    auto load_o = [&](int c0) {
+        const size_t at = ((size_t)tok * a.h_v + h) * a.d_v + c0 + col;
 #pragma unroll
-        for (int p = 0; p < kScanChunk * kScanChunk / 4 / 512; ++p) {
-            const int o = (p * 512 + tid) * 4;
-            st4(Yl + o / kScanChunk * LDY + o % kScanChunk, ld4(y + o));
-        }
-    }
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * m + 4 * g + r;
+                o[m][r] = i < len ? load_out(a.dout, at + i * o_row, a.out_dtype) : 0.f;
+            }
+    };
+    if (16 * wave < a.d_v) load_o(16 * wave);
+    for (int i = tid; i < kGateRows * kScanChunk; i += kBackThreads) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
+    stage_parts<TK, DK, LDK, kBackThreads>(a.k, tok, len, a.h_qk, hq, Kp);
+    stage_parts<TK, DK, LDK, kBackThreads>(a.q, tok, len, a.h_qk, hq, Qp);
+    const float* Y = a.Y + uh * (kScanChunk * kScanChunk) + lane * 4;  // tile (m, n) at (4 m + n) 256
     __syncthreads();
     const float *be = gt + 128, *er = gt + 320;
+    // P^T: rows j of the tiles up to this wave's, columns i of its own
+    f32x4 p[4] = {};
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+        bf16x8 qf[TK], kf[TK];
+        read_along<TK>(Qp + 16 * wave * LDK + 32 * kk, L::kPlK, LDK, qf);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            if (n <= wave) {
+                read_along<TK>(Kp + 16 * n * LDK + 32 * kk, L::kPlK, LDK, kf);
+                p[n] = mma_parts<TK, TK>(kf, qf, p[n]);
+            }
+    }
+    const int i0 = 16 * wave + col;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+        if (n <= wave)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = 16 * n + 4 * g + r;
+                p[n][r] = j <= i0 ? p[n][r] * decay_between(gt, gt + 64, i0, j) : 0.f;
+            }
     if (h % a.group == 0) {  // K and Q laid out for the state kernel
-        const size_t at = ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk);
-        for (int p = wave; p < DK / 8; p += 8) {  // key tile p / 2, tokens 32 (p % 2) ..
-            const int x = (32 * (p % 2) + 8 * g) * LDK + 16 * (p / 2) + col;
-            const size_t to = at + (p * TK * 64 + lane) * 8;
-            store_operand<TK>(a.Kt + to, ld_col4(Kl + x, LDK), ld_col4(Kl + x + 4 * LDK, LDK));
-            store_operand<TK>(a.Qt + to, ld_col4(QZ + x, LDK), ld_col4(QZ + x + 4 * LDK, LDK));
+        const size_t at = ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk) + lane * 8;
+        for (int x = wave; x < DK / 8; x += kBackThreads / 64) {  // key tile x / 2, tokens 32 (x % 2) ..
+            bf16x8 f[TK], q[TK];
+            read_across<false, TK>(Kp + 32 * (x % 2) * LDK + 16 * (x / 2), L::kPlK, LDK, f);
+            read_across<false, TK>(Qp + 32 * (x % 2) * LDK + 16 * (x / 2), L::kPlK, LDK, q);
+#pragma unroll
+            for (int t = 0; t < TK; ++t) {
+                *reinterpret_cast<bf16x8*>(a.Kt + at + (x * TK + t) * 512) = f[t];
+                *reinterpret_cast<bf16x8*>(a.Qt + at + (x * TK + t) * 512) = q[t];
+            }
         }
     }
-    // P, lower tiles
-    f32x4 p[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int t = wave + 8 * q;
-        if (t >= 10) continue;
-        int m, n;
-        lower_tile(t, m, n);
-        f32x4 c = {};
-#pragma unroll
-        for (int kk = 0; kk < DK; kk += 16)
-            c = mma16(ld4(QZ + (16 * m + col) * LDK + kk + 4 * g), ld4(Kl + (16 * n + col) * LDK + kk + 4 * g), c);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * m + 4 * g + r, j = 16 * n + col;
-            p[q][r] = j <= i ? c[r] * decay_between(gt, gt + 64, i, j) : 0.f;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int t = wave + 8 * q;
-        if (t >= 10) continue;
-        int m, n;
-        lower_tile(t, m, n);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) QZ[(16 * m + 4 * g + r) * LDY + 16 * n + col] = p[q][r];
-    }
-    __syncthreads();
-    // Z = P - P beta Y
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int t = wave + 8 * q;
-        if (t >= 10) continue;
-        int m, n;
-        lower_tile(t, m, n);
-        f32x4 c = {};
-        for (int kk = n; kk <= m; ++kk) {
-            const int j = 16 * kk + 4 * g;
-            f32x4 x = ld_col4(Yl + j * LDY + 16 * n + col, LDY);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) x[s] *= be[j + s];
-            c = mma16(ld4(QZ + (16 * m + col) * LDY + j), x, c);
-        }
-        p[q] -= c;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int t = wave + 8 * q;
-        if (t >= 10) continue;
-        int m, n;
-        lower_tile(t, m, n);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) QZ[(16 * m + 4 * g + r) * LDY + 16 * n + col] = p[q][r];
-    }
-    __syncthreads();
-    // Wb_j = 2^(b_63 - b_j) K_j - sum_{i > j} Y_ij beta_i 2^(b_63 - b_i) K_i, transposed
-    // and 32 key columns at a time: a lane has its piece of the state kernel's row operand
+    // Z^T = P^T - (beta Y)^T P^T, in beta P^T's order: row tile m takes the tiles n from m on
+    f32x4 z[4];
     {
-        constexpr int KS = DK / 32, MW = KS / 2 > 0 ? KS / 2 : 1;  // token tiles of a wave
-        uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + lane * 8;
-        const int n = wave % KS, m0 = wave / KS * MW;
-        if (m0 < 4) {
-            f32x4 c[MW][2] = {};
+        f32x4 bp[4];
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int i = 16 * kk + 4 * g;
-                f32x4 x = ld_col4(Kl + i * LDK + 32 * n + col, LDK), y = ld_col4(Kl + i * LDK + 32 * n + 16 + col, LDK);
-                const f32x4 f = ld4(be + i) * ld4(er + i);
-                x *= f;
-                y *= f;
+        for (int n = 0; n < 4; ++n)
+            if (n <= wave) bp[n] = ld4(be + 16 * n + 4 * g) * p[n];
 #pragma unroll
-                for (int m = 0; m < MW; ++m)
-                    if (m0 + m <= kk) {
-                        const f32x4 yl = ld_col4(Yl + i * LDY + 16 * (m0 + m) + col, LDY);
-                        c[m][0] = mma16(x, yl, c[m][0]);
-                        c[m][1] = mma16(y, yl, c[m][1]);
-                    }
-            }
+        for (int m = 0; m < 4; ++m) {
+            z[m] = f32x4{};
+            if (m > wave) continue;
+            z[m] = p[m];
 #pragma unroll
-            for (int m = 0; m < MW; ++m) {
-                const int j = 16 * (m0 + m) + col;
-                const float* kr = Kl + j * LDK + 32 * n + 4 * g;
-                store_operand<3>(w + ((m0 + m) * KS + n) * 3 * 512, er[j] * ld4(kr) - c[m][0], er[j] * ld4(kr + 16) - c[m][1]);
-            }
+            for (int n = m; n < 4; ++n)
+                if (n <= wave) z[m] = mma16(-ld4(Y + (4 * n + m) * 256), bp[n], z[m]);
         }
     }
-    // dR0_j = scale sum_{i >= j} Z_ij dO_i
-    for (int c0 = 16 * wave; c0 < a.d_v; c0 += 128) {
-        f32x4 c[4] = {};
+    __syncthreads();  // Q has been read
+    // rows i, j along them; zeros where a step of 32 tokens reaches above the diagonal
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            f32x4 x = {};
+    for (int m = 0; m < 4; ++m)
+        if (m <= (wave | 1)) store_parts<3>(Zp + i0 * kLdT + 16 * m + 4 * g, L::kPlZ, z[m]);
+    __syncthreads();
+    // dR0 = scale Z^T dO
+    for (int c0 = 16 * wave; c0 < a.d_v; c0 += 64) {
+        if (c0 >= 64) load_o(c0);
+        f32x4 x[4] = {};
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int i = 16 * kk + 4 * g + s;
-                if (i < len) x[s] = load_out(a.dout, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + col, a.out_dtype);
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8 of[3], zf[3];
+            operand_of(o[2 * kk], o[2 * kk + 1], of);
+#pragma unroll
+            for (int m = 0; m < 2 * kk + 2; ++m) {
+                read_across<true, 3>(Zp + 32 * kk * kLdT + 16 * m, L::kPlZ, kLdT, zf);
+                x[m] = mma_parts<3, 3>(zf, of, x[m]);
+            }
+        }
+        float* e = a.dR + uh * ((size_t)kScanChunk * a.d_v) + (c0 / 16 * 64 + lane) * 4;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) st4(e + m * 16 * a.d_v, a.scale * x[m]);
+    }
+    // Wb^T = (2^(b_63 - b) K)^T - K^T (beta 2^(b_63 - b) Y): wave m the tokens j of tile
+    // m, a lane its piece of the state kernel's row operand
+    {
+        uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + wave * KS * 3 * 512 + lane * 8;
+        bf16x8 yf[2][3];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+            if (2 * kk + 1 >= wave) {
+                f32x4 y[2] = {};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int n = 2 * kk + q;
+                    if (n >= wave) y[q] = ld4(be + 16 * n + 4 * g) * ld4(er + 16 * n + 4 * g) * ld4(Y + (4 * n + wave) * 256);
+                }
+                operand_of(y[0], y[1], yf[kk]);
             }
 #pragma unroll
-            for (int m = 0; m <= kk; ++m) c[m] = mma16(ld_col4(QZ + (16 * kk + 4 * g) * LDY + 16 * m + col, LDY), x, c[m]);
-        }
-        float* e = a.dR + uh * ((size_t)kScanChunk * a.d_v) + c0 * 16 + lane * 4;
+        for (int n = 0; n < KS; ++n) {
+            f32x4 x[2] = {};
 #pragma unroll
-        for (int m = 0; m < 4; ++m) st4(e + 16 * m * a.d_v, a.scale * c[m]);
+            for (int kk = 0; kk < 2; ++kk)
+                if (2 * kk + 1 >= wave)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        bf16x8 f[TK];
+                        read_across<true, TK>(Kp + 32 * kk * LDK + 32 * n + 16 * q, L::kPlK, LDK, f);
+                        x[q] = mma_parts<TK, 3>(f, yf[kk], x[q]);
+                    }
+            const uint16_t* kr = Kp + i0 * LDK + 32 * n + 4 * g;
+            store_operand<3>(w + n * 3 * 512, er[i0] * read_whole<TK>(kr, L::kPlK) - x[0], er[i0] * read_whole<TK>(kr + 16, L::kPlK) - x[1]);
+        }
     }
 }
 
@@ -340,17 +352,15 @@ __device__ __forceinline__ float wave_sum(float x) {
 // while this one's products run.
 constexpr int kGradThreads = 512;
 constexpr int kGradWaves = kGradThreads / 64;
-constexpr int kLdR = kScanChunk + 16;  // LDS rows of dR, E (64 tokens) and, below, of S0, G (d_k) for the
-                                       // transposing reads: 4 rows of a 16-lane group fall on different banks
 constexpr int kLdO = 32 + 8;           // rows of dout (32 value columns), read 16 bytes a lane
 
-template <int DK, int TO>
+template <int DK, int TK, int TO>
 struct GradLds {
-    static constexpr int kLdS = DK + 16, kPlS = 32 * kLdS, kPlR = 32 * kLdR, kPlO = kScanChunk * kLdO;  // in bf16
+    static constexpr int kLdS = DK + 16, kPlS = 32 * kLdS, kPlR = 32 * kLdT, kPlO = kScanChunk * kLdO;  // in bf16
     static constexpr int S = 0, G = S + 3 * kPlS * 2, R = G + 3 * kPlS * 2, E = R + 3 * kPlR * 2, O = E + 3 * kPlR * 2;
     static constexpr int kStaged = O + TO * kPlO * 2;
-    // in the staged tiles' place: K and Q (fp32) before and after the heads, M after a head's products
-    static constexpr int kLdK = DK + 4, K = 0, Q = kScanChunk * kLdK * 4, kInputs = 2 * Q, M = 0;
+    // in the staged tiles' place: K and Q before and after the heads, M after a head's products
+    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, K = 0, Q = TK * kPlK * 2, kInputs = 2 * Q, M = 0;
     static constexpr int kShared = kStaged > kInputs ? kStaged : kInputs;
     static constexpr int X = kShared, P = X + kScanChunk * kScanLdY * 4;  // sums over the heads
     static constexpr int kGates = P + kScanChunk * kScanLdY * 4, kY = kGates + kGateRows * kScanChunk * 4;
@@ -360,36 +370,17 @@ struct GradLds {
     static_assert(kBytes <= kMaxLdsBytes, "LDS of a compute unit");
 };
 
-// One operand step from rows of 16-bit values with the contraction as the row
-// index.  ds_read_b64_tr_b16 gives lane c of a 16-lane group the values c of the
-// four rows whose quarters the group's lanes address: lane 4 e + q row e,
-// columns 4 q ..+3.  Group g reads rows 8 g ..+7.
-__device__ __forceinline__ bf16x8 read_rows(const uint16_t* p, int ld) {
-    typedef short s4v __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s4v lds_s4;
-    const int lane = threadIdx.x & 63;
-    const uint16_t* q = p + (8 * (lane >> 4) + ((lane >> 2) & 3)) * ld + 4 * (lane & 3);
-    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)q));
-    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + 4 * ld)));
-    return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
-}
-
-template <int T>
-__device__ __forceinline__ void read_parts(const uint16_t* p, int plane, int ld, bf16x8 (&f)[T]) {
-#pragma unroll
-    for (int t = 0; t < T; ++t) f[t] = read_rows(p + t * plane, ld);
-}
-
 // TK, TO: parts of q, k and of dout.
 template <int DK, int TK, int TO>
 __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanArgs a, const ScanSeqs seqs) {
-    using L = GradLds<DK, TO>;
+    using L = GradLds<DK, TK, TO>;
     constexpr int LDK = L::kLdK, LDY = kScanLdY, LDS = L::kLdS;
     constexpr int NT = DK / 16, MW = NT / 2;
     constexpr int kSg = 2 * NT > kGradWaves ? 2 * NT / kGradWaves : 1;  // S0 (and G) tiles of a wave and step
     extern __shared__ __align__(16) float lds_raw[];
     unsigned char* lds = reinterpret_cast<unsigned char*>(lds_raw);
-    float *Kl = reinterpret_cast<float*>(lds + L::K), *Ql = reinterpret_cast<float*>(lds + L::Q), *Ml = reinterpret_cast<float*>(lds + L::M);
+    uint16_t *Kp = reinterpret_cast<uint16_t*>(lds + L::K), *Qp = reinterpret_cast<uint16_t*>(lds + L::Q);
+    float* Ml = reinterpret_cast<float*>(lds + L::M);
     float *Xl = reinterpret_cast<float*>(lds + L::X), *Ps = reinterpret_cast<float*>(lds + L::P);
     float *gt = reinterpret_cast<float*>(lds + L::kGates), *ry = reinterpret_cast<float*>(lds + L::kY), *rz = reinterpret_cast<float*>(lds + L::kZ);
     float *rb = reinterpret_cast<float*>(lds + L::kB), *rf = reinterpret_cast<float*>(lds + L::kF), *rg = reinterpret_cast<float*>(lds + L::kG);
@@ -429,8 +420,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         if (i < len && c < width) on = load4_out(a.dout, ((size_t)(tok + i) * a.h_v + hq * a.group + hh) * a.d_v + c0 + c, a.out_dtype);
     };
     load(0, 0);
-    stage_rows<DK, LDK, kGradThreads>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, Kl);
-    stage_rows<DK, LDK, kGradThreads>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, Ql);
+    stage_parts<TK, DK, LDK, kGradThreads>(a.k, tok, len, a.h_qk, hq, Kp);
+    stage_parts<TK, DK, LDK, kGradThreads>(a.q, tok, len, a.h_qk, hq, Qp);
     __syncthreads();
     f32x4 kk_[2] = {}, qk_[2] = {}, accq[MW] = {}, acck[MW] = {};
 #pragma unroll
@@ -440,10 +431,13 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         int m, n;
         lower_tile(t, m, n);
 #pragma unroll
-        for (int k = 0; k < DK; k += 16) {
-            const f32x4 x = ld4(Kl + (16 * n + col) * LDK + k + 4 * g);
-            kk_[q] = mma16(ld4(Kl + (16 * m + col) * LDK + k + 4 * g), x, kk_[q]);
-            qk_[q] = mma16(ld4(Ql + (16 * m + col) * LDK + k + 4 * g), x, qk_[q]);
+        for (int k = 0; k < DK; k += 32) {
+            bf16x8 x[TK], y[TK];
+            read_along<TK>(Kp + 16 * n * LDK + k, L::kPlK, LDK, x);
+            read_along<TK>(Kp + 16 * m * LDK + k, L::kPlK, LDK, y);
+            kk_[q] = mma_parts<TK, TK>(y, x, kk_[q]);
+            read_along<TK>(Qp + 16 * m * LDK + k, L::kPlK, LDK, y);
+            qk_[q] = mma_parts<TK, TK>(y, x, qk_[q]);
         }
     }
     // this wave's elements of K and Q: a bf16 pair in a word, or two words
@@ -452,13 +446,13 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
     for (int m = 0; m < MW; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int at = (16 * (m0 + m) + 4 * g + r) * LDK + 16 * nt + col;
-            const uint32_t x = __builtin_bit_cast(uint32_t, Kl[at]), y = __builtin_bit_cast(uint32_t, Ql[at]);
+            const int i = 16 * (m0 + m) + 4 * g + r, at = i * LDK + 16 * nt + col;
             if constexpr (TK == 1) {
-                kq[m][r][0] = __builtin_amdgcn_perm(y, x, 0x07060302);
+                kq[m][r][0] = (uint32_t)Kp[at] | (uint32_t)Qp[at] << 16;
             } else {
-                kq[m][r][0] = x;
-                kq[m][r][1] = y;
+                const size_t from = ((size_t)(tok + i) * a.h_qk + hq) * DK + 16 * nt + col;
+                kq[m][r][0] = i < len ? static_cast<const uint32_t*>(a.k)[from] : 0;
+                kq[m][r][1] = i < len ? static_cast<const uint32_t*>(a.q)[from] : 0;
             }
         }
 
@@ -485,7 +479,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 for (int r = 0; r < 4; ++r) gs = __builtin_fmaf(sn[q][r], gn[q][r], gs);
             }
             {
-                const int at = (16 * (wave % 2) + col) * kLdR + wave / 2 * 16 + 4 * g;
+                const int at = (16 * (wave % 2) + col) * kLdT + wave / 2 * 16 + 4 * g;
                 store_parts<3>(Rp + at, L::kPlR, rn);
                 store_parts<3>(Ep + at, L::kPlR, en);
                 store_parts<TO>(Op + tid / 8 * kLdO + tid % 8 * 4, L::kPlO, on);
@@ -502,16 +496,15 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 }
             {
                 bf16x8 sb[3], gb[3];
-                read_parts<3>(Sp + 16 * nt, L::kPlS, LDS, sb);
-                read_parts<3>(Gp + 16 * nt, L::kPlS, LDS, gb);
+                read_across<false, 3>(Sp + 16 * nt, L::kPlS, LDS, sb);
+                read_across<false, 3>(Gp + 16 * nt, L::kPlS, LDS, gb);
 #pragma unroll
                 for (int m = 0; m < MW; ++m) {
                     __builtin_amdgcn_sched_barrier(0);  // one row tile's operands at a time
                     bf16x8 ao[TO], ar[3], ae[3];
-#pragma unroll
-                    for (int t = 0; t < TO; ++t) ao[t] = ld_bf8(Op + t * L::kPlO + (16 * (m0 + m) + col) * kLdO + 8 * g);
-                    read_parts<3>(Rp + 16 * (m0 + m), L::kPlR, kLdR, ar);
-                    read_parts<3>(Ep + 16 * (m0 + m), L::kPlR, kLdR, ae);
+                    read_along<TO>(Op + 16 * (m0 + m) * kLdO, L::kPlO, kLdO, ao);
+                    read_across<false, 3>(Rp + 16 * (m0 + m), L::kPlR, kLdT, ar);
+                    read_across<false, 3>(Ep + 16 * (m0 + m), L::kPlR, kLdT, ae);
                     os[m] = mma_parts<TO, 3>(ao, sb, os[m]);
                     rs[m] = mma_parts<3, 3>(ar, sb, rs[m]);
                     eg[m] = mma_parts<3, 3>(ae, gb, eg[m]);
@@ -525,10 +518,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 int m, n;
                 lower_tile(t, m, n);
                 bf16x8 ao[TO], ar[3], be[3];
-#pragma unroll
-                for (int t2 = 0; t2 < TO; ++t2) ao[t2] = ld_bf8(Op + t2 * L::kPlO + (16 * m + col) * kLdO + 8 * g);
-                read_parts<3>(Rp + 16 * m, L::kPlR, kLdR, ar);
-                read_parts<3>(Ep + 16 * n, L::kPlR, kLdR, be);
+                read_along<TO>(Op + 16 * m * kLdO, L::kPlO, kLdO, ao);
+                read_across<false, 3>(Rp + 16 * m, L::kPlR, kLdT, ar);
+                read_across<false, 3>(Ep + 16 * n, L::kPlR, kLdT, be);
                 dp[q] = mma_parts<TO, 3>(ao, be, dp[q]);
                 da[q] = mma_parts<3, 3>(ar, be, da[q]);
             }
@@ -620,8 +612,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
 
     // dQ += Ps K, dK += (Xs + Xs^T) K + Ps^T Q: Xs made symmetric, Ps' upper tiles cleared
     __syncthreads();
-    stage_rows<DK, LDK, kGradThreads>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, Kl);
-    stage_rows<DK, LDK, kGradThreads>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, Ql);
+    stage_parts<TK, DK, LDK, kGradThreads>(a.k, tok, len, a.h_qk, hq, Kp);
+    stage_parts<TK, DK, LDK, kGradThreads>(a.q, tok, len, a.h_qk, hq, Qp);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int t = wave + kGradWaves * q;
@@ -637,14 +629,22 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
     }
     __syncthreads();
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-        const int j = 16 * kk + 4 * g;
-        const f32x4 kb = ld_col4(Kl + j * LDK + 16 * nt + col, LDK), qb = ld_col4(Ql + j * LDK + 16 * nt + col, LDK);
+    for (int kk = 0; kk < 2; ++kk) {
+        const int j = 32 * kk + 4 * g;
+        bf16x8 kb[TK], qb[TK];
+        read_across<true, TK>(Kp + 32 * kk * LDK + 16 * nt, L::kPlK, LDK, kb);
+        read_across<true, TK>(Qp + 32 * kk * LDK + 16 * nt, L::kPlK, LDK, qb);
 #pragma unroll
         for (int m = 0; m < MW; ++m) {
-            accq[m] = mma16(ld4(Ps + (16 * (m0 + m) + col) * LDY + j), kb, accq[m]);
-            acck[m] = mma16(ld4(Xl + (16 * (m0 + m) + col) * LDY + j), kb, acck[m]);
-            acck[m] = mma16(ld_col4(Ps + j * LDY + 16 * (m0 + m) + col, LDY), qb, acck[m]);
+            __builtin_amdgcn_sched_barrier(0);
+            const int i = 16 * (m0 + m) + col;
+            bf16x8 f[3];
+            operand_of(ld4(Ps + i * LDY + j), ld4(Ps + i * LDY + j + 16), f);
+            accq[m] = mma_parts<3, TK>(f, kb, accq[m]);
+            operand_of(ld4(Xl + i * LDY + j), ld4(Xl + i * LDY + j + 16), f);
+            acck[m] = mma_parts<3, TK>(f, kb, acck[m]);
+            operand_of(ld_col4(Ps + j * LDY + i, LDY), ld_col4(Ps + (j + 16) * LDY + i, LDY), f);
+            acck[m] = mma_parts<3, TK>(f, qb, acck[m]);
         }
     }
 #pragma unroll
@@ -664,7 +664,7 @@ template <int DK, int TK, int TO>
 hipError_t launch_grad(const ScanArgs& a, const ScanSeqs& seqs, hipStream_t st) {
     const hipError_t e = allow_max_lds<scan_grad_kernel<DK, TK, TO>>();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((scan_grad_kernel<DK, TK, TO>), dim3((unsigned)(a.units * a.h_qk)), dim3(kGradThreads), (GradLds<DK, TO>::kBytes), st, a, seqs);
+    hipLaunchKernelGGL((scan_grad_kernel<DK, TK, TO>), dim3((unsigned)(a.units * a.h_qk)), dim3(kGradThreads), (GradLds<DK, TK, TO>::kBytes), st, a, seqs);
     return hipGetLastError();
 }
 
@@ -673,11 +673,8 @@ hipError_t launch_backward(const ScanArgs& args, const ScanSeqs& seqs, hipStream
     ScanArgs a = args;
     hipError_t e;
     if (a.units > 0) {
-        constexpr int LDK = DK + 4;
-        constexpr size_t lds = sizeof(float) * (kScanChunk * LDK + kScanChunk * (LDK > kScanLdY ? LDK : kScanLdY) +
-                                                kScanChunk * kScanLdY + kGateRows * kScanChunk);
         if ((e = allow_max_lds<scan_back_prepare_kernel<DK, TK>>()) != hipSuccess) return e;
-        hipLaunchKernelGGL((scan_back_prepare_kernel<DK, TK>), dim3((unsigned)(a.units * a.h_v)), dim3(512), lds, st, a, seqs);
+        hipLaunchKernelGGL((scan_back_prepare_kernel<DK, TK>), dim3((unsigned)(a.units * a.h_v)), dim3(kBackThreads), (BackPrepLds<DK, TK>::kBytes), st, a, seqs);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     a.slices = a.d_v / 16;

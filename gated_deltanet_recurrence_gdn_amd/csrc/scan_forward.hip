@@ -7,8 +7,8 @@
 // E = E0 - W S^T, then the state.  scan_output, one workgroup per chunk and
 // value head, forms the outputs from the stored states and errors.
 //
-// Everything is fp32 with fp32 matrix instructions: the states and errors feed
-// the backward pass, whose gate gradients are held to fp32 accuracy.
+// Everything is held to fp32 accuracy: the states and errors feed the backward
+// pass, whose gate gradients are.
 #include "scan_internal.h"
 
 namespace gdn {
@@ -19,13 +19,50 @@ namespace {
 #endif
 constexpr int kPrepThreads = 256;
 
+// The inverse of a unit lower triangular 16 x 16 tile I + A, A in rows of `ld`
+// floats: each lane the column l % 16, by forward substitution; written to `t`
+// (rows of 20 floats).
+__device__ __forceinline__ void invert_tile(const float* A, int ld, float* t, int lane) {
+    const int col = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float y = i == col ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < i; j += 4) {
+            const f32x4 r = ld4(A + i * ld + j);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (j + s < i) y = __builtin_fmaf(-r[s], x[j + s], y);
+        }
+        x[i] = y;
+    }
+    if (lane < 16)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i * 20 + col] = x[i];
+}
+
+template <int DK, int TK>
+struct PrepLds {
+    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, kPlY = kScanChunk * kLdT;  // in bf16
+    static constexpr int K = 0, N = TK * kPlK * 2;       // K; N beta (fp32), then Y's parts
+    static constexpr int T = N + kScanChunk * kScanLdY * 4;  // the diagonal tiles' inverses [4][16][20]
+    static constexpr int kNT = T + 4 * 16 * 20 * 4, kY = N + 3 * kPlY * 2;
+    static constexpr int kGates = kNT > kY ? kNT : kY, kBytes = kGates + 4 * kScanChunk * 4;
+};
+
+// K in parts in LDS.  Wave c owns the column tile c of N and of Y: its tiles stay
+// in accumulators, which are the right operand of the next product as they are
+// (Y_mc = T_mm (N_mc - sum_n (N beta)_mn Y_nc), T_mm the inverse of the diagonal
+// tile), so the forward substitution over the four tile rows has no exchange.
 template <int DK, int TK>
 __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
-    constexpr int LDK = DK + 4, LDY = kScanLdY;
-    __shared__ __align__(16) float Kl[kScanChunk * LDK];
-    __shared__ __align__(16) float Yl[kScanChunk * LDY];
-    __shared__ __align__(16) float Vl[kScanChunk * LDY];
-    __shared__ float bh[kScanChunk], bl[kScanChunk], be[kScanChunk], eb[kScanChunk];
+    using L = PrepLds<DK, TK>;
+    constexpr int LDK = L::kLdK, LDY = kScanLdY, KS = DK / 32;
+    extern __shared__ __align__(16) unsigned char lds[];
+    uint16_t *Kp = reinterpret_cast<uint16_t*>(lds + L::K), *Yp = reinterpret_cast<uint16_t*>(lds + L::N);
+    float *Nl = reinterpret_cast<float*>(lds + L::N), *Tl = reinterpret_cast<float*>(lds + L::T);
+    float *bh = reinterpret_cast<float*>(lds + L::kGates), *bl = bh + kScanChunk, *be = bl + kScanChunk, *eb = be + kScanChunk;
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int unit = lb / a.h_v, h = lb % a.h_v, hq = h / a.group;
     int seq, tok, len;
@@ -33,6 +70,21 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
 
+    // V of this wave's first value tile: rows 16 m + 4 g + r of its column, on the way early
+    const size_t v_row = (size_t)a.h_v * a.d_v;
+    f32x4 v[4];
+    auto load_v = [&](int c0) {
+        const size_t at = ((size_t)tok * a.h_v + h) * a.d_v + c0 + col;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * m + 4 * g + r;
+                v[m][r] = i < len ? load_out(a.v, at + i * v_row, TK == 1 ? GDN_BF16 : GDN_F32) : 0.f;
+            }
+    };
+    if (16 * wave < a.d_v) load_v(16 * wave);
+    stage_parts<TK, DK, LDK, kPrepThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     if (wave == 0) {
         float al = 1.f, bt = 0.f;
         if (lane < len) {
@@ -63,119 +115,113 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
         gt[256] = e;
         gt[320] = er;
     }
-    stage_rows<DK, LDK, kPrepThreads>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, Kl);
     __syncthreads();
 
-    // N, lower tiles; zeros above
-    for (int t = wave; t < 10; t += 4) {
-        int m, n;
-        lower_tile(t, m, n);
-        f32x4 c = {};
+    // N, this wave's column tile
+    f32x4 y[4] = {};
 #pragma unroll
-        for (int kk = 0; kk < DK; kk += 16)
-            c = mma16(ld4(Kl + (16 * m + col) * LDK + kk + 4 * g), ld4(Kl + (16 * n + col) * LDK + kk + 4 * g), c);
+    for (int kk = 0; kk < KS; ++kk) {
+        bf16x8 kc[TK], km[TK];
+        read_along<TK>(Kp + 16 * wave * LDK + 32 * kk, L::kPlK, LDK, kc);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * m + 4 * g + r, j = 16 * n + col;
-            Yl[i * LDY + j] = j < i ? c[r] * decay_between(bh, bl, i, j) : 0.f;
-            if (m != n) Yl[(16 * n + 4 * g + r) * LDY + 16 * m + col] = 0.f;
-        }
-    }
-    __syncthreads();
-
-    // Y_i = N_i - sum_{j < i} N_ij beta_j Y_j, one column per lane of the first
-    // wave; the others lay K out for the state kernel
-    if (wave == 0) {
-        float z[kScanChunk];
-#pragma unroll
-        for (int i = 0; i < kScanChunk; ++i) {
-            float y = Yl[i * LDY + lane];
-#pragma unroll
-            for (int j = 0; j < i; j += 4) {
-                const f32x4 nn = ld4(Yl + i * LDY + j);
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    if (j + s < i) y = __builtin_fmaf(-nn[s], z[j + s], y);
+        for (int m = 0; m < 4; ++m)
+            if (m >= wave) {
+                read_along<TK>(Kp + 16 * m * LDK + 32 * kk, L::kPlK, LDK, km);
+                y[m] = mma_parts<TK, TK>(km, kc, y[m]);
             }
-            z[i] = be[i] * y;
-            Yl[i * LDY + lane] = y;
-        }
-    } else if (h % a.group == 0) {
-        uint16_t* kt = a.Kt + ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk);
-        for (int p = wave - 1; p < DK / 8; p += kPrepThreads / 64 - 1) {  // key tile p / 2, tokens 32 (p % 2) ..
-            const float* x = Kl + (32 * (p % 2) + 8 * g) * LDK + 16 * (p / 2) + col;
-            store_operand<TK>(kt + (p * TK * 64 + lane) * 8, ld_col4(x, LDK), ld_col4(x + 4 * LDK, LDK));
+    }
+    const int j0 = 16 * wave + col;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+        if (m >= wave)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * m + 4 * g + r;
+                y[m][r] = j0 < i ? y[m][r] * decay_between(bh, bl, i, j0) : 0.f;
+                Nl[i * LDY + j0] = be[j0] * y[m][r];
+            }
+    if (h % a.group == 0) {  // K laid out for the state kernel
+        uint16_t* kt = a.Kt + ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk) + lane * 8;
+        for (int p = wave; p < DK / 8; p += kPrepThreads / 64) {  // key tile p / 2, tokens 32 (p % 2) ..
+            bf16x8 f[TK];
+            read_across<false, TK>(Kp + 32 * (p % 2) * LDK + 16 * (p / 2), L::kPlK, LDK, f);
+#pragma unroll
+            for (int t = 0; t < TK; ++t) *reinterpret_cast<bf16x8*>(kt + (p * TK + t) * 512) = f[t];
         }
     }
     __syncthreads();
-    {
-        float* y = a.Y + uh * (kScanChunk * kScanChunk);
+    invert_tile(Nl + 16 * wave * (LDY + 1), LDY, Tl + wave * 320, lane);
+    __syncthreads();
+    // the tile rows from this wave's own on
 #pragma unroll
-        for (int p = 0; p < kScanChunk * kScanChunk / 4 / kPrepThreads; ++p) {
-            const int o = (p * kPrepThreads + tid) * 4;
-            st4(y + o, ld4(Yl + o / kScanChunk * LDY + o % kScanChunk));
-        }
-    }
-
-    // W^T = (2^b K)^T - (beta 2^b K)^T Y^T, 32 key columns at a time: a lane has
-    // its piece of the state kernel's row operand
-    uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + lane * 8;
-    constexpr int KS = DK / 32;
-    for (int q = wave; q < KS * (4 / KS); q += 4) {
-        const int n = q % KS, m0 = q / KS * KS;  // all waves have work where d_k is small
-        f32x4 c[KS][2] = {};
+    for (int m = 0; m < 4; ++m)
+        if (m >= wave) {
+            f32x4 x = y[m];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const int j = 16 * kk + 4 * g;
-            f32x4 x = ld_col4(Kl + j * LDK + 32 * n + col, LDK), y = ld_col4(Kl + j * LDK + 32 * n + 16 + col, LDK);
-            const f32x4 f = {be[j] * eb[j], be[j + 1] * eb[j + 1], be[j + 2] * eb[j + 2], be[j + 3] * eb[j + 3]};
-            x *= f;
-            y *= f;
-#pragma unroll
-            for (int m = 0; m < KS; ++m)
-                if (m0 + m >= kk) {
-                    const f32x4 yl = ld4(Yl + (16 * (m0 + m) + col) * LDY + j);
-                    c[m][0] = mma16(x, yl, c[m][0]);
-                    c[m][1] = mma16(y, yl, c[m][1]);
+            for (int n = 0; n < m; ++n)
+                if (n >= wave) {
+                    const f32x4 nb = ld4(Nl + (16 * m + col) * LDY + 16 * n + 4 * g);
+                    x = mma16(-nb, y[n], x);
                 }
+            y[m] = mma16(ld4(Tl + m * 320 + col * 20 + 4 * g), x, f32x4{});
+            st4(a.Y + uh * (kScanChunk * kScanChunk) + ((m * 4 + wave) * 64 + lane) * 4, y[m]);
         }
+    __syncthreads();
+    // Y beta's parts, transposed (rows j, tokens i along them); zeros where a step of 32 reaches above the diagonal
+    auto store_y = [&](float f) {
 #pragma unroll
-        for (int m = 0; m < KS; ++m) {
-            const int i = 16 * (m0 + m) + col;
-            const float* kr = Kl + i * LDK + 32 * n + 4 * g;
-            store_operand<3>(w + ((m0 + m) * KS + n) * 3 * 512, eb[i] * ld4(kr) - c[m][0], eb[i] * ld4(kr + 16) - c[m][1]);
+        for (int m = 0; m < 4; ++m)
+            if (m >= (wave & 2)) store_parts<3>(Yp + j0 * kLdT + 16 * m + 4 * g, L::kPlY, m >= wave ? f * y[m] : f32x4{});
+    };
+    store_y(be[j0]);
+    __syncthreads();
+    // E0 = V - (Y beta) V
+    for (int c0 = 16 * wave; c0 < a.d_v; c0 += 64) {
+        if (c0 >= 64) load_v(c0);
+        f32x4 x[4] = {};
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8 f[3], yf[3];
+            operand_of(v[2 * kk], v[2 * kk + 1], f);
+            bf16x8 vf[TK];
+#pragma unroll
+            for (int t = 0; t < TK; ++t) vf[t] = f[t];
+#pragma unroll
+            for (int m = 2 * kk; m < 4; ++m) {
+                read_across<true, 3>(Yp + 32 * kk * kLdT + 16 * m, L::kPlY, kLdT, yf);
+                x[m] = mma_parts<3, TK>(yf, vf, x[m]);
+            }
         }
+        float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + (c0 / 16 * 64 + lane) * 4;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) st4(e + m * 16 * a.d_v, v[m] - x[m]);
     }
-    // E0 = V - Y (beta V), 64 value columns at a time
-    for (int c0 = 0; c0 < a.d_v; c0 += 64) {
-        __syncthreads();
+    __syncthreads();
+    store_y(be[j0] * eb[j0]);
+    __syncthreads();
+    // W^T = (2^b K)^T - K^T (Y beta 2^b)^T: wave m the tokens of tile m, a lane its
+    // piece of the state kernel's row operand
+    {
+        uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + wave * KS * 3 * 512 + lane * 8;
+        const int i = 16 * wave + col;
+        bf16x8 yf[2][3];
 #pragma unroll
-        for (int p = 0; p < kScanChunk * 8 / kPrepThreads; ++p) {
-            const int i = (p * kPrepThreads + tid) / 8, c = (p * kPrepThreads + tid) % 8 * 8;
-            float y[8] = {};
-            if (i < len && c0 + c < a.d_v) load8_as_f32(a.v, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + c, a.qkv_bf16, y);
-            st4(Vl + i * LDY + c, f32x4{y[0], y[1], y[2], y[3]});
-            st4(Vl + i * LDY + c + 4, f32x4{y[4], y[5], y[6], y[7]});
-        }
-        __syncthreads();
-        if (c0 + 16 * wave >= a.d_v) continue;
-        f32x4 c[4] = {};
+        for (int kk = 0; kk < 2; ++kk)
+            if (2 * kk <= wave) read_across<false, 3>(Yp + 32 * kk * kLdT + 16 * wave, L::kPlY, kLdT, yf[kk]);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const int j = 16 * kk + 4 * g;
-            f32x4 x = ld_col4(Vl + j * LDY + 16 * wave + col, LDY);
+        for (int n = 0; n < KS; ++n) {
+            f32x4 x[2] = {};
 #pragma unroll
-            for (int s = 0; s < 4; ++s) x[s] *= be[j + s];
+            for (int kk = 0; kk < 2; ++kk)
+                if (2 * kk <= wave)
 #pragma unroll
-            for (int m = kk; m < 4; ++m) c[m] = mma16(ld4(Yl + (16 * m + col) * LDY + j), x, c[m]);
-        }
-        float* e = a.E + uh * ((size_t)kScanChunk * a.d_v) + ((c0 / 16 + wave) * 64 + lane) * 4;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            f32x4 y;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = Vl[(16 * m + 4 * g + r) * LDY + 16 * wave + col] - c[m][r];
-            st4(e + m * 16 * a.d_v, y);
+                    for (int q = 0; q < 2; ++q) {
+                        bf16x8 f[TK];
+                        read_across<false, TK>(Kp + 32 * kk * LDK + 32 * n + 16 * q, L::kPlK, LDK, f);
+                        x[q] = mma_parts<TK, 3>(f, yf[kk], x[q]);
+                    }
+            const uint16_t* kr = Kp + i * LDK + 32 * n + 4 * g;
+            store_operand<3>(w + n * 3 * 512, eb[i] * read_whole<TK>(kr, L::kPlK) - x[0], eb[i] * read_whole<TK>(kr + 16, L::kPlK) - x[1]);
         }
     }
 }
@@ -352,18 +398,27 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     }
 }
 
-// O = scale (2^b Q S0^T + P beta E).  Q and K are staged in LDS, P replaces K;
-// a wave takes 16 value columns at a time, with their rows of S0 and their
-// columns of E straight from memory (each is used by one wave only), the first
-// of them on their way before the staging starts.
+// O^T = scale (S0 (2^b Q)^T + (beta E)^T P^T).  Q's and K's parts are staged in
+// LDS, P's take K's place; a wave takes 16 value columns at a time, their rows of
+// S0 and columns of E straight from memory as they lie there (each is used by one
+// wave only), the first of them on their way before the staging starts.
 constexpr int kOutThreads = 512;
 
-template <int DK>
+template <int DK, int TK>
+struct OutLds {
+    static constexpr int kLdK = DK + 8, kPlK = kScanChunk * kLdK, kLdP = kScanChunk + 8, kPlP = kScanChunk * kLdP;  // in bf16
+    static constexpr int Q = 0, K = TK * kPlK * 2, P = K;
+    static constexpr int kGates = K + (TK * kPlK > 3 * kPlP ? TK * kPlK : 3 * kPlP) * 2;
+    static constexpr int kBytes = kGates + kGateRows * kScanChunk * 4;
+};
+
+template <int DK, int TK>
 __global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanArgs a, const ScanSeqs seqs) {
-    constexpr int LDK = DK + 4, LDY = kScanLdY, kKP = kScanChunk * (LDK > LDY ? LDK : LDY);
-    __shared__ __align__(16) float Ql[kScanChunk * LDK];
-    __shared__ __align__(16) float KP[kKP];
-    __shared__ __align__(16) float gt[kGateRows * kScanChunk];
+    using L = OutLds<DK, TK>;
+    constexpr int LDK = L::kLdK, LDP = L::kLdP, KS = DK / 32;
+    extern __shared__ __align__(16) unsigned char lds[];
+    uint16_t *Qp = reinterpret_cast<uint16_t*>(lds + L::Q), *Kp = reinterpret_cast<uint16_t*>(lds + L::K), *Pp = reinterpret_cast<uint16_t*>(lds + L::P);
+    float* gt = reinterpret_cast<float*>(lds + L::kGates);
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int unit = lb / a.h_v, h = lb % a.h_v, hq = h / a.group;
     int seq, tok, len;
@@ -372,7 +427,6 @@ __global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanA
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     int c0 = 16 * wave;
-    const int c_first = c0 < a.d_v ? c0 : 0;
     f32x4 sb[DK / 16], ee[4];
     auto load = [&](int c) {
         const float* st = a.S + uh * ((size_t)a.d_v * DK) + (size_t)c * DK + lane * 4;
@@ -382,58 +436,77 @@ __global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanA
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) ee[kk] = ld4(e + 16 * kk * a.d_v);
     };
-    load(c_first);
+    load(c0 < a.d_v ? c0 : 0);
     if (tid < kGateRows * kScanChunk) gt[tid] = a.gates[uh * (kGateRows * kScanChunk) + tid];
-    stage_rows<DK, LDK, kOutThreads>(a.q, a.qkv_bf16, tok, len, a.h_qk, hq, Ql);
-    stage_rows<DK, LDK, kOutThreads>(a.k, a.qkv_bf16, tok, len, a.h_qk, hq, KP);
+    stage_parts<TK, DK, LDK, kOutThreads>(a.q, tok, len, a.h_qk, hq, Qp);
+    stage_parts<TK, DK, LDK, kOutThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     __syncthreads();
-    f32x4 p[2];
+    // P^T, tiles on and below the diagonal of P, and the two above it that a step of 32 reaches
+    f32x4 p[2] = {};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int t = wave + 8 * q;
         if (t >= 10) continue;
         int m, n;
         lower_tile(t, m, n);
-        p[q] = f32x4{};
 #pragma unroll
-        for (int kk = 0; kk < DK; kk += 16)
-            p[q] = mma16(ld4(Ql + (16 * m + col) * LDK + kk + 4 * g), ld4(KP + (16 * n + col) * LDK + kk + 4 * g), p[q]);
+        for (int kk = 0; kk < KS; ++kk) {
+            bf16x8 kf[TK], qf[TK];
+            read_along<TK>(Kp + 16 * n * LDK + 32 * kk, L::kPlK, LDK, kf);
+            read_along<TK>(Qp + 16 * m * LDK + 32 * kk, L::kPlK, LDK, qf);
+            p[q] = mma_parts<TK, TK>(kf, qf, p[q]);
+        }
     }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int t = wave + 8 * q;
-        if (t >= 10) continue;
-        int m, n;
-        lower_tile(t, m, n);
+        if (t >= 12) continue;
+        int m = t == 10 ? 0 : 2, n = t == 10 ? 1 : 3;
+        if (t < 10) lower_tile(t, m, n);
+        const int i = 16 * m + col;
+        f32x4 x;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = 16 * m + 4 * g + r, j = 16 * n + col;
-            KP[i * LDY + j] = j <= i ? gt[128 + j] * p[q][r] * decay_between(gt, gt + 64, i, j) : 0.f;
+            const int j = 16 * n + 4 * g + r;
+            x[r] = j <= i ? gt[128 + j] * p[q][r] * decay_between(gt, gt + 64, i, j) : 0.f;
         }
+        store_parts<3>(Pp + i * LDP + 16 * n + 4 * g, L::kPlP, x);
     }
     __syncthreads();
     while (c0 < a.d_v) {
         f32x4 o[4] = {};
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
+        for (int kk = 0; kk < KS; ++kk) {
             __builtin_amdgcn_sched_barrier(0);  // not all reads at once: they would not fit the registers
+            bf16x8 sf[3];
+            operand_of(sb[2 * kk], sb[2 * kk + 1], sf);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) o[m] = mma16(ld4(Ql + (16 * m + col) * LDK + 16 * kk + 4 * g), sb[kk], o[m]);
+            for (int m = 0; m < 4; ++m) {
+                bf16x8 qf[TK];
+                read_along_tiles<TK>(Qp + 16 * m * LDK + 32 * kk, L::kPlK, LDK, qf);
+                o[m] = mma_parts<3, TK>(sf, qf, o[m]);
+            }
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) o[m] *= ld4(gt + 256 + 16 * m + 4 * g);
+        for (int m = 0; m < 4; ++m) o[m] *= gt[256 + 16 * m + col];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < 2; ++kk) {
+            __builtin_amdgcn_sched_barrier(0);
+            bf16x8 ef[3];
+            operand_of(ee[2 * kk], ee[2 * kk + 1], ef);
 #pragma unroll
-            for (int m = kk; m < 4; ++m) o[m] = mma16(ld4(KP + (16 * m + col) * LDY + 16 * kk + 4 * g), ee[kk], o[m]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * g + r;
-                if (i < len) store_out(a.out, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + col, a.scale * o[m][r], a.out_dtype);
+            for (int m = 2 * kk; m < 4; ++m) {
+                bf16x8 pf[3];
+                read_along_tiles<3>(Pp + 16 * m * LDP + 32 * kk, L::kPlP, LDP, pf);
+                o[m] = mma_parts<3, 3>(ef, pf, o[m]);
             }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int i = 16 * m + col;
+            if (i < len) store4_out(a.out, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + 4 * g, a.scale * o[m], a.out_dtype);
+        }
         c0 += 16 * (kOutThreads / 64);
         if (c0 < a.d_v) load(c0);
     }
@@ -444,16 +517,18 @@ hipError_t launch_forward(const ScanArgs& args, const ScanSeqs& seqs, hipStream_
     ScanArgs a = args;
     const unsigned heads = (unsigned)(a.units * a.h_v);
     if (heads > 0) {
-        hipLaunchKernelGGL((scan_prepare_kernel<DK, TK>), dim3(heads), dim3(kPrepThreads), 0, st, a, seqs);
-        const hipError_t e = hipGetLastError();
+        hipError_t e = allow_max_lds<scan_prepare_kernel<DK, TK>>();
         if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((scan_prepare_kernel<DK, TK>), dim3(heads), dim3(kPrepThreads), (PrepLds<DK, TK>::kBytes), st, a, seqs);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     constexpr int NS = SCAN_NS;
     a.slices = (a.d_v + 16 * NS - 1) / (16 * NS);
     hipLaunchKernelGGL((scan_state_kernel<DK, NS, TK>), dim3((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq), dim3(256), 0, st, a, seqs);
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess || heads == 0) return e;
-    hipLaunchKernelGGL(scan_output_kernel<DK>, dim3(heads), dim3(kOutThreads), 0, st, a, seqs);
+    if ((e = allow_max_lds<scan_output_kernel<DK, TK>>()) != hipSuccess) return e;
+    hipLaunchKernelGGL((scan_output_kernel<DK, TK>), dim3(heads), dim3(kOutThreads), (OutLds<DK, TK>::kBytes), st, a, seqs);
     return hipGetLastError();
 }
 

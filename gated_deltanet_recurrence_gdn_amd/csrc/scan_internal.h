@@ -28,6 +28,7 @@ namespace gdn {
 
 constexpr int kScanChunk = 64;
 constexpr int kScanLdY = kScanChunk + 4;  // rows of 64 floats in LDS: 4 rows apart are 16 banks apart
+constexpr int kLdT = kScanChunk + 16;      // rows of 64 bf16 that transposing reads go across: the 4 rows of a 16-lane group on different banks
 constexpr int kGateRows = 6;              // b (high, low part), beta, alpha, 2^b, 2^(b_63 - b)
 // alpha below this counts as this: its powers stay in the fp32 range, and a
 // state carried over with a factor of 2^-60 is below fp32's resolution of
@@ -48,7 +49,7 @@ struct ScanArgs {
     // tape, per chunk unit and value head (valid: per sequence)
     int32_t* valid;
     float* gates;  // [kGateRows][64]
-    float* Y;      // [64][64]
+    float* Y;      // [row tile][column tile] accumulators, the 10 on and below the diagonal are written
     float* E;      // the errors (E0 between the prepare and the state kernel), [token tile][value tile] accumulators
     float* S;      // the state before the chunk, transposed, [value tile][key tile] accumulators
     // workspace
@@ -216,20 +217,85 @@ __device__ __forceinline__ void find_unit(const ScanSeqs& s, int n_seq, int unit
     len = s.len[lo] - at < kScanChunk ? s.len[lo] - at : kScanChunk;
 }
 
-// Loads a chunk's rows of one head, [64][WIDTH] of a [tokens][heads][WIDTH]
-// array, into LDS as fp32 with zeros past the sequence's end.
-template <int WIDTH, int LD, int THREADS>
-__device__ __forceinline__ void stage_rows(const void* x, bool bf16, int tok, int len, int heads, int head, float* lds) {
+// Stages a chunk's rows of one head, [64][WIDTH] of a [tokens][heads][WIDTH]
+// array, in LDS as T parts of bf16 (T planes of [64][LD]) with zeros past the
+// sequence's end.  T = 1: the array is bf16, else fp32.
+template <int T, int WIDTH, int LD, int THREADS>
+__device__ __forceinline__ void stage_parts(const void* x, int tok, int len, int heads, int head, uint16_t* lds) {
     constexpr int kPer = WIDTH / 8;  // pieces of 8 per row
 #pragma unroll
     for (int p = 0; p < kScanChunk * kPer; p += THREADS) {
         const int i = (p + (int)threadIdx.x) / kPer, c = (p + (int)threadIdx.x) % kPer * 8;
         if (i >= kScanChunk) break;  // fewer pieces than threads
-        float y[8] = {};
-        if (i < len) load8_as_f32(x, ((size_t)(tok + i) * heads + head) * WIDTH + c, bf16, y);
-        st4(lds + i * LD + c, f32x4{y[0], y[1], y[2], y[3]});
-        st4(lds + i * LD + c + 4, f32x4{y[4], y[5], y[6], y[7]});
+        const size_t at = ((size_t)(tok + i) * heads + head) * WIDTH + c;
+        if constexpr (T == 1) {
+            u32x4 y = {};
+            if (i < len) y = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at);
+            *reinterpret_cast<u32x4*>(lds + i * LD + c) = y;
+        } else {
+            f32x4 y = {}, z = {};
+            if (i < len) {
+                y = ld4(static_cast<const float*>(x) + at);
+                z = ld4(static_cast<const float*>(x) + at + 4);
+            }
+            u32x2 u[3], v[3];
+            split4(y, u);
+            split4(z, v);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) *reinterpret_cast<u32x4*>(lds + t * kScanChunk * LD + i * LD + c) = u32x4{u[t][0], u[t][1], v[t][0], v[t][1]};
+        }
     }
+}
+
+// Operands from LDS, T planes `plane` apart.  rows: the contraction runs along
+// the rows (lane l: row l % 16, 8 (l / 16) ..+7 of it).
+template <int T>
+__device__ __forceinline__ void read_along(const uint16_t* p, int plane, int ld, bf16x8 (&f)[T]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int t = 0; t < T; ++t) f[t] = ld_bf8(p + t * plane + (lane & 15) * ld + 8 * (lane >> 4));
+}
+
+// The same with the indices in operand_of's order.
+template <int T>
+__device__ __forceinline__ void read_along_tiles(const uint16_t* p, int plane, int ld, bf16x8 (&f)[T]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const uint16_t* q = p + t * plane + (lane & 15) * ld + 4 * (lane >> 4);
+        const u32x2 x = *reinterpret_cast<const u32x2*>(q), y = *reinterpret_cast<const u32x2*>(q + 16);
+        f[t] = __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
+    }
+}
+
+// Operands whose contraction runs across the rows.  ds_read_b64_tr_b16 gives lane
+// c of a 16-lane group the values c of the four rows whose quarters the group's
+// lanes address: lane 4 e + q row e, columns 4 q ..+3.  Group g reads rows 8 g
+// ..+7, or (TILES, operand_of's order) 4 g ..+3 and 16 + 4 g ..+3.
+template <bool TILES, int T>
+__device__ __forceinline__ void read_across(const uint16_t* p, int plane, int ld, bf16x8 (&f)[T]) {
+    typedef short s4v __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4v lds_s4;
+    const int lane = threadIdx.x & 63;
+    const uint16_t* q = p + ((TILES ? 4 : 8) * (lane >> 4) + ((lane >> 2) & 3)) * ld + 4 * (lane & 3);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + t * plane)));
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + t * plane + (TILES ? 16 : 4) * ld)));
+        f[t] = __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
+    }
+}
+
+// Four neighbours of a staged row, whole again.
+template <int T>
+__device__ __forceinline__ f32x4 read_whole(const uint16_t* p, int plane) {
+    f32x4 x = {};
+#pragma unroll
+    for (int t = T - 1; t >= 0; --t) {  // the parts add up exactly
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p + t * plane);
+        x += f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+    }
+    return x;
 }
 
 __device__ __forceinline__ void store_typed(void* p, size_t i, float x, bool bf16) {
@@ -252,6 +318,15 @@ __device__ __forceinline__ float load_out(const void* p, size_t i, int dtype) {
     if (dtype == GDN_F32) return static_cast<const float*>(p)[i];
     if (dtype == GDN_F16) return (float)static_cast<const _Float16*>(p)[i];
     return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+}
+
+__device__ __forceinline__ void store4_out(void* p, size_t i, f32x4 x, int dtype) {
+    if (dtype != GDN_F16) {
+        store4_typed(p, i, x, dtype == GDN_BF16);
+    } else {
+        typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<f16x4*>(static_cast<_Float16*>(p) + i) = f16x4{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3]};
+    }
 }
 
 // Four neighbours; i is a multiple of 4 and p is 16-byte aligned.

@@ -514,7 +514,7 @@ int gdn_prefill_varlen(const gdn_shape* shape, const int32_t* cu_seqlens, const 
  * over it gives the same result.  Nothing is accumulated with atomics; results
  * repeat bit for bit.
  *
- * tape, workspaces, dout, dv, dfinal and dstate are 16-byte aligned, the
+ * tape, workspaces, out, dout, dv, dfinal and dstate are 16-byte aligned, the
  * other outputs 4-byte.  The workspaces' contents on entry are ignored; calls that
  * share one are ordered on one stream.
  */
