@@ -50,20 +50,10 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
     if (a.valid[a.seq0 + seq] == 0) return;
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
-    // dout of this wave's first value tile: rows 16 m + 4 g + r of its column, on the way early
-    const size_t o_row = (size_t)a.h_v * a.d_v;
-    f32x4 o[4];
-    auto load_o = [&](int c0) {
-        const size_t at = ((size_t)tok * a.h_v + h) * a.d_v + c0 + col;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * g + r;
-                o[m][r] = i < len ? load_out(a.dout, at + i * o_row, a.out_dtype) : 0.f;
-            }
-    };
-    if (16 * wave < a.d_v) load_o(16 * wave);
+    // dout of this wave's first value tile, on the way early
+    const size_t o_at = ((size_t)tok * a.h_v + h) * a.d_v + col, o_row = (size_t)a.h_v * a.d_v;
+    RawColumn raw;
+    load_column(a.dout, o_at + (16 * wave < a.d_v ? 16 * wave : 0), o_row, len, a.out_dtype, raw);
     for (int i = tid; i < kGateRows * kScanChunk; i += kBackThreads) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
     stage_parts<TK, DK, LDK, kBackThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     stage_parts<TK, DK, LDK, kBackThreads>(a.q, tok, len, a.h_qk, hq, Qp);
@@ -130,8 +120,9 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
     __syncthreads();
     // dR0 = scale Z^T dO
     for (int c0 = 16 * wave; c0 < a.d_v; c0 += 64) {
-        if (c0 >= 64) load_o(c0);
-        f32x4 x[4] = {};
+        f32x4 o[4], x[4] = {};
+        column_values(raw, len, a.out_dtype, o);
+        if (c0 + 64 < a.d_v) load_column(a.dout, o_at + c0 + 64, o_row, len, a.out_dtype, raw);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             bf16x8 of[3], zf[3];

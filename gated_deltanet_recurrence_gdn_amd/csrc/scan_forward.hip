@@ -70,20 +70,11 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
     const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
 
-    // V of this wave's first value tile: rows 16 m + 4 g + r of its column, on the way early
-    const size_t v_row = (size_t)a.h_v * a.d_v;
-    f32x4 v[4];
-    auto load_v = [&](int c0) {
-        const size_t at = ((size_t)tok * a.h_v + h) * a.d_v + c0 + col;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * g + r;
-                v[m][r] = i < len ? load_out(a.v, at + i * v_row, TK == 1 ? GDN_BF16 : GDN_F32) : 0.f;
-            }
-    };
-    if (16 * wave < a.d_v) load_v(16 * wave);
+    // V of this wave's first value tile, on the way early
+    constexpr int kIn = TK == 1 ? GDN_BF16 : GDN_F32;
+    const size_t v_at = ((size_t)tok * a.h_v + h) * a.d_v + col, v_row = (size_t)a.h_v * a.d_v;
+    RawColumn vr;
+    load_column(a.v, v_at + (16 * wave < a.d_v ? 16 * wave : 0), v_row, len, kIn, vr);
     stage_parts<TK, DK, LDK, kPrepThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     if (wave == 0) {
         float al = 1.f, bt = 0.f;
@@ -177,8 +168,9 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
     __syncthreads();
     // E0 = V - (Y beta) V
     for (int c0 = 16 * wave; c0 < a.d_v; c0 += 64) {
-        if (c0 >= 64) load_v(c0);
-        f32x4 x[4] = {};
+        f32x4 v[4], x[4] = {};
+        column_values(vr, len, kIn, v);
+        if (c0 + 64 < a.d_v) load_column(a.v, v_at + c0 + 64, v_row, len, kIn, vr);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             bf16x8 f[3], yf[3];

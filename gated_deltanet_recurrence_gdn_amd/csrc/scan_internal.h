@@ -339,6 +339,44 @@ __device__ __forceinline__ f32x4 load4_out(const void* p, size_t i, int dtype) {
     return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
 }
 
+// A lane's sixteen values of one column of a chunk, rows 16 m + 4 g + r, kept as
+// loaded: all loads are on their way at once, nothing waits for them before
+// column_values.  Rows past the sequence's end repeat its last one and become zero.
+struct RawColumn {
+    uint32_t x[4][4];
+};
+
+__device__ __forceinline__ void load_column(const void* p, size_t at, size_t row, int len, int dtype, RawColumn& c) {
+    const int g = (threadIdx.x & 63) >> 4;
+    if (dtype == GDN_F32) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int i = 16 * (k / 4) + 4 * g + k % 4;
+            c.x[k / 4][k % 4] = static_cast<const uint32_t*>(p)[at + (i < len ? i : len - 1) * row];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int i = 16 * (k / 4) + 4 * g + k % 4;
+            c.x[k / 4][k % 4] = static_cast<const uint16_t*>(p)[at + (i < len ? i : len - 1) * row];
+        }
+    }
+}
+
+__device__ __forceinline__ void column_values(const RawColumn& c, int len, int dtype, f32x4 (&v)[4]) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t x = c.x[m][r];
+            const float y = dtype == GDN_F32   ? __builtin_bit_cast(float, x)
+                            : dtype == GDN_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)x)
+                                               : __builtin_bit_cast(float, x << 16);
+            v[m][r] = 16 * m + 4 * g + r < len ? y : 0.f;
+        }
+}
+
 // 2^(b_i - b_j) from the two-part sums: the high parts' difference is rounded
 // relative to itself, not to the (much larger) sums.
 __device__ __forceinline__ float decay_between(const float* bh, const float* bl, int i, int j) {
