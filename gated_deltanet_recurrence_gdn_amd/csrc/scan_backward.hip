@@ -338,18 +338,22 @@ __device__ __forceinline__ float wave_sum(float x) {
 // instruction) at a time.  S0, G, dR and E arrive as accumulator tiles (a lane
 // holds four neighbours across d_v), are cut into parts and laid in LDS with d_v
 // as the row index; the transposing reads then give both operands of every
-// product.  A wave owns one 16-column tile of the 64 x d_k sums and one or two of
-// the ten lower tiles of the 64 x 64 ones.  The next step's tiles are loaded
-// while this one's products run.
+// product.  A wave owns one 16-column tile of the 64 x d_k sums, so its tiles of
+// S0 and G pass through a corner of LDS of its own, one after the other; dR, E and
+// dout serve all waves and are double-buffered: one barrier a step, and the
+// cutting of one wave runs beside another's products.  A wave also owns one or
+// two of the ten lower tiles of the 64 x 64 sums.
 constexpr int kGradThreads = 512;
 constexpr int kGradWaves = kGradThreads / 64;
-constexpr int kLdO = 32 + 8;           // rows of dout (32 value columns), read 16 bytes a lane
+constexpr int kLdO = 32 + 8;  // rows of dout (32 value columns), read 16 bytes a lane
+constexpr int kLdS = 16;      // rows of a wave's S0 or G (16 key columns): four are the 32 banks
 
 template <int DK, int TK, int TO>
 struct GradLds {
-    static constexpr int kLdS = DK + 16, kPlS = 32 * kLdS, kPlR = 32 * kLdT, kPlO = kScanChunk * kLdO;  // in bf16
-    static constexpr int S = 0, G = S + 3 * kPlS * 2, R = G + 3 * kPlS * 2, E = R + 3 * kPlR * 2, O = E + 3 * kPlR * 2;
-    static constexpr int kStaged = O + TO * kPlO * 2;
+    static constexpr int kPlS = 32 * kLdS, kPlR = 32 * kLdT, kPlO = kScanChunk * kLdO;  // in bf16
+    static constexpr int kS = 3 * kPlS;                                                   // a wave's corner
+    static constexpr int S = 0, R = kGradWaves * kS * 2, E = 3 * kPlR * 2, O = 2 * E;     // E, O: from R on
+    static constexpr int kBuffer = O + TO * kPlO * 2, kStaged = R + 2 * kBuffer;
     // in the staged tiles' place: K and Q before and after the heads, M after a head's products
     static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, K = 0, Q = TK * kPlK * 2, kInputs = 2 * Q, M = 0;
     static constexpr int kShared = kStaged > kInputs ? kStaged : kInputs;
@@ -357,7 +361,7 @@ struct GradLds {
     static constexpr int kGates = P + kScanChunk * kScanLdY * 4, kY = kGates + kGateRows * kScanChunk * 4;
     static constexpr int kZ = kY + 8 * kScanChunk * 4, kB = kZ + 8 * kScanChunk * 4, kF = kB + kScanChunk * 4, kG = kF + kScanChunk * 4;
     static constexpr int kBytes = kG + kGradWaves * 4;
-    static_assert(kScanChunk * kScanLdY * 4 <= R, "M lies in S0's and G's place");
+    static_assert(kScanChunk * kScanLdY * 4 <= kStaged, "M lies in the staged tiles' place");
     static_assert(kBytes <= kMaxLdsBytes, "LDS of a compute unit");
 };
 
@@ -365,9 +369,8 @@ struct GradLds {
 template <int DK, int TK, int TO>
 __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using L = GradLds<DK, TK, TO>;
-    constexpr int LDK = L::kLdK, LDY = kScanLdY, LDS = L::kLdS;
+    constexpr int LDK = L::kLdK, LDY = kScanLdY;
     constexpr int NT = DK / 16, MW = NT / 2;
-    constexpr int kSg = 2 * NT > kGradWaves ? 2 * NT / kGradWaves : 1;  // S0 (and G) tiles of a wave and step
     extern __shared__ __align__(16) float lds_raw[];
     unsigned char* lds = reinterpret_cast<unsigned char*>(lds_raw);
     uint16_t *Kp = reinterpret_cast<uint16_t*>(lds + L::K), *Qp = reinterpret_cast<uint16_t*>(lds + L::Q);
@@ -375,8 +378,6 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
     float *Xl = reinterpret_cast<float*>(lds + L::X), *Ps = reinterpret_cast<float*>(lds + L::P);
     float *gt = reinterpret_cast<float*>(lds + L::kGates), *ry = reinterpret_cast<float*>(lds + L::kY), *rz = reinterpret_cast<float*>(lds + L::kZ);
     float *rb = reinterpret_cast<float*>(lds + L::kB), *rf = reinterpret_cast<float*>(lds + L::kF), *rg = reinterpret_cast<float*>(lds + L::kG);
-    uint16_t *Sp = reinterpret_cast<uint16_t*>(lds + L::S), *Gp = reinterpret_cast<uint16_t*>(lds + L::G), *Rp = reinterpret_cast<uint16_t*>(lds + L::R);
-    uint16_t *Ep = reinterpret_cast<uint16_t*>(lds + L::E), *Op = reinterpret_cast<uint16_t*>(lds + L::O);
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int unit = lb / a.h_qk, hq = lb % a.h_qk;
     int seq, tok, len;
@@ -386,31 +387,69 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
     int lane = tid & 63, col = lane & 15, g = lane >> 4;
     const int nt = wave % NT, m0 = wave / NT * MW;  // this wave's key columns and row tiles
 
-    // the next step's tiles, in registers
-    f32x4 sn[kSg], gn[kSg], rn, en, on;
-    auto load = [&](int hh, int c0) {
-        const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + hq * a.group + hh;
-        const int width = a.d_v - c0;  // 16: the second value tile is zero
-        const float *st = a.S + uh * ((size_t)a.d_v * DK) + (size_t)c0 * DK + lane * 4, *gd = a.G + uh * ((size_t)a.d_v * DK) + (size_t)c0 * DK + lane * 4;
+    uint16_t* Sp = reinterpret_cast<uint16_t*>(lds + L::S) + wave * L::kS;
+
+    // Tiles in registers, loaded without branches (past d_v or the sequence's end:
+    // something else of the arrays) and used as loaded: S0 and G of the coming step,
+    // dR, E and dout of the one after it.
+    f32x4 sn[2], gn[2], rn, en;
+    u32x4 on = {};
+    const bool wide = a.out_dtype == GDN_F32;
+    auto load_s = [&](int hh, int c0) {
+        const size_t at = ((size_t)(a.unit_base + unit) * a.h_v + hq * a.group + hh) * ((size_t)a.d_v * DK) + (size_t)c0 * DK;
+        const int second = c0 + 16 < a.d_v ? NT : 0;  // the second value tile, or the first again
 #pragma unroll
-        for (int q = 0; q < kSg; ++q) {
-            const int t = wave * kSg + q;  // value tile t / NT, key tile t % NT
-            sn[q] = gn[q] = f32x4{};
-            if (t < 2 * NT && 16 * (t / NT) < width) {
-                sn[q] = ld4(st + t * 256);
-                gn[q] = ld4(gd + t * 256);
+        for (int q = 0; q < 2; ++q) {
+            sn[q] = ld4(a.S + at + (unsigned)((q * second + nt) * 256 + lane * 4));
+            gn[q] = ld4(a.G + at + (unsigned)((q * second + nt) * 256 + lane * 4));
+        }
+    };
+    auto load_r = [&](int hh, int c0) {
+        const int second = c0 + 16 < a.d_v ? 1 : 0;
+        const size_t at = ((size_t)(a.unit_base + unit) * a.h_v + hq * a.group + hh) * ((size_t)kScanChunk * a.d_v) + (size_t)(c0 / 16) * 256;
+        const unsigned ro = (unsigned)(wave / 2 * 16 * a.d_v + wave % 2 * second * 256 + lane * 4);  // token tile wave / 2, value tile wave % 2
+        rn = ld4(a.dR + at + ro);
+        en = ld4(a.E + at + ro);
+        const int i = tid / 8 < len ? tid / 8 : len - 1, c = tid % 8 * 4 % (16 + 16 * second);
+        const size_t from = ((size_t)(tok + i) * a.h_v + hq * a.group + hh) * a.d_v + c0 + c;
+        if (wide) {
+            on = *reinterpret_cast<const u32x4*>(static_cast<const float*>(a.dout) + from);
+        } else {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.dout) + from);
+            on[0] = x[0];
+            on[1] = x[1];
+        }
+    };
+    // dR, E and dout of columns c0 .. of head hh, loaded by load_r, into buffer `to`
+    auto stage_r = [&](int hh, int c0, int to) {
+        const bool second = c0 + 16 < a.d_v;
+        uint16_t* Rp = reinterpret_cast<uint16_t*>(lds + L::R + to * L::kBuffer);
+        const int at = (16 * (wave % 2) + col) * kLdT + wave / 2 * 16 + 4 * g;
+        if (wave % 2 == 1 && !second) rn = en = f32x4{};
+        store_parts<3>(Rp + at, L::kPlR, rn);
+        store_parts<3>(Rp + L::E / 2 + at, L::kPlR, en);
+        const int i = tid / 8, c = tid % 8 * 4;
+        if (i >= len || (c >= 16 && !second)) on = u32x4{};
+        uint16_t* op = Rp + L::O / 2 + i * kLdO + c;
+        if constexpr (TO == 1) {
+            *reinterpret_cast<u32x2*>(op) = u32x2{on[0], on[1]};
+        } else {
+            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+            const f16x4 x = __builtin_bit_cast(f16x4, u32x2{on[0], on[1]});
+            store_parts<3>(op, L::kPlO, wide ? __builtin_bit_cast(f32x4, on) : f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]});
+        }
+        if (wave % 2 == 0 || second) {  // dv = beta dR
+            const int h = hq * a.group + hh;
+            const f32x4 be = ld4(a.gates + ((size_t)(a.unit_base + unit) * a.h_v + h) * (kGateRows * kScanChunk) + 128 + wave / 2 * 16 + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = wave / 2 * 16 + 4 * g + r;
+                if (j < len) store_typed(a.dv, ((size_t)(tok + j) * a.h_v + h) * a.d_v + c0 + 16 * (wave % 2) + col, be[r] * rn[r], a.qkv_bf16);
             }
         }
-        rn = en = on = f32x4{};
-        if (16 * (wave % 2) < width) {  // token tile wave / 2, value tile wave % 2
-            const size_t at = uh * ((size_t)kScanChunk * a.d_v) + wave / 2 * 16 * a.d_v + (c0 / 16 + wave % 2) * 256 + lane * 4;
-            rn = ld4(a.dR + at);
-            en = ld4(a.E + at);
-        }
-        const int i = tid / 8, c = tid % 8 * 4;
-        if (i < len && c < width) on = load4_out(a.dout, ((size_t)(tok + i) * a.h_v + hq * a.group + hh) * a.d_v + c0 + c, a.out_dtype);
     };
-    load(0, 0);
+    load_s(0, 0);
+    load_r(0, 0);
     stage_parts<TK, DK, LDK, kGradThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     stage_parts<TK, DK, LDK, kGradThreads>(a.q, tok, len, a.h_qk, hq, Qp);
     __syncthreads();
@@ -455,51 +494,47 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         f32x4 os[MW] = {}, rs[MW] = {}, eg[MW] = {}, dp[2] = {}, da[2] = {};
         float gs = 0.f;
         const float gate = tid < kGateRows * kScanChunk ? a.gates[uh * (kGateRows * kScanChunk) + tid] : 0.f;
-        for (int c0 = 0; c0 < a.d_v; c0 += 32) {
-            __syncthreads();  // the last step's reads (or K's, Q's and M's) are done
-            if (c0 == 0 && tid < kGateRows * kScanChunk) gt[tid] = gate;
+        __syncthreads();  // K, Q or M have been read
+        if (tid < kGateRows * kScanChunk) gt[tid] = gate;
+        stage_r(hh, 0, 0);
+        if (32 < a.d_v) load_r(hh, 32);
+        __syncthreads();
+        for (int c0 = 0, buffer = 0; c0 < a.d_v; c0 += 32, buffer ^= 1) {
+            const uint16_t* Rp = reinterpret_cast<const uint16_t*>(lds + L::R + buffer * L::kBuffer);
+            const uint16_t *Ep = Rp + L::E / 2, *Op = Rp + L::O / 2;
+            if (c0 + 32 < a.d_v) {
+                stage_r(hh, c0 + 32, buffer ^ 1);
+                if (c0 + 64 < a.d_v) load_r(hh, c0 + 64);
+            }
+            if (c0 + 16 >= a.d_v) sn[1] = gn[1] = f32x4{};
+            bf16x8 sb[3], gb[3];
 #pragma unroll
-            for (int q = 0; q < kSg; ++q) {
-                const int t = wave * kSg + q;
-                if (t < 2 * NT) {
-                    const int at = (16 * (t / NT) + col) * LDS + 16 * (t % NT) + 4 * g;
-                    store_parts<3>(Sp + at, L::kPlS, sn[q]);
-                    store_parts<3>(Gp + at, L::kPlS, gn[q]);
-                }
+            for (int q = 0; q < 2; ++q) {
+                store_parts<3>(Sp + (16 * q + col) * kLdS + 4 * g, L::kPlS, sn[q]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) gs = __builtin_fmaf(sn[q][r], gn[q][r], gs);
             }
-            {
-                const int at = (16 * (wave % 2) + col) * kLdT + wave / 2 * 16 + 4 * g;
-                store_parts<3>(Rp + at, L::kPlR, rn);
-                store_parts<3>(Ep + at, L::kPlR, en);
-                store_parts<TO>(Op + tid / 8 * kLdO + tid % 8 * 4, L::kPlO, on);
+            read_across<false, 3>(Sp, L::kPlS, kLdS, sb);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) store_parts<3>(Sp + (16 * q + col) * kLdS + 4 * g, L::kPlS, gn[q]);
+            if (c0 + 32 < a.d_v) load_s(hh, c0 + 32);
+            else if (hh + 1 < a.group) load_s(hh + 1, 0);
+#pragma unroll
+            for (int m = 0; m < MW; ++m) {
+                __builtin_amdgcn_sched_barrier(0);  // one row tile's operands at a time
+                bf16x8 ao[TO], ar[3];
+                read_along<TO>(Op + 16 * (m0 + m) * kLdO, L::kPlO, kLdO, ao);
+                read_across<false, 3>(Rp + 16 * (m0 + m), L::kPlR, kLdT, ar);
+                os[m] = mma_parts<TO, 3>(ao, sb, os[m]);
+                rs[m] = mma_parts<3, 3>(ar, sb, rs[m]);
             }
-            const f32x4 dr = rn;
-            if (c0 + 32 < a.d_v) load(hh, c0 + 32);
-            else if (hh + 1 < a.group) load(hh + 1, 0);
-            __syncthreads();
-            if (c0 + 16 * (wave % 2) < a.d_v)
+            read_across<false, 3>(Sp, L::kPlS, kLdS, gb);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {  // dv = beta dR
-                    const int i = wave / 2 * 16 + 4 * g + r;
-                    if (i < len) store_typed(a.dv, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + 16 * (wave % 2) + col, gt[128 + i] * dr[r], a.qkv_bf16);
-                }
-            {
-                bf16x8 sb[3], gb[3];
-                read_across<false, 3>(Sp + 16 * nt, L::kPlS, LDS, sb);
-                read_across<false, 3>(Gp + 16 * nt, L::kPlS, LDS, gb);
-#pragma unroll
-                for (int m = 0; m < MW; ++m) {
-                    __builtin_amdgcn_sched_barrier(0);  // one row tile's operands at a time
-                    bf16x8 ao[TO], ar[3], ae[3];
-                    read_along<TO>(Op + 16 * (m0 + m) * kLdO, L::kPlO, kLdO, ao);
-                    read_across<false, 3>(Rp + 16 * (m0 + m), L::kPlR, kLdT, ar);
-                    read_across<false, 3>(Ep + 16 * (m0 + m), L::kPlR, kLdT, ae);
-                    os[m] = mma_parts<TO, 3>(ao, sb, os[m]);
-                    rs[m] = mma_parts<3, 3>(ar, sb, rs[m]);
-                    eg[m] = mma_parts<3, 3>(ae, gb, eg[m]);
-                }
+            for (int m = 0; m < MW; ++m) {
+                __builtin_amdgcn_sched_barrier(0);
+                bf16x8 ae[3];
+                read_across<false, 3>(Ep + 16 * (m0 + m), L::kPlR, kLdT, ae);
+                eg[m] = mma_parts<3, 3>(ae, gb, eg[m]);
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -515,8 +550,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 dp[q] = mma_parts<TO, 3>(ao, be, dp[q]);
                 da[q] = mma_parts<3, 3>(ar, be, da[q]);
             }
+            __syncthreads();
         }
-        __syncthreads();  // the staged tiles have been read: M takes their place
+        if (hh + 1 < a.group) load_r(hh + 1, 0);
         const float *be = gt + 128, *al = gt + 192, *eb = gt + 256, *er = gt + 320;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -559,7 +595,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                     rz[nt * kScanChunk + i] = z;
                 }
             }
-        gs = wave_sum(gs);
+        gs = wave_sum(m0 == 0 ? gs : 0.f);
         if (lane == 0) rg[wave] = gs;
         __syncthreads();
         // F_t = sum_{j < t <= i} M_ij: wave w the eight t from 8 w on, one column j per lane
