@@ -326,6 +326,17 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
         for (int i = 0; i < 2; ++i) st4(a.dstate + seq_at + 16 * i, G[i]);
 }
 
+// Sums over 16 lanes of two times four values.
+__device__ __forceinline__ void row_sums(f32x4& x, f32x4& y) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float u = x[r], v = y[r];
+        group_sum2<16>(u, v);
+        x[r] = u;
+        y[r] = v;
+    }
+}
+
 // Sum over 64 lanes.
 __device__ __forceinline__ float wave_sum(float x) {
     x = group_sum<16>(x);
@@ -354,14 +365,13 @@ struct GradLds {
     static constexpr int kS = 3 * kPlS;                                                   // a wave's corner
     static constexpr int S = 0, R = kGradWaves * kS * 2, E = 3 * kPlR * 2, O = 2 * E;     // E, O: from R on
     static constexpr int kBuffer = O + TO * kPlO * 2, kStaged = R + 2 * kBuffer;
-    // in the staged tiles' place: K and Q before and after the heads, M after a head's products
-    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, K = 0, Q = TK * kPlK * 2, kInputs = 2 * Q, M = 0;
+    // in the staged tiles' place: K and Q before and after the heads
+    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, K = 0, Q = TK * kPlK * 2, kInputs = 2 * Q;
     static constexpr int kShared = kStaged > kInputs ? kStaged : kInputs;
     static constexpr int X = kShared, P = X + kScanChunk * kScanLdY * 4;  // sums over the heads
-    static constexpr int kGates = P + kScanChunk * kScanLdY * 4, kY = kGates + kGateRows * kScanChunk * 4;
-    static constexpr int kZ = kY + 8 * kScanChunk * 4, kB = kZ + 8 * kScanChunk * 4, kF = kB + kScanChunk * 4, kG = kF + kScanChunk * 4;
-    static constexpr int kBytes = kG + kGradWaves * 4;
-    static_assert(kScanChunk * kScanLdY * 4 <= kStaged, "M lies in the staged tiles' place");
+    static constexpr int kGates = P + kScanChunk * kScanLdY * 4;  // of two heads
+    static constexpr int kY = kGates + 2 * kGateRows * kScanChunk * 4, kZ = kY + 8 * kScanChunk * 4, kB = kZ + 8 * kScanChunk * 4;
+    static constexpr int kF = kB + kScanChunk * 4, kG = kF + (2 * 160 + 16) * 4, kBytes = kG + kGradWaves * 4;
     static_assert(kBytes <= kMaxLdsBytes, "LDS of a compute unit");
 };
 
@@ -374,9 +384,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
     extern __shared__ __align__(16) float lds_raw[];
     unsigned char* lds = reinterpret_cast<unsigned char*>(lds_raw);
     uint16_t *Kp = reinterpret_cast<uint16_t*>(lds + L::K), *Qp = reinterpret_cast<uint16_t*>(lds + L::Q);
-    float* Ml = reinterpret_cast<float*>(lds + L::M);
     float *Xl = reinterpret_cast<float*>(lds + L::X), *Ps = reinterpret_cast<float*>(lds + L::P);
-    float *gt = reinterpret_cast<float*>(lds + L::kGates), *ry = reinterpret_cast<float*>(lds + L::kY), *rz = reinterpret_cast<float*>(lds + L::kZ);
+    float *gates = reinterpret_cast<float*>(lds + L::kGates), *ry = reinterpret_cast<float*>(lds + L::kY), *rz = reinterpret_cast<float*>(lds + L::kZ);
     float *rb = reinterpret_cast<float*>(lds + L::kB), *rf = reinterpret_cast<float*>(lds + L::kF), *rg = reinterpret_cast<float*>(lds + L::kG);
     const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
     const int unit = lb / a.h_qk, hq = lb % a.h_qk;
@@ -494,7 +503,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         f32x4 os[MW] = {}, rs[MW] = {}, eg[MW] = {}, dp[2] = {}, da[2] = {};
         float gs = 0.f;
         const float gate = tid < kGateRows * kScanChunk ? a.gates[uh * (kGateRows * kScanChunk) + tid] : 0.f;
-        __syncthreads();  // K, Q or M have been read
+        float* gt = gates + (hh & 1) * (kGateRows * kScanChunk);  // the last head's are still being read
+        if (hh == 0) __syncthreads();                            // K and Q have been read
         if (tid < kGateRows * kScanChunk) gt[tid] = gate;
         stage_r(hh, 0, 0);
         if (32 < a.d_v) load_r(hh, 32);
@@ -554,29 +564,68 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         }
         if (hh + 1 < a.group) load_r(hh + 1, 0);
         const float *be = gt + 128, *al = gt + 192, *eb = gt + 256, *er = gt + 320;
+        // The sums over M, by tiles.  A tile (m, n) adds to the t of tile m the sums of
+        // its rows i >= t (and columns j < t where m = n): a product with a triangle of
+        // ones; to the t of tile n < m the sums of its columns j < t; and to the t of
+        // the tiles between its total.
+        f32x4 triangle;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) triangle[r] = 4 * g + r >= col ? 1.f : 0.f;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int t = wave + kGradWaves * q;
             if (t >= 10) continue;
             int m, n;
             lower_tile(t, m, n);
+            const int i = 16 * m + 4 * g, j = 16 * n + col;
+            const f32x4 bh = ld4(gt + i), bl = ld4(gt + 64 + i), bi = ld4(be + i);
+            const float bhj = gt[j], blj = gt[64 + j], bj = be[j];
+            f32x4 xs = {}, ps = {}, mm;
+            if (hh > 0)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    xs[r] = Xl[(i + r) * LDY + j];
+                    ps[r] = Ps[(i + r) * LDY + j];
+                }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * g + r, j = 16 * n + col, at = i * LDY + j;
-                const float d = j <= i ? be[j] * decay_between(gt, gt + 64, i, j) : 0.f;
-                const float x = j < i ? -be[i] * d * da[q][r] : 0.f, p = a.scale * d * dp[q][r];
-                Xl[at] = hh == 0 ? x : Xl[at] + x;
-                Ps[at] = hh == 0 ? p : Ps[at] + p;
-                Ml[at] = j < i ? x * kk_[q][r] + p * qk_[q][r] : 0.f;
-                if (i == j) rb[i] = da[q][r];  // dbeta_i = dR_i . E_i
+                const float d = j <= i + r ? bj * __builtin_amdgcn_exp2f((bh[r] - bhj) + (bl[r] - blj)) : 0.f;
+                const float x = j < i + r ? -bi[r] * d * da[q][r] : 0.f, p = a.scale * d * dp[q][r];
+                xs[r] += x;
+                ps[r] += p;
+                mm[r] = j < i + r ? x * kk_[q][r] + p * qk_[q][r] : 0.f;
+                if (j == i + r) rb[j] = da[q][r];  // dbeta_i = dR_i . E_i
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                Xl[(i + r) * LDY + j] = xs[r];
+                Ps[(i + r) * LDY + j] = ps[r];
+            }
+            f32x4 f = mma16(triangle, mm, f32x4{}), e = mma16(f32x4{1.f, 1.f, 1.f, 1.f}, mm, f32x4{});
+            const float total = group_sum<16>(e[0]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool before = col < 4 * g + r;
+                f[r] = m == n && !before ? 0.f : f[r];
+                e[r] = before ? e[r] : 0.f;
+            }
+            row_sums(f, e);
+            if (col == 0) {
+                st4(rf + 16 * t + 4 * g, f);
+                st4(rf + 160 + 16 * t + 4 * g, e);
+                if (g == 0) rf[320 + t] = total;
             }
         }
 #pragma unroll
-        for (int m = 0; m < MW; ++m)
+        for (int m = 0; m < MW; ++m) {
+            const int i = 16 * (m0 + m) + 4 * g;
+            const f32x4 ebi = ld4(eb + i), bi = ld4(be + i), eri = ld4(er + i);
+            const f32x4 o = a.scale * ebi * os[m], x = bi * ebi * rs[m], e = eri * bi * eg[m];
+            accq[m] += o;
+            acck[m] += e - x;
+            f32x4 y, z;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                __builtin_amdgcn_sched_barrier(0);
-                const int i = 16 * (m0 + m) + 4 * g + r;
                 float kv, qv;
                 if constexpr (TK == 1) {
                     kv = bf16_lo(kq[m][r][0]);
@@ -585,35 +634,28 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                     kv = __builtin_bit_cast(float, kq[m][r][0]);
                     qv = __builtin_bit_cast(float, kq[m][r][1]);
                 }
-                const float o = a.scale * eb[i] * os[m][r], x = be[i] * eb[i] * rs[m][r], e = er[i] * be[i] * eg[m][r];
-                accq[m][r] += o;
-                acck[m][r] += e - x;
-                float y = qv * o - kv * x, z = kv * e;
-                group_sum2<16>(y, z);
-                if (col == 0) {
-                    ry[nt * kScanChunk + i] = y;
-                    rz[nt * kScanChunk + i] = z;
-                }
+                y[r] = qv * o[r] - kv * x[r];
+                z[r] = kv * e[r];
             }
+            row_sums(y, z);
+            if (col == 0) {
+                st4(ry + nt * kScanChunk + i, y);
+                st4(rz + nt * kScanChunk + i, z);
+            }
+        }
         gs = wave_sum(m0 == 0 ? gs : 0.f);
         if (lane == 0) rg[wave] = gs;
         __syncthreads();
-        // F_t = sum_{j < t <= i} M_ij: wave w the eight t from 8 w on, one column j per lane
-        {
-            const int t1 = 8 * wave + 7;
-            float run = 0.f;
-            for (int i = kScanChunk - 1; i > t1; --i) run += lane < i ? Ml[i * LDY + lane] : 0.f;
+        if (wave == 0) {  // beside the others' next head
+            float y = 0.f, z = 0.f, gsum = 0.f, f = 0.f;
+            const int tile = lane / 16, w = lane % 16;
 #pragma unroll
-            for (int t = 7; t >= 0; --t) {
-                const int i = 8 * wave + t;
-                run += lane < i ? Ml[i * LDY + lane] : 0.f;
-                const float f = wave_sum(lane < i ? run : 0.f);
-                if (lane == 0) rf[i] = f;
+            for (int n = 0; n < 4; ++n) {
+                if (n <= tile) f += rf[16 * (tile * (tile + 1) / 2 + n) + w];
+                if (n > tile) f += rf[160 + 16 * (n * (n + 1) / 2 + tile) + w];
             }
-        }
-        __syncthreads();
-        if (wave == 0) {
-            float y = 0.f, z = 0.f, gsum = 0.f;
+            if (tile == 1) f += rf[320 + 3] + rf[320 + 6];
+            if (tile == 2) f += rf[320 + 6] + rf[320 + 7];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 y += ry[n * kScanChunk + lane];
@@ -631,7 +673,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             if (lane == 0) z = 0.f;
             if (lane < len) {
                 const size_t at = (size_t)(tok + lane) * a.h_v + h;
-                a.dalpha[at] = (rf[lane] + y + z + eb[63] * gsum) / al[lane];
+                a.dalpha[at] = (f + y + z + eb[63] * gsum) / al[lane];
                 a.dbeta[at] = rb[lane];
             }
         }
