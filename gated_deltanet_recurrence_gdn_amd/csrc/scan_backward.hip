@@ -26,7 +26,7 @@ constexpr int kBackThreads = 256;
 
 template <int DK, int TK>
 struct BackPrepLds {
-    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, kPlZ = kScanChunk * kLdT;  // in bf16
+    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, kPlZ = rows_t(kScanChunk);  // in bf16
     static constexpr int K = 0, Q = TK * kPlK * 2, Z = Q;  // Z takes Q's place
     static constexpr int kGates = Q + (TK * kPlK > 3 * kPlZ ? TK * kPlK : 3 * kPlZ) * 2;
     static constexpr int kBytes = kGates + kGateRows * kScanChunk * 4;
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
     // rows i, j along them; zeros where a step of 32 tokens reaches above the diagonal
 #pragma unroll
     for (int m = 0; m < 4; ++m)
-        if (m <= (wave | 1)) store_parts<3>(Zp + i0 * kLdT + 16 * m + 4 * g, L::kPlZ, z[m]);
+        if (m <= (wave | 1)) store_parts<3>(Zp + row_t(i0) + 16 * m + 4 * g, L::kPlZ, z[m]);
     __syncthreads();
     // dR0 = scale Z^T dO
     for (int c0 = 16 * wave; c0 < a.d_v; c0 += 64) {
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
             operand_of(o[2 * kk], o[2 * kk + 1], of);
 #pragma unroll
             for (int m = 0; m < 2 * kk + 2; ++m) {
-                read_across<true, 3>(Zp + 32 * kk * kLdT + 16 * m, L::kPlZ, kLdT, zf);
+                read_across<true, 3, kSkew>(Zp + row_t(32 * kk) + 16 * m, L::kPlZ, kLdT, zf);
                 x[m] = mma_parts<3, 3>(zf, of, x[m]);
             }
         }
@@ -357,11 +357,12 @@ __device__ __forceinline__ float wave_sum(float x) {
 constexpr int kGradThreads = 512;
 constexpr int kGradWaves = kGradThreads / 64;
 constexpr int kLdO = 32 + 8;  // rows of dout (32 value columns), read 16 bytes a lane
-constexpr int kLdS = 16;      // rows of a wave's S0 or G (16 key columns): four are the 32 banks
+constexpr int kLdS = 16;      // rows of a wave's S0 or G (16 key columns), skewed as row_t's
 
 template <int DK, int TK, int TO>
 struct GradLds {
-    static constexpr int kPlS = 32 * kLdS, kPlR = 32 * kLdT, kPlO = kScanChunk * kLdO;  // in bf16
+    static constexpr int kSk = TO == 1 ? kSkew : 0;  // where dout has three parts, LDS has no room for the skew
+    static constexpr int kPlS = 32 * kLdS + 4 * kSk, kPlR = 32 * kLdT + 4 * kSk, kPlO = kScanChunk * kLdO;  // in bf16
     static constexpr int kS = 3 * kPlS;                                                   // a wave's corner
     static constexpr int S = 0, R = kGradWaves * kS * 2, E = 3 * kPlR * 2, O = 2 * E;     // E, O: from R on
     static constexpr int kBuffer = O + TO * kPlO * 2, kStaged = R + 2 * kBuffer;
@@ -401,7 +402,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
     // Tiles in registers, loaded without branches (past d_v or the sequence's end:
     // something else of the arrays) and used as loaded: S0 and G of the coming step,
     // dR, E and dout of the one after it.
-    f32x4 sn[2], gn[2], rn, en;
+    f32x4 sn[2], gn[2], rn, en, rv;  // rv: dR as staged
     u32x4 on = {};
     const bool wide = a.out_dtype == GDN_F32;
     auto load_s = [&](int hh, int c0) {
@@ -433,7 +434,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
     auto stage_r = [&](int hh, int c0, int to) {
         const bool second = c0 + 16 < a.d_v;
         uint16_t* Rp = reinterpret_cast<uint16_t*>(lds + L::R + to * L::kBuffer);
-        const int at = (16 * (wave % 2) + col) * kLdT + wave / 2 * 16 + 4 * g;
+        const int at = (16 * (wave % 2) + col) * kLdT + (16 * (wave % 2) + col) / 8 * L::kSk + wave / 2 * 16 + 4 * g;
         if (wave % 2 == 1 && !second) rn = en = f32x4{};
         store_parts<3>(Rp + at, L::kPlR, rn);
         store_parts<3>(Rp + L::E / 2 + at, L::kPlR, en);
@@ -447,15 +448,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             const f16x4 x = __builtin_bit_cast(f16x4, u32x2{on[0], on[1]});
             store_parts<3>(op, L::kPlO, wide ? __builtin_bit_cast(f32x4, on) : f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]});
         }
-        if (wave % 2 == 0 || second) {  // dv = beta dR
-            const int h = hq * a.group + hh;
-            const f32x4 be = ld4(a.gates + ((size_t)(a.unit_base + unit) * a.h_v + h) * (kGateRows * kScanChunk) + 128 + wave / 2 * 16 + 4 * g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = wave / 2 * 16 + 4 * g + r;
-                if (j < len) store_typed(a.dv, ((size_t)(tok + j) * a.h_v + h) * a.d_v + c0 + 16 * (wave % 2) + col, be[r] * rn[r], a.qkv_bf16);
-            }
-        }
+        rv = rn;
     };
     load_s(0, 0);
     load_r(0, 0);
@@ -512,21 +505,28 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         for (int c0 = 0, buffer = 0; c0 < a.d_v; c0 += 32, buffer ^= 1) {
             const uint16_t* Rp = reinterpret_cast<const uint16_t*>(lds + L::R + buffer * L::kBuffer);
             const uint16_t *Ep = Rp + L::E / 2, *Op = Rp + L::O / 2;
-            if (c0 + 32 < a.d_v) {
-                stage_r(hh, c0 + 32, buffer ^ 1);
-                if (c0 + 64 < a.d_v) load_r(hh, c0 + 64);
+            if (wave % 2 == 0 || c0 + 16 < a.d_v) {  // dv = beta dR
+                const f32x4 dv = ld4(gt + 128 + wave / 2 * 16 + 4 * g) * rv;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = wave / 2 * 16 + 4 * g + r;
+                    if (i < len) store_typed(a.dv, ((size_t)(tok + i) * a.h_v + h) * a.d_v + c0 + 16 * (wave % 2) + col, dv[r], a.qkv_bf16);
+                }
             }
+            if (c0 + 32 < a.d_v) stage_r(hh, c0 + 32, buffer ^ 1);
+            if (c0 + 64 < a.d_v) load_r(hh, c0 + 64);
+            else if (c0 + 32 >= a.d_v && hh + 1 < a.group) load_r(hh + 1, 0);
             if (c0 + 16 >= a.d_v) sn[1] = gn[1] = f32x4{};
             bf16x8 sb[3], gb[3];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                store_parts<3>(Sp + (16 * q + col) * kLdS + 4 * g, L::kPlS, sn[q]);
+                store_parts<3>(Sp + (16 * q + col) * kLdS + (16 * q + col) / 8 * L::kSk + 4 * g, L::kPlS, sn[q]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) gs = __builtin_fmaf(sn[q][r], gn[q][r], gs);
             }
-            read_across<false, 3>(Sp, L::kPlS, kLdS, sb);
+            read_across<false, 3, L::kSk>(Sp, L::kPlS, kLdS, sb);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) store_parts<3>(Sp + (16 * q + col) * kLdS + 4 * g, L::kPlS, gn[q]);
+            for (int q = 0; q < 2; ++q) store_parts<3>(Sp + (16 * q + col) * kLdS + (16 * q + col) / 8 * L::kSk + 4 * g, L::kPlS, gn[q]);
             if (c0 + 32 < a.d_v) load_s(hh, c0 + 32);
             else if (hh + 1 < a.group) load_s(hh + 1, 0);
 #pragma unroll
@@ -534,16 +534,16 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 __builtin_amdgcn_sched_barrier(0);  // one row tile's operands at a time
                 bf16x8 ao[TO], ar[3];
                 read_along<TO>(Op + 16 * (m0 + m) * kLdO, L::kPlO, kLdO, ao);
-                read_across<false, 3>(Rp + 16 * (m0 + m), L::kPlR, kLdT, ar);
+                read_across<false, 3, L::kSk>(Rp + 16 * (m0 + m), L::kPlR, kLdT, ar);
                 os[m] = mma_parts<TO, 3>(ao, sb, os[m]);
                 rs[m] = mma_parts<3, 3>(ar, sb, rs[m]);
             }
-            read_across<false, 3>(Sp, L::kPlS, kLdS, gb);
+            read_across<false, 3, L::kSk>(Sp, L::kPlS, kLdS, gb);
 #pragma unroll
             for (int m = 0; m < MW; ++m) {
                 __builtin_amdgcn_sched_barrier(0);
                 bf16x8 ae[3];
-                read_across<false, 3>(Ep + 16 * (m0 + m), L::kPlR, kLdT, ae);
+                read_across<false, 3, L::kSk>(Ep + 16 * (m0 + m), L::kPlR, kLdT, ae);
                 eg[m] = mma_parts<3, 3>(ae, gb, eg[m]);
             }
 #pragma unroll
@@ -555,14 +555,13 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 lower_tile(t, m, n);
                 bf16x8 ao[TO], ar[3], be[3];
                 read_along<TO>(Op + 16 * m * kLdO, L::kPlO, kLdO, ao);
-                read_across<false, 3>(Rp + 16 * m, L::kPlR, kLdT, ar);
-                read_across<false, 3>(Ep + 16 * n, L::kPlR, kLdT, be);
+                read_across<false, 3, L::kSk>(Rp + 16 * m, L::kPlR, kLdT, ar);
+                read_across<false, 3, L::kSk>(Ep + 16 * n, L::kPlR, kLdT, be);
                 dp[q] = mma_parts<TO, 3>(ao, be, dp[q]);
                 da[q] = mma_parts<3, 3>(ar, be, da[q]);
             }
             __syncthreads();
         }
-        if (hh + 1 < a.group) load_r(hh + 1, 0);
         const float *be = gt + 128, *al = gt + 192, *eb = gt + 256, *er = gt + 320;
         // The sums over M, by tiles.  A tile (m, n) adds to the t of tile m the sums of
         // its rows i >= t (and columns j < t where m = n): a product with a triangle of

@@ -44,7 +44,7 @@ __device__ __forceinline__ void invert_tile(const float* A, int ld, float* t, in
 
 template <int DK, int TK>
 struct PrepLds {
-    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, kPlY = kScanChunk * kLdT;  // in bf16
+    static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, kPlY = rows_t(kScanChunk);  // in bf16
     static constexpr int K = 0, N = TK * kPlK * 2;       // K; N beta (fp32), then Y's parts
     static constexpr int T = N + kScanChunk * kScanLdY * 4;  // the diagonal tiles' inverses [4][16][20]
     static constexpr int kNT = T + 4 * 16 * 20 * 4, kY = N + 3 * kPlY * 2;
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
     auto store_y = [&](float f) {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-            if (m >= (wave & 2)) store_parts<3>(Yp + j0 * kLdT + 16 * m + 4 * g, L::kPlY, m >= wave ? f * y[m] : f32x4{});
+            if (m >= (wave & 2)) store_parts<3>(Yp + row_t(j0) + 16 * m + 4 * g, L::kPlY, m >= wave ? f * y[m] : f32x4{});
     };
     store_y(be[j0]);
     __syncthreads();
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
             for (int t = 0; t < TK; ++t) vf[t] = f[t];
 #pragma unroll
             for (int m = 2 * kk; m < 4; ++m) {
-                read_across<true, 3>(Yp + 32 * kk * kLdT + 16 * m, L::kPlY, kLdT, yf);
+                read_across<true, 3, kSkew>(Yp + row_t(32 * kk) + 16 * m, L::kPlY, kLdT, yf);
                 x[m] = mma_parts<3, TK>(yf, vf, x[m]);
             }
         }
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
         bf16x8 yf[2][3];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
-            if (2 * kk <= wave) read_across<false, 3>(Yp + 32 * kk * kLdT + 16 * wave, L::kPlY, kLdT, yf[kk]);
+            if (2 * kk <= wave) read_across<false, 3, kSkew>(Yp + row_t(32 * kk) + 16 * wave, L::kPlY, kLdT, yf[kk]);
 #pragma unroll
         for (int n = 0; n < KS; ++n) {
             f32x4 x[2] = {};

@@ -28,7 +28,12 @@ namespace gdn {
 
 constexpr int kScanChunk = 64;
 constexpr int kScanLdY = kScanChunk + 4;  // rows of 64 floats in LDS: 4 rows apart are 16 banks apart
-constexpr int kLdT = kScanChunk + 16;      // rows of 64 bf16 that transposing reads go across: the 4 rows of a 16-lane group on different banks
+// Rows of 64 bf16 in LDS that transposing reads go across.  Such a read takes four
+// rows a 16-lane group, two groups at a time: with 40 words a row and 32 more after
+// every eight rows, they and the eight rows of a write cover the 64 banks once.
+constexpr int kLdT = kScanChunk + 16, kSkew = 64;
+__device__ __forceinline__ int row_t(int i) { return i * kLdT + i / 8 * kSkew; }
+constexpr int rows_t(int n) { return n * kLdT + n / 8 * kSkew; }
 constexpr int kGateRows = 6;              // b (high, low part), beta, alpha, 2^b, 2^(b_63 - b)
 // alpha below this counts as this: its powers stay in the fp32 range, and a
 // state carried over with a factor of 2^-60 is below fp32's resolution of
@@ -271,17 +276,18 @@ __device__ __forceinline__ void read_along_tiles(const uint16_t* p, int plane, i
 // Operands whose contraction runs across the rows.  ds_read_b64_tr_b16 gives lane
 // c of a 16-lane group the values c of the four rows whose quarters the group's
 // lanes address: lane 4 e + q row e, columns 4 q ..+3.  Group g reads rows 8 g
-// ..+7, or (TILES, operand_of's order) 4 g ..+3 and 16 + 4 g ..+3.
-template <bool TILES, int T>
+// ..+7, or (TILES, operand_of's order) 4 g ..+3 and 16 + 4 g ..+3.  SKEW: elements
+// after every eight rows (p is a multiple of eight rows from the first).
+template <bool TILES, int T, int SKEW = 0>
 __device__ __forceinline__ void read_across(const uint16_t* p, int plane, int ld, bf16x8 (&f)[T]) {
     typedef short s4v __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s4v lds_s4;
-    const int lane = threadIdx.x & 63;
-    const uint16_t* q = p + ((TILES ? 4 : 8) * (lane >> 4) + ((lane >> 2) & 3)) * ld + 4 * (lane & 3);
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const uint16_t* q = p + ((TILES ? 4 : 8) * g + ((lane >> 2) & 3)) * ld + (TILES ? g / 2 : g) * SKEW + 4 * (lane & 3);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + t * plane)));
-        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + t * plane + (TILES ? 16 : 4) * ld)));
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + t * plane + (TILES ? 16 * ld + 2 * SKEW : 4 * ld))));
         f[t] = __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
     }
 }
