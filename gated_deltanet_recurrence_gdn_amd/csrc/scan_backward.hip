@@ -175,11 +175,11 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
 // matrix operands (K and Q) and two exchanged right sides, the same two operand
 // sets that take turns.  OT: the type of dout, whose values stay as loaded until
 // they are used.
-template <int DK, int TK, typename OT>
+template <int DK, int NS, int TK, typename OT>
 struct BackOperands {
     bf16x8 w[DK / 32][3], kt[2][2][TK], qt[2][2][TK];
-    f32x4 e, be, eb;
-    OT o[4];
+    f32x4 e[NS], be, eb;
+    OT o[NS][4];
     float decay;
 };
 
@@ -187,17 +187,17 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(_Float16 x) { return (float)x; }
 __device__ __forceinline__ float to_f32(uint16_t x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }  // bf16
 
-template <int DK, int TK, typename OT>
+template <int DK, int NS, int TK, typename OT>
 __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs a, const ScanSeqs seqs) {
-    using Ops = BackOperands<DK, TK, OT>;
+    using Ops = BackOperands<DK, NS, TK, OT>;
     constexpr int KS = DK / 32;
-    constexpr int LDU = kScanChunk + 8, PU = 16 * LDU;  // a part's plane
-    __shared__ __align__(16) float Pl[KS * 4 * 256];  // partial products [key step][token tile][lane][4]
+    constexpr int LDU = kScanChunk + 8, PU = 16 * NS * LDU;  // a part's plane
+    __shared__ __align__(16) float Pl[KS * 4 * NS * 256];  // partial products [key step][token tile][value tile][lane][4]
     __shared__ __align__(16) uint16_t Ul[3 * PU];
     __shared__ __align__(16) uint16_t Ol[3 * PU];
     int s, h, slice;
     state_block(a, seqs, s, h, slice);
-    const int c0 = slice * 16;
+    const int c0 = slice * (16 * NS);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     const int ks = wave % KS, m0 = wave / KS * KS;
     const int b = a.seq0 + s, T = seqs.len[s], t0 = seqs.tok0[s], u0 = a.unit_base + seqs.unit0[s];
@@ -206,116 +206,166 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     const bool owns = KS == 4 || m0 == 0;
     const int k0 = 32 * ks + 4 * g, i0 = 16 * wave + 4 * g;
     const size_t head = (size_t)a.d_v * DK, e_unit = (size_t)kScanChunk * a.d_v;
-    f32x4 G[2] = {};
-    const size_t seq_at = ((size_t)b * a.h_v + h) * head + (size_t)(c0 + col) * DK + k0;
+    // a slice past d_v (NS = 2, odd number of tiles) repeats the first tile and stores nothing
+    int tn[NS];  // the value tile
+    bool in[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        in[n] = n == 0 || c0 + 16 * n < a.d_v;
+        tn[n] = c0 / 16 + (in[n] ? n : 0);
+    }
+    f32x4 G[2][NS] = {};
+    const size_t seq_at = ((size_t)b * a.h_v + h) * head + (size_t)col * DK + k0;
     if (a.dfinal != nullptr)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) G[i] = ld4(a.dfinal + seq_at + 16 * i);
-    const OT* dout = static_cast<const OT*>(a.dout) + (size_t)h * a.d_v + c0 + col;
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) G[i][n] = ld4(a.dfinal + seq_at + (size_t)tn[n] * (16 * DK) + 16 * i);
+    const OT* dout = static_cast<const OT*>(a.dout) + (size_t)h * a.d_v + col;
     auto load_o = [&](int c, Ops& o) {  // dout
         c = c < 0 ? 0 : c;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {  // past the sequence's end: its last token's, used as zero
             const int t = c * kScanChunk + i0 + r;
-            o.o[r] = dout[(size_t)(t0 + (t < T ? t : T - 1)) * a.h_v * a.d_v];
+#pragma unroll
+            for (int n = 0; n < NS; ++n) o.o[n][r] = dout[(size_t)(t0 + (t < T ? t : T - 1)) * a.h_v * a.d_v + 16 * tn[n]];
         }
         const float* gt = a.gates + ((size_t)(u0 + c) * a.h_v + h) * (kGateRows * kScanChunk);
         o.be = ld4(gt + 128 + i0);
         o.eb = ld4(gt + 256 + i0);
     };
-    auto load_w = [&](int c, Ops& o) {  // what dR needs
+    auto load_w = [&](int c, int m, Ops& o) {  // Wb of one token tile
         c = c < 0 ? 0 : c;
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
         const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
 #pragma unroll
-        for (int m = 0; m < KS; ++m)
-#pragma unroll
-            for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
-        o.e = ld4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4));
+        for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
     };
-    auto load_k = [&](int c, Ops& o) {  // what G needs
+    auto load_e = [&](int c, Ops& o) {  // dR0
         c = c < 0 ? 0 : c;
-        const size_t at = ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk);
-        const uint16_t *kt = a.Kt + at + (unsigned)(ks * 4 * TK * 512 + lane * 8), *qt = a.Qt + at + (unsigned)(ks * 4 * TK * 512 + lane * 8);
+        const float* e = a.dR + ((size_t)(u0 + c) * a.h_v + h) * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
+    };
+    auto load_t = [&](int c, int kk, const uint16_t* from, bf16x8 (&o)[2][2][TK]) {  // K^T or Q^T of 32 tokens
+        c = c < 0 ? 0 : c;
+        const uint16_t* t0 = from + ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(ks * 4 * TK * 512 + lane * 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int t = 0; t < TK; ++t) {
-                    o.qt[i][kk][t] = ld_bf8(qt + ((i * 2 + kk) * TK + t) * 512);
-                    o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
-                }
-        o.decay = a.gates[((size_t)(u0 + c) * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63];
+            for (int t = 0; t < TK; ++t) o[i][kk][t] = ld_bf8(t0 + ((i * 2 + kk) * TK + t) * 512);
     };
+    auto load_d = [&](int c, Ops& o) { o.decay = a.gates[((size_t)(u0 + (c < 0 ? 0 : c)) * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63]; };
     auto step = [&](int c, Ops& cur) {
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
         {
-            bf16x8 f[3];
-            operand_of(G[0], G[1], f);
-            f32x4 x[KS] = {};
+            bf16x8 f[NS][3];
 #pragma unroll
-            for (int m = 0; m < KS; ++m) x[m] = mma_parts<3, 3>(cur.w[m], f, x[m]);
-            f32x4 o;
+            for (int n = 0; n < NS; ++n) operand_of(G[0][n], G[1][n], f[n]);
+            f32x4 x[KS][NS] = {};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = c * kScanChunk + i0 + r < T ? a.scale * to_f32(cur.o[r]) : 0.f;
-            store_parts<3>(Ol + col * LDU + i0, PU, cur.eb * o);
+            for (int m = 0; m < KS; ++m) {
 #pragma unroll
-            for (int m = 0; m < KS; ++m) st4(Pl + (ks * 4 + m0 + m) * 256 + lane * 4, x[m]);
+                for (int n = 0; n < NS; ++n) x[m][n] = mma_parts<3, 3>(cur.w[m], f[n], x[m][n]);
+                load_w(c - 2, m, cur);
+                __builtin_amdgcn_sched_barrier(0);  // loads between the products, not in one burst
+            }
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                f32x4 o;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] = c * kScanChunk + i0 + r < T ? a.scale * to_f32(cur.o[n][r]) : 0.f;
+                store_parts<3>(Ol + (16 * n + col) * LDU + i0, PU, cur.eb * o);
+#pragma unroll
+                for (int m = 0; m < KS; ++m) st4(Pl + ((ks * 4 + m0 + m) * NS + n) * 256 + lane * 4, x[m][n]);
+            }
         }
         if (owns) {
-            float* st = a.G + uh * head + (unsigned)(c0 * DK + ks * 512 + lane * 4);
+            float* st = a.G + uh * head + (unsigned)(ks * 512 + lane * 4);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) st4(st + i * 256, G[i]);
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (in[n]) st4(st + tn[n] * (16 * DK) + i * 256, G[i][n]);
         }
         __syncthreads();
-        f32x4 y[2] = {};
+        f32x4 y[2][NS] = {};
         {
-            f32x4 x[KS];
-            bf16x8 f[2][3];
+            f32x4 x[NS][KS];
+            bf16x8 f[2][NS][3];
 #pragma unroll
-            for (int q = 0; q < KS; ++q) x[q] = ld4(Pl + (q * 4 + wave) * 256 + lane * 4);
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int q = 0; q < KS; ++q) x[n][q] = ld4(Pl + ((q * 4 + wave) * NS + n) * 256 + lane * 4);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Ol + t * PU + col * LDU + 32 * kk + 8 * g);
-            __builtin_amdgcn_sched_barrier(0);  // every read is on its way before anything waits
+                for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int q = 1; q < KS; ++q) x[0] += x[q];
-            const f32x4 dr = cur.e + x[0];
-            store_parts<3>(Ul + col * LDU + i0, PU, -(cur.eb * cur.be * dr));
-            st4(a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + 16 * c0 + lane * 4), dr);
+                    for (int t = 0; t < 3; ++t) f[kk][n][t] = ld_bf8(Ol + t * PU + (16 * n + col) * LDU + 32 * kk + 8 * g);
+            __builtin_amdgcn_sched_barrier(0);  // every read is on its way before anything waits
+            float* e = a.dR + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+#pragma unroll
+                for (int q = 1; q < KS; ++q) x[n][0] += x[n][q];
+                const f32x4 dr = cur.e[n] + x[n][0];
+                store_parts<3>(Ul + (16 * n + col) * LDU + i0, PU, -(cur.eb * cur.be * dr));
+                if (in[n]) st4(e + tn[n] * 256, dr);
+            }
             // dout's part of the new gradient needs no dR: it is formed while the others' is on its way
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+            for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) y[i] = mma_parts<TK, 3>(cur.qt[i][kk], f[kk], y[i]);
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) y[i][n] = mma_parts<TK, 3>(cur.qt[i][kk], f[kk][n], y[i][n]);
+                load_t(c - 2, kk, a.Qt, cur.qt);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
-        load_w(c - 2, cur);
+        load_e(c - 2, cur);
         load_o(c - 2, cur);
         __syncthreads();
-        bf16x8 f[2][3];
+        bf16x8 f[2][NS][3];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int t = 0; t < 3; ++t) f[kk][t] = ld_bf8(Ul + t * PU + col * LDU + 32 * kk + 8 * g);
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int t = 0; t < 3; ++t) f[kk][n][t] = ld_bf8(Ul + t * PU + (16 * n + col) * LDU + 32 * kk + 8 * g);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) y[i] = mma_parts<TK, 3>(cur.kt[i][kk], f[kk], y[i]);
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) G[i] = G[i] * cur.decay + y[i];
-        load_k(c - 2, cur);
+                for (int i = 0; i < 2; ++i) y[i][n] = mma_parts<TK, 3>(cur.kt[i][kk], f[kk][n], y[i][n]);
+            load_t(c - 2, kk, a.Kt, cur.kt);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) G[i][n] = G[i][n] * cur.decay + y[i][n];
+        load_d(c - 2, cur);
+    };
+    auto load_all = [&](int c, Ops& o) {
+#pragma unroll
+        for (int m = 0; m < KS; ++m) load_w(c, m, o);
+        load_e(c, o);
+        load_o(c, o);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            load_t(c, kk, a.Qt, o.qt);
+            load_t(c, kk, a.Kt, o.kt);
+        }
+        load_d(c, o);
     };
     if (n_units > 0) {
         Ops p, q;
-        load_w(n_units - 1, p);
-        load_o(n_units - 1, p);
-        load_k(n_units - 1, p);
-        load_w(n_units - 2, q);
-        load_o(n_units - 2, q);
-        load_k(n_units - 2, q);
+        load_all(n_units - 1, p);
+        load_all(n_units - 2, q);
         for (int c = n_units - 1; c >= 0; c -= 2) {
             step(c, p);
             if (c > 0) step(c - 1, q);
@@ -323,7 +373,10 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     }
     if (owns && a.dstate != nullptr)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) st4(a.dstate + seq_at + 16 * i, G[i]);
+        for (int n = 0; n < NS; ++n)
+            if (in[n])
+#pragma unroll
+                for (int i = 0; i < 2; ++i) st4(a.dstate + seq_at + (size_t)tn[n] * (16 * DK) + 16 * i, G[i][n]);
 }
 
 // Sums over 16 lanes of two times four values.
@@ -728,6 +781,16 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         }
 }
 
+template <int DK, int TK, typename OT>
+hipError_t launch_back_state(ScanArgs a, hipStream_t st, const ScanSeqs& seqs) {
+    const bool pair = two_tiles(a);
+    a.slices = pair ? (a.d_v + 31) / 32 : a.d_v / 16;
+    const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq);
+    if (pair) hipLaunchKernelGGL((scan_back_state_kernel<DK, 2, TK, OT>), grid, dim3(256), 0, st, a, seqs);
+    else hipLaunchKernelGGL((scan_back_state_kernel<DK, 1, TK, OT>), grid, dim3(256), 0, st, a, seqs);
+    return hipGetLastError();
+}
+
 template <int DK, int TK, int TO>
 hipError_t launch_grad(const ScanArgs& a, const ScanSeqs& seqs, hipStream_t st) {
     const hipError_t e = allow_max_lds<scan_grad_kernel<DK, TK, TO>>();
@@ -745,12 +808,10 @@ hipError_t launch_backward(const ScanArgs& args, const ScanSeqs& seqs, hipStream
         hipLaunchKernelGGL((scan_back_prepare_kernel<DK, TK>), dim3((unsigned)(a.units * a.h_v)), dim3(kBackThreads), (BackPrepLds<DK, TK>::kBytes), st, a, seqs);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    a.slices = a.d_v / 16;
-    const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq);
-    if (a.out_dtype == GDN_F32) hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, float>), grid, dim3(256), 0, st, a, seqs);
-    else if (a.out_dtype == GDN_F16) hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, _Float16>), grid, dim3(256), 0, st, a, seqs);
-    else hipLaunchKernelGGL((scan_back_state_kernel<DK, TK, uint16_t>), grid, dim3(256), 0, st, a, seqs);
-    if ((e = hipGetLastError()) != hipSuccess || a.units == 0) return e;
+    e = a.out_dtype == GDN_F32 ? launch_back_state<DK, TK, float>(a, st, seqs)
+      : a.out_dtype == GDN_F16 ? launch_back_state<DK, TK, _Float16>(a, st, seqs)
+                               : launch_back_state<DK, TK, uint16_t>(a, st, seqs);
+    if (e != hipSuccess || a.units == 0) return e;
     return a.out_dtype == GDN_BF16 ? launch_grad<DK, TK, 1>(a, seqs, st) : launch_grad<DK, TK, 3>(a, seqs, st);
 }
 

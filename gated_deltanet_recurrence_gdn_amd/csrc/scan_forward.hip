@@ -14,9 +14,6 @@
 namespace gdn {
 namespace {
 
-#ifndef SCAN_NS
-#define SCAN_NS 1
-#endif
 constexpr int kPrepThreads = 256;
 
 // The inverse of a unit lower triangular 16 x 16 tile I + A, A in rows of `ld`
@@ -284,13 +281,14 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 #pragma unroll
             for (int i = 0; i < 2; ++i) S[i][n] = ld4(st + (size_t)cn[n] * DK + 16 * i);
     }
-    auto load_w = [&](int c, Ops& o) {  // what the errors need
+    auto load_w = [&](int c, int m, Ops& o) {  // W of one token tile
         const size_t uh = (size_t)(u0 + (c < n_units ? c : n_units - 1)) * a.h_v + h;
         const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
 #pragma unroll
-        for (int m = 0; m < KS; ++m)
-#pragma unroll
-            for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
+        for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
+    };
+    auto load_e = [&](int c, Ops& o) {  // what else the errors need
+        const size_t uh = (size_t)(u0 + (c < n_units ? c : n_units - 1)) * a.h_v + h;
         const float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
 #pragma unroll
         for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
@@ -298,15 +296,16 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
         o.be = ld4(gt + 128 + 16 * wave + 4 * g);
         o.er = ld4(gt + 320 + 16 * wave + 4 * g);
     };
-    auto load_k = [&](int c, Ops& o) {  // what the state needs
+    auto load_k = [&](int c, int kk, Ops& o) {  // K^T of 32 tokens
         const int unit = u0 + (c < n_units ? c : n_units - 1);
         const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(ks * 4 * TK * 512 + lane * 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
+            for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
+    };
+    auto load_d = [&](int c, Ops& o) {
+        const int unit = u0 + (c < n_units ? c : n_units - 1);
         o.decay = a.gates[((size_t)unit * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63];
     };
     auto step = [&](int c, Ops& cur) {
@@ -317,9 +316,12 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
             for (int n = 0; n < NS; ++n) operand_of(S[0][n], S[1][n], f[n]);
             f32x4 x[KS][NS] = {};
 #pragma unroll
-            for (int m = 0; m < KS; ++m)
+            for (int m = 0; m < KS; ++m) {
 #pragma unroll
                 for (int n = 0; n < NS; ++n) x[m][n] = mma_parts<3, 3>(cur.w[m], f[n], x[m][n]);
+                load_w(c + 2, m, cur);
+                __builtin_amdgcn_sched_barrier(0);  // loads between the products, not in one burst
+            }
 #pragma unroll
             for (int m = 0; m < KS; ++m)
 #pragma unroll
@@ -346,7 +348,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
             store_parts<3>(Ul + (16 * n + col) * LDU + 16 * wave + 4 * g, PU, cur.be * cur.er * y);
             if (in[n]) st4(e + tn[n] * 256, y);
         }
-        load_w(c + 2, cur);
+        load_e(c + 2, cur);
         __syncthreads();
         bf16x8 f[2][NS][3];
 #pragma unroll
@@ -358,23 +360,32 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
         __builtin_amdgcn_sched_barrier(0);  // every read is on its way before the products start
         f32x4 y[2][NS] = {};
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) y[i][n] = mma_parts<TK, 3>(cur.kt[i][kk], f[kk][n], y[i][n]);
+            load_k(c + 2, kk, cur);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int n = 0; n < NS; ++n) S[i][n] = S[i][n] * cur.decay + y[i][n];
-        load_k(c + 2, cur);
+        load_d(c + 2, cur);
+    };
+    auto load_all = [&](int c, Ops& o) {
+#pragma unroll
+        for (int m = 0; m < KS; ++m) load_w(c, m, o);
+        load_e(c, o);
+        load_k(c, 0, o);
+        load_k(c, 1, o);
+        load_d(c, o);
     };
     if (n_units > 0) {
         Ops p, q;
-        load_w(0, p);
-        load_k(0, p);
-        load_w(1, q);
-        load_k(1, q);
+        load_all(0, p);
+        load_all(1, q);
         for (int c = 0; c < n_units; c += 2) {
             step(c, p);
             if (c + 1 < n_units) step(c + 1, q);
@@ -514,9 +525,11 @@ hipError_t launch_forward(const ScanArgs& args, const ScanSeqs& seqs, hipStream_
         hipLaunchKernelGGL((scan_prepare_kernel<DK, TK>), dim3(heads), dim3(kPrepThreads), (PrepLds<DK, TK>::kBytes), st, a, seqs);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    constexpr int NS = SCAN_NS;
-    a.slices = (a.d_v + 16 * NS - 1) / (16 * NS);
-    hipLaunchKernelGGL((scan_state_kernel<DK, NS, TK>), dim3((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq), dim3(256), 0, st, a, seqs);
+    const bool pair = two_tiles(a);
+    a.slices = pair ? (a.d_v + 31) / 32 : a.d_v / 16;
+    const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq);
+    if (pair) hipLaunchKernelGGL((scan_state_kernel<DK, 2, TK>), grid, dim3(256), 0, st, a, seqs);
+    else hipLaunchKernelGGL((scan_state_kernel<DK, 1, TK>), grid, dim3(256), 0, st, a, seqs);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || heads == 0) return e;
     if ((e = allow_max_lds<scan_output_kernel<DK, TK>>()) != hipSuccess) return e;

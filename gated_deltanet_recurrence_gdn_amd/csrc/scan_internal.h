@@ -104,6 +104,14 @@ __device__ __forceinline__ void state_block(const ScanArgs& a, const ScanSeqs& s
     slice = x % a.slices;
 }
 
+// Value tiles of a state kernel's workgroup.  Two halve what the workgroups read
+// of the operands that do not depend on the value columns (80 KB a chunk), but
+// take half as many workgroups with longer steps: where one tile each would give
+// every CU a workgroup and more, two are faster (4096 tokens of 48 heads, 384
+// workgroups of one tile: 226 against 186 us; packed sequences 196 against 136),
+// below that one (16384 tokens of 6 heads, 48 workgroups: 278 against 417 us).
+inline bool two_tiles(const ScanArgs& a) { return (int64_t)a.n_seq * a.h_v * (a.d_v / 16) > device_cus(); }
+
 // Parts of the inputs q, k: one in bf16, three in fp32.
 inline int input_parts(const ScanArgs& a) { return a.qkv_bf16 ? 1 : 3; }
 hipError_t launch_scan_forward(const ScanArgs& a, const ScanSeqs& seqs, int d_k, hipStream_t stream);
