@@ -483,6 +483,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             on[1] = x[1];
         }
     };
+    float gate;
+    auto load_g = [&](int hh) { gate = a.gates[((size_t)(a.unit_base + unit) * a.h_v + hq * a.group + hh) * (kGateRows * kScanChunk) + (tid < kGateRows * kScanChunk ? tid : 0)]; };
     // dR, E and dout of columns c0 .. of head hh, loaded by load_r, into buffer `to`
     auto stage_r = [&](int hh, int c0, int to) {
         const bool second = c0 + 16 < a.d_v;
@@ -503,10 +505,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         }
         rv = rn;
     };
-    load_s(0, 0);
-    load_r(0, 0);
     stage_parts<TK, DK, LDK, kGradThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     stage_parts<TK, DK, LDK, kGradThreads>(a.q, tok, len, a.h_qk, hq, Qp);
+    load_r(0, 0);
+    load_s(0, 0);
+    load_g(0);
     __syncthreads();
     f32x4 kk_[2] = {}, qk_[2] = {}, accq[MW] = {}, acck[MW] = {};
 #pragma unroll
@@ -525,30 +528,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             qk_[q] = mma_parts<TK, TK>(y, x, qk_[q]);
         }
     }
-    // this wave's elements of K and Q: a bf16 pair in a word, or two words
-    uint32_t kq[MW][4][TK == 1 ? 1 : 2];
-#pragma unroll
-    for (int m = 0; m < MW; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * (m0 + m) + 4 * g + r, at = i * LDK + 16 * nt + col;
-            if constexpr (TK == 1) {
-                kq[m][r][0] = (uint32_t)Kp[at] | (uint32_t)Qp[at] << 16;
-            } else {
-                const size_t from = ((size_t)(tok + i) * a.h_qk + hq) * DK + 16 * nt + col;
-                kq[m][r][0] = i < len ? static_cast<const uint32_t*>(a.k)[from] : 0;
-                kq[m][r][1] = i < len ? static_cast<const uint32_t*>(a.q)[from] : 0;
-            }
-        }
-
     for (int hh = 0; hh < a.group; ++hh) {
         // the lane's numbers are made opaque: hundreds of LDS addresses would otherwise be formed before the loop and kept
         asm volatile("" : "+v"(lane), "+v"(col), "+v"(g));
         const int h = hq * a.group + hh;
-        const size_t uh = (size_t)(a.unit_base + unit) * a.h_v + h;
         f32x4 os[MW] = {}, rs[MW] = {}, eg[MW] = {}, dp[2] = {}, da[2] = {};
         float gs = 0.f;
-        const float gate = tid < kGateRows * kScanChunk ? a.gates[uh * (kGateRows * kScanChunk) + tid] : 0.f;
         float* gt = gates + (hh & 1) * (kGateRows * kScanChunk);  // the last head's are still being read
         if (hh == 0) __syncthreads();                            // K and Q have been read
         if (tid < kGateRows * kScanChunk) gt[tid] = gate;
@@ -568,7 +553,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             }
             if (c0 + 32 < a.d_v) stage_r(hh, c0 + 32, buffer ^ 1);
             if (c0 + 64 < a.d_v) load_r(hh, c0 + 64);
-            else if (c0 + 32 >= a.d_v && hh + 1 < a.group) load_r(hh + 1, 0);
+            else if (c0 + 32 >= a.d_v && hh + 1 < a.group) {
+                load_r(hh + 1, 0);
+                load_g(hh + 1);
+            }
             if (c0 + 16 >= a.d_v) sn[1] = gn[1] = f32x4{};
             bf16x8 sb[3], gb[3];
 #pragma unroll
@@ -620,6 +608,22 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
         // its rows i >= t (and columns j < t where m = n): a product with a triangle of
         // ones; to the t of tile n < m the sums of its columns j < t; and to the t of
         // the tiles between its total.
+        // this wave's elements of K and Q for the row sums below, on the way meanwhile
+        uint32_t kv[MW][4], qv[MW][4];
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * (m0 + m) + 4 * g + r;
+                const size_t at = ((size_t)(tok + (i < len ? i : len - 1)) * a.h_qk + hq) * DK + 16 * nt + col;
+                if constexpr (TK == 1) {
+                    kv[m][r] = static_cast<const uint16_t*>(a.k)[at];
+                    qv[m][r] = static_cast<const uint16_t*>(a.q)[at];
+                } else {
+                    kv[m][r] = static_cast<const uint32_t*>(a.k)[at];
+                    qv[m][r] = static_cast<const uint32_t*>(a.q)[at];
+                }
+            }
         f32x4 triangle;
 #pragma unroll
         for (int r = 0; r < 4; ++r) triangle[r] = 4 * g + r >= col ? 1.f : 0.f;
@@ -678,16 +682,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             f32x4 y, z;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float kv, qv;
-                if constexpr (TK == 1) {
-                    kv = bf16_lo(kq[m][r][0]);
-                    qv = bf16_hi(kq[m][r][0]);
-                } else {
-                    kv = __builtin_bit_cast(float, kq[m][r][0]);
-                    qv = __builtin_bit_cast(float, kq[m][r][1]);
-                }
-                y[r] = qv * o[r] - kv * x[r];
-                z[r] = kv * e[r];
+                const bool row = i + r < len;
+                const float ke = row ? __builtin_bit_cast(float, TK == 1 ? kv[m][r] << 16 : kv[m][r]) : 0.f;
+                const float qe = row ? __builtin_bit_cast(float, TK == 1 ? qv[m][r] << 16 : qv[m][r]) : 0.f;
+                y[r] = qe * o[r] - ke * x[r];
+                z[r] = ke * e[r];
             }
             row_sums(y, z);
             if (col == 0) {
