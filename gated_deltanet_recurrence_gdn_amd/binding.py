@@ -191,6 +191,8 @@ def _expect(t, name, shape, dtype=None):
     """t must be a tensor of exactly `shape` (None = any size) and `dtype`."""
     if t is None:
         return
+    if isinstance(t, torch.Tensor) and t.shape == shape and (dtype is None or t.dtype is dtype):
+        return  # the usual case, in one comparison
     got = _shape_of(t, name, len(shape))
     for i, (g, e) in enumerate(zip(got, shape)):
         if e is not None and g != e:
@@ -579,6 +581,10 @@ def gdn_prefill_varlen(cu_seqlens, q, k, v, alpha, beta, state, out, *, chunk_st
 # ---------------------------------------------------------------------------
 # the training scan
 # ---------------------------------------------------------------------------
+def _address(x: np.ndarray) -> int:
+    return x.__array_interface__["data"][0]
+
+
 def _scan_shape(cu, q, k, v, alpha, beta, out, n_slots, scale, out_name="out") -> GdnShape:
     total, Hqk, dk = _shape_of(q, "q", 3)
     _expect(k, "k", (total, Hqk, dk), q.dtype)
@@ -602,7 +608,7 @@ def gdn_scan_tape_bytes(cu_seqlens, q, v) -> int:
     cu = _host_cu(cu_seqlens)
     total, Hqk, dk = _shape_of(q, "q", 3)
     sh = GdnShape(cu.size - 1, total, Hqk, v.shape[1], dk, v.shape[2], 0, _dtype_code(q), GDN_F32, GDN_F16, 1.0)
-    return int(lib().gdn_scan_tape_bytes(ctypes.byref(sh), cu.ctypes.data))
+    return int(lib().gdn_scan_tape_bytes(ctypes.byref(sh), _address(cu)))
 
 
 def gdn_scan_forward(cu_seqlens, q, k, v, alpha, beta, out, *, tape=None, state=None, state_slot=None,
@@ -620,17 +626,17 @@ def gdn_scan_forward(cu_seqlens, q, k, v, alpha, beta, out, *, tape=None, state=
     _expect(final_state, "final_state", (sh.batch, sh.h_v, sh.d_v, sh.d_k), torch.float32)
     _expect(tape, "tape", (None,), torch.uint8)
     _check_status(status)
-    _on_current_device("gdn_scan_forward", q, k, v, alpha, beta, out, tape, state, state_slot, final_state, workspace,
-                       status)
     if workspace is None:
-        need = lib().gdn_scan_forward_workspace_bytes(ctypes.byref(sh), cu.ctypes.data, int(tape is not None))
+        need = lib().gdn_scan_forward_workspace_bytes(ctypes.byref(sh), _address(cu), int(tape is not None))
         workspace = _workspace(int(need), q.device, stream)
-    args = (ctypes.byref(sh), _vp(cu.ctypes.data), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+    args = (ctypes.byref(sh), _vp(_address(cu)), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
             _dev_ptr(alpha, "alpha"), _dev_ptr(beta, "beta"), _dev_ptr(state, "state"),
             _dev_ptr(state_slot, "state_slot"), _dev_ptr(out, "out"), _dev_ptr(final_state, "final_state"),
             _dev_ptr(tape, "tape"), ctypes.c_size_t(0 if tape is None else _bytes_of(tape)),
             _dev_ptr(workspace, "workspace"), ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"),
             _stream(stream))
+    _on_current_device("gdn_scan_forward", q, k, v, alpha, beta, out, tape, state, state_slot, final_state, workspace,
+                       status)
     return _invoke("gdn_scan_forward", args, (sh, cu, q, k, v, alpha, beta, state, state_slot, out, final_state, tape,
                                               workspace, status), prepare)
 
@@ -648,17 +654,17 @@ def gdn_scan_backward(cu_seqlens, q, k, v, alpha, beta, tape, dout, dq, dk, dv, 
     for t, name in ((dfinal, "dfinal"), (dstate, "dstate")):
         _expect(t, name, (sh.batch, sh.h_v, sh.d_v, sh.d_k), torch.float32)
     _expect(tape, "tape", (None,), torch.uint8)
-    _on_current_device("gdn_scan_backward", q, k, v, alpha, beta, tape, dout, dq, dk, dv, dalpha, dbeta, dfinal, dstate,
-                       workspace)
     if workspace is None:
-        need = lib().gdn_scan_backward_workspace_bytes(ctypes.byref(sh), cu.ctypes.data)
+        need = lib().gdn_scan_backward_workspace_bytes(ctypes.byref(sh), _address(cu))
         workspace = _workspace(int(need), q.device, stream)
-    args = (ctypes.byref(sh), _vp(cu.ctypes.data), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+    args = (ctypes.byref(sh), _vp(_address(cu)), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
             _dev_ptr(alpha, "alpha"), _dev_ptr(beta, "beta"), _dev_ptr(tape, "tape"),
             ctypes.c_size_t(0 if tape is None else _bytes_of(tape)), _dev_ptr(dout, "dout"), _dev_ptr(dfinal, "dfinal"),
             _dev_ptr(dq, "dq"), _dev_ptr(dk, "dk"), _dev_ptr(dv, "dv"), _dev_ptr(dalpha, "dalpha"),
             _dev_ptr(dbeta, "dbeta"), _dev_ptr(dstate, "dstate"), _dev_ptr(workspace, "workspace"),
             ctypes.c_size_t(_bytes_of(workspace)), _stream(stream))
+    _on_current_device("gdn_scan_backward", q, k, v, alpha, beta, tape, dout, dq, dk, dv, dalpha, dbeta, dfinal, dstate,
+                       workspace)
     return _invoke("gdn_scan_backward", args, (sh, cu, q, k, v, alpha, beta, tape, dout, dfinal, dq, dk, dv, dalpha,
                                                dbeta, dstate, workspace), prepare)
 
@@ -673,20 +679,24 @@ def _pool_structs(pools, name="pools"):
     if not 1 <= len(pools) <= GDN_MAX_POOLS:
         raise ValueError(f"{name}: 1 to {GDN_MAX_POOLS} pools, got {len(pools)}")
     structs = (GdnPool * len(pools))()
-    for p, t in zip(structs, pools):
+    for i, t in enumerate(pools):
         if not isinstance(t, torch.Tensor) or t.dim() < 3:
             raise ValueError(f"{name} must be tensors [layers][slots][...]")
-        size, strides, row = t.shape, t.stride(), 1
-        for i in range(t.dim() - 1, 0, -1):  # the rows of a layer, and what a row holds, are dense
-            if size[i] != 1 and strides[i] != row:
-                raise ValueError(f"the rows of {name} must be contiguous within a layer")
-            row *= size[i]
-        slots, e = size[1], t.element_size()
+        size = t.shape
+        layers, slots, e = size[0], size[1], t.element_size()
+        row = 1  # elements of a layer
+        if t.is_contiguous() and layers > 0:
+            row = t.numel() // layers
+        else:
+            strides = t.stride()
+            for k in range(t.dim() - 1, 0, -1):  # the rows of a layer, and what a row holds, are dense
+                if size[k] != 1 and strides[k] != row:
+                    raise ValueError(f"the rows of {name} must be contiguous within a layer")
+                row *= size[k]
         if slots < 1 or row == 0:
             raise ValueError(f"{name} must hold at least one row")
-        p.data, p.row_bytes, p.n_layers, p.n_slots = t.data_ptr(), row // slots * e, size[0], slots
-        p.layer_bytes = (strides[0] if size[0] > 1 else row) * e
-        if slots != structs[0].n_slots:
+        structs[i] = GdnPool(t.data_ptr(), row // slots * e, (t.stride(0) if layers > 1 else row) * e, layers, slots)
+        if slots != pools[0].shape[1]:
             raise ValueError(f"the {name} must have the same number of rows")
     return structs, tuple(pools)
 
@@ -700,12 +710,10 @@ def _int_array(t, name, n=None):
 
 
 def _on_current_device(name, *tensors):
-    """Every tensor is on the current device, where the call launches."""
-    if not torch.cuda.is_available():  # no device at all: refused with the tensor's name below
-        return
+    """Every one of these device tensors is on the current device, where the call launches."""
     device = torch.cuda.current_device()
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != device:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{device}")
 
 
@@ -730,9 +738,9 @@ def gdn_pool_copy(pools, src_rows, dst_rows, *, src_pools=None, status=None, str
     _check_status(status)
     _pool_ptrs(keep)
     _pool_ptrs(keep_src, "src_pools")
-    _on_current_device("gdn_pool_copy", *keep, *keep_src, src_rows, dst_rows, status)
     args = (dst, src if src is not None else _vp(None), _i32(len(keep)), _dev_ptr(src_rows, "src_rows"),
             _dev_ptr(dst_rows, "dst_rows"), _i32(n), _dev_ptr(status, "status"), _stream(stream))
+    _on_current_device("gdn_pool_copy", *keep, *keep_src, src_rows, dst_rows, status)
     return _invoke("gdn_pool_copy", args, (keep, keep_src, src_rows, dst_rows, status), prepare)
 
 
@@ -771,13 +779,13 @@ def gdn_pool_fork(pools, table, parent, child, *, released=None, table_out=None,
     if n > GDN_POOL_MAX_SEQS:
         raise ValueError(f"{n} children, at most {GDN_POOL_MAX_SEQS}")
     _pool_ptrs(keep)
-    _on_current_device("gdn_pool_fork", *keep, table, table_out, released, parent, child, workspace, status)
     if workspace is None:
         workspace = _workspace(8 * n, keep[0].device, stream)
     args = (structs, _i32(len(keep)), _dev_ptr(table, "table"), _i32(m), _i32(n_rows), _dev_ptr(released, "released"),
             _i32(n_rel), _dev_ptr(parent, "parent"), _dev_ptr(child, "child"), _i32(n), _dev_ptr(table_out, "table_out"),
             _dev_ptr(workspace, "workspace"), ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"),
             _stream(stream))
+    _on_current_device("gdn_pool_fork", *keep, table, table_out, released, parent, child, workspace, status)
     return _invoke("gdn_pool_fork", args, (keep, table, released, parent, child, table_out, workspace, status), prepare)
 
 
@@ -788,10 +796,10 @@ def gdn_pool_compact(pools, table, *, released=None, table_out=None, count=None,
     structs, keep, m, n_rel, n_rows, table_out = _pool_table(pools, table, n_rows, released, table_out, status)
     _expect(count, "count", (1,), torch.int32)
     _pool_ptrs(keep)
-    _on_current_device("gdn_pool_compact", *keep, table, table_out, released, count, workspace, status)
     if workspace is None:
         workspace = _workspace(16 + 8 * n_rows, keep[0].device, stream)
     args = (structs, _i32(len(keep)), _dev_ptr(table, "table"), _i32(m), _i32(n_rows), _dev_ptr(released, "released"),
             _i32(n_rel), _dev_ptr(table_out, "table_out"), _dev_ptr(count, "count"), _dev_ptr(workspace, "workspace"),
             ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"), _stream(stream))
+    _on_current_device("gdn_pool_compact", *keep, table, table_out, released, count, workspace, status)
     return _invoke("gdn_pool_compact", args, (keep, table, released, table_out, count, workspace, status), prepare)
