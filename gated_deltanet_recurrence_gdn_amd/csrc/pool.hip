@@ -281,7 +281,7 @@ bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 
 // One past the last byte of a pool.
 const unsigned char* pool_end(const gdn_pool& p) {
-    return static_cast<const unsigned char*>(p.data) + (p.n_layers - 1) * p.layer_bytes + p.n_slots * p.row_bytes;
+    return static_cast<const unsigned char*>(p.data) + (int64_t)(p.n_layers - 1) * p.layer_bytes + (int64_t)p.n_slots * p.row_bytes;
 }
 
 bool overlap(const gdn_pool& a, const gdn_pool& b) {
@@ -297,6 +297,8 @@ int check_pools(const gdn_pool* pools, int32_t n_pools) {
         if (p.row_bytes < 16 || p.row_bytes % 16 != 0 || p.row_bytes > (int64_t{1} << 40)) return GDN_ERR_SHAPE;
         if (p.layer_bytes % 16 != 0 || p.layer_bytes > (int64_t{1} << 46)) return GDN_ERR_SHAPE;
         if (p.n_layers > 1 && p.layer_bytes / p.row_bytes < p.n_slots) return GDN_ERR_SHAPE;
+        // more than any memory: the sums below stay inside 64 bits
+        if ((double)p.n_layers * (double)p.layer_bytes + (double)p.n_slots * (double)p.row_bytes > 0x1p60) return GDN_ERR_SHAPE;
         if (p.n_layers == 0) continue;
         if (p.data == nullptr) return GDN_ERR_NULL;
         if (!aligned(p.data, 16)) return GDN_ERR_ALIGN;

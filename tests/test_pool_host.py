@@ -158,3 +158,9 @@ def test_layers_may_be_apart():
     assert (s[0].row_bytes, s[0].layer_bytes, s[0].n_layers, s[0].n_slots) == (32, 2 * 6 * 32, 2, 6)
     s, _ = gb._pool_structs(whole[:, :3])
     assert (s[0].row_bytes, s[0].layer_bytes, s[0].n_layers, s[0].n_slots) == (32, 6 * 32, 4, 3)
+
+
+@pytest.mark.parametrize("call", [copy, fork, compact])
+def test_pools_larger_than_any_memory_are_refused(call):
+    for p in (pool(row=1 << 40, slots=1 << 30, layers=1), pool(row=1 << 20, slots=8, layers=1 << 30, layer=1 << 46)):
+        assert call(pools(p)) == E["GDN_ERR_SHAPE"]
