@@ -46,7 +46,9 @@
  *  - The library built with -DGDN_DEBUG (libgdn_debug.so) checks the indices
  *    its kernels form into the caller's arrays and the workspace: one past
  *    its array's end stores GDN_ERR_INTERNAL into *status and is clamped into
- *    the array.  The release build carries no such checks.
+ *    the array.  The release build carries no such checks.  The kernels of
+ *    gdn_scan_* and gdn_pool_* have none in either build: their indices follow
+ *    from the shape, the offsets and the row numbers, which every build checks.
  */
 #ifndef GDN_H
 #define GDN_H
@@ -501,7 +503,7 @@ int gdn_prefill_varlen(const gdn_shape* shape, const int32_t* cu_seqlens, const 
  *
  * `tape` (gdn_scan_tape_bytes bytes) receives what the backward pass needs
  * besides the inputs: the state before every 64-token chunk, the delta rule's
- * errors, the chunks' triangular inverses and the gates, about 8.1 MB per 64
+ * errors, the chunks' triangular inverses and the gates, about 5.6 MB per 64
  * tokens at 48 value heads and d_k = d_v = 128.  Without one (NULL) the
  * workspace holds it during the call.
  *
@@ -513,6 +515,12 @@ int gdn_prefill_varlen(const gdn_shape* shape, const int32_t* cu_seqlens, const 
  * inputs and the initial states.  The tape is only read: a second backward pass
  * over it gives the same result.  Nothing is accumulated with atomics; results
  * repeat bit for bit.
+ *
+ * Apart from final_state = state, and dstate = dfinal, no output overlaps an
+ * input or another output.  A NaN or an infinity in q, k, v, alpha, beta, dout
+ * or a state makes NaN of what follows it in its sequence and heads, and may do
+ * so from the start of its 64-token chunk (forward) or from the end of it
+ * (backward); other sequences and heads do not see it.
  *
  * tape, workspaces, out, dout, dv, dfinal and dstate are 16-byte aligned, the
  * other outputs 4-byte.  The workspaces' contents on entry are ignored; calls that

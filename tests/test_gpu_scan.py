@@ -365,3 +365,76 @@ def test_sequences_forked_scanned_and_compacted():
         o, _ = ref([(0, T), (T + i * N, T + (i + 1) * N), (T + (2 + i) * N, T + (3 + i) * N)])
         assert off(out[i], o[T + N:]) <= 2 * TOL
     assert int(status.item()) == 0
+
+
+# ---------------------------------------------------------------------------
+# so many sequences, heads and value tiles that a workgroup walks two value tiles
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("hq,hv,dk,dv", [(1, 3, 32, 48), (2, 4, 64, 80), (1, 2, 128, 112), (4, 8, 128, 128)])
+@pytest.mark.parametrize("dtype,out_dtype", [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16),
+                                             (torch.float32, torch.float16), (torch.bfloat16, torch.float32)])
+def test_two_value_tiles_a_workgroup(hq, hv, dk, dv, dtype, out_dtype):
+    r = np.random.RandomState(dk + dv)
+    lens = [int(n) for n in r.choice([0, 1, 5, 63, 64, 65, 130], 60)]
+    say("two tiles", hq, hv, dk, dv, dtype, out_dtype, sum(lens))
+    assert len(lens) * hv * (dv // 16) > 2 * 256
+    x, dout, dfinal = inputs(41, lens, hq, hv, dk, dv, dtype)
+    check(x, lens, dk ** -0.5, out_dtype, dout, dfinal)
+
+
+def test_the_number_of_sequences_does_not_change_a_sequence():
+    """The tiles a workgroup walks follow from the call's size; the arithmetic of a sequence does not."""
+    lens = [100, 30, 64, 7] * 16
+    x, dout, dfinal = inputs(42, lens, 1, 4, 64, 80, torch.bfloat16)
+    out, fin, tape = forward(x, lens)
+    grads = backward(x, lens, tape, dout, dfinal)
+    n, B = sum(lens[:4]), 4
+    y = {m: (t[:B] if m == "state" else t[:n]).contiguous() for m, t in x.items()}
+    out2, fin2, tape2 = forward(y, lens[:4])
+    few = backward(y, lens[:4], tape2, dout[:n].contiguous(), dfinal[:B].contiguous())
+    assert torch.equal(out[:n], out2) and torch.equal(fin[:B], fin2)
+    for m in few:
+        assert torch.equal(few[m], grads[m][:few[m].shape[0]]), m
+
+
+@pytest.mark.parametrize("where", ["v", "alpha", "beta", "dout"])
+def test_a_nan_stays_in_its_sequence_and_head(where):
+    lens = [70, 200, 1, 33]
+    x, dout, dfinal = inputs(43, lens, 2, 4, 64, 48)
+    _, _, tape = first = forward(x, lens)
+    grads = backward(x, lens, tape, dout, dfinal)
+    x, dout = {n: t.clone() for n, t in x.items()}, dout.clone()
+    (dout if where == "dout" else x[where])[70 + 100, 1] = float("nan")
+    out, fin, tape = forward(x, lens)
+    bad = backward(x, lens, tape, dout, dfinal)
+    # value head 1 of sequence 1 from its chunk on (forward) and up to its chunk (backward) may be NaN; q/k head 0 sums it
+    token = torch.ones(sum(lens), dtype=torch.bool, device=DEV)
+    token[70:270] = False
+    heads = [0, 2, 3]
+    assert torch.equal(out[:, heads], first[0][:, heads]) and torch.equal(fin[:, heads], first[1][:, heads])
+    assert torch.equal(out[token], first[0][token]) and torch.equal(fin[[0, 2, 3]], first[1][[0, 2, 3]])
+    assert torch.equal(out[70:70 + 64], first[0][70:70 + 64])
+    for n in ("dv", "dalpha", "dbeta"):
+        assert torch.equal(bad[n][:, heads], grads[n][:, heads]), n
+    for n in ("dq", "dk"):
+        assert torch.equal(bad[n][:, 1], grads[n][:, 1]), n
+    for n in ("dq", "dk", "dv", "dalpha", "dbeta"):
+        assert torch.equal(bad[n][token], grads[n][token]), n
+    assert torch.equal(bad["dstate"][[0, 2, 3]], grads["dstate"][[0, 2, 3]])
+    if where != "dout":  # not hidden where it is an input of the rule
+        assert bool(out[70 + 100, 1].isnan().any()) and bool(fin[1, 1].isnan().any())
+    if where == "v":  # the rule is affine in the state: no value stands in the state's gradient
+        assert torch.equal(bad["dstate"], grads["dstate"])
+    else:
+        assert bool(bad["dstate"][1, 1].isnan().any())
+
+
+def test_gradient_of_the_state_in_place():
+    lens = [70, 0, 130]
+    x, dout, dfinal = inputs(44, lens, 1, 2, 64, 48)
+    _, _, tape = forward(x, lens)
+    want = backward(x, lens, tape, dout, dfinal)
+    d, g = dfinal.clone(), {n: torch.empty_like(x[n]) for n in ("q", "k", "v", "alpha", "beta")}
+    gb.gdn_scan_backward(offsets(lens), x["q"], x["k"], x["v"], x["alpha"], x["beta"], tape, dout, g["q"], g["k"], g["v"],
+                         g["alpha"], g["beta"], dfinal=d, dstate=d)
+    assert torch.equal(d, want["dstate"]) and all(torch.equal(g[n], want["d" + n]) for n in g)
