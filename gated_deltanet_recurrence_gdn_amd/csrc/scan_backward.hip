@@ -3,8 +3,9 @@
 // Three launches (notation in scan_internal.h).  scan_back_prepare, one
 // workgroup per chunk and value head, forms what does not depend on the state's
 // gradient: Wb and dR0.  scan_back_state, one workgroup per sequence, value head
-// and 16 value columns, walks the chunks backwards: dR = dR0 + Wb G^T, then
-// the gradient G of the state before the chunk.  scan_grad, one workgroup per
+// and 16 or 32 value columns, walks the chunks backwards: dR = dR0 + Wb G^T, then
+// the gradient G of the state before the chunk (two launches over segments where
+// the forward pass has them).  scan_grad, one workgroup per
 // chunk and q/k head, forms the other gradients from the stored states, errors
 // and their gradients, its value heads one after the other: the gradients of a
 // shared q/k head are summed in registers, in a fixed order.
@@ -195,13 +196,18 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     __shared__ __align__(16) float Pl[KS * 4 * NS * 256];  // partial products [key step][token tile][value tile][lane][4]
     __shared__ __align__(16) uint16_t Ul[3 * PU];
     __shared__ __align__(16) uint16_t Ol[3 * PU];
-    int s, h, slice;
-    state_block(a, seqs, s, h, slice);
+    int s, h, slice, seg;
+    state_block(a, seqs, s, h, slice, seg);
     const int c0 = slice * (16 * NS);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     const int ks = wave % KS, m0 = wave / KS * KS;
     const int b = a.seq0 + s, T = seqs.len[s], t0 = seqs.tok0[s], u0 = a.unit_base + seqs.unit0[s];
     const int n_units = (T + kScanChunk - 1) / kScanChunk;
+    // the chunks of this segment; the last one's gradient is known in pass 1
+    const int begin = NS == 1 && seg > 0 ? seg * a.seg_len : 0, end = NS == 1 && n_units - begin > a.seg_len ? begin + a.seg_len : n_units;
+    const bool last = end == n_units, real = NS == 2 || a.pass == 2 || last;
+    if (NS == 1 && (a.pass == 2 ? last : seg == 0 && !last)) return;
+    if (NS == 1 && seg > 0 && begin >= n_units) return;
     if (a.valid[b] == 0) return;
     const bool owns = KS == 4 || m0 == 0;
     const int k0 = 32 * ks + 4 * g, i0 = 16 * wave + 4 * g;
@@ -213,17 +219,30 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     for (int n = 0; n < NS; ++n) {
         in[n] = n == 0 || c0 + 16 * n < a.d_v;
         tn[n] = c0 / 16 + (in[n] ? n : 0);
+        in[n] = in[n] && real;
     }
     f32x4 G[2][NS] = {};
     const size_t seq_at = ((size_t)b * a.h_v + h) * head + (size_t)col * DK + k0;
-    if (a.dfinal != nullptr)
+    if (NS == 1 && !last) {
+        if (real) {  // from the last segment's start over the ones behind this one
+            const int from = (n_units - 1) / a.seg_len;
+            const float* ends = a.ends + ((size_t)seqs.part0[s] * a.h_v + h) * head + (unsigned)(tn[0] * 16 * DK);
+            f32x4 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[i] = ld4(ends + (size_t)from * a.h_v * head + (2 * ks + i) * 256 + lane * 4);
+            for (int p = from - 1; p > seg; --p)
+                join_step<DK, true>(x, a.A + ((size_t)(seqs.part0[s] + p) * a.h_v + h) * (DK * DK), ends + (size_t)p * a.h_v * head, ks, owns, Pl);
+            G[0][0] = x[0];
+            G[1][0] = x[1];
+        }
+    } else if (a.dfinal != nullptr)
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) G[i][n] = ld4(a.dfinal + seq_at + (size_t)tn[n] * (16 * DK) + 16 * i);
     const OT* dout = static_cast<const OT*>(a.dout) + (size_t)h * a.d_v + col;
     auto load_o = [&](int c, Ops& o) {  // dout
-        c = c < 0 ? 0 : c;
+        c = c < begin ? begin : c;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {  // past the sequence's end: its last token's, used as zero
             const int t = c * kScanChunk + i0 + r;
@@ -235,27 +254,27 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
         o.eb = ld4(gt + 256 + i0);
     };
     auto load_w = [&](int c, int m, Ops& o) {  // Wb of one token tile
-        c = c < 0 ? 0 : c;
+        c = c < begin ? begin : c;
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
         const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
 #pragma unroll
         for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
     };
     auto load_e = [&](int c, Ops& o) {  // dR0
-        c = c < 0 ? 0 : c;
+        c = c < begin ? begin : c;
         const float* e = a.dR + ((size_t)(u0 + c) * a.h_v + h) * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
 #pragma unroll
         for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
     };
     auto load_t = [&](int c, int kk, const uint16_t* from, bf16x8 (&o)[2][2][TK]) {  // K^T or Q^T of 32 tokens
-        c = c < 0 ? 0 : c;
+        c = c < begin ? begin : c;
         const uint16_t* t0 = from + ((size_t)(u0 + c) * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(ks * 4 * TK * 512 + lane * 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int t = 0; t < TK; ++t) o[i][kk][t] = ld_bf8(t0 + ((i * 2 + kk) * TK + t) * 512);
     };
-    auto load_d = [&](int c, Ops& o) { o.decay = a.gates[((size_t)(u0 + (c < 0 ? 0 : c)) * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63]; };
+    auto load_d = [&](int c, Ops& o) { o.decay = a.gates[((size_t)(u0 + (c < begin ? begin : c)) * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63]; };
     auto step = [&](int c, Ops& cur) {
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
         {
@@ -362,14 +381,22 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
         }
         load_d(c, o);
     };
-    if (n_units > 0) {
+    if (end > begin) {
         Ops p, q;
-        load_all(n_units - 1, p);
-        load_all(n_units - 2, q);
-        for (int c = n_units - 1; c >= 0; c -= 2) {
+        load_all(end - 1, p);
+        load_all(end - 2, q);
+        for (int c = end - 1; c >= begin; c -= 2) {
             step(c, p);
-            if (c > 0) step(c - 1, q);
+            if (c > begin) step(c - 1, q);
         }
+    }
+    if (NS == 1 && seg > 0) {  // for the segments before this one
+        if (a.pass == 1 && owns) {
+            float* st = a.ends + ((size_t)(seqs.part0[s] + seg) * a.h_v + h) * head + c0 * DK + ks * 512 + lane * 4;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) st4(st + i * 256, G[i][0]);
+        }
+        return;
     }
     if (owns && a.dstate != nullptr)
 #pragma unroll
@@ -784,10 +811,14 @@ template <int DK, int TK, typename OT>
 hipError_t launch_back_state(ScanArgs a, hipStream_t st, const ScanSeqs& seqs) {
     const bool pair = two_tiles(a);
     a.slices = pair ? (a.d_v + 31) / 32 : a.d_v / 16;
-    const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq);
-    if (pair) hipLaunchKernelGGL((scan_back_state_kernel<DK, 2, TK, OT>), grid, dim3(256), 0, st, a, seqs);
-    else hipLaunchKernelGGL((scan_back_state_kernel<DK, 1, TK, OT>), grid, dim3(256), 0, st, a, seqs);
-    return hipGetLastError();
+    const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)(a.n_seq * a.n_seg));
+    hipError_t e = hipSuccess;
+    for (a.pass = 1; a.pass <= (a.n_seg > 1 ? 2 : 1) && e == hipSuccess; ++a.pass) {
+        if (pair) hipLaunchKernelGGL((scan_back_state_kernel<DK, 2, TK, OT>), grid, dim3(256), 0, st, a, seqs);
+        else hipLaunchKernelGGL((scan_back_state_kernel<DK, 1, TK, OT>), grid, dim3(256), 0, st, a, seqs);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 template <int DK, int TK, int TO>

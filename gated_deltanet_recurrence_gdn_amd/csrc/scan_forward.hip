@@ -4,7 +4,8 @@
 // per chunk and value head, forms everything that does not depend on the state:
 // the gates, Y by forward substitution, W and E0.  scan_state, one workgroup
 // per sequence, value head and 16 or 32 value columns, walks the chunks:
-// E = E0 - W S^T, then the state.  scan_output, one workgroup per chunk and
+// E = E0 - W S^T, then the state; long walks on few CUs run as two launches over
+// segments.  scan_output, one workgroup per chunk and
 // value head, forms the outputs from the stored states and errors.
 //
 // Everything is held to fp32 accuracy: the states and errors feed the backward
@@ -241,13 +242,18 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     constexpr int LDU = kScanChunk + 8, PU = 16 * NS * LDU;  // a part's plane
     __shared__ __align__(16) float Pl[KS * 4 * NS * 256];  // partial products [key step][token tile][value tile][lane][4]
     __shared__ __align__(16) uint16_t Ul[3 * PU];
-    int s, h, slice;
-    state_block(a, seqs, s, h, slice);
+    int s, h, slice, seg;
+    state_block(a, seqs, s, h, slice, seg);
     const int c0 = slice * (16 * NS);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, g = lane >> 4;
     const int ks = wave % KS, m0 = wave / KS * KS;
     const int b = a.seq0 + s, n_units = (seqs.len[s] + kScanChunk - 1) / kScanChunk, u0 = a.unit_base + seqs.unit0[s];
-    const bool lead = h == 0 && c0 == 0 && tid == 0;
+    // the chunks of this segment; rows of the identity, the value tiles behind the last, are walked in pass 1
+    const int begin = NS == 1 && seg > 0 ? seg * a.seg_len : 0, end = NS == 1 && n_units - begin > a.seg_len ? begin + a.seg_len : n_units;
+    const bool real = NS == 2 || a.pass == 2 || seg == 0, identity = NS == 1 && c0 >= a.d_v;
+    if (NS == 1 && (a.pass == 2 ? seg == 0 : seg == 0 ? identity : end == n_units)) return;
+    if (NS == 1 && seg > 0 && begin >= n_units) return;
+    const bool lead = h == 0 && c0 == 0 && tid == 0 && seg == 0;
     int row = b;
     if (a.state != nullptr && a.state_slot != nullptr) {
         row = a.state_slot[b];
@@ -269,12 +275,29 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
         in[n] = n == 0 || c0 + 16 * n < a.d_v;
-        tn[n] = c0 / 16 + (in[n] ? n : 0);
+        tn[n] = identity ? 0 : c0 / 16 + (in[n] ? n : 0);
         cn[n] = 16 * tn[n] + col;
+        in[n] = in[n] && real;
     }
     const size_t head = (size_t)a.d_v * DK, e_unit = (size_t)kScanChunk * a.d_v;
     f32x4 S[2][NS] = {};
-    if (a.state != nullptr) {
+    if (identity) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[i][0][r] = k0 + 16 * i + r == c0 - a.d_v + col ? 1.f : 0.f;
+    } else if (NS == 1 && seg > 0) {
+        if (real) {  // from the first segment's end over the ends before this one
+            const float* ends = a.ends + ((size_t)seqs.part0[s] * a.h_v + h) * head + (unsigned)(tn[0] * 16 * DK);
+            f32x4 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[i] = ld4(ends + (2 * ks + i) * 256 + lane * 4);
+            for (int p = 1; p < seg; ++p)
+                join_step<DK, false>(x, a.A + ((size_t)(seqs.part0[s] + p) * a.h_v + h) * (DK * DK), ends + (size_t)p * a.h_v * head, ks, owns, Pl);
+            S[0][0] = x[0];
+            S[1][0] = x[1];
+        }
+    } else if (a.state != nullptr) {
         const float* st = a.state + ((size_t)row * a.h_v + h) * head + k0;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -282,13 +305,13 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
             for (int i = 0; i < 2; ++i) S[i][n] = ld4(st + (size_t)cn[n] * DK + 16 * i);
     }
     auto load_w = [&](int c, int m, Ops& o) {  // W of one token tile
-        const size_t uh = (size_t)(u0 + (c < n_units ? c : n_units - 1)) * a.h_v + h;
+        const size_t uh = (size_t)(u0 + (c < end ? c : end - 1)) * a.h_v + h;
         const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
 #pragma unroll
         for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
     };
     auto load_e = [&](int c, Ops& o) {  // what else the errors need
-        const size_t uh = (size_t)(u0 + (c < n_units ? c : n_units - 1)) * a.h_v + h;
+        const size_t uh = (size_t)(u0 + (c < end ? c : end - 1)) * a.h_v + h;
         const float* e = a.E + uh * e_unit + (unsigned)(16 * wave * a.d_v + lane * 4);
 #pragma unroll
         for (int n = 0; n < NS; ++n) o.e[n] = ld4(e + tn[n] * 256);
@@ -297,7 +320,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
         o.er = ld4(gt + 320 + 16 * wave + 4 * g);
     };
     auto load_k = [&](int c, int kk, Ops& o) {  // K^T of 32 tokens
-        const int unit = u0 + (c < n_units ? c : n_units - 1);
+        const int unit = u0 + (c < end ? c : end - 1);
         const uint16_t* kt = a.Kt + ((size_t)unit * a.h_qk + h / a.group) * (TK * DK * kScanChunk) + (unsigned)(ks * 4 * TK * 512 + lane * 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -305,7 +328,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
             for (int t = 0; t < TK; ++t) o.kt[i][kk][t] = ld_bf8(kt + ((i * 2 + kk) * TK + t) * 512);
     };
     auto load_d = [&](int c, Ops& o) {
-        const int unit = u0 + (c < n_units ? c : n_units - 1);
+        const int unit = u0 + (c < end ? c : end - 1);
         o.decay = a.gates[((size_t)unit * a.h_v + h) * (kGateRows * kScanChunk) + 256 + 63];
     };
     auto step = [&](int c, Ops& cur) {
@@ -344,7 +367,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
             for (int q = 0; q < KS; ++q) x[q] = ld4(Pl + ((q * 4 + wave) * NS + n) * 256 + lane * 4);
 #pragma unroll
             for (int q = 1; q < KS; ++q) x[0] += x[q];
-            const f32x4 y = cur.e[n] - x[0];
+            const f32x4 y = (identity ? f32x4{} : cur.e[n]) - x[0];
             store_parts<3>(Ul + (16 * n + col) * LDU + 16 * wave + 4 * g, PU, cur.be * cur.er * y);
             if (in[n]) st4(e + tn[n] * 256, y);
         }
@@ -382,14 +405,23 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
         load_k(c, 1, o);
         load_d(c, o);
     };
-    if (n_units > 0) {
+    if (end > begin) {
         Ops p, q;
-        load_all(0, p);
-        load_all(1, q);
-        for (int c = 0; c < n_units; c += 2) {
+        load_all(begin, p);
+        load_all(begin + 1, q);
+        for (int c = begin; c < end; c += 2) {
             step(c, p);
-            if (c + 1 < n_units) step(c + 1, q);
+            if (c + 1 < end) step(c + 1, q);
         }
+    }
+    if (NS == 1 && end < n_units) {  // for the segments behind this one
+        if (a.pass == 1 && owns) {
+            const size_t part = (size_t)(seqs.part0[s] + seg) * a.h_v + h;
+            float* st = (identity ? a.A + part * (DK * DK) + (c0 - a.d_v) * DK : a.ends + part * head + c0 * DK) + ks * 512 + lane * 4;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) st4(st + i * 256, S[i][0]);
+        }
+        return;
     }
     if (owns && a.final_state != nullptr) {
         float* st = a.final_state + ((size_t)b * a.h_v + h) * head + k0;
@@ -526,11 +558,14 @@ hipError_t launch_forward(const ScanArgs& args, const ScanSeqs& seqs, hipStream_
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const bool pair = two_tiles(a);
-    a.slices = pair ? (a.d_v + 31) / 32 : a.d_v / 16;
-    const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)a.n_seq);
-    if (pair) hipLaunchKernelGGL((scan_state_kernel<DK, 2, TK>), grid, dim3(256), 0, st, a, seqs);
-    else hipLaunchKernelGGL((scan_state_kernel<DK, 1, TK>), grid, dim3(256), 0, st, a, seqs);
-    hipError_t e = hipGetLastError();
+    hipError_t e = hipSuccess;
+    for (a.pass = 1; a.pass <= (a.n_seg > 1 ? 2 : 1) && e == hipSuccess; ++a.pass) {
+        a.slices = pair ? (a.d_v + 31) / 32 : (a.d_v + (a.n_seg > 1 && a.pass == 1 ? DK : 0)) / 16;
+        const dim3 grid((unsigned)(a.h_v * a.slices), (unsigned)(a.n_seq * a.n_seg));
+        if (pair) hipLaunchKernelGGL((scan_state_kernel<DK, 2, TK>), grid, dim3(256), 0, st, a, seqs);
+        else hipLaunchKernelGGL((scan_state_kernel<DK, 1, TK>), grid, dim3(256), 0, st, a, seqs);
+        e = hipGetLastError();
+    }
     if (e != hipSuccess || heads == 0) return e;
     if ((e = allow_max_lds<scan_output_kernel<DK, TK>>()) != hipSuccess) return e;
     hipLaunchKernelGGL((scan_output_kernel<DK, TK>), dim3(heads), dim3(kOutThreads), (OutLds<DK, TK>::kBytes), st, a, seqs);

@@ -57,12 +57,14 @@ struct ScanArgs {
     float* Y;      // [row tile][column tile] accumulators, the 10 on and below the diagonal are written
     float* E;      // the errors (E0 between the prepare and the state kernel), [token tile][value tile] accumulators
     float* S;      // the state before the chunk, transposed, [value tile][key tile] accumulators
+    float* A;      // per segment and value head: what becomes of a state (the identity) over it, as S
     // workspace
     uint16_t* W;   // forward W, backward Wb, in three parts, per unit and value head: row operands [token tile][key step][part]
     uint16_t* Kt;  // K and Q transposed, per unit and q/k head: row operands [key tile][token step][part]
     uint16_t* Qt;
     float* dR;  // gradients of the errors' system, as E (dR0 between the prepare and the state kernel)
     float* G;   // the gradient of the state after the chunk, as S
+    float* ends;  // per segment and value head: the state (backward: its gradient) the segment's walk ends with, as S
     // backward
     const void* dout;
     const float* dfinal;  // nullable: zeros
@@ -75,6 +77,7 @@ struct ScanArgs {
     int32_t h_qk, h_v, d_v, group, n_slots, slices;
     int32_t qkv_bf16, out_dtype;
     int32_t n_seq, seq0, units, unit_base;
+    int32_t seg_len, n_seg, pass;  // chunks of a segment (kWhole: none are cut), segments of the longest sequence, 1 or 2
     float scale;
 };
 
@@ -86,20 +89,23 @@ struct ScanArgs {
 // columns 4 (l / 16) ..+3 and 16 + 4 (l / 16) ..+3, as operand_of).
 
 // The sequences of a launch: first token, tokens, first chunk unit (one entry
-// more), and their order by length, longest first (the state kernels' workgroups
-// are started in that order).
+// more), first segment, and their order by length, longest first (the state
+// kernels' workgroups are started in that order).
 constexpr int kScanSeqs = 64;
+constexpr int32_t kWhole = 0x7fffffff;
 struct ScanSeqs {
-    int32_t tok0[kScanSeqs], len[kScanSeqs], unit0[kScanSeqs + 1];
+    int32_t tok0[kScanSeqs], len[kScanSeqs], unit0[kScanSeqs + 1], part0[kScanSeqs];
     uint8_t order[kScanSeqs];
 };
 
 // Workgroups of a state kernel: blockIdx.x is one of h_v * slices, contiguous
 // runs of them on one XCD (the slices of a head read the same operands), the
-// same for every sequence, so that the XCDs have equal shares of each.
-__device__ __forceinline__ void state_block(const ScanArgs& a, const ScanSeqs& seqs, int& s, int& h, int& slice) {
+// same for every sequence, so that the XCDs have equal shares of each; blockIdx.y
+// one of a sequence's segments.
+__device__ __forceinline__ void state_block(const ScanArgs& a, const ScanSeqs& seqs, int& s, int& h, int& slice, int& seg) {
     const int x = xcd_logical_block(blockIdx.x, gridDim.x);
-    s = seqs.order[blockIdx.y];
+    s = seqs.order[blockIdx.y % a.n_seq];
+    seg = blockIdx.y / a.n_seq;
     h = x / a.slices;
     slice = x % a.slices;
 }
@@ -110,7 +116,16 @@ __device__ __forceinline__ void state_block(const ScanArgs& a, const ScanSeqs& s
 // every CU a workgroup and more, two are faster (4096 tokens of 48 heads, 384
 // workgroups of one tile: 226 against 186 us; packed sequences 196 against 136),
 // below that one (16384 tokens of 6 heads, 48 workgroups: 278 against 417 us).
-inline bool two_tiles(const ScanArgs& a) { return (int64_t)a.n_seq * a.h_v * (a.d_v / 16) > device_cus(); }
+inline bool two_tiles(const ScanArgs& a) { return a.seg_len == kWhole && (int64_t)a.n_seq * a.h_v * (a.d_v / 16) > device_cus(); }
+
+// A walk of many chunks on few CUs is cut into segments.  Over a segment the state
+// goes S -> S A + B (A d_k x d_k, B as S), so two passes do with all segments at
+// once: pass 1 walks the first segment as it is, and the others but the last one
+// from zeros (B) and from the identity (A); pass 2 forms a segment's first state
+// from the ends before it, S <- S A + B from one segment to the next, and walks
+// it.  The gradient goes G -> G A^T + B' the other way, with the A of the forward
+// pass (they are on the tape).  16384 tokens of 6 heads, 6 segments: forward 162
+// us for both passes against 277 of one walk, backward 198 against 420.
 
 // Parts of the inputs q, k: one in bf16, three in fp32.
 inline int input_parts(const ScanArgs& a) { return a.qkv_bf16 ? 1 : 3; }
@@ -389,6 +404,37 @@ __device__ __forceinline__ void column_values(const RawColumn& c, int len, int d
                                                : __builtin_bit_cast(float, x << 16);
             v[m][r] = 16 * m + 4 * g + r < len ? y : 0.f;
         }
+}
+
+// One step of a join of segments: X <- X A + B (BACK: X A^T + B), all transposed, in
+// accumulators: this wave's key tiles 2 ks, 2 ks + 1 of one value tile in x.  The
+// old X passes through `lds` (DK * 16 floats), written by the waves that own it.
+template <int DK, bool BACK>
+__device__ __forceinline__ void join_step(f32x4 (&x)[2], const float* A, const float* B, int ks, bool owns, float* lds) {
+    constexpr int NT = DK / 16;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    f32x4 y[2], f[2][NT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int kt = 2 * ks + i;
+        y[i] = ld4(B + kt * 256 + lane * 4);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            f[i][t] = BACK ? ld4(A + (kt * NT + t) * 256 + lane * 4) : ld_col4(A + (t * NT + kt) * 256 + (col / 4 * 16 + 4 * g) * 4 + col % 4, 4);
+    }
+    if (owns)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) st4(lds + (2 * ks + i) * 256 + lane * 4, x[i]);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const f32x4 b = ld4(lds + t * 256 + lane * 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y[i] = mma16(f[i][t], b, y[i]);
+    }
+    __syncthreads();
+    x[0] = y[0];
+    x[1] = y[1];
 }
 
 // 2^(b_i - b_j) from the two-part sums: the high parts' difference is rounded

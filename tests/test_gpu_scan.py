@@ -438,3 +438,63 @@ def test_gradient_of_the_state_in_place():
     gb.gdn_scan_backward(offsets(lens), x["q"], x["k"], x["v"], x["alpha"], x["beta"], tape, dout, g["q"], g["k"], g["v"],
                          g["alpha"], g["beta"], dfinal=d, dstate=d)
     assert torch.equal(d, want["dstate"]) and all(torch.equal(g[n], want["d" + n]) for n in g)
+
+
+# ---------------------------------------------------------------------------
+# long sequences on few heads: the walks are cut into segments
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("lens,hq,hv,dk,dv,dtype", [
+    ([1537], 1, 1, 32, 16, torch.float32),
+    ([1500, 70, 0, 1100, 449, 1], 1, 2, 64, 48, torch.bfloat16),
+    ([2500], 2, 2, 128, 32, torch.float32),
+    ([1664, 1665], 1, 3, 128, 64, torch.bfloat16),
+])
+def test_segments(lens, hq, hv, dk, dv, dtype):
+    say("segments", lens, hq, hv, dk, dv, dtype)
+    x, dout, dfinal = inputs(45, lens, hq, hv, dk, dv, dtype)
+    check(x, lens, dk ** -0.5, dtype, dout, dfinal)
+
+
+def test_segments_with_slots_and_in_place():
+    lens = [1600, 1700, 64, 1601]
+    x, dout, dfinal = inputs(46, lens, 1, 2, 64, 32)
+    want, fin, tape = forward(x, lens)
+    grads = backward(x, lens, tape, dout, dfinal)
+    slot = torch.tensor([2, 9, 0, 1], dtype=torch.int32, device=DEV)  # the second is outside the pool
+    pool = torch.zeros(3, 2, 32, 64, device=DEV)
+    for b in (0, 2, 3):
+        pool[slot[b].long()] = x["state"][b]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, fin2, tape2 = forward(x, lens, state=pool, state_slot=slot, status=status)
+    assert int(status.item()) == gb.CODES["GDN_ERR_SLOT"]
+    keep = torch.ones(sum(lens), dtype=torch.bool, device=DEV)
+    keep[1600:3300] = False
+    assert torch.equal(out[keep], want[keep]) and bool(out[~keep].isnan().all())
+    assert torch.equal(fin2[[0, 2, 3]], fin[[0, 2, 3]]) and bool(fin2[1].isnan().all())
+    g2 = backward(x, lens, tape2, dout, dfinal)
+    for n in ("dq", "dk", "dv", "dalpha", "dbeta"):
+        assert torch.equal(g2[n][keep], grads[n][keep]) and bool(g2[n][~keep].isnan().all()), n
+    assert torch.equal(g2["dstate"][[0, 2, 3]], grads["dstate"][[0, 2, 3]])
+    state = x["state"].clone()
+    out = torch.empty_like(want)
+    gb.gdn_scan_forward(offsets(lens), x["q"], x["k"], x["v"], x["alpha"], x["beta"], out, state=state, final_state=state)
+    assert torch.equal(out, want) and torch.equal(state, fin)
+
+
+def test_segments_with_gates_at_their_ends():
+    lens = [1700]
+    for alpha, beta in (("zeros", "ends"), ("one", "mixed")):
+        x, dout, dfinal = inputs(47, lens, 1, 2, 64, 32, alpha=alpha, beta=beta)
+        check(x, lens, 0.125, torch.float32, dout, dfinal)
+
+
+def test_a_nan_passes_from_segment_to_segment():
+    lens = [1600, 1200]
+    x, dout, dfinal = inputs(48, lens, 1, 2, 64, 32)
+    want, fin, _ = forward(x, lens)
+    x["v"][500, 1, 3] = float("nan")
+    out, fin2, tape = forward(x, lens)
+    chunk = 500 // 64 * 64
+    assert torch.equal(out[:chunk], want[:chunk]) and torch.equal(out[1600:], want[1600:])
+    assert torch.equal(out[:, 0], want[:, 0]) and torch.equal(fin2[1], fin[1])
+    assert bool(out[500:1600, 1, 3].isnan().all()) and bool(fin2[0, 1, 3].isnan().all())
