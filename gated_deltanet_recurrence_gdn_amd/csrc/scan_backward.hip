@@ -36,6 +36,8 @@ struct BackPrepLds {
 // Wave c owns the tokens i of tile c as columns: P^T's tiles (rows j) stay in
 // accumulators, the right operand of Z^T = P^T - (beta Y)^T P^T as they are, with
 // Y's tiles straight from memory as the left one.  Z's parts go through LDS once.
+// 4096 packed tokens of 16 / 48 heads, d 128, bf16: 140 us, 435 MB at 3.1 TB/s (294
+// written: Wb's parts, dR0), matrix cores 9% busy: its phases wait for one another.
 template <int DK, int TK>
 __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using L = BackPrepLds<DK, TK>;
@@ -175,7 +177,8 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
 // The gradient's walk, the mirror image of scan_state: G^T in accumulators, two
 // matrix operands (K and Q) and two exchanged right sides, the same two operand
 // sets that take turns.  OT: the type of dout, whose values stay as loaded until
-// they are used.
+// they are used.  4096 packed tokens of 48 heads: 193 us, 666 MB at 3.4 TB/s; 6 heads
+// of one sequence, one tile each: 1.6 us a chunk.
 template <int DK, int NS, int TK, typename OT>
 struct BackOperands {
     bf16x8 w[DK / 32][3], kt[2][2][TK], qt[2][2][TK];
@@ -433,7 +436,11 @@ __device__ __forceinline__ float wave_sum(float x) {
 // S0 and G pass through a corner of LDS of its own, one after the other; dR, E and
 // dout serve all waves and are double-buffered: one barrier a step, and the
 // cutting of one wave runs beside another's products.  A wave also owns one or
-// two of the ten lower tiles of the 64 x 64 sums.
+// two of the ten lower tiles of the 64 x 64 sums.  4096 packed tokens of 16 / 48
+// heads, d 128, bf16: 386 us, 985 MB at 2.6 TB/s, matrix cores 14% busy: one
+// workgroup of 120 KB a CU, two waves a SIMD, bound by the cutting and the LDS reads
+// between its barriers (9000 vector and 1400 LDS instructions a wave), in five rounds
+// of 256 for 1056 workgroups.
 constexpr int kGradThreads = 512;
 constexpr int kGradWaves = kGradThreads / 64;
 constexpr int kLdO = 32 + 8;  // rows of dout (32 value columns), read 16 bytes a lane

