@@ -438,7 +438,7 @@ __device__ __forceinline__ float wave_sum(float x) {
 // cutting of one wave runs beside another's products.  A wave also owns one or
 // two of the ten lower tiles of the 64 x 64 sums.  4096 packed tokens of 16 / 48
 // heads, d 128, bf16: 386 us, 985 MB at 2.6 TB/s, matrix cores 14% busy: one
-// workgroup of 120 KB a CU, two waves a SIMD, bound by the cutting and the LDS reads
+// workgroup of 155 KB of LDS a CU, two waves a SIMD, bound by the cutting and the LDS reads
 // between its barriers (9000 vector and 1400 LDS instructions a wave), in five rounds
 // of 256 for 1056 workgroups.
 constexpr int kGradThreads = 512;
