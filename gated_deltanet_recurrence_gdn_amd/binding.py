@@ -159,10 +159,11 @@ class PreparedCall:
 
 
 def _invoke(name, args, keep, prepare):
-    call = PreparedCall(name, args, keep)
     if prepare:
-        return call
-    call()
+        return PreparedCall(name, args, keep)
+    rc = _raw(name)(*args)
+    if rc != 0:
+        raise GdnError(rc, name)
     return None
 
 
@@ -212,8 +213,8 @@ def _dev_ptr(t, name: str):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        return _vp(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # torch.cuda.current_stream().cuda_stream, without building a Stream (2.7 us)
+        return _vp(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return _vp(stream)
     return _vp(stream.cuda_stream)
@@ -587,16 +588,20 @@ def _address(x: np.ndarray) -> int:
 
 def _scan_shape(cu, q, k, v, alpha, beta, out, n_slots, scale, out_name="out") -> GdnShape:
     total, Hqk, dk = _shape_of(q, "q", 3)
-    _expect(k, "k", (total, Hqk, dk), q.dtype)
-    _expect(v, "v", (total, None, None), q.dtype)
-    if q.dtype not in _QKV:
-        raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
-    Hv, dv = v.shape[1], v.shape[2]
+    dtype = q.dtype
+    _expect(k, "k", (total, Hqk, dk), dtype)
+    if not isinstance(v, torch.Tensor) or v.dim() != 3 or v.shape[0] != total or v.dtype is not dtype:
+        _expect(v, "v", (total, None, None), dtype)
+    if dtype not in _QKV:
+        raise TypeError(f"q must be float32 or bfloat16, got {dtype}")
+    _, Hv, dv = v.shape
     _expect(alpha, "alpha", (total, Hv), torch.float32)
     _expect(beta, "beta", (total, Hv), torch.float32)
     if out is None:
         raise ValueError(f"{out_name} is required")
-    _expect(out, out_name, (total, Hv, dv), _OUT)
+    _expect(out, out_name, (total, Hv, dv))
+    if out.dtype not in _OUT:
+        _expect(out, out_name, (total, Hv, dv), _OUT)
     if int(cu[-1]) != total:
         raise ValueError(f"cu_seqlens ends at {int(cu[-1])}, the inputs hold {total} tokens")
     return GdnShape(cu.size - 1, total, Hqk, Hv, dk, dv, n_slots, _dtype_code(q), _dtype_code(out), GDN_F16,
@@ -618,6 +623,7 @@ def gdn_scan_forward(cu_seqlens, q, k, v, alpha, beta, out, *, tape=None, state=
     array [B + 1]); see include/gdn.h.  ``tape``: uint8 device tensor of gdn_scan_tape_bytes bytes, for
     :func:`gdn_scan_backward`.  ``workspace`` is allocated here with torch when omitted."""
     cu = _host_cu(cu_seqlens)
+    offsets = _address(cu)
     sh = _scan_shape(cu, q, k, v, alpha, beta, out, state.shape[0] if state is not None else 0, scale)
     if state is not None:
         _check_state(state, state_slot, sh.batch, sh.h_v, sh.d_v, sh.d_k)
@@ -627,9 +633,9 @@ def gdn_scan_forward(cu_seqlens, q, k, v, alpha, beta, out, *, tape=None, state=
     _expect(tape, "tape", (None,), torch.uint8)
     _check_status(status)
     if workspace is None:
-        need = lib().gdn_scan_forward_workspace_bytes(ctypes.byref(sh), _address(cu), int(tape is not None))
+        need = lib().gdn_scan_forward_workspace_bytes(ctypes.byref(sh), offsets, int(tape is not None))
         workspace = _workspace(int(need), q.device, stream)
-    args = (ctypes.byref(sh), _vp(_address(cu)), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+    args = (ctypes.byref(sh), _vp(offsets), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
             _dev_ptr(alpha, "alpha"), _dev_ptr(beta, "beta"), _dev_ptr(state, "state"),
             _dev_ptr(state_slot, "state_slot"), _dev_ptr(out, "out"), _dev_ptr(final_state, "final_state"),
             _dev_ptr(tape, "tape"), ctypes.c_size_t(0 if tape is None else _bytes_of(tape)),
@@ -646,6 +652,7 @@ def gdn_scan_backward(cu_seqlens, q, k, v, alpha, beta, tape, dout, dq, dk, dv, 
     """The gradients of :func:`gdn_scan_forward` from its tape, written to dq, dk, dv (q's dtype), dalpha, dbeta and
     ``dstate`` (fp32); ``dfinal``: the gradient of the final states (zeros when omitted).  See include/gdn.h."""
     cu = _host_cu(cu_seqlens)
+    offsets = _address(cu)
     sh = _scan_shape(cu, q, k, v, alpha, beta, dout, 0, scale, "dout")
     for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v), (dalpha, "dalpha", alpha), (dbeta, "dbeta", beta)):
         if t is None:
@@ -655,9 +662,9 @@ def gdn_scan_backward(cu_seqlens, q, k, v, alpha, beta, tape, dout, dq, dk, dv, 
         _expect(t, name, (sh.batch, sh.h_v, sh.d_v, sh.d_k), torch.float32)
     _expect(tape, "tape", (None,), torch.uint8)
     if workspace is None:
-        need = lib().gdn_scan_backward_workspace_bytes(ctypes.byref(sh), _address(cu))
+        need = lib().gdn_scan_backward_workspace_bytes(ctypes.byref(sh), offsets)
         workspace = _workspace(int(need), q.device, stream)
-    args = (ctypes.byref(sh), _vp(_address(cu)), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+    args = (ctypes.byref(sh), _vp(offsets), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
             _dev_ptr(alpha, "alpha"), _dev_ptr(beta, "beta"), _dev_ptr(tape, "tape"),
             ctypes.c_size_t(0 if tape is None else _bytes_of(tape)), _dev_ptr(dout, "dout"), _dev_ptr(dfinal, "dfinal"),
             _dev_ptr(dq, "dq"), _dev_ptr(dk, "dk"), _dev_ptr(dv, "dv"), _dev_ptr(dalpha, "dalpha"),
@@ -678,8 +685,8 @@ def _pool_structs(pools, name="pools"):
         pools = (pools,)
     if not 1 <= len(pools) <= GDN_MAX_POOLS:
         raise ValueError(f"{name}: 1 to {GDN_MAX_POOLS} pools, got {len(pools)}")
-    structs = (GdnPool * len(pools))()
-    for i, t in enumerate(pools):
+    structs = []
+    for t in pools:
         if not isinstance(t, torch.Tensor) or t.dim() < 3:
             raise ValueError(f"{name} must be tensors [layers][slots][...]")
         size = t.shape
@@ -695,18 +702,19 @@ def _pool_structs(pools, name="pools"):
                 row *= size[k]
         if slots < 1 or row == 0:
             raise ValueError(f"{name} must hold at least one row")
-        structs[i] = GdnPool(t.data_ptr(), row // slots * e, (t.stride(0) if layers > 1 else row) * e, layers, slots)
-        if slots != pools[0].shape[1]:
+        structs.append((t.data_ptr(), row // slots * e, (t.stride(0) if layers > 1 else row) * e, layers, slots))
+        if slots != structs[0][4]:
             raise ValueError(f"the {name} must have the same number of rows")
-    return structs, tuple(pools)
+    return (GdnPool * len(structs))(*structs), tuple(pools)
 
 
-def _int_array(t, name, n=None):
+def _int_array(t, name):
     """The length of an int32 vector (0 where it is not given)."""
     if t is None:
         return 0
-    _expect(t, name, (n,), torch.int32)
-    return t.shape[0]
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 1):
+        _expect(t, name, (None,), torch.int32)
+    return t.numel()
 
 
 def _on_current_device(name, *tensors):
