@@ -36,7 +36,7 @@ struct BackPrepLds {
 // Wave c owns the tokens i of tile c as columns: P^T's tiles (rows j) stay in
 // accumulators, the right operand of Z^T = P^T - (beta Y)^T P^T as they are, with
 // Y's tiles straight from memory as the left one.  Z's parts go through LDS once.
-// 4096 packed tokens of 16 / 48 heads, d 128, bf16: 140 us, 435 MB at 3.1 TB/s (294
+// 4096 packed tokens of 16 / 48 heads, d 128, bf16: 137 us, 435 MB at 3.2 TB/s (294
 // written: Wb's parts, dR0), matrix cores 9% busy: its phases wait for one another.
 template <int DK, int TK>
 __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
@@ -77,14 +77,18 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
             }
     }
     const int i0 = 16 * wave + col;
+    const float bhi = gt[i0], bli = gt[64 + i0];
 #pragma unroll
     for (int n = 0; n < 4; ++n)
-        if (n <= wave)
+        if (n <= wave) {
+            const int j = 16 * n + 4 * g;
+            const f32x4 bhj = ld4(gt + j), blj = ld4(gt + 64 + j);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int j = 16 * n + 4 * g + r;
-                p[n][r] = j <= i0 ? p[n][r] * decay_between(gt, gt + 64, i0, j) : 0.f;
+                const float d = decay_between(bhi, bli, bhj[r], blj[r]);
+                p[n][r] = j + r <= i0 ? p[n][r] * d : 0.f;
             }
+        }
     if (h % a.group == 0) {  // K and Q laid out for the state kernel
         const size_t at = ((size_t)(a.unit_base + unit) * a.h_qk + hq) * (TK * DK * kScanChunk) + lane * 8;
         for (int x = wave; x < DK / 8; x += kBackThreads / 64) {  // key tile x / 2, tokens 32 (x % 2) ..
@@ -679,7 +683,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float d = j <= i + r ? bj * __builtin_amdgcn_exp2f((bh[r] - bhj) + (bl[r] - blj)) : 0.f;
+                const float d = j <= i + r ? bj * decay_between(bh[r], bl[r], bhj, blj) : 0.f;
                 const float x = j < i + r ? -bi[r] * d * da[q][r] : 0.f, p = a.scale * d * dp[q][r];
                 xs[r] += x;
                 ps[r] += p;

@@ -439,8 +439,8 @@ __device__ __forceinline__ void join_step(f32x4 (&x)[2], const float* A, const f
 
 // 2^(b_i - b_j) from the two-part sums: the high parts' difference is rounded
 // relative to itself, not to the (much larger) sums.
-__device__ __forceinline__ float decay_between(const float* bh, const float* bl, int i, int j) {
-    return __builtin_amdgcn_exp2f((bh[i] - bh[j]) + (bl[i] - bl[j]));
+__device__ __forceinline__ float decay_between(float bh_i, float bl_i, float bh_j, float bl_j) {
+    return __builtin_amdgcn_exp2f((bh_i - bh_j) + (bl_i - bl_j));
 }
 
 }  // namespace gdn
