@@ -19,25 +19,31 @@ constexpr int kPrepThreads = 256;
 
 // The inverse of a unit lower triangular 16 x 16 tile I + A, A in rows of `ld`
 // floats: each lane the column l % 16, by forward substitution; written to `t`
-// (rows of 20 floats).
+// (rows of 20 floats).  A lane holds its column of A; an element reaches the other
+// lanes of its row of 16 by a broadcast on the way into the product.
+template <int I, int J>
+__device__ __forceinline__ void eliminate(const float (&r)[16], float (&x)[16]) {
+    if constexpr (J < I) {
+        // row_newbcast: lane J of the 16
+        const int b = __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, r[I]), 0x150 + J, 0xF, 0xF, true);
+        x[I] = __builtin_fmaf(-__builtin_bit_cast(float, b), x[J], x[I]);
+        eliminate<I, J + 1>(r, x);
+    } else if constexpr (I < 15) {
+        eliminate<I + 1, 0>(r, x);
+    }
+}
+
 __device__ __forceinline__ void invert_tile(const float* A, int ld, float* t, int lane) {
     const int col = lane & 15;
-    float x[16];
+    float r[16], x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float y = i == col ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 0; j < i; j += 4) {
-            const f32x4 r = ld4(A + i * ld + j);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                if (j + s < i) y = __builtin_fmaf(-r[s], x[j + s], y);
-        }
-        x[i] = y;
+        r[i] = A[i * ld + col];
+        x[i] = i == col ? 1.f : 0.f;
     }
-    if (lane < 16)
+    eliminate<1, 0>(r, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t[i * 20 + col] = x[i];
+    for (int i = 0; i < 16; ++i) t[i * 20 + col] = x[i];  // in a branch the sums would move behind the broadcasts, which cannot
 }
 
 template <int DK, int TK>
