@@ -39,7 +39,7 @@ int check_scan(const gdn_shape* sh, const int32_t* cu, int64_t* units) {
 
 // Chunks per segment of the walks of sequences s0 .. s0 + ns - 1 (kWhole: no cut).
 // As many segments as give every CU a workgroup in pass 2 (16384 tokens of 6 heads,
-// 48 workgroups: 6 segments; 5 took 8 us more of 79 a pass, 9 took 6 more); no more
+// 48 workgroups: 6 segments; 5 took 12 us more of 81 a pass, 9 took 6 more); no more
 // than the root of the chunks, as every segment costs the last one a step of the
 // join; and four at least, as the two passes walk two segments' lengths.  Below 24
 // chunks the second launch costs what the cut saves (6 heads, forward and backward:
