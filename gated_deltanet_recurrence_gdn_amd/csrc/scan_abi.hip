@@ -98,7 +98,7 @@ size_t carve_tape(const gdn_shape* sh, int64_t units, int64_t parts, void* base,
 size_t carve_forward(const gdn_shape* sh, int64_t units, int64_t parts, bool tape_inside, void* base, ScanArgs* a) {
     Carver c{static_cast<unsigned char*>(base)};
     const size_t chunk = (size_t)kScanChunk * sh->d_k;
-    a->W = c.take<uint16_t>((size_t)units * sh->h_v * 3 * chunk);
+    a->W = c.take<float>((size_t)units * sh->h_v * chunk);
     a->Kt = c.take<uint16_t>((size_t)units * sh->h_qk * (sh->qkv_dtype == GDN_BF16 ? 1 : 3) * chunk);
     a->ends = c.take<float>((size_t)parts * sh->h_v * sh->d_v * sh->d_k);
     if (tape_inside) c.used += carve_tape(sh, units, parts, base == nullptr ? nullptr : c.base + c.used, a);
@@ -109,7 +109,7 @@ size_t carve_backward(const gdn_shape* sh, int64_t units, int64_t parts, void* b
     Carver c{static_cast<unsigned char*>(base)};
     const size_t heads = (size_t)units * sh->h_v, chunk = (size_t)kScanChunk * sh->d_k;
     const size_t qk = (size_t)units * sh->h_qk * (sh->qkv_dtype == GDN_BF16 ? 1 : 3) * chunk;
-    a->W = c.take<uint16_t>(heads * 3 * chunk);
+    a->W = c.take<float>(heads * chunk);
     a->Kt = c.take<uint16_t>(qk);
     a->Qt = c.take<uint16_t>(qk);
     a->dR = c.take<float>(heads * kScanChunk * sh->d_v);

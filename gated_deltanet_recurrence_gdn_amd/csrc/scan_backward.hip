@@ -36,8 +36,8 @@ struct BackPrepLds {
 // Wave c owns the tokens i of tile c as columns: P^T's tiles (rows j) stay in
 // accumulators, the right operand of Z^T = P^T - (beta Y)^T P^T as they are, with
 // Y's tiles straight from memory as the left one.  Z's parts go through LDS once.
-// 4096 packed tokens of 16 / 48 heads, d 128, bf16: 137 us, 435 MB at 3.2 TB/s (294
-// written: Wb's parts, dR0), matrix cores 9% busy: its phases wait for one another.
+// 4096 packed tokens of 16 / 48 heads, d 128, bf16: 133 us, 383 MB at 2.9 TB/s (242
+// written: Wb, dR0), matrix cores 9% busy: its phases wait for one another.
 template <int DK, int TK>
 __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using L = BackPrepLds<DK, TK>;
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
     // Wb^T = (2^(b_63 - b) K)^T - K^T (beta 2^(b_63 - b) Y): wave m the tokens j of tile
     // m, a lane its piece of the state kernel's row operand
     {
-        uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + wave * KS * 3 * 512 + lane * 8;
+        float* w = a.W + uh * (kScanChunk * DK) + wave * KS * 512 + lane * 8;
         bf16x8 yf[2][3];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
@@ -173,7 +173,8 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
                         x[q] = mma_parts<TK, 3>(f, yf[kk], x[q]);
                     }
             const uint16_t* kr = Kp + i0 * LDK + 32 * n + 4 * g;
-            store_operand<3>(w + n * 3 * 512, er[i0] * read_whole<TK>(kr, L::kPlK) - x[0], er[i0] * read_whole<TK>(kr + 16, L::kPlK) - x[1]);
+            st4(w + n * 512, er[i0] * read_whole<TK>(kr, L::kPlK) - x[0]);
+            st4(w + n * 512 + 4, er[i0] * read_whole<TK>(kr + 16, L::kPlK) - x[1]);
         }
     }
 }
@@ -181,12 +182,12 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
 // The gradient's walk, the mirror image of scan_state: G^T in accumulators, two
 // matrix operands (K and Q) and two exchanged right sides, the same two operand
 // sets that take turns.  OT: the type of dout, whose values stay as loaded until
-// they are used.  4096 packed tokens of 48 heads: 193 us, 666 MB at 3.4 TB/s; 6 heads
+// they are used.  4096 packed tokens of 48 heads: 193 us, 614 MB at 3.2 TB/s; 6 heads
 // of one sequence, one tile each: 1.6 us a chunk.
 template <int DK, int NS, int TK, typename OT>
 struct BackOperands {
-    bf16x8 w[DK / 32][3], kt[2][2][TK], qt[2][2][TK];
-    f32x4 e[NS], be, eb;
+    bf16x8 kt[2][2][TK], qt[2][2][TK];
+    f32x4 w[DK / 32][2], e[NS], be, eb;
     OT o[NS][4];
     float decay;
 };
@@ -263,9 +264,9 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
     auto load_w = [&](int c, int m, Ops& o) {  // Wb of one token tile
         c = c < begin ? begin : c;
         const size_t uh = (size_t)(u0 + c) * a.h_v + h;
-        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
+        const float* w = a.W + uh * (kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 512 + lane * 8);
 #pragma unroll
-        for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
+        for (int t = 0; t < 2; ++t) o.w[m][t] = ld4(w + m * KS * 512 + 4 * t);
     };
     auto load_e = [&](int c, Ops& o) {  // dR0
         c = c < begin ? begin : c;
@@ -291,8 +292,10 @@ __global__ __launch_bounds__(256, 1) void scan_back_state_kernel(const ScanArgs 
             f32x4 x[KS][NS] = {};
 #pragma unroll
             for (int m = 0; m < KS; ++m) {
+                bf16x8 wf[3];
+                operand_of(cur.w[m][0], cur.w[m][1], wf);
 #pragma unroll
-                for (int n = 0; n < NS; ++n) x[m][n] = mma_parts<3, 3>(cur.w[m], f[n], x[m][n]);
+                for (int n = 0; n < NS; ++n) x[m][n] = mma_parts<3, 3>(wf, f[n], x[m][n]);
                 load_w(c - 2, m, cur);
                 __builtin_amdgcn_sched_barrier(0);  // loads between the products, not in one burst
             }

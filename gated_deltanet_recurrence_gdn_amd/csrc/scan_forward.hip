@@ -59,8 +59,8 @@ struct PrepLds {
 // in accumulators, which are the right operand of the next product as they are
 // (Y_mc = T_mm (N_mc - sum_n (N beta)_mn Y_nc), T_mm the inverse of the diagonal
 // tile), so the forward substitution over the four tile rows has no exchange.
-// 4096 tokens of 16 / 48 heads, d 128, bf16: 89 us, 370 MB at 4.2 TB/s, 300 of them
-// written (W's parts, E0, Y): bound by those writes, then by its dependent phases.
+// 4096 tokens of 16 / 48 heads, d 128, bf16: 86 us, 320 MB at 3.7 TB/s, 250 of them
+// written (W, E0, Y): bound by those writes, then by its dependent phases.
 template <int DK, int TK>
 __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
     using L = PrepLds<DK, TK>;
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
     // W^T = (2^b K)^T - K^T (Y beta 2^b)^T: wave m the tokens of tile m, a lane its
     // piece of the state kernel's row operand
     {
-        uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + wave * KS * 3 * 512 + lane * 8;
+        float* w = a.W + uh * (kScanChunk * DK) + wave * KS * 512 + lane * 8;
         const int i = 16 * wave + col;
         bf16x8 yf[2][3];
 #pragma unroll
@@ -218,7 +218,8 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
                         x[q] = mma_parts<TK, 3>(f, yf[kk], x[q]);
                     }
             const uint16_t* kr = Kp + i * LDK + 32 * n + 4 * g;
-            store_operand<3>(w + n * 3 * 512, eb[i] * read_whole<TK>(kr, L::kPlK) - x[0], eb[i] * read_whole<TK>(kr + 16, L::kPlK) - x[1]);
+            st4(w + n * 512, eb[i] * read_whole<TK>(kr, L::kPlK) - x[0]);
+            st4(w + n * 512 + 4, eb[i] * read_whole<TK>(kr + 16, L::kPlK) - x[1]);
         }
     }
 }
@@ -233,13 +234,14 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 // that take turns (nothing is copied between them), each part of a set loaded
 // for the chunk after next as soon as its last use is issued, without branches
 // (past the end, the last chunk's again) and used as loaded, so that no step
-// waits for its own loads or for its stores.  4096 tokens of 48 heads: 183 us, 2.9
-// a chunk (192 workgroups read 80 KB each a chunk, mostly from the L2s); packed
-// sequences of as many tokens: 140 us, 612 MB at 4.4 TB/s; 6 heads of one sequence,
-// one tile each: 1.1 us a chunk, 0.82 of it with all operands in the cache.
+// waits for its own loads or for its stores.  4096 tokens of 48 heads: 170 us, 2.7
+// a chunk (192 workgroups read 56 KB each a chunk, mostly from the L2s); packed
+// sequences of as many tokens: 127 us, 558 MB at 4.4 TB/s; 6 heads of one sequence,
+// one tile each: 1.1 us a chunk, 0.8 of it with all operands in the cache.
 template <int DK, int NS, int TK>
 struct StateOperands {
-    bf16x8 w[DK / 32][3], kt[2][2][TK];  // W of this wave's token tiles, K^T of its key tiles
+    bf16x8 kt[2][2][TK];  // K^T of this wave's key tiles
+    f32x4 w[DK / 32][2];  // W of its token tiles
     f32x4 e[NS], be, er;
     float decay;
 };
@@ -316,9 +318,9 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
     }
     auto load_w = [&](int c, int m, Ops& o) {  // W of one token tile
         const size_t uh = (size_t)(u0 + (c < end ? c : end - 1)) * a.h_v + h;
-        const uint16_t* w = a.W + uh * (3 * kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 3 * 512 + lane * 8);
+        const float* w = a.W + uh * (kScanChunk * DK) + (unsigned)((m0 * KS + ks) * 512 + lane * 8);
 #pragma unroll
-        for (int t = 0; t < 3; ++t) o.w[m][t] = ld_bf8(w + (m * KS * 3 + t) * 512);
+        for (int t = 0; t < 2; ++t) o.w[m][t] = ld4(w + m * KS * 512 + 4 * t);
     };
     auto load_e = [&](int c, Ops& o) {  // what else the errors need
         const size_t uh = (size_t)(u0 + (c < end ? c : end - 1)) * a.h_v + h;
@@ -350,8 +352,10 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
             f32x4 x[KS][NS] = {};
 #pragma unroll
             for (int m = 0; m < KS; ++m) {
+                bf16x8 wf[3];
+                operand_of(cur.w[m][0], cur.w[m][1], wf);
 #pragma unroll
-                for (int n = 0; n < NS; ++n) x[m][n] = mma_parts<3, 3>(cur.w[m], f[n], x[m][n]);
+                for (int n = 0; n < NS; ++n) x[m][n] = mma_parts<3, 3>(wf, f[n], x[m][n]);
                 load_w(c + 2, m, cur);
                 __builtin_amdgcn_sched_barrier(0);  // loads between the products, not in one burst
             }

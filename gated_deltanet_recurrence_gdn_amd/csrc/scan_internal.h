@@ -59,7 +59,7 @@ struct ScanArgs {
     float* S;      // the state before the chunk, transposed, [value tile][key tile] accumulators
     float* A;      // per segment and value head: what becomes of a state (the identity) over it, as S
     // workspace
-    uint16_t* W;   // forward W, backward Wb, in three parts, per unit and value head: row operands [token tile][key step][part]
+    float* W;      // forward W, backward Wb, per unit and value head: row operands [token tile][key step], whole
     uint16_t* Kt;  // K and Q transposed, per unit and q/k head: row operands [key tile][token step][part]
     uint16_t* Qt;
     float* dR;  // gradients of the errors' system, as E (dR0 between the prepare and the state kernel)
@@ -85,8 +85,11 @@ struct ScanArgs {
 // instructions' registers, so that a wave's load or store is one contiguous
 // kilobyte: accumulators as [tile][lane][4] floats (lane l: rows 4 (l / 16) ..+3,
 // column l % 16 of the 16 x 16 tile), row operands as [tile][step][part][lane][8]
-// bf16 (lane l: row l % 16, columns 8 (l / 16) ..+7 of the 16 x 32 tile; W's
-// columns 4 (l / 16) ..+3 and 16 + 4 (l / 16) ..+3, as operand_of).
+// bf16 (lane l: row l % 16, columns 8 (l / 16) ..+7 of the 16 x 32 tile), W's as
+// [tile][step][lane][8] floats (columns 4 (l / 16) ..+3 and 16 + 4 (l / 16) ..+3, as
+// operand_of), which the walk cuts into parts itself: in three parts it would be half
+// as much again to write and read (4096 tokens of 48 heads: prepare 90 against 86
+// us, walk 187 against 170).
 
 // The sequences of a launch: first token, tokens, first chunk unit (one entry
 // more), first segment, and their order by length, longest first (the state
@@ -111,11 +114,12 @@ __device__ __forceinline__ void state_block(const ScanArgs& a, const ScanSeqs& s
 }
 
 // Value tiles of a state kernel's workgroup.  Two halve what the workgroups read
-// of the operands that do not depend on the value columns (80 KB a chunk), but
+// of the operands that do not depend on the value columns (48 KB a chunk), but
 // take half as many workgroups with longer steps: where one tile each would give
 // every CU a workgroup and more, two are faster (4096 tokens of 48 heads, 384
-// workgroups of one tile: 226 against 186 us; packed sequences 196 against 136),
-// below that one (16384 tokens of 6 heads, 48 workgroups: 278 against 417 us).
+// workgroups of one tile: 200 against 170 us; packed sequences 174 against 126,
+// backward 210 against 193), below that one (1099 packed tokens of 8 heads, 240
+// workgroups: 19 against 24 us).
 inline bool two_tiles(const ScanArgs& a) { return a.seg_len == kWhole && (int64_t)a.n_seq * a.h_v * (a.d_v / 16) > device_cus(); }
 
 // A walk of many chunks on few CUs is cut into segments.  Over a segment the state
@@ -205,16 +209,6 @@ __device__ __forceinline__ void operand_of(f32x4 x, f32x4 y, bf16x8 (&p)[3]) {
 }
 
 __device__ __forceinline__ bf16x8 ld_bf8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
-
-// Writes the T parts of eight neighbours as a lane's piece of a row operand.
-template <int T>
-__device__ __forceinline__ void store_operand(uint16_t* p, f32x4 x, f32x4 y) {
-    u32x2 w[3], v[3];
-    split4(x, w);
-    split4(y, v);
-#pragma unroll
-    for (int t = 0; t < T; ++t) *reinterpret_cast<u32x4*>(p + t * 512) = u32x4{w[t][0], w[t][1], v[t][0], v[t][1]};
-}
 
 // Writes the T parts of four neighbours, T arrays `plane` elements apart.
 template <int T>
