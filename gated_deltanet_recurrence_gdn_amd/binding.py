@@ -768,11 +768,12 @@ def _pool_table(pools, table, n_rows, released, table_out, status):
 
 
 def _workspace(need, device, stream):
-    """A workspace of this call's own, not handed out again before `stream` is done with it."""
-    workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    if stream is not None:
-        workspace.record_stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
-    return workspace
+    """A workspace of this call's own out of the memory of the stream it launches on: whatever had the block before,
+    or has it next, is ordered on that stream.  (A block of the current stream's may still be in use there.)"""
+    if stream is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
 
 def gdn_pool_fork(pools, table, parent, child, *, released=None, table_out=None, n_rows=None, workspace=None,
