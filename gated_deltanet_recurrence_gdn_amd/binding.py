@@ -473,6 +473,15 @@ def gdn_prefill_workspace_bytes(q, v, state, out, scale: float = 1.0) -> int:
     return int(lib().gdn_prefill_workspace_bytes(ctypes.byref(sh)))
 
 
+def _workspace(need, device, stream):
+    """A workspace of this call's own out of the memory of the stream it launches on: whatever had the block before,
+    or has it next, is ordered on that stream.  (A block of the current stream's may still be in use there.)"""
+    if stream is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+
 def _bytes_of(t) -> int:
     return t.numel() * t.element_size()
 
@@ -487,7 +496,7 @@ def gdn_prefill_chunked(q, k, v, alpha, beta, state, out, *, state_slot=None, st
     sh = _prefill_shape(q, k, v, alpha, beta, state, state_slot, out, status, scale)
     if workspace is None:
         need = int(lib().gdn_prefill_workspace_bytes(ctypes.byref(sh)))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     args = (ctypes.byref(sh), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(alpha, "alpha"),
             _dev_ptr(beta, "beta"), _dev_ptr(state, "state"), _dev_ptr(state_slot, "state_slot"),
             _dev_ptr(out, "out"), _dev_ptr(workspace, "workspace"), ctypes.c_size_t(_bytes_of(workspace)),
@@ -569,7 +578,7 @@ def gdn_prefill_varlen(cu_seqlens, q, k, v, alpha, beta, state, out, *, chunk_st
             raise ValueError(f"chunk_states holds {chunk_states.shape[0]} states; the call emits {need}")
     if workspace is None:
         need = int(lib().gdn_prefill_varlen_workspace_bytes(ctypes.byref(sh), cu.ctypes.data))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     args = (ctypes.byref(sh), _vp(cu.ctypes.data), _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
             _dev_ptr(alpha, "alpha"), _dev_ptr(beta, "beta"), _dev_ptr(state, "state"),
             _dev_ptr(state_slot, "state_slot"), _dev_ptr(out, "out"), _dev_ptr(chunk_states, "chunk_states"),
@@ -765,15 +774,6 @@ def _pool_table(pools, table, n_rows, released, table_out, status):
     if m > GDN_POOL_MAX_SEQS:
         raise ValueError(f"table holds {m} sequences, at most {GDN_POOL_MAX_SEQS}")
     return structs, keep, m, n_rel, n_rows, table if table_out is None else table_out
-
-
-def _workspace(need, device, stream):
-    """A workspace of this call's own out of the memory of the stream it launches on: whatever had the block before,
-    or has it next, is ordered on that stream.  (A block of the current stream's may still be in use there.)"""
-    if stream is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
 
 def gdn_pool_fork(pools, table, parent, child, *, released=None, table_out=None, n_rows=None, workspace=None,

@@ -61,6 +61,13 @@ def call(name, device, **kw):
     out = torch.zeros_like(x[2])
     ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=device)  # noqa: E731
     pool = torch.zeros(2, 4, 8, device=device)
+    if name.startswith("prefill"):
+        state = torch.zeros(2, 4, 32, 32, device=device)
+        v = torch.zeros(6, 4, 32, device=device)
+        if name == "prefill_varlen":
+            return gb.gdn_prefill_varlen(CU, x[0], x[1], v, x[3], x[4], state, torch.zeros_like(v), **kw)
+        b = [t.view(2, 3, *t.shape[1:]) for t in (x[0], x[1], v, x[3], x[4])]
+        return gb.gdn_prefill_chunked(*b, state, torch.zeros_like(b[2]), **kw)
     if name == "scan_forward":
         return gb.gdn_scan_forward(CU, *x, out, **kw)
     if name == "scan_backward":
@@ -71,7 +78,7 @@ def call(name, device, **kw):
     return gb.gdn_pool_compact(pool, ints(2, -1), **kw)
 
 
-@pytest.mark.parametrize("name", ["scan_forward", "scan_backward"])
+@pytest.mark.parametrize("name", ["scan_forward", "scan_backward", "prefill_chunked", "prefill_varlen"])
 def test_entry_points_on_the_host(name, allocations):
     s = Stream()
     with pytest.raises(TypeError, match="device tensor"):
@@ -89,7 +96,8 @@ def segment_stream(t):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("handle", [False, True])
-@pytest.mark.parametrize("name", ["scan_forward", "scan_backward", "pool_fork", "pool_compact"])
+@pytest.mark.parametrize("name", ["scan_forward", "scan_backward", "pool_fork", "pool_compact",
+                                  "prefill_chunked", "prefill_varlen"])
 def test_entry_points_on_the_gpu(name, handle):
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
