@@ -650,8 +650,8 @@ def gdn_scan_forward(cu_seqlens, q, k, v, alpha, beta, out, *, tape=None, state=
             _dev_ptr(tape, "tape"), ctypes.c_size_t(0 if tape is None else _bytes_of(tape)),
             _dev_ptr(workspace, "workspace"), ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"),
             _stream(stream))
-    _on_current_device("gdn_scan_forward", q, k, v, alpha, beta, out, tape, state, state_slot, final_state, workspace,
-                       status)
+    _on_current_device("gdn_scan_forward", stream, q, k, v, alpha, beta, out, tape, state, state_slot, final_state,
+                       workspace, status)
     return _invoke("gdn_scan_forward", args, (sh, cu, q, k, v, alpha, beta, state, state_slot, out, final_state, tape,
                                               workspace, status), prepare)
 
@@ -679,8 +679,8 @@ def gdn_scan_backward(cu_seqlens, q, k, v, alpha, beta, tape, dout, dq, dk, dv, 
             _dev_ptr(dq, "dq"), _dev_ptr(dk, "dk"), _dev_ptr(dv, "dv"), _dev_ptr(dalpha, "dalpha"),
             _dev_ptr(dbeta, "dbeta"), _dev_ptr(dstate, "dstate"), _dev_ptr(workspace, "workspace"),
             ctypes.c_size_t(_bytes_of(workspace)), _stream(stream))
-    _on_current_device("gdn_scan_backward", q, k, v, alpha, beta, tape, dout, dq, dk, dv, dalpha, dbeta, dfinal, dstate,
-                       workspace)
+    _on_current_device("gdn_scan_backward", stream, q, k, v, alpha, beta, tape, dout, dq, dk, dv, dalpha, dbeta, dfinal,
+                       dstate, workspace)
     return _invoke("gdn_scan_backward", args, (sh, cu, q, k, v, alpha, beta, tape, dout, dfinal, dq, dk, dv, dalpha,
                                                dbeta, dstate, workspace), prepare)
 
@@ -726,9 +726,12 @@ def _int_array(t, name):
     return t.numel()
 
 
-def _on_current_device(name, *tensors):
-    """Every one of these device tensors is on the current device, where the call launches."""
+def _on_current_device(name, stream, *tensors):
+    """The stream and every one of these device tensors are on the current device, where the call launches."""
     device = torch.cuda.current_device()
+    on = getattr(stream, "device_index", device)  # a handle (int) does not say
+    if on != device:
+        raise ValueError(f"{name}: the stream is on cuda:{on}, the current device is cuda:{device}")
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{device}")
@@ -757,7 +760,7 @@ def gdn_pool_copy(pools, src_rows, dst_rows, *, src_pools=None, status=None, str
     _pool_ptrs(keep_src, "src_pools")
     args = (dst, src if src is not None else _vp(None), _i32(len(keep)), _dev_ptr(src_rows, "src_rows"),
             _dev_ptr(dst_rows, "dst_rows"), _i32(n), _dev_ptr(status, "status"), _stream(stream))
-    _on_current_device("gdn_pool_copy", *keep, *keep_src, src_rows, dst_rows, status)
+    _on_current_device("gdn_pool_copy", stream, *keep, *keep_src, src_rows, dst_rows, status)
     return _invoke("gdn_pool_copy", args, (keep, keep_src, src_rows, dst_rows, status), prepare)
 
 
@@ -794,7 +797,7 @@ def gdn_pool_fork(pools, table, parent, child, *, released=None, table_out=None,
             _i32(n_rel), _dev_ptr(parent, "parent"), _dev_ptr(child, "child"), _i32(n), _dev_ptr(table_out, "table_out"),
             _dev_ptr(workspace, "workspace"), ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"),
             _stream(stream))
-    _on_current_device("gdn_pool_fork", *keep, table, table_out, released, parent, child, workspace, status)
+    _on_current_device("gdn_pool_fork", stream, *keep, table, table_out, released, parent, child, workspace, status)
     return _invoke("gdn_pool_fork", args, (keep, table, released, parent, child, table_out, workspace, status), prepare)
 
 
@@ -810,5 +813,5 @@ def gdn_pool_compact(pools, table, *, released=None, table_out=None, count=None,
     args = (structs, _i32(len(keep)), _dev_ptr(table, "table"), _i32(m), _i32(n_rows), _dev_ptr(released, "released"),
             _i32(n_rel), _dev_ptr(table_out, "table_out"), _dev_ptr(count, "count"), _dev_ptr(workspace, "workspace"),
             ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"), _stream(stream))
-    _on_current_device("gdn_pool_compact", *keep, table, table_out, released, count, workspace, status)
+    _on_current_device("gdn_pool_compact", stream, *keep, table, table_out, released, count, workspace, status)
     return _invoke("gdn_pool_compact", args, (keep, table, released, table_out, count, workspace, status), prepare)

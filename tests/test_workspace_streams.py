@@ -108,3 +108,13 @@ def test_entry_points_on_the_gpu(name, handle):
     side.wait_stream(torch.cuda.current_stream())  # the inputs were made on the current stream
     prepared()
     torch.cuda.synchronize()
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    other = Stream()
+    other.device_index = 1
+    with pytest.raises(ValueError, match="the stream is on cuda:1, the current device is cuda:0"):
+        gb._on_current_device("gdn_scan_forward", other)
+    for s in (None, 0x1230, Stream()):
+        gb._on_current_device("gdn_scan_forward", s, None)
