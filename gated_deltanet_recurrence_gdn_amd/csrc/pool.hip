@@ -286,8 +286,22 @@ const unsigned char* pool_end(const gdn_pool& p) {
     return static_cast<const unsigned char*>(p.data) + (int64_t)(p.n_layers - 1) * p.layer_bytes + (int64_t)p.n_slots * p.row_bytes;
 }
 
-bool overlap(const gdn_pool& a, const gdn_pool& b) {
-    return a.n_layers > 0 && b.n_layers > 0 && a.data < pool_end(b) && b.data < pool_end(a);
+// Whether two pools share a byte.  A layer's rows are one range, and a pool's layers
+// may lie between another's: for each layer of the pool with fewer of them, only the
+// other's last layer that starts before its end can reach into it.
+bool overlap(const gdn_pool& x, const gdn_pool& y) {
+    if (x.n_layers == 0 || y.n_layers == 0 || x.data >= pool_end(y) || y.data >= pool_end(x)) return false;
+    const gdn_pool &a = x.n_layers <= y.n_layers ? x : y, &b = x.n_layers <= y.n_layers ? y : x;
+    const int64_t size = a.n_slots * a.row_bytes, b_size = b.n_slots * b.row_bytes;
+    // a's layer from b's first byte
+    int64_t at = static_cast<const unsigned char*>(a.data) - static_cast<const unsigned char*>(b.data);
+    for (int32_t l = 0; l < a.n_layers; ++l, at += a.layer_bytes) {
+        if (at + size <= 0) continue;
+        int64_t m = b.n_layers > 1 ? (at + size - 1) / b.layer_bytes : 0;
+        if (m >= b.n_layers) m = b.n_layers - 1;
+        if (m * b.layer_bytes + b_size > at) return true;
+    }
+    return false;
 }
 
 int check_pools(const gdn_pool* pools, int32_t n_pools) {

@@ -287,8 +287,9 @@ int gdn_commit_index(const int32_t* accepted_node, int32_t* state_slot, int32_t 
  *
  * A gdn_pool is one array of rows for several layers: row r of layer l starts
  * at data + l layer_bytes + r row_bytes.  The pools of one call have the same
- * n_slots, do not overlap, and row r means row r of every layer of each of
- * them.  Rows hold anything (bytes are moved).
+ * n_slots, share no byte (the layers of one may lie between another's), and row
+ * r means row r of every layer of each of them.  Rows hold anything (bytes are
+ * moved).
  */
 typedef struct gdn_pool {
     void* data;          /* 16-byte aligned (not read where n_layers is 0) */
@@ -302,8 +303,8 @@ typedef struct gdn_pool {
  * Copy rows: row dst_row[i] of every dst pool <- row src_row[i] of the src pool
  * of the same place, for i < n (restoring a cached prefix into a sequence's
  * row, keeping a row as a checkpoint).  src NULL copies within dst; otherwise
- * src[p] has dst[p]'s row_bytes and n_layers, rows of its own number, and does
- * not overlap any dst pool.  src_row and dst_row are DEVICE arrays [n].  A
+ * src[p] has dst[p]'s row_bytes and n_layers, rows of its own number, and shares
+ * no byte with any dst pool.  src_row and dst_row are DEVICE arrays [n].  A
  * source row of -1 zero-fills the destination row (a fresh sequence); a pair
  * whose destination row is -1 is passed over.  One source may be named by any
  * number of pairs.  A pair with a row outside the pools, and every pair whose
