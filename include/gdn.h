@@ -484,8 +484,11 @@ int gdn_prefill_varlen(const gdn_shape* shape, const int32_t* cu_seqlens, const 
 /*
  * The training scan: the recurrence over packed sequences at fp32 accuracy,
  * with its gradients.  gdn_prefill_varlen evaluates the same rule for serving,
- * with f16 matrix operands; here every product is fp32 (over the whole fp32
- * range), so the gradients, those of the gates included, are accurate to fp32.
+ * with f16 matrix operands; here every product has fp32's accuracy (sums are
+ * rounded to fp32, what is left out of a product is below 2^-23 of it and of
+ * either sign), so the gradients, those of the gates included, are accurate to
+ * fp32.  That holds for magnitudes from 2^-109 to 3.39e38: of smaller values what
+ * lies below 2^-126 is lost, and 2^128 - 2^119 and above count as infinite.
  *
  * cu_seqlens is a HOST array [batch + 1] as for gdn_prefill_varlen (batch
  * equal sequences [B][T] are the offsets 0, T, 2 T, ...), and q, k [total]
