@@ -17,7 +17,9 @@
 // the gradient of log alpha_t is the sum of every term whose decay spans t,
 //     sum_{i >= t > j} M_ij + sum_{i >= t} y_i + sum_{j < t} z_j + 2^(b_63) <G, S0>.
 // It is summed in that form, with nothing subtracted: all terms carry the factor
-// alpha_t, so the quotient by alpha_t keeps its accuracy however small it is.
+// alpha_t, so the quotient by alpha_t keeps its accuracy.  Where alpha_t is so small
+// that they could leave the fp32 range, or 0, they are formed with it lifted into
+// [1, 2), and such a gate is its lifted value in the quotient.
 #include "scan_internal.h"
 
 namespace gdn {
@@ -30,7 +32,7 @@ struct BackPrepLds {
     static constexpr int kLdK = DK + 16, kPlK = kScanChunk * kLdK, kPlZ = rows_t(kScanChunk);  // in bf16
     static constexpr int K = 0, Q = TK * kPlK * 2, Z = Q;  // Z takes Q's place
     static constexpr int kGates = Q + (TK * kPlK > 3 * kPlZ ? TK * kPlK : 3 * kPlZ) * 2;
-    static constexpr int kBytes = kGates + kGateRows * kScanChunk * 4;
+    static constexpr int kBytes = kGates + kDecayRows * kScanChunk * 4;
 };
 
 // Wave c owns the tokens i of tile c as columns: P^T's tiles (rows j) stay in
@@ -57,7 +59,7 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
     const size_t o_at = ((size_t)tok * a.h_v + h) * a.d_v + col, o_row = (size_t)a.h_v * a.d_v;
     RawColumn raw;
     load_column(a.dout, o_at + (16 * wave < a.d_v ? 16 * wave : 0), o_row, len, a.out_dtype, raw);
-    for (int i = tid; i < kGateRows * kScanChunk; i += kBackThreads) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
+    for (int i = tid; i < kDecayRows * kScanChunk; i += kBackThreads) gt[i] = a.gates[uh * (kGateRows * kScanChunk) + i];
     stage_parts<TK, DK, LDK, kBackThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     stage_parts<TK, DK, LDK, kBackThreads>(a.q, tok, len, a.h_qk, hq, Qp);
     const float* Y = a.Y + uh * (kScanChunk * kScanChunk) + lane * 4;  // tile (m, n) at (4 m + n) 256
@@ -427,6 +429,19 @@ __device__ __forceinline__ void row_sums(f32x4& x, f32x4& y) {
     }
 }
 
+// Gates as scan_prepare leaves them -> their decays with the gates below kMinAlpha
+// lifted, 0 where one has none of them or more than one in its span.  Lane i of one
+// wave forms token i's.
+__device__ __forceinline__ void lift_gates(float* gt) {
+    const int i = threadIdx.x & 63, v = __builtin_bit_cast(int, gt[384 + i]), last = __builtin_bit_cast(int, gt[384 + 63]);
+    constexpr int kPowers = (1 << kLiftBits) - 1;
+    const float b = gt[i] + (float)(v & kPowers), bl = gt[64 + i];
+    const float b63 = gt[63] + (float)(last & kPowers), bl63 = gt[64 + 63];
+    gt[i] = b;
+    gt[256 + i] = v >> kLiftBits == 1 ? __builtin_amdgcn_exp2f(b + bl) : 0.f;
+    gt[320 + i] = (last >> kLiftBits) - (v >> kLiftBits) == 1 ? decay_between(b63, bl63, b, bl) : 0.f;
+}
+
 // Sum over 64 lanes.
 __device__ __forceinline__ float wave_sum(float x) {
     x = group_sum<16>(x);
@@ -569,18 +584,26 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             qk_[q] = mma_parts<TK, TK>(y, x, qk_[q]);
         }
     }
-    for (int hh = 0; hh < a.group; ++hh) {
+    // A head with gates below kMinAlpha in this chunk takes a second turn, `lifted`, for
+    // their gradients alone: by the terms whose decay spans one of them, that one lifted.
+    for (int hh = 0, turn = 0, lifted = 0, next; hh < a.group; hh = next, ++turn) {
         // the lane's numbers are made opaque: hundreds of LDS addresses would otherwise be formed before the loop and kept
         asm volatile("" : "+v"(lane), "+v"(col), "+v"(g));
         const int h = hq * a.group + hh;
         f32x4 os[MW] = {}, rs[MW] = {}, eg[MW] = {}, dp[2] = {}, da[2] = {};
         float gs = 0.f;
-        float* gt = gates + (hh & 1) * (kGateRows * kScanChunk);  // the last head's are still being read
-        if (hh == 0) __syncthreads();                            // K and Q have been read
+        float* gt = gates + (turn & 1) * (kGateRows * kScanChunk);  // the last turn's are still being read
+        if (turn == 0) __syncthreads();                            // K and Q have been read
         if (tid < kGateRows * kScanChunk) gt[tid] = gate;
         stage_r(hh, 0, 0);
         if (32 < a.d_v) load_r(hh, 32);
         __syncthreads();
+        if (lifted) {
+            if (tid < kScanChunk) lift_gates(gt);
+            __syncthreads();
+        }
+        const bool again = !lifted && __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, gt[384 + 63])) != 0;
+        next = again ? hh : hh + 1;
         for (int c0 = 0, buffer = 0; c0 < a.d_v; c0 += 32, buffer ^= 1) {
             const uint16_t* Rp = reinterpret_cast<const uint16_t*>(lds + L::R + buffer * L::kBuffer);
             const uint16_t *Ep = Rp + L::E / 2, *Op = Rp + L::O / 2;
@@ -594,9 +617,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             }
             if (c0 + 32 < a.d_v) stage_r(hh, c0 + 32, buffer ^ 1);
             if (c0 + 64 < a.d_v) load_r(hh, c0 + 64);
-            else if (c0 + 32 >= a.d_v && hh + 1 < a.group) {
-                load_r(hh + 1, 0);
-                load_g(hh + 1);
+            else if (c0 + 32 >= a.d_v && next < a.group) {
+                load_r(next, 0);
+                load_g(next);
             }
             if (c0 + 16 >= a.d_v) sn[1] = gn[1] = f32x4{};
             bf16x8 sb[3], gb[3];
@@ -610,7 +633,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
 #pragma unroll
             for (int q = 0; q < 2; ++q) store_parts<3>(Sp + (16 * q + col) * kLdS + (16 * q + col) / 8 * L::kSk + 4 * g, L::kPlS, gn[q]);
             if (c0 + 32 < a.d_v) load_s(hh, c0 + 32);
-            else if (hh + 1 < a.group) load_s(hh + 1, 0);
+            else if (next < a.group) load_s(next, 0);
 #pragma unroll
             for (int m = 0; m < MW; ++m) {
                 __builtin_amdgcn_sched_barrier(0);  // one row tile's operands at a time
@@ -678,7 +701,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             const f32x4 bh = ld4(gt + i), bl = ld4(gt + 64 + i), bi = ld4(be + i);
             const float bhj = gt[j], blj = gt[64 + j], bj = be[j];
             f32x4 xs = {}, ps = {}, mm;
-            if (hh > 0)
+            if (turn > 0)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     xs[r] = Xl[(i + r) * LDY + j];
@@ -693,10 +716,20 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
                 mm[r] = j < i + r ? x * kk_[q][r] + p * qk_[q][r] : 0.f;
                 if (j == i + r) rb[j] = da[q][r];  // dbeta_i = dR_i . E_i
             }
+            if (lifted) {  // the spans of one lifted gate only
+                const f32x4 li = ld4(gt + 384 + i);
+                const int lj = __builtin_bit_cast(int, gt[384 + j]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                Xl[(i + r) * LDY + j] = xs[r];
-                Ps[(i + r) * LDY + j] = ps[r];
+                for (int r = 0; r < 4; ++r) {
+                    const float l = li[r];
+                    mm[r] = (__builtin_bit_cast(int, l) - lj) >> kLiftBits == 1 ? mm[r] : 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    Xl[(i + r) * LDY + j] = xs[r];
+                    Ps[(i + r) * LDY + j] = ps[r];
+                }
             }
             f32x4 f = mma16(triangle, mm, f32x4{}), e = mma16(f32x4{1.f, 1.f, 1.f, 1.f}, mm, f32x4{});
             const float total = group_sum<16>(e[0]);
@@ -718,8 +751,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             const int i = 16 * (m0 + m) + 4 * g;
             const f32x4 ebi = ld4(eb + i), bi = ld4(be + i), eri = ld4(er + i);
             const f32x4 o = a.scale * ebi * os[m], x = bi * ebi * rs[m], e = eri * bi * eg[m];
-            accq[m] += o;
-            acck[m] += e - x;
+            accq[m] += lifted ? f32x4{} : o;
+            acck[m] += lifted ? f32x4{} : e - x;
             f32x4 y, z;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -763,12 +796,14 @@ __global__ __launch_bounds__(kGradThreads, 2) void scan_grad_kernel(const ScanAr
             }
             z = __shfl_up(z, 1);  // over j < t
             if (lane == 0) z = 0.f;
-            if (lane < len) {
+            const int l = __builtin_bit_cast(int, gt[384 + lane]), before = __builtin_bit_cast(int, gt[384 + (lane > 0 ? lane - 1 : 0)]);
+            if (lane < len && (!lifted || l != (lane > 0 ? before : 0))) {
                 const size_t at = (size_t)(tok + lane) * a.h_v + h;
                 a.dalpha[at] = (f + y + z + eb[63] * gsum) / al[lane];
                 a.dbeta[at] = rb[lane];
             }
         }
+        lifted = again;
     }
 
     // dQ += Ps K, dK += (Xs + Xs^T) K + Ps^T Q: Xs made symmetric, Ps' upper tiles cleared

@@ -88,10 +88,22 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
             al = a.alpha[(size_t)(tok + lane) * a.h_v + h];
             bt = a.beta[(size_t)(tok + lane) * a.h_v + h];
         }
-        al = al < kMinAlpha ? kMinAlpha : al;
+        const bool zero = al <= 0.f, small = al < kMinAlpha;
         // the sums run over up to 64 logarithms and differences of them are
         // taken: in 64 bits, kept as two floats
-        double s = log2((double)al);
+        double s = zero ? (double)-kLogZero : log2((double)al);
+        int lift = 0;
+        if (__any(small)) {
+            if (small) {
+                lift = (1 << kLiftBits) + (zero ? kLogZero : 1 - __builtin_amdgcn_frexp_expf(al));
+                al = zero ? 1.f : 2 * __builtin_amdgcn_frexp_mantf(al);
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int y = __shfl_up(lift, o);
+                if (lane >= o) lift += y;
+            }
+        }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const double y = __shfl_up(s, o);
@@ -111,6 +123,7 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
         gt[192] = al;
         gt[256] = e;
         gt[320] = er;
+        gt[384] = __builtin_bit_cast(float, lift);
     }
     __syncthreads();
 
@@ -459,7 +472,7 @@ struct OutLds {
     static constexpr int kLdK = DK + 8, kPlK = kScanChunk * kLdK, kLdP = kScanChunk + 8, kPlP = kScanChunk * kLdP;  // in bf16
     static constexpr int Q = 0, K = TK * kPlK * 2, P = K;
     static constexpr int kGates = K + (TK * kPlK > 3 * kPlP ? TK * kPlK : 3 * kPlP) * 2;
-    static constexpr int kBytes = kGates + kGateRows * kScanChunk * 4;
+    static constexpr int kBytes = kGates + kDecayRows * kScanChunk * 4;
 };
 
 template <int DK, int TK>
@@ -487,7 +500,7 @@ __global__ __launch_bounds__(kOutThreads, 4) void scan_output_kernel(const ScanA
         for (int kk = 0; kk < 4; ++kk) ee[kk] = ld4(e + 16 * kk * a.d_v);
     };
     load(c0 < a.d_v ? c0 : 0);
-    if (tid < kGateRows * kScanChunk) gt[tid] = a.gates[uh * (kGateRows * kScanChunk) + tid];
+    if (tid < kDecayRows * kScanChunk) gt[tid] = a.gates[uh * (kGateRows * kScanChunk) + tid];
     stage_parts<TK, DK, LDK, kOutThreads>(a.q, tok, len, a.h_qk, hq, Qp);
     stage_parts<TK, DK, LDK, kOutThreads>(a.k, tok, len, a.h_qk, hq, Kp);
     __syncthreads();

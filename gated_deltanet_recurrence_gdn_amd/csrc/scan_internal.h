@@ -34,11 +34,18 @@ constexpr int kScanLdY = kScanChunk + 4;  // rows of 64 floats in LDS: 4 rows ap
 constexpr int kLdT = kScanChunk + 16, kSkew = 64;
 __device__ __forceinline__ int row_t(int i) { return i * kLdT + i / 8 * kSkew; }
 constexpr int rows_t(int n) { return n * kLdT + n / 8 * kSkew; }
-constexpr int kGateRows = 6;              // b (high, low part), beta, alpha, 2^b, 2^(b_63 - b)
-// alpha below this counts as this: its powers stay in the fp32 range, and a
-// state carried over with a factor of 2^-60 is below fp32's resolution of
-// anything added to it
+// b (high, low part), beta, alpha, 2^b, 2^(b_63 - b); for the gates below kMinAlpha
+// their running count times 2^21 plus the running sum of the powers of two that bring
+// each into [1, 2) (as bits of an integer), where their row of alpha has them.
+// The first six are what kernels keep in LDS but for the gradient kernel.
+constexpr int kGateRows = 7, kDecayRows = 6;
+// A term of a gate's gradient carries the gate as a factor and is divided by it.  Below
+// this that product could leave the fp32 range, so the gradients of such gates are
+// formed from decays with the gate lifted into [1, 2).
 constexpr float kMinAlpha = 0x1p-60f;
+// A gate of 0 forgets the state: its log2 is taken as -2^14, which no other gates make
+// up for (63 of at most 2^128), so every decay over it is 0.
+constexpr int kLogZero = 1 << 14, kLiftBits = 21;
 
 struct ScanArgs {
     const void* q;

@@ -495,8 +495,9 @@ int gdn_prefill_varlen(const gdn_shape* shape, const int32_t* cu_seqlens, const 
  * [h_qk][d_k], v, out [total][h_v][d_v], alpha, beta [total][h_v] are packed
  * alike (total = shape.n_nodes).  q, k, v are F32 or BF16, out F32, F16 or
  * BF16; d_k is 32, 64 or 128, d_v a multiple of 16 up to 256.  alpha is at
- * least 0; below 2^-60 it counts as 2^-60 (a state carried over with that
- * factor leaves no trace in fp32).
+ * least 0; a gate of 0 forgets the state before it, of any finite size, and has
+ * its gradient all the same.  (In the gradient of a gate below 2^-60, another one
+ * below 2^-60 in its chunk counts as 0.)
  *
  * gdn_scan_forward starts sequence b from state[slot(b)] (only read), or from
  * zeros where `state` is NULL, and writes `out` and the fp32 state after the
