@@ -522,10 +522,11 @@ int gdn_prefill_varlen(const gdn_shape* shape, const int32_t* cu_seqlens, const 
  * repeat bit for bit.
  *
  * Apart from final_state = state, and dstate = dfinal, no output overlaps an
- * input or another output.  A NaN or an infinity in q, k, v, alpha, beta, dout
- * or a state makes NaN of what follows it in its sequence and heads, and may do
- * so from the start of its 64-token chunk (forward) or from the end of it
- * (backward); other sequences and heads do not see it.
+ * input or another output.  A NaN or an infinity in q, k, v, alpha, beta, dout,
+ * dfinal or a state leaves nothing finite of what the rule computes from it, and
+ * may reach other results of its sequence and heads: outputs from the start of
+ * its 64-token chunk on, gradients of the whole sequence (one in dout: up to the
+ * end of its chunk).  Other sequences and heads do not see it.
  *
  * tape, workspaces, out, dout, dv, dfinal and dstate are 16-byte aligned, the
  * other outputs 4-byte.  The workspaces' contents on entry are ignored; calls that
