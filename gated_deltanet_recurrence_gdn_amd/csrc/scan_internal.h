@@ -351,12 +351,6 @@ __device__ __forceinline__ void store4_typed(void* p, size_t i, f32x4 x, bool bf
     }
 }
 
-__device__ __forceinline__ float load_out(const void* p, size_t i, int dtype) {
-    if (dtype == GDN_F32) return static_cast<const float*>(p)[i];
-    if (dtype == GDN_F16) return (float)static_cast<const _Float16*>(p)[i];
-    return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-}
-
 __device__ __forceinline__ void store4_out(void* p, size_t i, f32x4 x, int dtype) {
     if (dtype != GDN_F16) {
         store4_typed(p, i, x, dtype == GDN_BF16);
@@ -364,16 +358,6 @@ __device__ __forceinline__ void store4_out(void* p, size_t i, f32x4 x, int dtype
         typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
         *reinterpret_cast<f16x4*>(static_cast<_Float16*>(p) + i) = f16x4{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3]};
     }
-}
-
-// Four neighbours; i is a multiple of 4 and p is 16-byte aligned.
-__device__ __forceinline__ f32x4 load4_out(const void* p, size_t i, int dtype) {
-    if (dtype == GDN_F32) return ld4(static_cast<const float*>(p) + i);
-    const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i);
-    if (dtype == GDN_BF16) return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
-    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-    const f16x4 x = __builtin_bit_cast(f16x4, w);
-    return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
 }
 
 // A lane's sixteen values of one column of a chunk, rows 16 m + 4 g + r, kept as
