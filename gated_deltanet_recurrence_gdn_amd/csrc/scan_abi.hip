@@ -157,7 +157,8 @@ int launch_all(const gdn_shape* sh, const int32_t* cu, ScanArgs* a, hipStream_t 
             longest = std::max(longest, n);
         }
         for (int i = 0; i < ns; ++i) seqs.order[i] = (uint8_t)i;
-        std::stable_sort(seqs.order, seqs.order + ns, [&](uint8_t x, uint8_t y) { return seqs.len[x] > seqs.len[y]; });
+        // in place, as the library allocates nothing; equal lengths in their own order
+        std::sort(seqs.order, seqs.order + ns, [&](uint8_t x, uint8_t y) { return seqs.len[x] != seqs.len[y] ? seqs.len[x] > seqs.len[y] : x < y; });
         a->n_seq = ns;
         a->n_seg = a->seg_len == kWhole ? 1 : (int32_t)segments_of(longest, a->seg_len);
         a->seq0 = s0;
