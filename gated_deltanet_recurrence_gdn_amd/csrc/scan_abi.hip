@@ -125,7 +125,7 @@ int check_inputs(const gdn_shape* sh, const void* q, const void* k, const void* 
 }
 
 int check_memory(const void* p, size_t have, size_t need) {
-    if (p == nullptr || have < need) return GDN_ERR_WORKSPACE;
+    if (have < need || (p == nullptr && need > 0)) return GDN_ERR_WORKSPACE;  // sequences without tokens need none
     return aligned(p, 16) ? GDN_OK : GDN_ERR_ALIGN;
 }
 
