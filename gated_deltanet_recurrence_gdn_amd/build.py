@@ -33,8 +33,11 @@ HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # matrix-core results in ordinary VGPRs (the kernels fit in 256): no
-    # accumulator-register copies around the vector ALU work between products
+    # matrix-core results in ordinary VGPRs: no accumulator-register copies around
+    # the vector ALU work between products.  The kernels fit in 256 but for the training
+    # scan's walks of two value tiles and those with fp32 inputs, where accumulator
+    # registers hold the rest (and scratch, for the gradient's with both: 67 registers at
+    # d_k = 128, 6 at 64), and its gradient kernel at d_k = 128 (20 to 26 in scratch)
     "-Xarch_device", "-mllvm=-amdgpu-mfma-vgpr-form",
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
     "-Wall", "-Wno-unused-function",

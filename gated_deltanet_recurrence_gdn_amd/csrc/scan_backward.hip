@@ -38,7 +38,7 @@ struct BackPrepLds {
 // Wave c owns the tokens i of tile c as columns: P^T's tiles (rows j) stay in
 // accumulators, the right operand of Z^T = P^T - (beta Y)^T P^T as they are, with
 // Y's tiles straight from memory as the left one.  Z's parts go through LDS once.
-// 4096 packed tokens of 16 / 48 heads, d 128, bf16: 133 us, 383 MB at 2.9 TB/s (242
+// 4096 packed tokens of 16 / 48 heads, d 128, bf16: 134 us, 383 MB at 2.9 TB/s (242
 // written: Wb, dR0), matrix cores 9% busy: its phases wait for one another.
 template <int DK, int TK>
 __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
@@ -184,8 +184,8 @@ __global__ __launch_bounds__(kBackThreads) void scan_back_prepare_kernel(const S
 // The gradient's walk, the mirror image of scan_state: G^T in accumulators, two
 // matrix operands (K and Q) and two exchanged right sides, the same two operand
 // sets that take turns.  OT: the type of dout, whose values stay as loaded until
-// they are used.  4096 packed tokens of 48 heads: 193 us, 614 MB at 3.2 TB/s; 6 heads
-// of one sequence, one tile each: 1.6 us a chunk.
+// they are used.  4096 packed tokens of 48 heads: 195 us, 614 MB at 3.1 TB/s; 6 heads
+// of one sequence, one tile each: 1.7 us a chunk.
 template <int DK, int NS, int TK, typename OT>
 struct BackOperands {
     bf16x8 kt[2][2][TK], qt[2][2][TK];
@@ -459,10 +459,10 @@ __device__ __forceinline__ float wave_sum(float x) {
 // dout serve all waves and are double-buffered: one barrier a step, and the
 // cutting of one wave runs beside another's products.  A wave also owns one or
 // two of the ten lower tiles of the 64 x 64 sums.  4096 packed tokens of 16 / 48
-// heads, d 128, bf16: 386 us, 985 MB at 2.6 TB/s, matrix cores 14% busy: one
+// heads, d 128, bf16: 398 us, 986 MB at 2.5 TB/s, matrix cores 14% busy: one
 // workgroup of 155 KB of LDS a CU, two waves a SIMD, bound by the cutting and the LDS reads
-// between its barriers (9000 vector and 1400 LDS instructions a wave), in five rounds
-// of 256 for 1056 workgroups.
+// between its barriers (9200 vector and 1440 LDS instructions a wave), in five rounds
+// of 256 for 1056 workgroups.  At d_k = 128 20 to 26 registers lie in scratch.
 constexpr int kGradThreads = 512;
 constexpr int kGradWaves = kGradThreads / 64;
 constexpr int kLdO = 32 + 8;  // rows of dout (32 value columns), read 16 bytes a lane

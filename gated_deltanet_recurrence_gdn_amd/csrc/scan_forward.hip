@@ -59,7 +59,7 @@ struct PrepLds {
 // in accumulators, which are the right operand of the next product as they are
 // (Y_mc = T_mm (N_mc - sum_n (N beta)_mn Y_nc), T_mm the inverse of the diagonal
 // tile), so the forward substitution over the four tile rows has no exchange.
-// 4096 tokens of 16 / 48 heads, d 128, bf16: 86 us, 320 MB at 3.7 TB/s, 250 of them
+// 4096 tokens of 16 / 48 heads, d 128, bf16: 87 us, 320 MB at 3.7 TB/s, 250 of them
 // written (W, E0, Y): bound by those writes, then by its dependent phases.
 template <int DK, int TK>
 __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanArgs a, const ScanSeqs seqs) {
@@ -249,8 +249,8 @@ __global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanAr
 // (past the end, the last chunk's again) and used as loaded, so that no step
 // waits for its own loads or for its stores.  4096 tokens of 48 heads: 170 us, 2.7
 // a chunk (192 workgroups read 56 KB each a chunk, mostly from the L2s); packed
-// sequences of as many tokens: 127 us, 558 MB at 4.4 TB/s; 6 heads of one sequence,
-// one tile each: 1.1 us a chunk, 0.8 of it with all operands in the cache.
+// sequences of as many tokens: 125 us, 559 MB at 4.5 TB/s; 6 heads of one sequence,
+// one tile each: 1.3 us a chunk.
 template <int DK, int NS, int TK>
 struct StateOperands {
     bf16x8 kt[2][2][TK];  // K^T of this wave's key tiles
@@ -464,7 +464,7 @@ __global__ __launch_bounds__(256, 1) void scan_state_kernel(const ScanArgs a, co
 // LDS, P's take K's place; a wave takes 16 value columns at a time, their rows of
 // S0 and columns of E straight from memory as they lie there (each is used by one
 // wave only), the first of them on their way before the staging starts.  4096 tokens
-// of 16 / 48 heads: 108 us for 390 MB (S0 and E, read once): 3.6 TB/s.
+// of 16 / 48 heads: 109 us for 390 MB (S0 and E, read once): 3.6 TB/s.
 constexpr int kOutThreads = 512;
 
 template <int DK, int TK>

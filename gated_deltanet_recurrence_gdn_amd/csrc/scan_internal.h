@@ -126,7 +126,10 @@ __device__ __forceinline__ void state_block(const ScanArgs& a, const ScanSeqs& s
 // every CU a workgroup and more, two are faster (4096 tokens of 48 heads, 384
 // workgroups of one tile: 200 against 170 us; packed sequences 174 against 126,
 // backward 210 against 193), below that one (1099 packed tokens of 8 heads, 240
-// workgroups: 19 against 24 us).
+// workgroups: 19 against 24 us).  These are bf16 inputs; with fp32 ones the backward
+// walk of two tiles spills at d_k = 128.  Sequences count alike whatever their length:
+// an empty one beside one of 4096 tokens of 24 heads turns one tile into two (forward
+// 180 -> 221 us, training step 521 -> 623).
 inline bool two_tiles(const ScanArgs& a) { return a.seg_len == kWhole && (int64_t)a.n_seq * a.h_v * (a.d_v / 16) > device_cus(); }
 
 // A walk of many chunks on few CUs is cut into segments.  Over a segment the state
@@ -135,8 +138,8 @@ inline bool two_tiles(const ScanArgs& a) { return a.seg_len == kWhole && (int64_
 // from zeros (B) and from the identity (A); pass 2 forms a segment's first state
 // from the ends before it, S <- S A + B from one segment to the next, and walks
 // it.  The gradient goes G -> G A^T + B' the other way, with the A of the forward
-// pass (they are on the tape).  16384 tokens of 6 heads, 6 segments: forward 162
-// us for both passes against 277 of one walk, backward 198 against 420.
+// pass (they are on the tape).  16384 tokens of 6 heads, 6 segments: forward 173
+// us for both passes against 336 of one walk, backward 197 against 441.
 
 // Parts of the inputs q, k: one in bf16, three in fp32.
 inline int input_parts(const ScanArgs& a) { return a.qkv_bf16 ? 1 : 3; }
