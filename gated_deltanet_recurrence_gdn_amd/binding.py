@@ -478,7 +478,9 @@ def _workspace(need, device, stream):
     or has it next, is ordered on that stream.  (A block of the current stream's may still be in use there.)"""
     if stream is None:
         return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+    if isinstance(stream, int):  # torch takes the handle 0 for none at all
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
         return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
 

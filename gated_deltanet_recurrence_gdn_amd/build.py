@@ -35,9 +35,10 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # matrix-core results in ordinary VGPRs: no accumulator-register copies around
     # the vector ALU work between products.  The kernels fit in 256 but for the training
-    # scan's walks of two value tiles and those with fp32 inputs, where accumulator
-    # registers hold the rest (and scratch, for the gradient's with both: 67 registers at
-    # d_k = 128, 6 at 64), and its gradient kernel at d_k = 128 (20 to 26 in scratch)
+    # scan's walks: the gradient's of two value tiles or with fp32 inputs, and the
+    # forward one of both, keep the rest in accumulator registers (the gradient's of both
+    # also 67 registers in scratch at d_k = 128, 6 at 64).  Its gradient kernel keeps 20
+    # to 26 in scratch at d_k = 128
     "-Xarch_device", "-mllvm=-amdgpu-mfma-vgpr-form",
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
     "-Wall", "-Wno-unused-function",

@@ -34,6 +34,7 @@ def allocations(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
     monkeypatch.setattr(torch, "empty", record)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
     return got
@@ -108,6 +109,19 @@ def test_entry_points_on_the_gpu(name, handle):
     side.wait_stream(torch.cuda.current_stream())  # the inputs were made on the current stream
     prepared()
     torch.cuda.synchronize()
+
+
+def test_the_handle_of_the_default_stream(allocations):
+    """torch takes a handle of 0 for no handle at all: an ExternalStream of it is some other stream."""
+    gb._workspace(7, torch.device("cpu"), 0)
+    assert allocations == [("default", 16)]
+
+
+@pytest.mark.gpu
+def test_the_handle_of_the_default_stream_on_the_gpu():
+    with torch.cuda.stream(torch.cuda.Stream()):
+        workspace = gb._workspace(7, torch.device("cuda:0"), 0)
+    assert segment_stream(workspace) == torch.cuda.default_stream().cuda_stream == 0
 
 
 def test_a_stream_of_another_device_is_refused(monkeypatch):
