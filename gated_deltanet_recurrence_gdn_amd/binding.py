@@ -25,7 +25,7 @@ _LIB_PATH = os.environ.get("GDN_LIBRARY") or os.path.join(os.path.dirname(os.pat
 _lib = None
 _raw_fns: dict = {}
 
-GDN_F32, GDN_BF16, GDN_F16 = 0, 1, 2
+GDN_F32, GDN_BF16, GDN_F16, GDN_E8M0 = 0, 1, 2, 3
 GDN_MAX_NODES = 32
 GDN_MAX_TREE_DEPTH = 16
 GDN_PREFILL_CHUNK = 64
@@ -34,6 +34,9 @@ GDN_MAX_POOLS = 8
 GDN_POOL_MAX_ROWS = 65536
 GDN_POOL_MAX_SEQS = 8192
 GDN_F16_MAX = 65504.0
+GDN_GROUP = 128
+GDN_MAX_PARTS = 8
+GDN_MAX_WIDTH = 16384
 GDN_PREFILL_SCRATCH_BYTES = 32 << 20
 
 STATUS = {
@@ -68,6 +71,30 @@ class GdnPool(ctypes.Structure):
                 ("n_layers", ctypes.c_int32), ("n_slots", ctypes.c_int32)]
 
 
+class GdnNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("width", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("scale_stride", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class GdnGatedNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("h_v", ctypes.c_int32), ("d_v", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("z_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("scale_stride", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class GdnProjectPart(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("columns", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class GdnProjectShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("a_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+                ("inner", ctypes.c_int32), ("a_scale_stride", ctypes.c_int32), ("w_scale_stride", ctypes.c_int32),
+                ("w_scale_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _SIGS = {
@@ -98,11 +125,22 @@ _SIGS = {
     "gdn_pool_fork": [_vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp],
     "gdn_pool_compact_workspace_bytes": [_i32],
     "gdn_pool_compact": [_vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp],
+    "gdn_pool_pack": [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp],
+    "gdn_pool_unpack": [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp],
+    "gdn_norm_forward": [ctypes.POINTER(GdnNormShape)] + [_vp] * 8,
+    "gdn_norm_backward_workspace_bytes": [ctypes.POINTER(GdnNormShape)],
+    "gdn_norm_backward": [ctypes.POINTER(GdnNormShape)] + [_vp] * 7 + [ctypes.c_size_t, _vp],
+    "gdn_gated_norm_forward": [ctypes.POINTER(GdnGatedNormShape)] + [_vp] * 7,
+    "gdn_gated_norm_backward_workspace_bytes": [ctypes.POINTER(GdnGatedNormShape)],
+    "gdn_gated_norm_backward": [ctypes.POINTER(GdnGatedNormShape)] + [_vp] * 8 + [ctypes.c_size_t, _vp],
+    "gdn_project": [ctypes.POINTER(GdnProjectShape)] + [_vp] * 5 + [_i32, _vp],
 }
 _RESTYPES = {"gdn_status_string": ctypes.c_char_p, "gdn_prefill_workspace_bytes": ctypes.c_size_t,
              "gdn_prefill_varlen_workspace_bytes": ctypes.c_size_t, "gdn_prefill_boundary_states": ctypes.c_int64,
              "gdn_scan_tape_bytes": ctypes.c_size_t, "gdn_scan_forward_workspace_bytes": ctypes.c_size_t,
              "gdn_scan_backward_workspace_bytes": ctypes.c_size_t,
+             "gdn_norm_backward_workspace_bytes": ctypes.c_size_t,
+             "gdn_gated_norm_backward_workspace_bytes": ctypes.c_size_t,
              "gdn_pool_fork_workspace_bytes": ctypes.c_size_t, "gdn_pool_compact_workspace_bytes": ctypes.c_size_t}
 
 
@@ -817,3 +855,229 @@ def gdn_pool_compact(pools, table, *, released=None, table_out=None, count=None,
             ctypes.c_size_t(_bytes_of(workspace)), _dev_ptr(status, "status"), _stream(stream))
     _on_current_device("gdn_pool_compact", stream, *keep, table, table_out, released, count, workspace, status)
     return _invoke("gdn_pool_compact", args, (keep, table, released, table_out, count, workspace, status), prepare)
+
+
+def _pack_pools(states, codes, scales):
+    L, _, H, dv, dk = _shape_of(states, "states", 5)
+    slots = _shape_of(codes, "codes", 5)[1]
+    _expect(codes, "codes", (L, slots, H, dv, dk), torch.int8)
+    _expect(scales, "scales", (L, slots, H, dv), torch.float32)
+    structs = [_pool_structs(t, n)[0] for t, n in ((states, "states"), (codes, "codes"), (scales, "scales"))]
+    return structs, dk, _dtype_code(states)
+
+
+def _pool_rows(name, pools, src_rows, dst_rows, status, stream):
+    n = _int_array(src_rows, "src_rows")
+    _expect(dst_rows, "dst_rows", (n,), torch.int32)
+    _check_status(status)
+    _pool_ptrs(pools, "states, codes and scales")
+    rows = (_dev_ptr(src_rows, "src_rows"), _dev_ptr(dst_rows, "dst_rows"), _i32(n), _dev_ptr(status, "status"), _stream(stream))
+    _on_current_device(name, stream, *pools, src_rows, dst_rows, status)
+    return rows
+
+
+def gdn_pool_pack(states, codes, scales, src_rows, dst_rows, *, status=None, stream=None, prepare: bool = False):
+    """Write state rows src_rows[i] (``states`` [layers][slots][h_v][d_v][d_k], fp32, f16 or bf16) in 8 bits to rows
+    dst_rows[i] of ``codes`` (int8, the same but for its slots) and ``scales`` (fp32 [layers][slots][h_v][d_v]); see
+    include/gdn.h.  Persisted node states [B][N][h_v][d_v][d_k] are a pool of one layer: ``persist.flatten(0, 1)[None]``."""
+    (st, co, sc), dk, dtype = _pack_pools(states, codes, scales)
+    rows = _pool_rows("gdn_pool_pack", (states, codes, scales), src_rows, dst_rows, status, stream)
+    return _invoke("gdn_pool_pack", (st, co, sc, _i32(dk), _i32(dtype), *rows),
+                   (states, codes, scales, src_rows, dst_rows, status), prepare)
+
+
+def gdn_pool_unpack(codes, scales, states, src_rows, dst_rows, *, status=None, stream=None, prepare: bool = False):
+    """Read 8-bit rows src_rows[i] of ``codes`` and ``scales`` back to rows dst_rows[i] of ``states``; the arguments are
+    those of :func:`gdn_pool_pack`."""
+    (st, co, sc), dk, dtype = _pack_pools(states, codes, scales)
+    rows = _pool_rows("gdn_pool_unpack", (states, codes, scales), src_rows, dst_rows, status, stream)
+    return _invoke("gdn_pool_unpack", (co, sc, st, _i32(dk), _i32(dtype), *rows),
+                   (states, codes, scales, src_rows, dst_rows, status), prepare)
+
+
+# ---------------------------------------------------------------------------
+# around the rule: norms and projections
+# ---------------------------------------------------------------------------
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _rows_of(t, name, tail):
+    """(rows, elements from one to the next) of a device tensor whose last ``tail`` dimensions are one dense row.  With
+    one dimension before them the rows may be apart, with more the tensor is contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    d = t.dim() - tail
+    if d < 1:
+        raise ValueError(f"{name} must have at least {tail + 1} dimensions, got shape {tuple(t.shape)}")
+    row = 1
+    for k in range(d, t.dim()):
+        row *= t.shape[k]
+    if t.is_contiguous():
+        return (t.numel() // row if row else 0), row
+    size, strides, want = t.shape, t.stride(), 1
+    for k in range(t.dim() - 1, d - 1, -1):
+        if size[k] != 1 and strides[k] != want:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        want *= size[k]
+    if d != 1:
+        raise ValueError(f"{name} must be contiguous, or have one dimension of rows")
+    return size[0], strides[0] if size[0] > 1 else row
+
+
+def _check_codes(codes, scales, rows, width):
+    """The scales' stride in bytes of 8-bit outputs or operands [rows][width]."""
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales come together")
+    if codes is None:
+        return 0
+    _expect(codes, "codes", (rows, width), _E4M3)
+    _expect(scales, "scales", (rows, None), _E8M0)
+    groups, stride = -(-width // GDN_GROUP), scales.shape[1]
+    if stride < groups or stride % 4:
+        raise ValueError(f"scales must have a multiple of 4 columns, at least {groups}, got {stride}")
+    return stride
+
+
+def gdn_scales_like(codes):
+    """An e8m0 tensor for the scales of e4m3 ``codes`` [rows][width]: a byte for each 128 channels, rows padded to four."""
+    rows, width = _shape_of(codes, "codes", 2)
+    return torch.empty(rows, -(-width // (4 * GDN_GROUP)) * 4, dtype=torch.uint8, device=codes.device).view(_E8M0)
+
+
+def gdn_norm_forward(x, weight, *, out=None, codes=None, scales=None, residual=None, residual_out=None,
+                     eps: float = 1e-6, weight_offset: float = 0.0, stream=None, prepare: bool = False):
+    """Root mean square norm of x + ``residual`` (rows in the last dimension; the rows of a 2-D ``x`` may be apart), the
+    sum kept in ``residual_out``; to ``out`` and, or, to e4m3 ``codes`` [rows][width] with e8m0 ``scales``; see
+    include/gdn.h."""
+    rows, stride = _rows_of(x, "x", 1)
+    width = x.shape[-1]
+    _expect(weight, "weight", (width,))
+    _expect(out, "out", x.shape, x.dtype)
+    _expect(residual, "residual", x.shape)
+    _expect(residual_out, "residual_out", x.shape, None if residual is None else residual.dtype)
+    scale_stride = _check_codes(codes, scales, rows, width)
+    dtype = _dtype_code(x)
+    sh = GdnNormShape(rows, stride, width, dtype, dtype if residual is None else _dtype_code(residual), _dtype_code(weight),
+                      scale_stride, eps, weight_offset)
+    args = (ctypes.byref(sh), _vp(x.data_ptr()), _dev_ptr(residual, "residual"), _dev_ptr(weight, "weight"),
+            _dev_ptr(residual_out, "residual_out"), _dev_ptr(out, "out"), _dev_ptr(codes, "codes"),
+            _dev_ptr(scales, "scales"), _stream(stream))
+    _on_current_device("gdn_norm_forward", stream, x, residual, weight, residual_out, out, codes, scales)
+    return _invoke("gdn_norm_forward", args, (sh, x, residual, weight, residual_out, out, codes, scales), prepare)
+
+
+def gdn_norm_backward(dout, r, weight, dx=None, dweight=None, *, dresidual=None, eps: float = 1e-6,
+                      weight_offset: float = 0.0, workspace=None, stream=None, prepare: bool = False):
+    """The gradients of :func:`gdn_norm_forward`: ``r`` is its residual_out (its x without a residual), ``dresidual`` the
+    gradient that reached residual_out; ``dx`` (r's dtype) is the gradient of x and of the residual, ``dweight`` (fp32)
+    that of the weight.  ``workspace`` is allocated here with torch when omitted."""
+    rows, stride = _rows_of(r, "r", 1)
+    width = r.shape[-1]
+    _expect(dout, "dout", r.shape)
+    if dout is None:
+        raise ValueError("dout is required")
+    _expect(weight, "weight", (width,))
+    _expect(dresidual, "dresidual", r.shape, r.dtype)
+    _expect(dx, "dx", r.shape, r.dtype)
+    _expect(dweight, "dweight", (width,), torch.float32)
+    sh = GdnNormShape(rows, stride, width, _dtype_code(dout), _dtype_code(r), _dtype_code(weight), 0, eps, weight_offset)
+    if workspace is None and dweight is not None:
+        need = lib().gdn_norm_backward_workspace_bytes(ctypes.byref(sh))
+        workspace = _workspace(int(need), r.device, stream)
+    args = (ctypes.byref(sh), _dev_ptr(dout, "dout"), _vp(r.data_ptr()), _dev_ptr(weight, "weight"),
+            _dev_ptr(dresidual, "dresidual"), _dev_ptr(dx, "dx"), _dev_ptr(dweight, "dweight"),
+            _dev_ptr(workspace, "workspace"), ctypes.c_size_t(0 if workspace is None else _bytes_of(workspace)),
+            _stream(stream))
+    _on_current_device("gdn_norm_backward", stream, dout, r, weight, dresidual, dx, dweight, workspace)
+    return _invoke("gdn_norm_backward", args, (sh, dout, r, weight, dresidual, dx, dweight, workspace), prepare)
+
+
+def _gated_shape(x, z, weight, scale_stride, eps):
+    rows, x_stride = _rows_of(x, "x", 2)
+    _expect(z, "z", x.shape)
+    z_rows, z_stride = _rows_of(z, "z", 2)
+    Hv, dv = x.shape[-2:]
+    _expect(weight, "weight", (dv,))
+    return GdnGatedNormShape(rows, x_stride, z_stride, Hv, dv, _dtype_code(x), _dtype_code(z), _dtype_code(weight),
+                             scale_stride, eps)
+
+
+def gdn_gated_norm_forward(x, z, weight, *, out=None, codes=None, scales=None, eps: float = 1e-6, stream=None,
+                           prepare: bool = False):
+    """The rule's outputs ``x`` [...][h_v][d_v], normed head by head and gated by silu(``z``) (the rows of 3-D x and z may
+    be apart); to ``out`` (z's dtype) and, or, to e4m3 ``codes`` [rows][h_v d_v] with e8m0 ``scales``; see
+    include/gdn.h."""
+    sh = _gated_shape(x, z, weight, 0, eps)
+    sh.scale_stride = _check_codes(codes, scales, sh.rows, sh.h_v * sh.d_v)
+    _expect(out, "out", x.shape, z.dtype)
+    args = (ctypes.byref(sh), _vp(x.data_ptr()), _vp(z.data_ptr()), _dev_ptr(weight, "weight"), _dev_ptr(out, "out"),
+            _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), _stream(stream))
+    _on_current_device("gdn_gated_norm_forward", stream, x, z, weight, out, codes, scales)
+    return _invoke("gdn_gated_norm_forward", args, (sh, x, z, weight, out, codes, scales), prepare)
+
+
+def gdn_gated_norm_backward(dout, x, z, weight, dx=None, dz=None, dweight=None, *, eps: float = 1e-6, workspace=None,
+                            stream=None, prepare: bool = False):
+    """The gradients of :func:`gdn_gated_norm_forward`: ``dx`` (x's dtype), ``dz`` (z's) and ``dweight`` (fp32), from
+    ``dout`` (z's).  ``workspace`` is allocated here with torch when omitted."""
+    sh = _gated_shape(x, z, weight, 0, eps)
+    if dout is None:
+        raise ValueError("dout is required")
+    _expect(dout, "dout", x.shape, z.dtype)
+    _expect(dx, "dx", x.shape, x.dtype)
+    _expect(dz, "dz", x.shape, z.dtype)
+    _expect(dweight, "dweight", (sh.d_v,), torch.float32)
+    if workspace is None and dweight is not None:
+        need = lib().gdn_gated_norm_backward_workspace_bytes(ctypes.byref(sh))
+        workspace = _workspace(int(need), x.device, stream)
+    args = (ctypes.byref(sh), _dev_ptr(dout, "dout"), _vp(x.data_ptr()), _vp(z.data_ptr()), _dev_ptr(weight, "weight"),
+            _dev_ptr(dx, "dx"), _dev_ptr(dz, "dz"), _dev_ptr(dweight, "dweight"), _dev_ptr(workspace, "workspace"),
+            ctypes.c_size_t(0 if workspace is None else _bytes_of(workspace)), _stream(stream))
+    _on_current_device("gdn_gated_norm_backward", stream, dout, x, z, weight, dx, dz, dweight, workspace)
+    return _invoke("gdn_gated_norm_backward", args, (sh, dout, x, z, weight, dx, dz, dweight, workspace), prepare)
+
+
+def gdn_project(a, a_scales, w, w_scales, outs, *, stream=None, prepare: bool = False):
+    """a [tokens][inner] times w [columns][inner] transposed, both e4m3, with the scales of groups of 128 (``a_scales``
+    e8m0 [tokens][>= groups], a multiple of 4) and of blocks of 128 x 128 (``w_scales`` fp32 [column blocks][groups], or
+    e8m0, padded alike); the columns go to ``outs``, a tensor or up to 8 of bf16 or f16: [tokens][...] each, whose rows may
+    be apart where they are 2-D.  See include/gdn.h."""
+    M, K = _shape_of(a, "a", 2)
+    N = _shape_of(w, "w", 2)[0]
+    _expect(a, "a", (M, K), _E4M3)
+    _expect(w, "w", (N, K), _E4M3)
+    _, a_stride = _rows_of(a, "a", 1)
+    _, w_stride = _rows_of(w, "w", 1)
+    groups, blocks = -(-K // GDN_GROUP), -(-N // GDN_GROUP)
+    _expect(a_scales, "a_scales", (M, None), _E8M0)
+    _expect(w_scales, "w_scales", (blocks, None))
+    if a_scales.shape[1] < groups or a_scales.shape[1] % 4:
+        raise ValueError(f"a_scales must have a multiple of 4 columns, at least {groups}, got {a_scales.shape[1]}")
+    if w_scales.dtype not in (torch.float32, _E8M0):
+        raise TypeError(f"w_scales must be float32 or float8_e8m0fnu, got {w_scales.dtype}")
+    if w_scales.shape[1] < groups or (w_scales.dtype is _E8M0 and w_scales.shape[1] % 4):
+        raise ValueError(f"w_scales must have at least {groups} columns (e8m0: a multiple of 4), got {w_scales.shape[1]}")
+    if isinstance(outs, torch.Tensor):
+        outs = (outs,)
+    if not 1 <= len(outs) <= GDN_MAX_PARTS:
+        raise ValueError(f"1 to {GDN_MAX_PARTS} outputs, got {len(outs)}")
+    parts, columns = (GdnProjectPart * len(outs))(), 0
+    for i, t in enumerate(outs):
+        if not isinstance(t, torch.Tensor) or t.dim() < 2:
+            raise ValueError("outs must be tensors [tokens][...]")
+        if t.shape[0] != M or t.dtype is not outs[0].dtype:
+            raise ValueError("outs must have a row for each token and one dtype")
+        rows, stride = _rows_of(t, "outs", t.dim() - 1)
+        n = t.numel() // M if M else stride
+        parts[i] = GdnProjectPart(t.data_ptr(), stride, n, 0)
+        columns += n
+    if columns != N:
+        raise ValueError(f"the outputs have {columns} columns, the weights {N}")
+    if outs[0].dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"outs must be bfloat16 or float16, got {outs[0].dtype}")
+    sh = GdnProjectShape(M, a_stride, w_stride, K, a_scales.shape[1], w_scales.shape[1],
+                         GDN_F32 if w_scales.dtype is torch.float32 else GDN_E8M0, _dtype_code(outs[0]))
+    args = (ctypes.byref(sh), _vp(a.data_ptr()), _dev_ptr(a_scales, "a_scales"), _vp(w.data_ptr()),
+            _dev_ptr(w_scales, "w_scales"), parts, _i32(len(outs)), _stream(stream))
+    _on_current_device("gdn_project", stream, a, a_scales, w, w_scales, *outs)
+    return _invoke("gdn_project", args, (sh, a, a_scales, w, w_scales, tuple(outs)), prepare)

@@ -1,0 +1,301 @@
+// gated_norm.hip -- the gated norm of the rule's outputs, head by head, its 8-bit
+// output and its gradients (gfx950).
+//
+//     s = 1 / sqrt(mean x^2 + eps) over a head,  n = x s,  a = 1 / (1 + e^-z)
+//     y = n w z a
+//     g = dout w z a:  dx = s (g - n mean(g n)),  dz = dout n w a (1 + z (1 - a)),  dw = sum dout n z a
+//
+// A lane holds eight channels, so a head is d_v / 8 lanes and a group of 128
+// channels 16.  A row is cut into pieces of whole heads and whole groups (the
+// least common multiple of d_v and 128 channels): 16 or 32 lanes where d_v is a
+// power of two, whose sums are lane exchanges; up to 240 lanes otherwise, whose
+// heads are summed through LDS.  No piece needs another, so both passes read
+// their inputs once and are bound by their bytes.
+#include <cmath>
+#include <type_traits>
+
+#include "norm_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPart = kThreads + 32;  // lanes past the last piece sum over a head's width too
+constexpr int kBackGrid = 1024;  // workgroups of a backward pass, each with its own partial of dweight
+
+struct GatedArgs {
+    const void* x;
+    const void* z;
+    const void* weight;
+    void* out;
+    uint8_t* codes;
+    uint8_t* scales;
+    const void* dout;
+    void* dx;
+    void* dz;
+    float* partial;      // [workgroups][d_v]
+    int64_t rows, x_stride, z_stride;
+    uint32_t pieces;     // of a row
+    uint32_t total;      // of the call
+    int32_t lanes;       // of a piece
+    int32_t per_wg;      // pieces of a workgroup
+    int32_t vectors;     // of a row: h_v d_v / 8
+    int32_t head_lanes;  // d_v / 8
+    int32_t weight_dtype, scale_stride;
+    float eps;
+};
+
+// a = 1 / (1 + e^-z) to about an ulp.  -z log2(e) goes to the exponential in two parts; from z = -87 on, where
+// a is below 2^-126, it is held there.
+__device__ __forceinline__ float logistic(float z) {
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;  // log2(e)
+    const float hi = -z * kHi, lo = __builtin_fmaf(-z, kHi, -hi) - z * kLo;
+    const float p = __builtin_amdgcn_exp2f(__builtin_fminf(hi, 125.0f));
+    const float d = 1.0f + __builtin_fmaf(p, lo * 0.693147180559945f, p);  // 2^lo = 1 + lo ln 2
+    const float q = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(q, __builtin_fmaf(-d, q, 1.0f), q);
+}
+
+// The sums of a head's lanes.  L lanes a head (2, 4, 8, 16 or 32), or any number through LDS (0).
+template <int L>
+__device__ __forceinline__ float head_sum(float x, float* part, int first, int head_lanes) {
+    if constexpr (L != 0) return lanes_sum<L>(x);
+    __syncthreads();  // an earlier sum's readers are done
+    part[threadIdx.x] = x;
+    __syncthreads();
+    float s = 0;
+    for (int k = 0; k < head_lanes; ++k) s += part[first + k];
+    return s;
+}
+
+template <int DX, int DZ, int L>
+__global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const GatedArgs a) {
+    __shared__ float part[L == 0 ? kPart : 1];
+    const int lanes = L == 0 ? a.lanes : L < 16 ? 16 : L, head_lanes = L == 0 ? a.head_lanes : L;
+    const int in_wg = threadIdx.x / lanes, p = threadIdx.x % lanes;
+    const uint32_t at = blockIdx.x * (uint32_t)a.per_wg + in_wg;
+    const bool mine = in_wg < a.per_wg && at < a.total;
+    const uint32_t piece = mine ? at : 0;
+    const int64_t row = piece / a.pieces;
+    const int i = (int)(piece % a.pieces) * lanes + p;
+    const bool live = mine && i < a.vectors;
+    // lanes without a vector read one all the same: whole heads, whose sums nothing uses
+    const int64_t c = (i < a.vectors ? i : i % head_lanes) * kVec;
+    float x[kVec], z[kVec], w[kVec], y[kVec];
+    load8<DX>(a.x, row * a.x_stride + c, x);
+    load8<DZ>(a.z, row * a.z_stride + c, z);
+    load8(a.weight, i % head_lanes * kVec, a.weight_dtype, w);
+    float s = 0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) s += x[k] * x[k];
+    s = head_sum<L>(s, part, (int)threadIdx.x - p % head_lanes, head_lanes);
+    const float rs = inverse_rms(s, (float)(head_lanes * kVec), a.eps);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * (z[k] * logistic(z[k]));
+    const int64_t o = row * (int64_t)a.vectors * kVec + i * (int64_t)kVec;
+    if (live && a.out != nullptr) store8<DZ>(a.out, o, y);
+    if (a.codes != nullptr) {
+        float down;
+        const uint32_t byte = scale_byte(lanes16_max(live ? top8(y) : 0), &down);
+        if (live) {
+            *reinterpret_cast<u32x2*>(a.codes + o) = codes8(y, down);
+            if ((i & 15) == 0) a.scales[row * a.scale_stride + (i >> 4)] = (uint8_t)byte;
+        }
+    }
+}
+
+template <int DX, int DZ, int L>
+__global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const GatedArgs a) {
+    __shared__ float part[L == 0 ? kPart : 1];
+    __shared__ float share[kThreads][kVec + 1];
+    const int lanes = L == 0 ? a.lanes : L < 16 ? 16 : L, head_lanes = L == 0 ? a.head_lanes : L;
+    const int in_wg = threadIdx.x / lanes, p = threadIdx.x % lanes, column = p % head_lanes;
+    float w[kVec], dw[kVec];
+    load8(a.weight, column * kVec, a.weight_dtype, w);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) dw[k] = 0;
+    const uint32_t stride = gridDim.x * (uint32_t)a.per_wg;
+    // every lane takes part in every turn: the sums are over lanes
+    for (uint64_t first = blockIdx.x * (uint32_t)a.per_wg; first < a.total; first += stride) {
+        const bool mine = in_wg < a.per_wg && first + in_wg < a.total;
+        const uint32_t piece = mine ? (uint32_t)first + in_wg : 0;
+        const int64_t row = piece / a.pieces;
+        const int i = (int)(piece % a.pieces) * lanes + p;
+        const bool live = mine && i < a.vectors;
+        const int64_t c = (i < a.vectors ? i : column) * kVec, o = row * (int64_t)a.vectors * kVec + c;
+        float x[kVec], z[kVec], d[kVec], g[kVec], gate[kVec];
+        load8<DX>(a.x, row * a.x_stride + c, x);
+        load8<DZ>(a.z, row * a.z_stride + c, z);
+        load8<DZ>(a.dout, o, d);
+        float xx = 0, gx = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            gate[k] = logistic(z[k]);
+            g[k] = d[k] * w[k] * (z[k] * gate[k]);
+            xx += x[k] * x[k];
+            gx += g[k] * x[k];
+        }
+        const int lead = (int)threadIdx.x - column;
+        xx = head_sum<L>(xx, part, lead, head_lanes);
+        gx = head_sum<L>(gx, part, lead, head_lanes);
+        const float size = (float)(head_lanes * kVec), rs = inverse_rms(xx, size, a.eps), mean = rs * gx / size;
+        float dx[kVec], dz[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            const float n = x[k] * rs, dn = d[k] * n;
+            dx[k] = rs * (g[k] - n * mean);
+            dz[k] = dn * w[k] * gate[k] * (1 + z[k] * (1 - gate[k]));
+            dw[k] += live ? dn * (z[k] * gate[k]) : 0;
+        }
+        if (live && a.dx != nullptr) store8<DX>(a.dx, o, dx);
+        if (live && a.dz != nullptr) store8<DZ>(a.dz, o, dz);
+    }
+    if (a.partial == nullptr) return;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) share[threadIdx.x][k] = dw[k];
+    __syncthreads();
+    if ((int)threadIdx.x < head_lanes * kVec) {
+        float s = 0;
+        for (int t = threadIdx.x / kVec; t < a.per_wg * lanes; t += head_lanes) s += share[t][threadIdx.x % kVec];
+        a.partial[(int64_t)blockIdx.x * (head_lanes * kVec) + threadIdx.x] = s;
+    }
+}
+
+int check_gated(const gdn_gated_norm_shape* sh) {
+    if (sh == nullptr) return GDN_ERR_NULL;
+    if (sh->rows < 0 || sh->rows > 0x7fffffffLL || sh->h_v < 1 || sh->h_v > (1 << 20)) return GDN_ERR_SHAPE;
+    if (sh->d_v < 16 || sh->d_v > 256 || sh->d_v % 16 != 0) return GDN_ERR_SHAPE;
+    const int64_t width = (int64_t)sh->h_v * sh->d_v;
+    for (int64_t s : {sh->x_stride, sh->z_stride})
+        if (s < width || s % kVec != 0 || s > (int64_t{1} << 31)) return GDN_ERR_SHAPE;
+    if (!real_dtype(sh->x_dtype) || !real_dtype(sh->z_dtype) || !real_dtype(sh->weight_dtype)) return GDN_ERR_DTYPE;
+    if (!(sh->eps >= 0) || !(sh->eps < INFINITY)) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+
+// The pieces of a call; *grid workgroups of them, at most `most`.
+int plan_gated(const gdn_gated_norm_shape* sh, int64_t most, GatedArgs* a, int* grid) {
+    const int head = sh->d_v / kVec;
+    int lanes = head;  // a multiple of both 16 lanes and a head
+    while (lanes % 16 != 0) lanes += head;
+    a->vectors = sh->h_v * head;
+    a->head_lanes = head;
+    a->lanes = lanes;
+    a->per_wg = kThreads / lanes;
+    a->pieces = (uint32_t)((a->vectors + lanes - 1) / lanes);
+    const int64_t total = sh->rows * (int64_t)a->pieces;
+    if (total > 0xffffffffLL) return GDN_ERR_SHAPE;
+    a->total = (uint32_t)total;
+    const int64_t wgs = (total + a->per_wg - 1) / a->per_wg;
+    *grid = (int)(wgs < most ? wgs : most);
+    a->rows = sh->rows;
+    a->x_stride = sh->x_stride;
+    a->z_stride = sh->z_stride;
+    a->weight_dtype = sh->weight_dtype;
+    a->scale_stride = sh->scale_stride;
+    a->eps = sh->eps;
+    return GDN_OK;
+}
+
+template <bool BACK>
+hipError_t launch(const gdn_gated_norm_shape* sh, const GatedArgs& a, int grid, hipStream_t stream) {
+    auto go = [&](auto dx, auto dz, auto l) {
+        constexpr int DX = decltype(dx)::value, DZ = decltype(dz)::value, L = decltype(l)::value;
+        if constexpr (BACK) hipLaunchKernelGGL((gated_norm_backward_kernel<DX, DZ, L>), dim3(grid), dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL((gated_norm_forward_kernel<DX, DZ, L>), dim3(grid), dim3(kThreads), 0, stream, a);
+        return hipGetLastError();
+    };
+    auto head = [&](auto dx, auto dz) {
+        switch (a.head_lanes) {
+            case 2: return go(dx, dz, std::integral_constant<int, 2>{});
+            case 4: return go(dx, dz, std::integral_constant<int, 4>{});
+            case 8: return go(dx, dz, std::integral_constant<int, 8>{});
+            case 16: return go(dx, dz, std::integral_constant<int, 16>{});
+            case 32: return go(dx, dz, std::integral_constant<int, 32>{});
+            default: return go(dx, dz, std::integral_constant<int, 0>{});
+        }
+    };
+    auto gate = [&](auto dx) {
+        if (sh->z_dtype == GDN_F32) return head(dx, std::integral_constant<int, GDN_F32>{});
+        if (sh->z_dtype == GDN_BF16) return head(dx, std::integral_constant<int, GDN_BF16>{});
+        return head(dx, std::integral_constant<int, GDN_F16>{});
+    };
+    if (sh->x_dtype == GDN_F32) return gate(std::integral_constant<int, GDN_F32>{});
+    if (sh->x_dtype == GDN_BF16) return gate(std::integral_constant<int, GDN_BF16>{});
+    return gate(std::integral_constant<int, GDN_F16>{});
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+int gdn_gated_norm_forward(const gdn_gated_norm_shape* shape, const void* x, const void* z, const void* weight,
+                           void* out, void* codes, void* scales, void* stream) {
+    int rc = check_gated(shape);
+    if (rc != GDN_OK) return rc;
+    const int64_t width = (int64_t)shape->h_v * shape->d_v;
+    if (codes != nullptr && (shape->scale_stride % 4 != 0 || shape->scale_stride < (width + GDN_GROUP - 1) / GDN_GROUP))
+        return GDN_ERR_SHAPE;
+    GatedArgs a = {};
+    int grid = 0;
+    if ((rc = plan_gated(shape, 0x7fffffffLL, &a, &grid)) != GDN_OK) return rc;
+    if (shape->rows == 0) return GDN_OK;
+    if (x == nullptr || z == nullptr || weight == nullptr) return GDN_ERR_NULL;
+    if ((codes == nullptr) != (scales == nullptr) || (out == nullptr && codes == nullptr)) return GDN_ERR_NULL;
+    if (!aligned_to(x, 16) || !aligned_to(z, 16) || !aligned_to(weight, 16) || !aligned_to(out, 16) || !aligned_to(codes, 8) ||
+        !aligned_to(scales, 4))
+        return GDN_ERR_ALIGN;
+    a.x = x;
+    a.z = z;
+    a.weight = weight;
+    a.out = out;
+    a.codes = static_cast<uint8_t*>(codes);
+    a.scales = static_cast<uint8_t*>(scales);
+    return launch<false>(shape, a, grid, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_gated_norm_backward_workspace_bytes(const gdn_gated_norm_shape* shape) {
+    GatedArgs a = {};
+    int grid = 0;
+    if (check_gated(shape) != GDN_OK || plan_gated(shape, kBackGrid, &a, &grid) != GDN_OK) return 0;
+    return (size_t)grid * shape->d_v * sizeof(float);
+}
+
+int gdn_gated_norm_backward(const gdn_gated_norm_shape* shape, const void* dout, const void* x, const void* z,
+                            const void* weight, void* dx, void* dz, float* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    int rc = check_gated(shape);
+    if (rc != GDN_OK) return rc;
+    GatedArgs a = {};
+    int grid = 0;
+    if ((rc = plan_gated(shape, kBackGrid, &a, &grid)) != GDN_OK) return rc;
+    if (dx == nullptr && dz == nullptr && dweight == nullptr) return GDN_ERR_NULL;
+    if (!aligned_to(dweight, 16)) return GDN_ERR_ALIGN;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (shape->rows == 0) {
+        if (dweight == nullptr) return GDN_OK;
+        return launch_sum_partials(nullptr, 0, shape->d_v, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    }
+    if (dout == nullptr || x == nullptr || z == nullptr || weight == nullptr) return GDN_ERR_NULL;
+    for (const void* p : {dout, x, z, weight, static_cast<const void*>(dx), static_cast<const void*>(dz)})
+        if (!aligned_to(p, 16)) return GDN_ERR_ALIGN;
+    if (dweight != nullptr) {
+        if (workspace == nullptr || workspace_bytes < gdn_gated_norm_backward_workspace_bytes(shape)) return GDN_ERR_WORKSPACE;
+        if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGN;
+    }
+    a.x = x;
+    a.z = z;
+    a.weight = weight;
+    a.dout = dout;
+    a.dx = dx;
+    a.dz = dz;
+    a.partial = dweight != nullptr ? static_cast<float*>(workspace) : nullptr;
+    if (launch<true>(shape, a, grid, st) != hipSuccess) return GDN_ERR_HIP;
+    if (dweight == nullptr) return GDN_OK;
+    return launch_sum_partials(a.partial, grid, shape->d_v, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,385 @@
+// norm.hip -- root mean square norm with the residual's addition, its 8-bit
+// output and its gradients (gfx950).
+//
+//     r = x + residual (as stored),  s = 1 / sqrt(mean r^2 + eps),  y = r s (w + w0)
+//     g = dout (w + w0):  dx = dresidual + s g - r s^3 mean(g r),  dw = sum over rows of dout r s
+//
+// Both passes read a row once and keep it in registers between the sums and the
+// outputs, so they are bound by their bytes.
+#include <cmath>
+#include <type_traits>
+
+#include "norm_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxWalkers = 512;  // rows in flight of a backward pass, each with its own partial of dweight
+
+struct NormArgs {
+    const void* x;       // forward: x; backward: r
+    const void* residual;
+    const void* weight;
+    void* residual_out;
+    void* out;
+    uint8_t* codes;
+    uint8_t* scales;
+    const void* dout;
+    const void* dresidual;
+    void* dx;
+    float* partial;      // [walkers][width]
+    int64_t rows, x_stride;
+    int32_t width, weight_dtype, scale_stride;
+    float eps, weight_offset;
+};
+
+// Sum over the LANES lanes of a row: part of a wave, or the workgroup (LANES = 0).
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x, float* wave_sum) {
+    if constexpr (LANES != 0) return lanes_sum<LANES>(x);
+    x = lanes_sum<64>(x);
+    const int waves = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float sum = 0;
+    for (int w = 0; w < waves; ++w) sum += wave_sum[w];
+    return sum;
+}
+
+// DX: type of x and out, DR: of the residual; V vectors a lane.
+template <int DX, int DR, int V, int LANES>
+__global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel(const NormArgs a) {
+    __shared__ float wave_sum[kMaxThreads / 64];
+    const int lanes = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % LANES : threadIdx.x;
+    const int64_t at = LANES ? (int64_t)blockIdx.x * (blockDim.x / (LANES ? LANES : 1)) + threadIdx.x / (LANES ? LANES : 1) : blockIdx.x;
+    const int64_t row = at < a.rows ? at : a.rows - 1;
+    const int n = a.width / kVec;
+    float r[V][kVec], w[V][kVec];
+    // lanes past the row's end read its last vector
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = t + v * lanes;
+        load8<DX>(a.x, row * a.x_stride + (i < n ? i : n - 1) * kVec, r[v]);
+    }
+    if (a.residual != nullptr) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = t + v * lanes;
+            float z[kVec];
+            load8<DR>(a.residual, row * a.width + (i < n ? i : n - 1) * kVec, z);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) r[v][k] = stored<DR>(r[v][k] + z[k]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = t + v * lanes;
+        load8(a.weight, (i < n ? i : n - 1) * kVec, a.weight_dtype, w[v]);
+    }
+    float sum = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float s = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) s += r[v][k] * r[v][k];
+        sum += t + v * lanes < n ? s : 0;
+    }
+    const float rs = inverse_rms(row_sum<LANES>(sum, wave_sum), (float)a.width, a.eps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = t + v * lanes;
+        const bool live = i < n && at < a.rows;
+        float y[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) y[k] = r[v][k] * rs * (w[v][k] + a.weight_offset);
+        const int64_t o = row * a.width + i * kVec;
+        if (live && a.residual_out != nullptr) store8<DR>(a.residual_out, o, r[v]);
+        if (live && a.out != nullptr) store8<DX>(a.out, o, y);
+        if (a.codes != nullptr) {
+            float down;
+            const uint32_t byte = scale_byte(lanes16_max(live ? top8(y) : 0), &down);
+            if (live) {
+                *reinterpret_cast<u32x2*>(a.codes + o) = codes8(y, down);
+                if ((t & 15) == 0) a.scales[row * a.scale_stride + (i >> 4)] = (uint8_t)byte;
+            }
+        }
+    }
+}
+
+template <int DX, int DR, int V, int LANES>
+__global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_backward_kernel(const NormArgs a) {
+    __shared__ float wave_sum[2][2][kMaxThreads / 64];
+    const int lanes = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % LANES : threadIdx.x;
+    const int per_wg = LANES ? blockDim.x / (LANES ? LANES : 1) : 1;
+    const int64_t walker = (int64_t)blockIdx.x * per_wg + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
+    const int64_t walkers = (int64_t)gridDim.x * per_wg;
+    const int n = a.width / kVec;
+    float w[V][kVec], dw[V][kVec];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = t + v * lanes;
+        load8(a.weight, (i < n ? i : n - 1) * kVec, a.weight_dtype, w[v]);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            w[v][k] += a.weight_offset;
+            dw[v][k] = 0;
+        }
+    }
+    int turn = 0;
+    for (int64_t row = walker; row < a.rows; row += walkers, turn ^= 1) {
+        float r[V][kVec], d[V][kVec];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = t + v * lanes, c = (i < n ? i : n - 1) * kVec;
+            load8<DR>(a.x, row * a.x_stride + c, r[v]);
+            load8<DX>(a.dout, row * a.width + c, d[v]);
+        }
+        float rr = 0, gr = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float p = 0, q = 0;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                p += r[v][k] * r[v][k];
+                q += d[v][k] * w[v][k] * r[v][k];
+            }
+            if (t + v * lanes < n) {
+                rr += p;
+                gr += q;
+            }
+        }
+        if constexpr (LANES != 0) {
+            rr = lanes_sum<LANES>(rr);
+            gr = lanes_sum<LANES>(gr);
+        } else {  // two copies of the sums: the next row's do not wait for this row's readers
+            rr = lanes_sum<64>(rr);
+            gr = lanes_sum<64>(gr);
+            if ((threadIdx.x & 63) == 0) {
+                wave_sum[turn][0][threadIdx.x >> 6] = rr;
+                wave_sum[turn][1][threadIdx.x >> 6] = gr;
+            }
+            __syncthreads();
+            rr = gr = 0;
+            for (int k = 0; k < (int)(blockDim.x >> 6); ++k) {
+                rr += wave_sum[turn][0][k];
+                gr += wave_sum[turn][1][k];
+            }
+        }
+        const float rs = inverse_rms(rr, (float)a.width, a.eps), mean = rs * gr / (float)a.width;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = t + v * lanes;
+            const int64_t o = row * a.width + i * kVec;
+            float dx[kVec];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                const float norm = r[v][k] * rs;
+                dx[k] = rs * (d[v][k] * w[v][k] - norm * mean);
+                dw[v][k] += d[v][k] * norm;
+            }
+            if (i < n && a.dx != nullptr) {
+                if (a.dresidual != nullptr) {
+                    float z[kVec];
+                    load8<DR>(a.dresidual, o, z);
+#pragma unroll
+                    for (int k = 0; k < kVec; ++k) dx[k] += z[k];
+                }
+                store8<DR>(a.dx, o, dx);
+            }
+        }
+    }
+    if (a.partial == nullptr) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = t + v * lanes;
+        if (i < n) store8<GDN_F32>(a.partial, walker * a.width + i * kVec, dw[v]);
+    }
+}
+
+// 32 columns a workgroup, 32 slices of the partials, joined in LDS.
+__global__ __launch_bounds__(1024) void sum_partials_kernel(const float* partial, int n_partials, int width, float* out) {
+    __shared__ float part[32][33];
+    const int c = threadIdx.x % 32, slice = threadIdx.x / 32, col = blockIdx.x * 32 + c;
+    float s = 0;
+    if (col < width)
+        for (int p = slice; p < n_partials; p += 32) s += partial[(int64_t)p * width + col];
+    part[slice][c] = s;
+    __syncthreads();
+    if (slice == 0 && col < width) {
+        s = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s += part[k][c];
+        out[col] = s;
+    }
+}
+
+struct NormPlan {
+    int lanes;    // of a row: 16, 64 or the workgroup (0)
+    int vectors;  // a lane: 1, 2 or 4
+    int threads, grid;
+};
+
+int32_t walkers_of(const NormPlan& p) { return p.lanes != 0 ? p.grid * (p.threads / p.lanes) : p.grid; }
+
+// Rows of up to 256 channels take 16 lanes, up to 2048 a wave, longer ones a workgroup.
+NormPlan plan_rows(int64_t rows, int32_t width, int64_t most_rows) {
+    const int n = width / kVec;
+    NormPlan p;
+    if (n <= 256) {
+        p.lanes = n <= 32 ? 16 : 64;
+        p.vectors = n <= p.lanes ? 1 : n <= 2 * p.lanes ? 2 : 4;
+        p.threads = 256;
+    } else {
+        p.lanes = 0;
+        p.vectors = n <= 1024 ? 1 : 2;
+        p.threads = (((n + p.vectors - 1) / p.vectors + 63) / 64) * 64;
+    }
+    const int per_wg = p.lanes != 0 ? p.threads / p.lanes : 1;
+    const int64_t walk = rows < most_rows ? rows : most_rows;
+    p.grid = (int)((walk + per_wg - 1) / per_wg);
+    return p;
+}
+
+NormPlan plan_backward(const gdn_norm_shape* sh) {
+    NormPlan p = plan_rows(sh->rows, sh->width, kMaxWalkers);
+    if (p.lanes == 16) {  // a wave a row: fewer partials
+        p = NormPlan{64, 1, 256, 0};
+        const int64_t walk = sh->rows < kMaxWalkers ? sh->rows : kMaxWalkers;
+        p.grid = (int)((walk + 3) / 4);
+    }
+    return p;
+}
+
+template <int DX, int DR, bool BACK>
+hipError_t launch(const NormPlan& p, const NormArgs& a, hipStream_t stream) {
+    auto go = [&](auto v, auto lanes) {
+        constexpr int V = decltype(v)::value, L = decltype(lanes)::value;
+        if constexpr (BACK) hipLaunchKernelGGL((norm_backward_kernel<DX, DR, V, L>), dim3(p.grid), dim3(p.threads), 0, stream, a);
+        else hipLaunchKernelGGL((norm_forward_kernel<DX, DR, V, L>), dim3(p.grid), dim3(p.threads), 0, stream, a);
+        return hipGetLastError();
+    };
+    auto pick = [&](auto lanes) {
+        if (p.vectors == 1) return go(std::integral_constant<int, 1>{}, lanes);
+        if constexpr (decltype(lanes)::value == 64)
+            if (p.vectors == 4) return go(std::integral_constant<int, 4>{}, lanes);
+        return go(std::integral_constant<int, 2>{}, lanes);
+    };
+    if constexpr (!BACK)
+        if (p.lanes == 16) return pick(std::integral_constant<int, 16>{});
+    if (p.lanes == 64) return pick(std::integral_constant<int, 64>{});
+    return pick(std::integral_constant<int, 0>{});
+}
+
+template <bool BACK>
+hipError_t launch(const gdn_norm_shape* sh, const NormPlan& p, const NormArgs& a, hipStream_t stream) {
+    auto by = [&](auto dx) {
+        constexpr int DX = decltype(dx)::value;
+        if (sh->residual_dtype == GDN_F32) return launch<DX, GDN_F32, BACK>(p, a, stream);
+        if (sh->residual_dtype == GDN_BF16) return launch<DX, GDN_BF16, BACK>(p, a, stream);
+        return launch<DX, GDN_F16, BACK>(p, a, stream);
+    };
+    if (sh->dtype == GDN_F32) return by(std::integral_constant<int, GDN_F32>{});
+    if (sh->dtype == GDN_BF16) return by(std::integral_constant<int, GDN_BF16>{});
+    return by(std::integral_constant<int, GDN_F16>{});
+}
+
+int check_norm(const gdn_norm_shape* sh) {
+    if (sh == nullptr) return GDN_ERR_NULL;
+    if (sh->rows < 0 || sh->rows > 0x7fffffffLL) return GDN_ERR_SHAPE;
+    if (sh->width < kVec || sh->width > GDN_MAX_WIDTH || sh->width % kVec != 0) return GDN_ERR_SHAPE;
+    if (sh->x_stride < sh->width || sh->x_stride % kVec != 0 || sh->x_stride > (int64_t{1} << 31)) return GDN_ERR_SHAPE;
+    if (!real_dtype(sh->dtype) || !real_dtype(sh->residual_dtype) || !real_dtype(sh->weight_dtype)) return GDN_ERR_DTYPE;
+    if (!(sh->eps >= 0) || !(sh->eps < INFINITY) || !(fabsf(sh->weight_offset) < INFINITY)) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+
+NormArgs args_of(const gdn_norm_shape* sh) {
+    NormArgs a = {};
+    a.rows = sh->rows;
+    a.x_stride = sh->x_stride;
+    a.width = sh->width;
+    a.weight_dtype = sh->weight_dtype;
+    a.scale_stride = sh->scale_stride;
+    a.eps = sh->eps;
+    a.weight_offset = sh->weight_offset;
+    return a;
+}
+
+}  // namespace
+
+hipError_t launch_sum_partials(const float* partial, int32_t n_partials, int32_t width, float* out, hipStream_t stream) {
+    hipLaunchKernelGGL(sum_partials_kernel, dim3((width + 31) / 32), dim3(1024), 0, stream, partial, n_partials, width, out);
+    return hipGetLastError();
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+int gdn_norm_forward(const gdn_norm_shape* shape, const void* x, const void* residual, const void* weight,
+                     void* residual_out, void* out, void* codes, void* scales, void* stream) {
+    const int rc = check_norm(shape);
+    if (rc != GDN_OK) return rc;
+    if (codes != nullptr && (shape->scale_stride % 4 != 0 || shape->scale_stride < (shape->width + GDN_GROUP - 1) / GDN_GROUP))
+        return GDN_ERR_SHAPE;
+    if (shape->rows == 0) return GDN_OK;
+    if (x == nullptr || weight == nullptr) return GDN_ERR_NULL;
+    if ((codes == nullptr) != (scales == nullptr)) return GDN_ERR_NULL;
+    if (out == nullptr && codes == nullptr && residual_out == nullptr) return GDN_ERR_NULL;
+    if (residual == nullptr && residual_out != nullptr) return GDN_ERR_NULL;
+    if (!aligned_to(x, 16) || !aligned_to(residual, 16) || !aligned_to(weight, 16) || !aligned_to(residual_out, 16) ||
+        !aligned_to(out, 16) || !aligned_to(codes, 8) || !aligned_to(scales, 4))
+        return GDN_ERR_ALIGN;
+    NormArgs a = args_of(shape);
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.residual_out = residual_out;
+    a.out = out;
+    a.codes = static_cast<uint8_t*>(codes);
+    a.scales = static_cast<uint8_t*>(scales);
+    const NormPlan p = plan_rows(shape->rows, shape->width, shape->rows);
+    return launch<false>(shape, p, a, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_norm_backward_workspace_bytes(const gdn_norm_shape* shape) {
+    if (check_norm(shape) != GDN_OK) return 0;
+    return (size_t)walkers_of(plan_backward(shape)) * shape->width * sizeof(float);
+}
+
+int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void* r, const void* weight,
+                      const void* dresidual, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+    const int rc = check_norm(shape);
+    if (rc != GDN_OK) return rc;
+    if (dx == nullptr && dweight == nullptr) return GDN_ERR_NULL;
+    if (!aligned_to(dweight, 16)) return GDN_ERR_ALIGN;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (shape->rows == 0) {
+        if (dweight == nullptr) return GDN_OK;
+        return launch_sum_partials(nullptr, 0, shape->width, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    }
+    if (dout == nullptr || r == nullptr || weight == nullptr) return GDN_ERR_NULL;
+    if (!aligned_to(dout, 16) || !aligned_to(r, 16) || !aligned_to(weight, 16) || !aligned_to(dresidual, 16) || !aligned_to(dx, 16))
+        return GDN_ERR_ALIGN;
+    const NormPlan p = plan_backward(shape);
+    if (dweight != nullptr) {
+        if (workspace == nullptr || workspace_bytes < gdn_norm_backward_workspace_bytes(shape)) return GDN_ERR_WORKSPACE;
+        if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGN;
+    }
+    NormArgs a = args_of(shape);
+    a.x = r;
+    a.dout = dout;
+    a.weight = weight;
+    a.dresidual = dresidual;
+    a.dx = dx;
+    a.partial = dweight != nullptr ? static_cast<float*>(workspace) : nullptr;
+    if (launch<true>(shape, p, a, st) != hipSuccess) return GDN_ERR_HIP;
+    if (dweight == nullptr) return GDN_OK;
+    return launch_sum_partials(a.partial, walkers_of(p), shape->width, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+}  // extern "C"

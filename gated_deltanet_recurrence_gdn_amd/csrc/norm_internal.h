@@ -1,0 +1,139 @@
+// norm_internal.h -- what the norms share: elements of three types as fp32,
+// sums over lanes, 8-bit codes with a power of two for each group of 128
+// channels, and the sum of the weight gradients' partials.
+//
+// Eight consecutive channels of a row are one lane's (16 bytes of 16-bit
+// elements), so a group of 128 channels is an aligned row of 16 lanes and its
+// largest magnitude is found by lane exchanges alone.
+#pragma once
+
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+constexpr int kVec = 8;  // channels of a lane
+
+inline bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline bool real_dtype(int32_t t) { return t == GDN_F32 || t == GDN_BF16 || t == GDN_F16; }
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* base, int64_t i, float (&x)[kVec]) {
+    if constexpr (DT == GDN_F32) {
+        const float* p = static_cast<const float*>(base) + i;
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[k] = a[k];
+            x[4 + k] = b[k];
+        }
+    } else if constexpr (DT == GDN_BF16) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[2 * k] = bf16_lo(w[k]);
+            x[2 * k + 1] = bf16_hi(w[k]);
+        }
+    } else {
+        const f16x8 h = *reinterpret_cast<const f16x8*>(static_cast<const _Float16*>(base) + i);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) x[k] = (float)h[k];
+    }
+}
+
+// Rounds to the nearest, ties to even.
+template <int DT>
+__device__ __forceinline__ void store8(void* base, int64_t i, const float (&x)[kVec]) {
+    if constexpr (DT == GDN_F32) {
+        float* p = static_cast<float*>(base) + i;
+        *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+        *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    } else if constexpr (DT == GDN_BF16) {
+        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+        bf16x8 h;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) h[k] = (__bf16)x[k];
+        *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(base) + i) = h;
+    } else {
+        f16x8 h;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) h[k] = (_Float16)x[k];
+        *reinterpret_cast<f16x8*>(static_cast<_Float16*>(base) + i) = h;
+    }
+}
+
+// A value as it is stored.
+template <int DT>
+__device__ __forceinline__ float stored(float x) {
+    if constexpr (DT == GDN_BF16) return (float)(__bf16)x;
+    if constexpr (DT == GDN_F16) return (float)(_Float16)x;
+    return x;
+}
+
+// Weights: a type known at run time only, read once and from the caches.
+__device__ __forceinline__ void load8(const void* base, int64_t i, int dtype, float (&x)[kVec]) {
+    if (dtype == GDN_F32) load8<GDN_F32>(base, i, x);
+    else if (dtype == GDN_BF16) load8<GDN_BF16>(base, i, x);
+    else load8<GDN_F16>(base, i, x);
+}
+
+// Sum over aligned groups of L lanes, L = 2, 4, 8, 16, 32 or 64; all of a group receive it.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+    if constexpr (L == 2) return x + dpp_f32<0xB1>(x);
+    else x = group_sum<(L < 16 ? L : 16)>(x);
+    if constexpr (L >= 32) x += __shfl_xor(x, 16);
+    if constexpr (L >= 64) x += __shfl_xor(x, 32);
+    return x;
+}
+
+// The largest of 16 lanes' values.
+__device__ __forceinline__ uint32_t lanes16_max(uint32_t x) {
+    auto step = [&](uint32_t y) { x = x > y ? x : y; };
+    step(__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, false));
+    return x;
+}
+
+// The largest magnitude of eight values as its bits: NaN above infinity above all others.
+__device__ __forceinline__ uint32_t top8(const float (&y)[kVec]) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, y[k]) & 0x7fffffffu;
+        t = t > b ? t : b;
+    }
+    return t;
+}
+
+// Scale byte of a group whose largest magnitude has these bits (e + 127 for the smallest e >= -126 with
+// top 2^-e <= 448 = 1.75 * 2^8), and 2^-e; 255 and NaN for a group with a NaN or an infinity.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top, float* down) {
+    int b = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
+    b = b < 1 ? 1 : b;
+    const bool bad = top >= 0x7f800000u;
+    *down = __builtin_bit_cast(float, bad ? 0x7fc00000u : (uint32_t)(254 - b) << 23);
+    return bad ? 255u : (uint32_t)b;
+}
+
+// Eight values times 2^-e as e4m3 codes.  The products are exact but below 2^-126, far under half of
+// the smallest code, so each value is rounded once.
+__device__ __forceinline__ u32x2 codes8(const float (&y)[kVec], float down) {
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * down, y[1] * down, 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * down, y[3] * down, lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * down, y[5] * down, 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * down, y[7] * down, hi, true);
+    return u32x2{(uint32_t)lo, (uint32_t)hi};
+}
+
+// 1 / sqrt(sum / n + eps), each step rounded to the nearest.
+__device__ __forceinline__ float inverse_rms(float sum, float n, float eps) { return 1.0f / sqrtf(sum / n + eps); }
+
+// out[c] = sum of partial[p][c] over p, in an order that depends on the sizes alone.
+hipError_t launch_sum_partials(const float* partial, int32_t n_partials, int32_t width, float* out, hipStream_t stream);
+
+}  // namespace gdn

@@ -24,7 +24,7 @@
 #include <cstring>
 
 #include "gdn_device.h"
-#include "gdn_internal.h"
+#include "pool_internal.h"
 
 namespace gdn {
 namespace {
@@ -56,17 +56,6 @@ struct CopyRowsArgs {
     int32_t same;   // 1: sources and destinations are rows of the same pools
 };
 
-// Whether pair i may be copied: rows in range, and its destination neither
-// another pair's destination nor, within one pool, another pair's source.  The
-// whole workgroup asks together.
-__device__ bool pair_stands(const CopyRowsArgs& a, int i, int s, int d) {
-    bool bad = s < -1 || s >= a.src_slots || d >= a.dst_slots || d < -1;
-    if (!bad && d >= 0)
-        for (int j = threadIdx.x; j < a.n; j += kCopyThreads)
-            if (j != i && (a.dst_row[j] == d || (a.same && a.src_row[j] == d))) bad = true;
-    return __syncthreads_or(bad) == 0;
-}
-
 __global__ __launch_bounds__(kCopyThreads) void pool_copy_kernel(const CopyRowsArgs a) {
     const int n = a.n_dev != nullptr ? *a.n_dev : a.n;
     const uint32_t total = (uint32_t)n * (uint32_t)a.per_pair;
@@ -81,7 +70,7 @@ __global__ __launch_bounds__(kCopyThreads) void pool_copy_kernel(const CopyRowsA
             d = a.dst_row[pair];
             go = true;
             if (a.check) {
-                go = pair_stands(a, pair, s, d);
+                go = pair_stands<kCopyThreads>(a, pair, s, d);
                 if (!go && threadIdx.x == 0 && a.status != nullptr) a.status[0] = GDN_ERR_SLOT;
             }
             if (d < 0 || (a.same && s == d)) go = false;
@@ -277,49 +266,6 @@ __global__ __launch_bounds__(kPlanThreads) void pool_compact_plan_kernel(const P
         *a.n_pairs = live - kept;
         if (a.count != nullptr) *a.count = live;
     }
-}
-
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// One past the last byte of a pool.
-const unsigned char* pool_end(const gdn_pool& p) {
-    return static_cast<const unsigned char*>(p.data) + (int64_t)(p.n_layers - 1) * p.layer_bytes + (int64_t)p.n_slots * p.row_bytes;
-}
-
-// Whether two pools share a byte.  A layer's rows are one range, and a pool's layers
-// may lie between another's: for each layer of the pool with fewer of them, only the
-// other's last layer that starts before its end can reach into it.
-bool overlap(const gdn_pool& x, const gdn_pool& y) {
-    if (x.n_layers == 0 || y.n_layers == 0 || x.data >= pool_end(y) || y.data >= pool_end(x)) return false;
-    const gdn_pool &a = x.n_layers <= y.n_layers ? x : y, &b = x.n_layers <= y.n_layers ? y : x;
-    const int64_t size = a.n_slots * a.row_bytes, b_size = b.n_slots * b.row_bytes;
-    // a's layer from b's first byte
-    int64_t at = static_cast<const unsigned char*>(a.data) - static_cast<const unsigned char*>(b.data);
-    for (int32_t l = 0; l < a.n_layers; ++l, at += a.layer_bytes) {
-        if (at + size <= 0) continue;
-        int64_t m = b.n_layers > 1 ? (at + size - 1) / b.layer_bytes : 0;
-        if (m >= b.n_layers) m = b.n_layers - 1;
-        if (m * b.layer_bytes + b_size > at) return true;
-    }
-    return false;
-}
-
-int check_pools(const gdn_pool* pools, int32_t n_pools) {
-    if (n_pools < 1 || n_pools > GDN_MAX_POOLS) return GDN_ERR_SHAPE;
-    if (pools == nullptr) return GDN_ERR_NULL;
-    for (int i = 0; i < n_pools; ++i) {
-        const gdn_pool& p = pools[i];
-        if (p.n_layers < 0 || p.n_slots < 1 || p.n_slots != pools[0].n_slots) return GDN_ERR_SHAPE;
-        if (p.row_bytes < 16 || p.row_bytes % 16 != 0 || p.row_bytes > (int64_t{1} << 40)) return GDN_ERR_SHAPE;
-        if (p.layer_bytes % 16 != 0 || p.layer_bytes > (int64_t{1} << 46)) return GDN_ERR_SHAPE;
-        if (p.n_layers > 1 && p.layer_bytes / p.row_bytes < p.n_slots) return GDN_ERR_SHAPE;
-        // more than any memory: the sums below stay inside 64 bits
-        if ((double)p.n_layers * (double)p.layer_bytes + (double)p.n_slots * (double)p.row_bytes > 0x1p60) return GDN_ERR_SHAPE;
-        if (p.n_layers == 0) continue;
-        if (p.data == nullptr) return GDN_ERR_NULL;
-        if (!aligned(p.data, 16)) return GDN_ERR_ALIGN;
-    }
-    return GDN_OK;
 }
 
 // Fills the copy's pool parts; per_pair * n has to fit the kernel's 32-bit tile count.

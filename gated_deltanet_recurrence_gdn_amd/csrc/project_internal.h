@@ -1,0 +1,85 @@
+// project_internal.h -- what the kernels of gdn_project share: the call's
+// arguments, the scaled matrix instruction and the stores to the parts.
+//
+// Operands of v_mfma_scale_f32_16x16x128 as the kernels use it: lane l holds 32
+// consecutive e4m3 codes (k = 32 (l / 16) ...) of row l % 16 of either side and the
+// row's scale byte; of the result, lane l holds rows 4 (l / 16) .. + 3 of the first
+// operand against row l % 16 of the second.  The weights are the first operand, so a
+// lane ends with four consecutive columns of one token.  One instruction is one group
+// of 128, so a row's scale is the same in all four of its lanes.
+#pragma once
+
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kOne = 127;  // the scale byte of 1
+
+struct ProjectPart {
+    void* data;
+    int64_t stride;  // elements
+    int32_t begin;   // its first column
+    int32_t wide;    // 1: four columns from a multiple of four of the whole on can be stored at once
+};
+
+struct ProjectArgs {
+    const uint8_t* a;
+    const uint8_t* a_scales;
+    const uint8_t* w;
+    const void* w_scales;
+    int64_t a_stride, w_stride;  // bytes
+    int32_t tokens, columns, inner, groups;
+    int32_t a_scale_stride, w_scale_stride;
+    int32_t n_parts;
+    ProjectPart part[GDN_MAX_PARTS];
+};
+
+__device__ __forceinline__ f32x4 mfma_scaled(i32x8 w, i32x8 a, f32x4 c, int w_scale, int a_scale) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, w_scale, 0, a_scale);
+}
+
+template <int DT>
+__device__ __forceinline__ uint16_t half_bits(float x) {
+    if constexpr (DT == GDN_BF16) return f32_to_bf16(x);
+    return __builtin_bit_cast(uint16_t, (_Float16)x);
+}
+
+// The part that holds column n (n < columns).
+__device__ __forceinline__ int part_of(const ProjectArgs& p, int n) {
+    int i = 0;
+    while (i + 1 < p.n_parts && n >= p.part[i + 1].begin) ++i;
+    return i;
+}
+
+// Columns n .. n + 3 (n a multiple of four) of token m, as far as there are any.  `home`: the part of all of them
+// where one holds them all, or -1.
+template <int DT>
+__device__ __forceinline__ void store_columns(const ProjectArgs& p, int home, int m, int n, f32x4 y) {
+    const uint16_t h[4] = {half_bits<DT>(y[0]), half_bits<DT>(y[1]), half_bits<DT>(y[2]), half_bits<DT>(y[3])};
+    if (home >= 0 && p.part[home].wide) {
+        const ProjectPart& q = p.part[home];
+        uint16_t* at = static_cast<uint16_t*>(q.data) + (int64_t)m * q.stride + (n - q.begin);
+        *reinterpret_cast<u32x2*>(at) = u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (n + j >= p.columns) break;
+        const ProjectPart& q = p.part[part_of(p, n + j)];
+        static_cast<uint16_t*>(q.data)[(int64_t)m * q.stride + (n + j - q.begin)] = h[j];
+    }
+}
+
+// The part that holds columns n0 .. n0 + count - 1, or -1 where there is no single one.
+__device__ __forceinline__ int home_of(const ProjectArgs& p, int n0, int count) {
+    if (n0 + count > p.columns) return -1;
+    const int i = part_of(p, n0);
+    const int end = i + 1 < p.n_parts ? p.part[i + 1].begin : p.columns;
+    return n0 + count <= end ? i : -1;
+}
+
+}  // namespace gdn

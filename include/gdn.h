@@ -47,8 +47,9 @@
  *    its kernels form into the caller's arrays and the workspace: one past
  *    its array's end stores GDN_ERR_INTERNAL into *status and is clamped into
  *    the array.  The release build carries no such checks.  The kernels of
- *    gdn_scan_* and gdn_pool_* have none in either build: their indices follow
- *    from the shape, the offsets and the row numbers, which every build checks.
+ *    gdn_scan_*, gdn_pool_*, gdn_norm_*, gdn_gated_norm_* and gdn_project have
+ *    none in either build: their indices follow from the shape, the offsets and
+ *    the row numbers, which every build checks.
  */
 #ifndef GDN_H
 #define GDN_H
@@ -360,6 +361,33 @@ int gdn_pool_compact(const gdn_pool* pools, int32_t n_pools, const int32_t* tabl
                      const int32_t* released, int32_t n_released, int32_t* table_out, int32_t* count, void* workspace,
                      size_t workspace_bytes, int32_t* status, void* stream);
 
+/*
+ * State rows in 8 bits: cached prefixes in 26 % of the room (d_k = 128).  A row
+ * of a state pool holds n = row_bytes / (element size * d_k) value channels of
+ * d_k states each (n = h_v d_v); channel c of a packed row is
+ *     scale[c] = max(max_k |S[c][k]| / 127, 2^-126)       fp32, rounded to nearest
+ *     code[c][k] = S[c][k] / scale[c] to the nearest integer, ties to even  int8
+ * and stands for code * scale.  Uniform steps: a value is off by at most half a
+ * scale, amax / 254.  A channel that holds a NaN or an infinity is packed as
+ * scale NaN and codes 0: all of it reads back as NaN, other channels do not see
+ * it.
+ *
+ * `states` is a pool of fp32, f16 or bf16 states (the persisted node states of a
+ * verify are one too: one layer, a row per node), `codes` and `scales` are pools
+ * of int8 rows [n][d_k] and of fp32 rows [n]: row_bytes n d_k and 4 n, the same
+ * n_layers, and n_slots of their own, the same in both.  d_k is 32, 64 or 128, n a
+ * multiple of 4.  No two of the three share a byte.
+ *
+ * gdn_pool_pack writes packed row dst_row[i] from state row src_row[i] in every
+ * layer, gdn_pool_unpack state row dst_row[i] from packed row src_row[i], i < n.
+ * src_row, dst_row, their order, the row numbers -1 (a source of -1: a row of
+ * zeros) and device errors are those of gdn_pool_copy with a src.
+ */
+int gdn_pool_pack(const gdn_pool* states, const gdn_pool* codes, const gdn_pool* scales, int32_t d_k, int32_t dtype,
+                  const int32_t* src_row, const int32_t* dst_row, int32_t n, int32_t* status, void* stream);
+int gdn_pool_unpack(const gdn_pool* codes, const gdn_pool* scales, const gdn_pool* states, int32_t d_k, int32_t dtype,
+                    const int32_t* src_row, const int32_t* dst_row, int32_t n, int32_t* status, void* stream);
+
 /* Shape of a causal-convolution history commit. */
 typedef struct gdn_conv_shape {
     int32_t batch;    /* sequences, >= 0 */
@@ -543,6 +571,143 @@ int gdn_scan_backward(const gdn_shape* shape, const int32_t* cu_seqlens, const v
                       const float* alpha, const float* beta, const void* tape, size_t tape_bytes, const void* dout,
                       const float* dfinal, void* dq, void* dk, void* dv, float* dalpha, float* dbeta, float* dstate,
                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Around the rule in a layer: the input norm, the projections to q, k, v and the
+ * output gate, the gated norm of the rule's outputs, the output projection.
+ * Serving keeps the operands of the projections in 8 bits:
+ *   activations  e4m3 codes [rows][width] and a scale byte for each GDN_GROUP
+ *                channels of a row (the last group may be shorter), a power of
+ *                two: byte b stands for 2^(b - 127), 255 for NaN (e8m0).  Scales
+ *                are [rows][scale_stride] bytes, scale_stride a multiple of 4 and
+ *                at least the number of groups; the bytes behind the last group
+ *                are neither written nor used.
+ *   weights      e4m3 codes [columns][inner] and a scale for each block of
+ *                GDN_GROUP columns x GDN_GROUP inner channels (the last ones may
+ *                be shorter), fp32 (GDN_F32) or a power of two as above (GDN_E8M0).
+ * e4m3 is the OCP format: values up to 448, steps of 2^-3 of the power of two below
+ * a value, 2^-9 at the least.  The codes a norm writes are y 2^-e to the nearest, ties to even, with the
+ * smallest e from -126 on that leaves no |y| 2^-e of the group above 448.  A group
+ * with a NaN or an infinity has scale byte 255 and codes NaN.
+ */
+#define GDN_GROUP 128       /* channels that share a scale */
+#define GDN_MAX_PARTS 8     /* outputs of one gdn_project call */
+#define GDN_MAX_WIDTH 16384 /* channels of gdn_norm_forward and gdn_norm_backward */
+#define GDN_E8M0 3          /* scale type of gdn_project: a power of two in a byte */
+
+typedef struct gdn_norm_shape {
+    int64_t rows;          /* tokens, 0 .. 2^31 - 1 */
+    int64_t x_stride;      /* elements from one row of x (backward: of r) to the next, a multiple of 8, at least width */
+    int32_t width;         /* channels, a multiple of 8 up to GDN_MAX_WIDTH */
+    int32_t dtype;         /* of x, out and dout: GDN_F32, GDN_BF16 or GDN_F16 */
+    int32_t residual_dtype;/* of residual, residual_out, r, dresidual and dx */
+    int32_t weight_dtype;
+    int32_t scale_stride;  /* bytes from one row's scales to the next (ignored without codes) */
+    float eps;             /* at least 0 */
+    float weight_offset;   /* w0: 1 where weights are stored as differences from 1 */
+} gdn_norm_shape;
+
+/*
+ * Root mean square norm with the residual's addition:
+ *     r = x + residual, rounded to residual_dtype;  residual_out = r
+ *     y = r / sqrt(mean_k r_k^2 + eps) * (w + w0)
+ * The norm is of r as stored, so the backward pass needs nothing but r.  Without a
+ * residual (NULL; residual_out is NULL then) r is x.  y goes to `out` (nullable, dtype)
+ * and, or, to `codes` and `scales` (nullable, both or none).  Sums and products
+ * are fp32.
+ * residual, residual_out, out and codes are dense [rows][width]; residual_out may be
+ * residual (no other output overlaps an input).  x, residual, residual_out, out and
+ * weight are 16-byte aligned, codes 8-byte.
+ *
+ * gdn_norm_backward: from dout [rows][width] (dtype) and r (residual_dtype; x itself, in
+ * residual_dtype = dtype, where there was no residual)
+ *     g = dout (w + w0),  s = 1 / sqrt(mean r^2 + eps)
+ *     dx = dresidual + s g - r s^3 mean_k g_k r_k,   dweight = sum_rows dout r s
+ * dx (residual_dtype; the gradient of x and of residual alike) may be dresidual
+ * (nullable: zeros).  dweight is fp32 [width]; its sums are taken in a fixed order
+ * and repeat bit for bit.  With no rows it is zero.  dx and dweight are nullable.
+ * `workspace`: gdn_norm_backward_workspace_bytes(shape) bytes, 16-byte aligned;
+ * calls that share one are ordered on one stream.
+ */
+int gdn_norm_forward(const gdn_norm_shape* shape, const void* x, const void* residual, const void* weight,
+                     void* residual_out, void* out, void* codes, void* scales, void* stream);
+size_t gdn_norm_backward_workspace_bytes(const gdn_norm_shape* shape);
+int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void* r, const void* weight,
+                      const void* dresidual, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+typedef struct gdn_gated_norm_shape {
+    int64_t rows;          /* tokens, 0 .. 2^31 - 1 */
+    int64_t x_stride;      /* elements from one row of x to the next, a multiple of 8, at least h_v d_v */
+    int64_t z_stride;      /* of z, likewise */
+    int32_t h_v;           /* value heads, >= 1, at most 2^20 */
+    int32_t d_v;           /* value channels: a multiple of 16 up to 256 */
+    int32_t x_dtype;       /* of x and dx: GDN_F32, GDN_BF16 or GDN_F16 */
+    int32_t z_dtype;       /* of z, out, dout and dz */
+    int32_t weight_dtype;
+    int32_t scale_stride;  /* bytes from one row's scales to the next (ignored without codes) */
+    float eps;             /* at least 0 */
+} gdn_gated_norm_shape;
+
+/*
+ * Gated norm of the rule's outputs, head by head:
+ *     n = x / sqrt(mean_j x_j^2 + eps)  over the d_v channels of a head
+ *     y = n w silu(z),   silu(z) = z / (1 + e^-z)
+ * x is `out` of a verify, prefill or scan ([rows][h_v][d_v]), z the gate's projection,
+ * weight [d_v].  y goes to `out` (nullable, z_dtype) and, or, to `codes` and `scales`
+ * (nullable, both or none), [rows][h_v d_v] as the output projection reads them.
+ *
+ * gdn_gated_norm_backward: with s = 1 / sqrt(mean x^2 + eps), a = 1 / (1 + e^-z) and
+ * g = dout w silu(z)
+ *     dx = s g - x s^3 mean_j g_j x_j,   dz = dout n w a (1 + z (1 - a)),
+ *     dweight = sum over rows and heads of dout n silu(z)   (fp32 [d_v])
+ * dx, dz and dweight are nullable.  Alignment, the sums' order and the workspace are
+ * those of gdn_norm_backward; dz may be dout or z, dx may be x (the same rows, dense).
+ */
+int gdn_gated_norm_forward(const gdn_gated_norm_shape* shape, const void* x, const void* z, const void* weight,
+                           void* out, void* codes, void* scales, void* stream);
+size_t gdn_gated_norm_backward_workspace_bytes(const gdn_gated_norm_shape* shape);
+int gdn_gated_norm_backward(const gdn_gated_norm_shape* shape, const void* dout, const void* x, const void* z,
+                            const void* weight, void* dx, void* dz, float* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* One output of gdn_project: columns [tokens][columns], rows `stride` elements apart. */
+typedef struct gdn_project_part {
+    void* data;       /* aligned to its element size; 16 bytes for the widest stores */
+    int64_t stride;   /* at least columns */
+    int32_t columns;  /* >= 1 */
+    int32_t reserved; /* 0 */
+} gdn_project_part;
+
+typedef struct gdn_project_shape {
+    int64_t tokens;       /* M >= 0, below 2^31 */
+    int64_t a_stride;     /* bytes from one row of a to the next, a multiple of 16, at least inner */
+    int64_t w_stride;     /* of w, likewise */
+    int32_t inner;        /* K, a multiple of 16, at least 16 */
+    int32_t a_scale_stride; /* bytes from one row of a_scales to the next, a multiple of 4, at least ceil(K / 128) */
+    int32_t w_scale_stride; /* GDN_E8M0: likewise; GDN_F32: elements, at least ceil(K / 128) */
+    int32_t w_scale_dtype;  /* GDN_F32 or GDN_E8M0 */
+    int32_t out_dtype;      /* GDN_BF16 or GDN_F16 */
+} gdn_project_shape;
+
+/*
+ * Projections of 8-bit activations by 8-bit weights,
+ *     y[m][n] = sum_g 2^(a_scales[m][g] - 127) w_scale[n / 128][g] sum_{k in group g} a[m][k] w[n][k],
+ * the columns n = 0 .. N - 1 (N = the parts' columns together) cut into parts[0],
+ * parts[1], ...: one call writes q, k, v, the gate z and the rest in the layouts the
+ * verify, the prefill and the gated norm take.  a [M][K] and w [N][K] are e4m3 codes
+ * with the scales above (a: codes and scales of gdn_norm_forward or
+ * gdn_gated_norm_forward), 16-byte aligned; a_scales and GDN_E8M0 scales are
+ * 4-byte aligned.
+ *
+ * Groups are summed in fp32, in an order that depends on the shape alone, so results
+ * repeat bit for bit; the matrix instruction adds the products within a group with
+ * about 17 bits below the largest (2e-5 of the 2-norm of y, of normal operands), which
+ * is why y is bf16 or f16 and not fp32.  f16 outputs above 65504 become infinite.  A
+ * scale of NaN, or a NaN code, makes NaN every y that it has part in.
+ */
+int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_scales, const void* w,
+                const void* w_scales, const gdn_project_part* parts, int32_t n_parts, void* stream);
 
 /*
  * Plan (and validate) the walk gdn_verify_tree takes through one tree.
