@@ -90,7 +90,8 @@ hipError_t launch(const ProjectArgs& p, hipStream_t stream) {
     };
     if (p.tokens <= 16) return go(std::integral_constant<int, 1>{});
     if (p.tokens <= 32) return go(std::integral_constant<int, 2>{});
-    return go(std::integral_constant<int, 4>{});
+    if (p.tokens <= 64) return go(std::integral_constant<int, 4>{});
+    return launch_project_tiles(p, E8M0, DT, stream);
 }
 
 }  // namespace
@@ -107,7 +108,7 @@ int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_sca
     if (shape->inner < 16 || shape->inner % 16 != 0) return GDN_ERR_SHAPE;
     const int groups = (shape->inner + GDN_GROUP - 1) / GDN_GROUP;
     for (int64_t s : {shape->a_stride, shape->w_stride})
-        if (s < shape->inner || s % 16 != 0 || s > (int64_t{1} << 31)) return GDN_ERR_SHAPE;
+        if (s < shape->inner || s % 16 != 0 || s > (int64_t{1} << 22)) return GDN_ERR_SHAPE;
     if (shape->w_scale_dtype != GDN_F32 && shape->w_scale_dtype != GDN_E8M0) return GDN_ERR_DTYPE;
     if (shape->out_dtype != GDN_BF16 && shape->out_dtype != GDN_F16) return GDN_ERR_DTYPE;
     if (shape->a_scale_stride < groups || shape->a_scale_stride % 4 != 0) return GDN_ERR_SHAPE;
@@ -128,6 +129,8 @@ int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_sca
         columns += q.columns;
         if (columns > 0x7fffffffLL - 1024) return GDN_ERR_SHAPE;
     }
+    // workgroups of the smallest tiles
+    if ((shape->tokens + 63) / 64 * ((columns + 63) / 64) > 0x7fffffffLL) return GDN_ERR_SHAPE;
     if (shape->tokens == 0) return GDN_OK;
     if (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr) return GDN_ERR_NULL;
     if (!aligned_to(a, 16) || !aligned_to(w, 16) || !aligned_to(a_scales, 4) || !aligned_to(w_scales, 4)) return GDN_ERR_ALIGN;

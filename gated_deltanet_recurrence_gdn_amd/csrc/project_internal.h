@@ -38,6 +38,9 @@ struct ProjectArgs {
     ProjectPart part[GDN_MAX_PARTS];
 };
 
+// The product in tiles (project_tile.hip).
+hipError_t launch_project_tiles(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t stream);
+
 __device__ __forceinline__ f32x4 mfma_scaled(i32x8 w, i32x8 a, f32x4 c, int w_scale, int a_scale) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, w_scale, 0, a_scale);
 }
