@@ -51,38 +51,69 @@ __device__ __forceinline__ uint16_t half_bits(float x) {
     return __builtin_bit_cast(uint16_t, (_Float16)x);
 }
 
-// The part that holds column n (n < columns).
-__device__ __forceinline__ int part_of(const ProjectArgs& p, int n) {
-    int i = 0;
-    while (i + 1 < p.n_parts && n >= p.part[i + 1].begin) ++i;
-    return i;
+// The part that holds column n (n < columns).  Selected, not indexed: an index that only the device knows would
+// put the arguments into scratch memory.
+struct Home {
+    uint16_t* data;  // of its first column
+    int64_t stride;
+    int32_t begin, end, wide;
+};
+
+__device__ __forceinline__ Home home_of(const ProjectArgs& p, int n) {
+    Home h = {static_cast<uint16_t*>(p.part[0].data), p.part[0].stride, 0, p.columns, p.part[0].wide};
+#pragma unroll
+    for (int i = 1; i < GDN_MAX_PARTS; ++i) {
+        if (i >= p.n_parts) continue;
+        const ProjectPart& q = p.part[i];
+        if (n >= q.begin) {
+            h = Home{static_cast<uint16_t*>(q.data), q.stride, q.begin, p.columns, q.wide};
+        } else if (q.begin < h.end) {
+            h.end = q.begin;
+        }
+    }
+    return h;
 }
 
-// Columns n .. n + 3 (n a multiple of four) of token m, as far as there are any.  `home`: the part of all of them
-// where one holds them all, or -1.
+// Four columns at once.
 template <int DT>
-__device__ __forceinline__ void store_columns(const ProjectArgs& p, int home, int m, int n, f32x4 y) {
+__device__ __forceinline__ void store_wide(uint16_t* at, f32x4 y) {
     const uint16_t h[4] = {half_bits<DT>(y[0]), half_bits<DT>(y[1]), half_bits<DT>(y[2]), half_bits<DT>(y[3])};
-    if (home >= 0 && p.part[home].wide) {
-        const ProjectPart& q = p.part[home];
-        uint16_t* at = static_cast<uint16_t*>(q.data) + (int64_t)m * q.stride + (n - q.begin);
-        *reinterpret_cast<u32x2*>(at) = u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
-        return;
-    }
+    *reinterpret_cast<u32x2*>(at) = u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+}
+
+// Columns n .. n + 3 of token m one by one, as far as there are any, each to the part that holds it.
+template <int DT>
+__device__ __forceinline__ void store_narrow(const ProjectArgs& p, int64_t m, int n, f32x4 y) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (n + j >= p.columns) break;
-        const ProjectPart& q = p.part[part_of(p, n + j)];
-        static_cast<uint16_t*>(q.data)[(int64_t)m * q.stride + (n + j - q.begin)] = h[j];
+        const Home h = home_of(p, n + j);
+        h.data[m * h.stride + (n + j - h.begin)] = half_bits<DT>(y[j]);
     }
 }
 
-// The part that holds columns n0 .. n0 + count - 1, or -1 where there is no single one.
-__device__ __forceinline__ int home_of(const ProjectArgs& p, int n0, int count) {
-    if (n0 + count > p.columns) return -1;
-    const int i = part_of(p, n0);
-    const int end = i + 1 < p.n_parts ? p.part[i + 1].begin : p.columns;
-    return n0 + count <= end ? i : -1;
+// FN x FM results of a wave: columns c0 + 16 s + 4 quarter .. + 3 of tokens m0 + 16 t + r.
+template <int DT, int FN, int FM>
+__device__ __forceinline__ void store_results(const ProjectArgs& p, int64_t m0, int c0, int r, int quarter, const f32x4 (&y)[FN][FM]) {
+    if (c0 >= p.columns) return;
+    const Home home = home_of(p, c0);
+    if (home.wide && c0 + 16 * FN <= home.end) {
+        uint16_t* at = home.data + (m0 + r) * home.stride + (c0 - home.begin + 4 * quarter);
+#pragma unroll
+        for (int t = 0; t < FM; ++t) {
+            if (m0 + 16 * t + r < p.tokens) {
+#pragma unroll
+                for (int s = 0; s < FN; ++s) store_wide<DT>(at + 16 * s, y[s][t]);
+            }
+            at += 16 * home.stride;
+        }
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < FM; ++t)
+#pragma unroll
+        for (int s = 0; s < FN; ++s)
+            if (m0 + 16 * t + r < p.tokens) store_narrow<DT>(p, m0 + 16 * t + r, c0 + 16 * s + 4 * quarter, y[s][t]);
 }
 
 }  // namespace gdn

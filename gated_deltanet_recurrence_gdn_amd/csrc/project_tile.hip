@@ -94,19 +94,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const Pro
         }
     };
 
-    // scales: a's as four bytes of four groups; w's block is the wave's own
+    // Scales: a's as the bytes of four groups, w's (the wave's own block) one by one.  Both are loaded ahead and
+    // first used behind a step's wait for everything, so that no use waits for the rows on their way to LDS; vector
+    // loads, as scalar ones would make every wait for an LDS read one for all of them.
     const uint8_t* sa[T::FM];
-    uint32_t quad[T::FM];
+    uint32_t quad[T::FM], ahead[T::FM];
 #pragma unroll
     for (int t = 0; t < T::FM; ++t) {
         const int64_t m = m0 + (wm * T::FM + t) * 16 + r;
         sa[t] = p.a_scales + (m < p.tokens ? m : p.tokens - 1) * p.a_scale_stride;
-        quad[t] = 0;
+        ahead[t] = *reinterpret_cast<const uint32_t*>(sa[t]);
     }
+    int lane_zero;
+    asm("v_mov_b32 %0, 0" : "=v"(lane_zero));
     const int64_t block = min(n0 + wn * T::FN * 16, p.columns - 1) / GDN_GROUP;
     auto w_scale = [&](int g) -> float {
-        if constexpr (E8M0) return __builtin_bit_cast(float, (int)(static_cast<const uint8_t*>(p.w_scales) + block * p.w_scale_stride)[g]);
-        return (static_cast<const float*>(p.w_scales) + block * p.w_scale_stride)[g];
+        if constexpr (E8M0) return __builtin_bit_cast(float, (int)(static_cast<const uint8_t*>(p.w_scales) + block * p.w_scale_stride)[g + lane_zero]);
+        return (static_cast<const float*>(p.w_scales) + block * p.w_scale_stride)[g + lane_zero];
     };
 
     f32x4 acc[T::FN][T::FM];
@@ -124,9 +128,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const Pro
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         const float sw = next;
-        if ((g & 3) == 0)
+        if ((g & 3) == 0) {
 #pragma unroll
-            for (int t = 0; t < T::FM; ++t) quad[t] = *reinterpret_cast<const uint32_t*>(sa[t] + g);
+            for (int t = 0; t < T::FM; ++t) {
+                quad[t] = ahead[t];
+                if (g + 4 < p.groups) ahead[t] = *reinterpret_cast<const uint32_t*>(sa[t] + g + 4);
+            }
+        }
         if (g + 1 < p.groups) {
             stage(g + 1, (g + 1) & 1);
             next = w_scale(g + 1);
@@ -159,14 +167,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const Pro
             }
         }
     }
-    const int c0 = n0 + wn * T::FN * 16, home = home_of(p, c0, T::FN * 16);
-#pragma unroll
-    for (int t = 0; t < T::FM; ++t) {
-        const int64_t m = m0 + (wm * T::FM + t) * 16 + r;
-        if (m >= p.tokens) continue;
-#pragma unroll
-        for (int s = 0; s < T::FN; ++s) store_columns<DT>(p, home, (int)m, c0 + 16 * s + 4 * quarter, acc[s][t]);
-    }
+    store_results<DT>(p, m0 + wm * T::FM * 16, n0 + wn * T::FN * 16, r, quarter, acc);
 }
 
 template <int DT, bool E8M0, int TM, int TN, int WM, int WN>
