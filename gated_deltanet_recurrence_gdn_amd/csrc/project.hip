@@ -35,9 +35,9 @@ __global__ __launch_bounds__(64 * kWaves) void project_rows_kernel(const Project
         a[t] = p.a + (int64_t)m * p.a_stride;
         sa[t] = p.a_scales + (int64_t)m * p.a_scale_stride;
     }
-    f32x4 acc[1][MT];
+    f32x4 acc[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[0][t] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
     const i32x4 zero = {0, 0, 0, 0};
     auto piece = [&](const uint8_t* row, int k) { return k < p.inner ? *reinterpret_cast<const i32x4*>(row + k) : zero; };
     auto operand = [&](const uint8_t* row, int k) {
@@ -55,24 +55,29 @@ __global__ __launch_bounds__(64 * kWaves) void project_rows_kernel(const Project
         for (int t = 0; t < MT; ++t) {
             const i32x8 av = operand(a[t], k);
             if constexpr (E8M0) {
-                acc[0][t] = mfma_scaled(wv, av, acc[0][t], sw, sa[t][g]);
+                acc[t] = mfma_scaled(wv, av, acc[t], sw, sa[t][g]);
             } else {
                 const f32x4 s = mfma_scaled(wv, av, f32x4{0, 0, 0, 0}, kOne, sa[t][g]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[0][t][j] += fw * s[j];
+                for (int j = 0; j < 4; ++j) acc[t][j] += fw * s[j];
             }
         }
     }
     if (wave > 0)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) part[wave - 1][t][lane] = acc[0][t];
+        for (int t = 0; t < MT; ++t) part[wave - 1][t][lane] = acc[t];
     __syncthreads();
     if (wave > 0) return;
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int v = 0; v < kWaves - 1; ++v) acc[0][t] += part[v][t][lane];
-    store_results<DT>(p, m0, n0, r, quarter, acc);
+        for (int v = 0; v < kWaves - 1; ++v) acc[t] += part[v][t][lane];
+    const int at = n0 + 4 * quarter;
+    if (at >= p.columns) return;
+    const Home home = home_of(p, at);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+        if (m0 + 16 * t + r < p.tokens) store_four<DT>(p, home, m0 + 16 * t + r, at, acc[t]);
 }
 
 bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -122,7 +127,9 @@ int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_sca
         p.part[i].data = q.data;
         p.part[i].stride = q.stride;
         p.part[i].begin = (int32_t)columns;
-        p.part[i].wide = columns % 4 == 0 && q.stride % 4 == 0 && aligned_to(q.data, 8);
+        p.part[i].wide = 0;
+        if (columns % 4 == 0 && q.stride % 4 == 0 && aligned_to(q.data, 8)) p.part[i].wide = 1;
+        if (columns % 8 == 0 && q.stride % 8 == 0 && aligned_to(q.data, 16)) p.part[i].wide = 2;
         columns += q.columns;
         if (columns > 0x7fffffffLL - 1024) return GDN_ERR_SHAPE;
     }

@@ -23,7 +23,7 @@ struct ProjectPart {
     void* data;
     int64_t stride;  // elements
     int32_t begin;   // its first column
-    int32_t wide;    // 1: four columns from a multiple of four of the whole on can be stored at once
+    int32_t wide;    // columns that can be stored at once, from multiples of them on: 0 (one), 1 (four), 2 (eight)
 };
 
 struct ProjectArgs {
@@ -74,11 +74,10 @@ __device__ __forceinline__ Home home_of(const ProjectArgs& p, int n) {
     return h;
 }
 
-// Four columns at once.
 template <int DT>
-__device__ __forceinline__ void store_wide(uint16_t* at, f32x4 y) {
+__device__ __forceinline__ u32x2 four(f32x4 y) {
     const uint16_t h[4] = {half_bits<DT>(y[0]), half_bits<DT>(y[1]), half_bits<DT>(y[2]), half_bits<DT>(y[3])};
-    *reinterpret_cast<u32x2*>(at) = u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+    return u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
 }
 
 // Columns n .. n + 3 of token m one by one, as far as there are any, each to the part that holds it.
@@ -92,28 +91,11 @@ __device__ __forceinline__ void store_narrow(const ProjectArgs& p, int64_t m, in
     }
 }
 
-// FN x FM results of a wave: columns c0 + 16 s + 4 quarter .. + 3 of tokens m0 + 16 t + r.
-template <int DT, int FN, int FM>
-__device__ __forceinline__ void store_results(const ProjectArgs& p, int64_t m0, int c0, int r, int quarter, const f32x4 (&y)[FN][FM]) {
-    if (c0 >= p.columns) return;
-    const Home home = home_of(p, c0);
-    if (home.wide && c0 + 16 * FN <= home.end) {
-        uint16_t* at = home.data + (m0 + r) * home.stride + (c0 - home.begin + 4 * quarter);
-#pragma unroll
-        for (int t = 0; t < FM; ++t) {
-            if (m0 + 16 * t + r < p.tokens) {
-#pragma unroll
-                for (int s = 0; s < FN; ++s) store_wide<DT>(at + 16 * s, y[s][t]);
-            }
-            at += 16 * home.stride;
-        }
-        return;
-    }
-#pragma unroll
-    for (int t = 0; t < FM; ++t)
-#pragma unroll
-        for (int s = 0; s < FN; ++s)
-            if (m0 + 16 * t + r < p.tokens) store_narrow<DT>(p, m0 + 16 * t + r, c0 + 16 * s + 4 * quarter, y[s][t]);
+// Columns n .. n + 3 of token m; `home` holds column n.
+template <int DT>
+__device__ __forceinline__ void store_four(const ProjectArgs& p, const Home& home, int64_t m, int n, f32x4 y) {
+    if (home.wide && n + 4 <= home.end) *reinterpret_cast<u32x2*>(home.data + m * home.stride + (n - home.begin)) = four<DT>(y);
+    else store_narrow<DT>(p, m, n, y);
 }
 
 }  // namespace gdn
