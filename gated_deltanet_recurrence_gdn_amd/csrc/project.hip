@@ -7,7 +7,7 @@
 // power of two (and the weights', where they are e8m0) goes into the instruction, so
 // only fp32 weight scales cost vector operations, one multiply-add an accumulator and
 // group.
-#include <cmath>
+#include <algorithm>
 #include <type_traits>
 
 #include "project_internal.h"
@@ -15,84 +15,120 @@
 namespace gdn {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kMaxWaves = 8;
 
-// 16 columns and 16 MT tokens a workgroup; its waves share the groups and are summed
-// through LDS in their order.
-template <int DT, bool E8M0, int MT>
-__global__ __launch_bounds__(64 * kWaves) void project_rows_kernel(const ProjectArgs p) {
-    __shared__ f32x4 part[kWaves - 1][MT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Few tokens: the weights are read once, at the memory's rate.  16 NT columns and 16 MT tokens a workgroup.  Its waves
+// take the groups in turn, each for itself: a group's rows come into the wave's own LDS in whole lines (loads straight
+// into an operand's registers touch 16 rows with every 16 lanes, which the address unit takes one by one: 16 tokens x
+// 16384 x 5120 31 us so, 17 through LDS, 4.9 TB/s of weights), and the next group's are on their way during the
+// products.  The waves' sums are joined through LDS in their order.
+template <int DT, bool E8M0, int MT, int NT>
+__global__ __launch_bounds__(64 * kMaxWaves) void project_rows_kernel(const ProjectArgs p) {
+    extern __shared__ __align__(16) unsigned char rows_lds[];
+    constexpr int kRows = 16 * (NT + MT), kStage = kRows * GDN_GROUP;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int r = lane & 15, quarter = lane >> 4;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
-    const int n = n0 + r < p.columns ? n0 + r : p.columns - 1;
-    const uint8_t* w = p.w + (int64_t)n * p.w_stride;
-    const uint8_t* a[MT];
-    const uint8_t* sa[MT];
+    const int blocks_n = (p.columns + 16 * NT - 1) / (16 * NT);
+    const int n0 = blockIdx.x % blocks_n * (16 * NT), m0 = blockIdx.x / blocks_n * (16 * MT);
+    // rows past the last token or column, channels past the last one: past the buffers' ends, zeros
+    const uint32_t as = (uint32_t)p.a_stride, ws = (uint32_t)p.w_stride;
+    const int rows_a = min(16 * MT, p.tokens - m0);
+    const rsrc_t ra = rsrc_of(p.a + (int64_t)m0 * p.a_stride, (rows_a - 1) * as + p.inner);
+    const rsrc_t rw = rsrc_of(p.w + (int64_t)n0 * p.w_stride, (min(16 * NT, p.columns - n0) - 1) * ws + p.inner);
+    const rsrc_t rs = rsrc_of(p.a_scales + (int64_t)m0 * p.a_scale_stride, rows_a * p.a_scale_stride);
+    const int64_t block = (int64_t)(n0 / GDN_GROUP) * p.w_scale_stride;
+    const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;  // of row lane / 8 of the eight a load takes
+    const uint32_t oa = (lane >> 3) * as + chunk, ow = (lane >> 3) * ws + chunk, os = r * p.a_scale_stride;
+    unsigned char* own = rows_lds + wave * kStage;
+    int scale[MT];
+    float sw;
+    auto stage = [&](int g) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int m = m0 + 16 * t + r < p.tokens ? m0 + 16 * t + r : p.tokens - 1;
-        a[t] = p.a + (int64_t)m * p.a_stride;
-        sa[t] = p.a_scales + (int64_t)m * p.a_scale_stride;
-    }
-    f32x4 acc[MT];
+        for (int t = 0; t < MT; ++t) scale[t] = load_byte(rs, os, g + t * 16 * p.a_scale_stride);
+        if constexpr (E8M0) sw = __builtin_bit_cast(float, (int)static_cast<const uint8_t*>(p.w_scales)[block + g]);
+        else sw = static_cast<const float*>(p.w_scales)[block + g];
+        const bool in_row = g * GDN_GROUP + chunk < p.inner;
+        const uint32_t fw = in_row ? ow + g * GDN_GROUP : kPast, fa = in_row ? oa + g * GDN_GROUP : kPast;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
-    const i32x4 zero = {0, 0, 0, 0};
-    auto piece = [&](const uint8_t* row, int k) { return k < p.inner ? *reinterpret_cast<const i32x4*>(row + k) : zero; };
-    auto operand = [&](const uint8_t* row, int k) {
-        const i32x4 lo = piece(row, k), hi = piece(row, k + 16);
+        for (int b = 0; b < 2 * NT; ++b) load_lds(rw, own + b * 1024, fw + b * 8 * ws);
+#pragma unroll
+        for (int b = 0; b < 2 * MT; ++b) load_lds(ra, own + (2 * NT + b) * 1024, fa + b * 8 * as);
+    };
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int s = 0; s < NT; ++s)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[s][t] = f32x4{0, 0, 0, 0};
+    const int o0 = r * GDN_GROUP + (((2 * quarter) ^ (r & 7)) * 16), o1 = o0 ^ 16;
+    auto operand = [&](int row) {
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(own + row * GDN_GROUP + o0), hi = *reinterpret_cast<const i32x4*>(own + row * GDN_GROUP + o1);
         return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
-    for (int g = wave; g < p.groups; g += kWaves) {
-        const int k = g * GDN_GROUP + quarter * 32;
-        const i32x8 wv = operand(w, k);
-        int sw = kOne;
-        float fw = 1;
-        if constexpr (E8M0) sw = static_cast<const uint8_t*>(p.w_scales)[(int64_t)(n0 / GDN_GROUP) * p.w_scale_stride + g];
-        else fw = static_cast<const float*>(p.w_scales)[(int64_t)(n0 / GDN_GROUP) * p.w_scale_stride + g];
+    if (wave < p.groups) stage(wave);
+    for (int g = wave; g < p.groups; g += waves) {
+        wait_loads();
+        i32x8 wv[NT], av[MT];
+        int by[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const i32x8 av = operand(a[t], k);
-            if constexpr (E8M0) {
-                acc[t] = mfma_scaled(wv, av, acc[t], sw, sa[t][g]);
-            } else {
-                const f32x4 s = mfma_scaled(wv, av, f32x4{0, 0, 0, 0}, kOne, sa[t][g]);
+        for (int s = 0; s < NT; ++s) wv[s] = operand(16 * s);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[t][j] += fw * s[j];
+        for (int t = 0; t < MT; ++t) av[t] = operand(16 * (NT + t));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) by[t] = scale[t];
+        const float now = sw;
+        wait_reads();
+        if (g + waves < p.groups) stage(g + waves);
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if constexpr (E8M0) {
+                    acc[s][t] = mfma_scaled(wv[s], av[t], acc[s][t], __builtin_bit_cast(int, now), by[t]);
+                } else {
+                    acc[s][t] += now * mfma_scaled(wv[s], av[t], f32x4{0, 0, 0, 0}, kOne, by[t]);
+                }
             }
-        }
     }
-    if (wave > 0)
+    // every wave's own LDS is free: its loads are done
+    f32x4* part = reinterpret_cast<f32x4*>(own);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) part[wave - 1][t][lane] = acc[t];
+    for (int s = 0; s < NT; ++s)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) part[(s * MT + t) * 64 + lane] = acc[s][t];
     __syncthreads();
-    if (wave > 0) return;
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int v = 0; v < kWaves - 1; ++v) acc[t] += part[v][t][lane];
-    const int at = n0 + 4 * quarter;
-    if (at >= p.columns) return;
-    const Home home = home_of(p, at);
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        if (m0 + 16 * t + r < p.tokens) store_four<DT>(p, home, m0 + 16 * t + r, at, acc[t]);
+    for (int i = wave; i < NT * MT; i += waves) {
+        const f32x4* from = reinterpret_cast<const f32x4*>(rows_lds) + i * 64 + lane;
+        f32x4 y = *from;
+        for (int v = 1; v < waves; ++v) y += from[v * (kStage / 16)];
+        const int at = n0 + 16 * (i / MT) + 4 * quarter, m = m0 + 16 * (i % MT) + r;
+        if (at < p.columns && m < p.tokens) store_four<DT>(p, home_of(p, at), m, at, y);
+    }
 }
 
 bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 template <int DT, bool E8M0>
 hipError_t launch(const ProjectArgs& p, hipStream_t stream) {
-    auto go = [&](auto mt) {
-        constexpr int MT = decltype(mt)::value;
-        const dim3 grid((p.columns + 15) / 16, (p.tokens + 16 * MT - 1) / (16 * MT));
-        hipLaunchKernelGGL((project_rows_kernel<DT, E8M0, MT>), grid, dim3(64 * kWaves), 0, stream, p);
+    auto go = [&](auto mt, auto nt) {
+        constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, kStage = 16 * (NT + MT) * GDN_GROUP;
+        static_assert(kMaxWaves * kStage <= kMaxLdsBytes && NT * MT * 1024 <= kStage, "");
+        const hipError_t e = allow_max_lds<&project_rows_kernel<DT, E8M0, MT, NT>>();
+        if (e != hipSuccess) return e;
+        const int waves = std::min(p.groups, kMaxWaves);
+        const int64_t grid = ((int64_t)p.columns + 16 * NT - 1) / (16 * NT) * ((p.tokens + 16 * MT - 1) / (16 * MT));
+        hipLaunchKernelGGL((project_rows_kernel<DT, E8M0, MT, NT>), dim3((unsigned)grid), dim3(64 * waves), waves * kStage, stream, p);
         return hipGetLastError();
     };
-    if (p.tokens <= 16) return go(std::integral_constant<int, 1>{});
-    if (p.tokens <= 32) return go(std::integral_constant<int, 2>{});
-    if (p.tokens <= 64) return go(std::integral_constant<int, 4>{});
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 2> two;
+    constexpr std::integral_constant<int, 4> four;
+    // 64 columns a workgroup read a less often, 32 give more workgroups: 64 tokens x 16384 x 5120 take 23 and 29 us,
+    // x 5120 x 6144 20 and 13
+    const bool wide = (p.columns + 63) / 64 >= device_cus();
+    if (p.tokens <= 16) return wide ? go(one, four) : go(one, two);
+    if (p.tokens <= 32) return wide ? go(two, four) : go(two, two);
+    // from 65 tokens on a tile (128 tokens x 16384 x 5120: 32 us; rows for 64 tokens twice: 47)
+    if (p.tokens <= 64) return wide ? go(four, four) : go(four, two);
     return launch_project_tiles(p, E8M0, DT, stream);
 }
 

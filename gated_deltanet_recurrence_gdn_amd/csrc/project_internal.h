@@ -45,6 +45,54 @@ __device__ __forceinline__ f32x4 mfma_scaled(i32x8 w, i32x8 a, f32x4 c, int w_sc
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, w_scale, 0, a_scale);
 }
 
+// Buffers: loads past `bytes` give zeros.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef __attribute__((address_space(3))) void lds_void;
+constexpr uint32_t kPast = 0x80000000u;  // past the end of every buffer here, whatever row is added
+
+__device__ __forceinline__ rsrc_t rsrc_of(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+}
+
+__device__ __forceinline__ i32x4 load_regs(rsrc_t from, uint32_t offset) {
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(from, offset, 0, 0));
+}
+
+__device__ __forceinline__ int load_word(rsrc_t from, uint32_t offset) {
+    return __builtin_amdgcn_raw_buffer_load_b32(from, offset, 0, 0);
+}
+
+__device__ __forceinline__ int load_byte(rsrc_t from, uint32_t lane_offset, int offset) {
+    return __builtin_amdgcn_raw_buffer_load_b8(from, lane_offset, offset, 0);
+}
+
+__device__ __forceinline__ float load_float(rsrc_t from, int offset) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, 0, offset, 0));
+}
+
+// 16 bytes a lane into LDS, lane after lane from `to` on.
+__device__ __forceinline__ void load_lds(rsrc_t from, unsigned char* to, uint32_t offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void*)to, 16, offset, 0, 0, 0);
+}
+
+__device__ __forceinline__ void load_lds_word(rsrc_t from, unsigned char* to, uint32_t offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void*)to, 4, offset, 0, 0, 0);
+}
+
+// This wave's loads, into registers and LDS, are there.
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
+// This wave's LDS reads are done: what they read may be overwritten.
+__device__ __forceinline__ void wait_reads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
 template <int DT>
 __device__ __forceinline__ uint16_t half_bits(float x) {
     if constexpr (DT == GDN_BF16) return f32_to_bf16(x);

@@ -149,3 +149,14 @@ def test_another_stream():
     gb.gdn_project(*x, outs, stream=side.cuda_stream)
     side.synchronize()
     check(*x, outs)
+
+
+# sizes that take each of the tiles: 256 x 256, 128 x 128 two and one a CU, 64 x 128; more than 64 groups
+@pytest.mark.parametrize("scales", ["f32", "e8m0"])
+@pytest.mark.parametrize("M,parts,K", [(1000, [16000, 380], 272), (300, [16380], 400), (500, [5000, 100], 640), (70, [5100], 384),
+                                       (70, [300], 8400), (300, [16384], 8336), (1024, [16384], 8464), (3, [200], 8400), (60, [16400], 1168)])
+def test_tiles(M, parts, K, scales):
+    x = operands(M, M, sum(parts), K, scales)
+    outs = outputs(M, parts, torch.bfloat16)
+    gb.gdn_project(*x, outs)
+    check(*x, outs)
