@@ -726,6 +726,45 @@ def gdn_scan_backward(cu_seqlens, q, k, v, alpha, beta, tape, dout, dq, dk, dv, 
 
 
 # ---------------------------------------------------------------------------
+# calls whose addresses go to ctypes as plain integers (a third of the time of an object for each)
+# ---------------------------------------------------------------------------
+def _site(name, stream):
+    """The current device and the handle of the stream to launch on, which is one of that device."""
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    if isinstance(stream, int):
+        return device, stream
+    on = getattr(stream, "device_index", device)
+    if on != device:
+        raise ValueError(f"{name}: the stream is on cuda:{on}, the current device is cuda:{device}")
+    return device, stream.cuda_stream
+
+
+def _at(t, name, device, dense=True):
+    """The address of a tensor on the current device, which is contiguous where it has to be dense."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a device tensor")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(name, args, keep, prepare):
+    if prepare:
+        typed = [a if isinstance(a, (ctypes.Array, type(ctypes.byref(_i32())))) else t(a) for a, t in zip(args, _SIGS[name])]
+        return PreparedCall(name, typed, (*keep, args))
+    rc = getattr(_lib or lib(), name)(*args)
+    if rc != 0:
+        raise GdnError(rc, name)
+    return None
+
+
+# ---------------------------------------------------------------------------
 # rows of a state pool
 # ---------------------------------------------------------------------------
 def _pool_structs(pools, name="pools"):
@@ -866,14 +905,17 @@ def _pack_pools(states, codes, scales):
     return structs, dk, _dtype_code(states)
 
 
-def _pool_rows(name, pools, src_rows, dst_rows, status, stream):
+def _pool_call(name, pools, structs, dk, dtype, src_rows, dst_rows, status, stream, prepare):
     n = _int_array(src_rows, "src_rows")
     _expect(dst_rows, "dst_rows", (n,), torch.int32)
     _check_status(status)
     _pool_ptrs(pools, "states, codes and scales")
-    rows = (_dev_ptr(src_rows, "src_rows"), _dev_ptr(dst_rows, "dst_rows"), _i32(n), _dev_ptr(status, "status"), _stream(stream))
-    _on_current_device(name, stream, *pools, src_rows, dst_rows, status)
-    return rows
+    device, handle = _site(name, stream)
+    for t in pools:
+        _at(t, "states, codes and scales", device, False)
+    args = (*structs, dk, dtype, _at(src_rows, "src_rows", device), _at(dst_rows, "dst_rows", device), n,
+            _at(status, "status", device), handle)
+    return _call(name, args, (*pools, src_rows, dst_rows, status), prepare)
 
 
 def gdn_pool_pack(states, codes, scales, src_rows, dst_rows, *, status=None, stream=None, prepare: bool = False):
@@ -881,24 +923,28 @@ def gdn_pool_pack(states, codes, scales, src_rows, dst_rows, *, status=None, str
     dst_rows[i] of ``codes`` (int8, the same but for its slots) and ``scales`` (fp32 [layers][slots][h_v][d_v]); see
     include/gdn.h.  Persisted node states [B][N][h_v][d_v][d_k] are a pool of one layer: ``persist.flatten(0, 1)[None]``."""
     (st, co, sc), dk, dtype = _pack_pools(states, codes, scales)
-    rows = _pool_rows("gdn_pool_pack", (states, codes, scales), src_rows, dst_rows, status, stream)
-    return _invoke("gdn_pool_pack", (st, co, sc, _i32(dk), _i32(dtype), *rows),
-                   (states, codes, scales, src_rows, dst_rows, status), prepare)
+    return _pool_call("gdn_pool_pack", (states, codes, scales), (st, co, sc), dk, dtype, src_rows, dst_rows, status, stream,
+                      prepare)
 
 
 def gdn_pool_unpack(codes, scales, states, src_rows, dst_rows, *, status=None, stream=None, prepare: bool = False):
     """Read 8-bit rows src_rows[i] of ``codes`` and ``scales`` back to rows dst_rows[i] of ``states``; the arguments are
     those of :func:`gdn_pool_pack`."""
     (st, co, sc), dk, dtype = _pack_pools(states, codes, scales)
-    rows = _pool_rows("gdn_pool_unpack", (states, codes, scales), src_rows, dst_rows, status, stream)
-    return _invoke("gdn_pool_unpack", (co, sc, st, _i32(dk), _i32(dtype), *rows),
-                   (states, codes, scales, src_rows, dst_rows, status), prepare)
+    return _pool_call("gdn_pool_unpack", (states, codes, scales), (co, sc, st), dk, dtype, src_rows, dst_rows, status, stream,
+                      prepare)
 
 
 # ---------------------------------------------------------------------------
 # around the rule: norms and projections
 # ---------------------------------------------------------------------------
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_CODE = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float16: GDN_F16}
+
+
+def _code(t) -> int:
+    c = _CODE.get(t.dtype)
+    return _dtype_code(t) if c is None else c
 
 
 def _rows_of(t, name, tail):
@@ -906,16 +952,17 @@ def _rows_of(t, name, tail):
     one dimension before them the rows may be apart, with more the tensor is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
-    d = t.dim() - tail
+    size = t.shape
+    d = len(size) - tail
     if d < 1:
-        raise ValueError(f"{name} must have at least {tail + 1} dimensions, got shape {tuple(t.shape)}")
-    row = 1
-    for k in range(d, t.dim()):
-        row *= t.shape[k]
+        raise ValueError(f"{name} must have at least {tail + 1} dimensions, got shape {tuple(size)}")
+    row = size[d]
+    for k in range(d + 1, d + tail):
+        row *= size[k]
     if t.is_contiguous():
         return (t.numel() // row if row else 0), row
-    size, strides, want = t.shape, t.stride(), 1
-    for k in range(t.dim() - 1, d - 1, -1):
+    strides, want = t.stride(), 1
+    for k in range(d + tail - 1, d - 1, -1):
         if size[k] != 1 and strides[k] != want:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
         want *= size[k]
@@ -931,8 +978,8 @@ def _check_codes(codes, scales, rows, width):
     if codes is None:
         return 0
     _expect(codes, "codes", (rows, width), _E4M3)
-    _expect(scales, "scales", (rows, None), _E8M0)
-    groups, stride = -(-width // GDN_GROUP), scales.shape[1]
+    groups, stride = -(-width // GDN_GROUP), _shape_of(scales, "scales", 2)[1]
+    _expect(scales, "scales", (rows, stride), _E8M0)
     if stride < groups or stride % 4:
         raise ValueError(f"scales must have a multiple of 4 columns, at least {groups}, got {stride}")
     return stride
@@ -950,20 +997,20 @@ def gdn_norm_forward(x, weight, *, out=None, codes=None, scales=None, residual=N
     sum kept in ``residual_out``; to ``out`` and, or, to e4m3 ``codes`` [rows][width] with e8m0 ``scales``; see
     include/gdn.h."""
     rows, stride = _rows_of(x, "x", 1)
-    width = x.shape[-1]
+    shape, dtype = x.shape, _code(x)
+    width = shape[-1]
     _expect(weight, "weight", (width,))
-    _expect(out, "out", x.shape, x.dtype)
-    _expect(residual, "residual", x.shape)
-    _expect(residual_out, "residual_out", x.shape, None if residual is None else residual.dtype)
-    scale_stride = _check_codes(codes, scales, rows, width)
-    dtype = _dtype_code(x)
-    sh = GdnNormShape(rows, stride, width, dtype, dtype if residual is None else _dtype_code(residual), _dtype_code(weight),
+    _expect(out, "out", shape, x.dtype)
+    _expect(residual, "residual", shape)
+    _expect(residual_out, "residual_out", shape, None if residual is None else residual.dtype)
+    scale_stride = 0 if codes is None and scales is None else _check_codes(codes, scales, rows, width)
+    sh = GdnNormShape(rows, stride, width, dtype, dtype if residual is None else _code(residual), _code(weight),
                       scale_stride, eps, weight_offset)
-    args = (ctypes.byref(sh), _vp(x.data_ptr()), _dev_ptr(residual, "residual"), _dev_ptr(weight, "weight"),
-            _dev_ptr(residual_out, "residual_out"), _dev_ptr(out, "out"), _dev_ptr(codes, "codes"),
-            _dev_ptr(scales, "scales"), _stream(stream))
-    _on_current_device("gdn_norm_forward", stream, x, residual, weight, residual_out, out, codes, scales)
-    return _invoke("gdn_norm_forward", args, (sh, x, residual, weight, residual_out, out, codes, scales), prepare)
+    device, handle = _site("gdn_norm_forward", stream)
+    args = (ctypes.byref(sh), _at(x, "x", device, False), _at(residual, "residual", device), _at(weight, "weight", device),
+            _at(residual_out, "residual_out", device), _at(out, "out", device), _at(codes, "codes", device),
+            _at(scales, "scales", device), handle)
+    return _call("gdn_norm_forward", args, (sh, x, residual, weight, residual_out, out, codes, scales), prepare)
 
 
 def gdn_norm_backward(dout, r, weight, dx=None, dweight=None, *, dresidual=None, eps: float = 1e-6,
@@ -972,34 +1019,34 @@ def gdn_norm_backward(dout, r, weight, dx=None, dweight=None, *, dresidual=None,
     gradient that reached residual_out; ``dx`` (r's dtype) is the gradient of x and of the residual, ``dweight`` (fp32)
     that of the weight.  ``workspace`` is allocated here with torch when omitted."""
     rows, stride = _rows_of(r, "r", 1)
-    width = r.shape[-1]
-    _expect(dout, "dout", r.shape)
+    shape, dtype = r.shape, r.dtype
+    width = shape[-1]
     if dout is None:
         raise ValueError("dout is required")
+    _expect(dout, "dout", shape)
     _expect(weight, "weight", (width,))
-    _expect(dresidual, "dresidual", r.shape, r.dtype)
-    _expect(dx, "dx", r.shape, r.dtype)
+    _expect(dresidual, "dresidual", shape, dtype)
+    _expect(dx, "dx", shape, dtype)
     _expect(dweight, "dweight", (width,), torch.float32)
-    sh = GdnNormShape(rows, stride, width, _dtype_code(dout), _dtype_code(r), _dtype_code(weight), 0, eps, weight_offset)
+    sh = GdnNormShape(rows, stride, width, _code(dout), _code(r), _code(weight), 0, eps, weight_offset)
+    ref = ctypes.byref(sh)
     if workspace is None and dweight is not None:
-        need = lib().gdn_norm_backward_workspace_bytes(ctypes.byref(sh))
-        workspace = _workspace(int(need), r.device, stream)
-    args = (ctypes.byref(sh), _dev_ptr(dout, "dout"), _vp(r.data_ptr()), _dev_ptr(weight, "weight"),
-            _dev_ptr(dresidual, "dresidual"), _dev_ptr(dx, "dx"), _dev_ptr(dweight, "dweight"),
-            _dev_ptr(workspace, "workspace"), ctypes.c_size_t(0 if workspace is None else _bytes_of(workspace)),
-            _stream(stream))
-    _on_current_device("gdn_norm_backward", stream, dout, r, weight, dresidual, dx, dweight, workspace)
-    return _invoke("gdn_norm_backward", args, (sh, dout, r, weight, dresidual, dx, dweight, workspace), prepare)
+        workspace = _workspace(lib().gdn_norm_backward_workspace_bytes(ref), r.device, stream)
+    device, handle = _site("gdn_norm_backward", stream)
+    args = (ref, _at(dout, "dout", device), _at(r, "r", device, False), _at(weight, "weight", device),
+            _at(dresidual, "dresidual", device), _at(dx, "dx", device), _at(dweight, "dweight", device),
+            _at(workspace, "workspace", device), 0 if workspace is None else _bytes_of(workspace), handle)
+    return _call("gdn_norm_backward", args, (sh, dout, r, weight, dresidual, dx, dweight, workspace), prepare)
 
 
-def _gated_shape(x, z, weight, scale_stride, eps):
+def _gated_shape(x, z, weight, eps):
     rows, x_stride = _rows_of(x, "x", 2)
-    _expect(z, "z", x.shape)
-    z_rows, z_stride = _rows_of(z, "z", 2)
-    Hv, dv = x.shape[-2:]
+    shape = x.shape
+    _expect(z, "z", shape)
+    _, z_stride = _rows_of(z, "z", 2)
+    Hv, dv = shape[-2:]
     _expect(weight, "weight", (dv,))
-    return GdnGatedNormShape(rows, x_stride, z_stride, Hv, dv, _dtype_code(x), _dtype_code(z), _dtype_code(weight),
-                             scale_stride, eps)
+    return GdnGatedNormShape(rows, x_stride, z_stride, Hv, dv, _code(x), _code(z), _code(weight), 0, eps)
 
 
 def gdn_gated_norm_forward(x, z, weight, *, out=None, codes=None, scales=None, eps: float = 1e-6, stream=None,
@@ -1007,34 +1054,35 @@ def gdn_gated_norm_forward(x, z, weight, *, out=None, codes=None, scales=None, e
     """The rule's outputs ``x`` [...][h_v][d_v], normed head by head and gated by silu(``z``) (the rows of 3-D x and z may
     be apart); to ``out`` (z's dtype) and, or, to e4m3 ``codes`` [rows][h_v d_v] with e8m0 ``scales``; see
     include/gdn.h."""
-    sh = _gated_shape(x, z, weight, 0, eps)
-    sh.scale_stride = _check_codes(codes, scales, sh.rows, sh.h_v * sh.d_v)
+    sh = _gated_shape(x, z, weight, eps)
+    if codes is not None or scales is not None:
+        sh.scale_stride = _check_codes(codes, scales, sh.rows, sh.h_v * sh.d_v)
     _expect(out, "out", x.shape, z.dtype)
-    args = (ctypes.byref(sh), _vp(x.data_ptr()), _vp(z.data_ptr()), _dev_ptr(weight, "weight"), _dev_ptr(out, "out"),
-            _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), _stream(stream))
-    _on_current_device("gdn_gated_norm_forward", stream, x, z, weight, out, codes, scales)
-    return _invoke("gdn_gated_norm_forward", args, (sh, x, z, weight, out, codes, scales), prepare)
+    device, handle = _site("gdn_gated_norm_forward", stream)
+    args = (ctypes.byref(sh), _at(x, "x", device, False), _at(z, "z", device, False), _at(weight, "weight", device),
+            _at(out, "out", device), _at(codes, "codes", device), _at(scales, "scales", device), handle)
+    return _call("gdn_gated_norm_forward", args, (sh, x, z, weight, out, codes, scales), prepare)
 
 
 def gdn_gated_norm_backward(dout, x, z, weight, dx=None, dz=None, dweight=None, *, eps: float = 1e-6, workspace=None,
                             stream=None, prepare: bool = False):
     """The gradients of :func:`gdn_gated_norm_forward`: ``dx`` (x's dtype), ``dz`` (z's) and ``dweight`` (fp32), from
     ``dout`` (z's).  ``workspace`` is allocated here with torch when omitted."""
-    sh = _gated_shape(x, z, weight, 0, eps)
+    sh = _gated_shape(x, z, weight, eps)
     if dout is None:
         raise ValueError("dout is required")
     _expect(dout, "dout", x.shape, z.dtype)
     _expect(dx, "dx", x.shape, x.dtype)
     _expect(dz, "dz", x.shape, z.dtype)
     _expect(dweight, "dweight", (sh.d_v,), torch.float32)
+    ref = ctypes.byref(sh)
     if workspace is None and dweight is not None:
-        need = lib().gdn_gated_norm_backward_workspace_bytes(ctypes.byref(sh))
-        workspace = _workspace(int(need), x.device, stream)
-    args = (ctypes.byref(sh), _dev_ptr(dout, "dout"), _vp(x.data_ptr()), _vp(z.data_ptr()), _dev_ptr(weight, "weight"),
-            _dev_ptr(dx, "dx"), _dev_ptr(dz, "dz"), _dev_ptr(dweight, "dweight"), _dev_ptr(workspace, "workspace"),
-            ctypes.c_size_t(0 if workspace is None else _bytes_of(workspace)), _stream(stream))
-    _on_current_device("gdn_gated_norm_backward", stream, dout, x, z, weight, dx, dz, dweight, workspace)
-    return _invoke("gdn_gated_norm_backward", args, (sh, dout, x, z, weight, dx, dz, dweight, workspace), prepare)
+        workspace = _workspace(lib().gdn_gated_norm_backward_workspace_bytes(ref), x.device, stream)
+    device, handle = _site("gdn_gated_norm_backward", stream)
+    args = (ref, _at(dout, "dout", device), _at(x, "x", device, False), _at(z, "z", device, False),
+            _at(weight, "weight", device), _at(dx, "dx", device), _at(dz, "dz", device), _at(dweight, "dweight", device),
+            _at(workspace, "workspace", device), 0 if workspace is None else _bytes_of(workspace), handle)
+    return _call("gdn_gated_norm_backward", args, (sh, dout, x, z, weight, dx, dz, dweight, workspace), prepare)
 
 
 def gdn_project(a, a_scales, w, w_scales, outs, *, stream=None, prepare: bool = False):
@@ -1046,38 +1094,39 @@ def gdn_project(a, a_scales, w, w_scales, outs, *, stream=None, prepare: bool = 
     N = _shape_of(w, "w", 2)[0]
     _expect(a, "a", (M, K), _E4M3)
     _expect(w, "w", (N, K), _E4M3)
-    _, a_stride = _rows_of(a, "a", 1)
-    _, w_stride = _rows_of(w, "w", 1)
-    groups, blocks = -(-K // GDN_GROUP), -(-N // GDN_GROUP)
-    _expect(a_scales, "a_scales", (M, None), _E8M0)
-    _expect(w_scales, "w_scales", (blocks, None))
-    if a_scales.shape[1] < groups or a_scales.shape[1] % 4:
-        raise ValueError(f"a_scales must have a multiple of 4 columns, at least {groups}, got {a_scales.shape[1]}")
-    if w_scales.dtype not in (torch.float32, _E8M0):
-        raise TypeError(f"w_scales must be float32 or float8_e8m0fnu, got {w_scales.dtype}")
-    if w_scales.shape[1] < groups or (w_scales.dtype is _E8M0 and w_scales.shape[1] % 4):
-        raise ValueError(f"w_scales must have at least {groups} columns (e8m0: a multiple of 4), got {w_scales.shape[1]}")
+    a_stride, w_stride = _rows_of(a, "a", 1)[1], _rows_of(w, "w", 1)[1]
+    groups = -(-K // GDN_GROUP)
+    a_pad, w_pad = _shape_of(a_scales, "a_scales", 2)[1], _shape_of(w_scales, "w_scales", 2)[1]
+    _expect(a_scales, "a_scales", (M, a_pad), _E8M0)
+    _expect(w_scales, "w_scales", (-(-N // GDN_GROUP), w_pad))
+    w_dtype = w_scales.dtype
+    if a_pad < groups or a_pad % 4:
+        raise ValueError(f"a_scales must have a multiple of 4 columns, at least {groups}, got {a_pad}")
+    if w_dtype is not torch.float32 and w_dtype is not _E8M0:
+        raise TypeError(f"w_scales must be float32 or float8_e8m0fnu, got {w_dtype}")
+    if w_pad < groups or (w_dtype is _E8M0 and w_pad % 4):
+        raise ValueError(f"w_scales must have at least {groups} columns (e8m0: a multiple of 4), got {w_pad}")
     if isinstance(outs, torch.Tensor):
         outs = (outs,)
     if not 1 <= len(outs) <= GDN_MAX_PARTS:
         raise ValueError(f"1 to {GDN_MAX_PARTS} outputs, got {len(outs)}")
-    parts, columns = (GdnProjectPart * len(outs))(), 0
-    for i, t in enumerate(outs):
-        if not isinstance(t, torch.Tensor) or t.dim() < 2:
-            raise ValueError("outs must be tensors [tokens][...]")
-        if t.shape[0] != M or t.dtype is not outs[0].dtype:
-            raise ValueError("outs must have a row for each token and one dtype")
-        rows, stride = _rows_of(t, "outs", t.dim() - 1)
+    parts, columns, dtype = [], 0, outs[0].dtype
+    for t in outs:
+        if not isinstance(t, torch.Tensor) or t.dim() < 2 or t.shape[0] != M or t.dtype is not dtype:
+            raise ValueError("outs must be tensors [tokens][...], a row for each token, of one dtype")
+        stride = _rows_of(t, "outs", t.dim() - 1)[1]
         n = t.numel() // M if M else stride
-        parts[i] = GdnProjectPart(t.data_ptr(), stride, n, 0)
+        parts.append((t.data_ptr(), stride, n, 0))
         columns += n
     if columns != N:
         raise ValueError(f"the outputs have {columns} columns, the weights {N}")
-    if outs[0].dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"outs must be bfloat16 or float16, got {outs[0].dtype}")
-    sh = GdnProjectShape(M, a_stride, w_stride, K, a_scales.shape[1], w_scales.shape[1],
-                         GDN_F32 if w_scales.dtype is torch.float32 else GDN_E8M0, _dtype_code(outs[0]))
-    args = (ctypes.byref(sh), _vp(a.data_ptr()), _dev_ptr(a_scales, "a_scales"), _vp(w.data_ptr()),
-            _dev_ptr(w_scales, "w_scales"), parts, _i32(len(outs)), _stream(stream))
-    _on_current_device("gdn_project", stream, a, a_scales, w, w_scales, *outs)
-    return _invoke("gdn_project", args, (sh, a, a_scales, w, w_scales, tuple(outs)), prepare)
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"outs must be bfloat16 or float16, got {dtype}")
+    sh = GdnProjectShape(M, a_stride, w_stride, K, a_pad, w_pad, GDN_F32 if w_dtype is torch.float32 else GDN_E8M0,
+                         GDN_BF16 if dtype is torch.bfloat16 else GDN_F16)
+    device, handle = _site("gdn_project", stream)
+    for t in outs:
+        _at(t, "outs", device, False)
+    args = (ctypes.byref(sh), _at(a, "a", device, False), _at(a_scales, "a_scales", device), _at(w, "w", device, False),
+            _at(w_scales, "w_scales", device), (GdnProjectPart * len(parts))(*parts), len(parts), handle)
+    return _call("gdn_project", args, (sh, a, a_scales, w, w_scales, tuple(outs)), prepare)

@@ -35,6 +35,7 @@ struct GatedArgs {
     void* dz;
     float* partial;      // [workgroups][d_v]
     int64_t rows, x_stride, z_stride;
+    double inverse_size; // 1 / d_v
     uint32_t pieces;     // of a row
     uint32_t total;      // of the call
     int32_t lanes;       // of a piece
@@ -85,11 +86,8 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     load8<DX>(a.x, row * a.x_stride + c, x);
     load8<DZ>(a.z, row * a.z_stride + c, z);
     load8(a.weight, i % head_lanes * kVec, a.weight_dtype, w);
-    float s = 0;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) s += x[k] * x[k];
-    s = head_sum<L>(s, part, (int)threadIdx.x - p % head_lanes, head_lanes);
-    const float rs = inverse_rms(s, (float)(head_lanes * kVec), a.eps);
+    const float s = head_sum<L>(squares8(x), part, (int)threadIdx.x - p % head_lanes, head_lanes);
+    const float rs = inverse_rms(s, a.inverse_size, a.eps);
 #pragma unroll
     for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * (z[k] * logistic(z[k]));
     const int64_t o = row * (int64_t)a.vectors * kVec + i * (int64_t)kVec;
@@ -127,18 +125,17 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const Gat
         load8<DX>(a.x, row * a.x_stride + c, x);
         load8<DZ>(a.z, row * a.z_stride + c, z);
         load8<DZ>(a.dout, o, d);
-        float xx = 0, gx = 0;
+        float gx = 0;
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
             gate[k] = logistic(z[k]);
             g[k] = d[k] * w[k] * (z[k] * gate[k]);
-            xx += x[k] * x[k];
             gx += g[k] * x[k];
         }
         const int lead = (int)threadIdx.x - column;
-        xx = head_sum<L>(xx, part, lead, head_lanes);
+        const float xx = head_sum<L>(squares8(x), part, lead, head_lanes);
         gx = head_sum<L>(gx, part, lead, head_lanes);
-        const float size = (float)(head_lanes * kVec), rs = inverse_rms(xx, size, a.eps), mean = rs * gx / size;
+        const float rs = inverse_rms(xx, a.inverse_size, a.eps), mean = rs * (float)(gx * a.inverse_size);
         float dx[kVec], dz[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
@@ -180,6 +177,7 @@ int plan_gated(const gdn_gated_norm_shape* sh, int64_t most, GatedArgs* a, int* 
     while (lanes % 16 != 0) lanes += head;
     a->vectors = sh->h_v * head;
     a->head_lanes = head;
+    a->inverse_size = 1.0 / sh->d_v;
     a->lanes = lanes;
     a->per_wg = kThreads / lanes;
     a->pieces = (uint32_t)((a->vectors + lanes - 1) / lanes);

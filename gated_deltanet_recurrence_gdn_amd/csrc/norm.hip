@@ -6,6 +6,7 @@
 //
 // Both passes read a row once and keep it in registers between the sums and the
 // outputs, so they are bound by their bytes.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -15,7 +16,7 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kMaxWalkers = 512;  // rows in flight of a backward pass, each with its own partial of dweight
+constexpr int kMaxBackThreads = 512;
 
 struct NormArgs {
     const void* x;       // forward: x; backward: r
@@ -28,21 +29,22 @@ struct NormArgs {
     const void* dout;
     const void* dresidual;
     void* dx;
-    float* partial;      // [walkers][width]
+    float* partial;      // [workgroups][width]
     int64_t rows, x_stride;
+    double inverse_width;
     int32_t width, weight_dtype, scale_stride;
     float eps, weight_offset;
 };
 
 // Sum over the LANES lanes of a row: part of a wave, or the workgroup (LANES = 0).
 template <int LANES>
-__device__ __forceinline__ float row_sum(float x, float* wave_sum) {
+__device__ __forceinline__ double row_sum(float x, float* wave_sum) {
     if constexpr (LANES != 0) return lanes_sum<LANES>(x);
     x = lanes_sum<64>(x);
     const int waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = x;
     __syncthreads();
-    float sum = 0;
+    double sum = 0;
     for (int w = 0; w < waves; ++w) sum += wave_sum[w];
     return sum;
 }
@@ -79,13 +81,8 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
     }
     float sum = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float s = 0;
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) s += r[v][k] * r[v][k];
-        sum += t + v * lanes < n ? s : 0;
-    }
-    const float rs = inverse_rms(row_sum<LANES>(sum, wave_sum), (float)a.width, a.eps);
+    for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8(r[v]) : 0;
+    const float rs = inverse_rms(row_sum<LANES>(sum, wave_sum), a.inverse_width, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int i = t + v * lanes;
@@ -107,109 +104,147 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
     }
 }
 
+// A walker (a wave, or the workgroup) takes every walkers-th row and sums its part of dweight in registers; the next
+// row's loads are under way while a row is worked on.
 template <int DX, int DR, int V, int LANES>
-__global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_backward_kernel(const NormArgs a) {
-    __shared__ float wave_sum[2][2][kMaxThreads / 64];
-    const int lanes = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % LANES : threadIdx.x;
-    const int per_wg = LANES ? blockDim.x / (LANES ? LANES : 1) : 1;
-    const int64_t walker = (int64_t)blockIdx.x * per_wg + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
-    const int64_t walkers = (int64_t)gridDim.x * per_wg;
+__global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_kernel(const NormArgs a) {
+    constexpr int kWaves = LANES ? 4 : 1;  // walkers of a workgroup
+    __shared__ float wave_sum[2][2][kMaxBackThreads / 64];
+    __shared__ float share[LANES ? 3 : 1][LANES ? V * 64 * kVec : 1];
+    const int lanes = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % 64 : threadIdx.x;
+    const int wave = LANES ? threadIdx.x / 64 : 0;
+    const int64_t walker = (int64_t)blockIdx.x * kWaves + wave, walkers = (int64_t)gridDim.x * kWaves;
     const int n = a.width / kVec;
+    int c[V];  // this lane's channels; lanes past the row's end read its last vector
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = (t + v * lanes < n ? t + v * lanes : n - 1) * kVec;
     float w[V][kVec], dw[V][kVec];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int i = t + v * lanes;
-        load8(a.weight, (i < n ? i : n - 1) * kVec, a.weight_dtype, w[v]);
+        load8(a.weight, c[v], a.weight_dtype, w[v]);
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
             w[v][k] += a.weight_offset;
             dw[v][k] = 0;
         }
     }
-    int turn = 0;
-    for (int64_t row = walker; row < a.rows; row += walkers, turn ^= 1) {
-        float r[V][kVec], d[V][kVec];
+    Raw8<DR> r_next[V], z_next[V];
+    Raw8<DX> d_next[V];
+    auto fetch = [&](int64_t row) {
+        row = row < a.rows ? row : a.rows - 1;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int i = t + v * lanes, c = (i < n ? i : n - 1) * kVec;
-            load8<DR>(a.x, row * a.x_stride + c, r[v]);
-            load8<DX>(a.dout, row * a.width + c, d[v]);
+            r_next[v] = load_raw8<DR>(a.x, row * a.x_stride + c[v]);
+            d_next[v] = load_raw8<DX>(a.dout, row * a.width + c[v]);
         }
+        if (a.dresidual != nullptr)
+#pragma unroll
+            for (int v = 0; v < V; ++v) z_next[v] = load_raw8<DR>(a.dresidual, row * a.width + c[v]);
+    };
+    fetch(walker);
+    int turn = 0;
+    for (int64_t row = walker; row < a.rows; row += walkers, turn ^= 1) {
+        float r[V][kVec], d[V][kVec], z[V][kVec];
         float rr = 0, gr = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float p = 0, q = 0;
+            widen8<DR>(r_next[v], r[v]);
+            widen8<DX>(d_next[v], d[v]);
+            if (a.dresidual != nullptr) {
+                widen8<DR>(z_next[v], z[v]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                p += r[v][k] * r[v][k];
-                q += d[v][k] * w[v][k] * r[v][k];
+                for (int k = 0; k < kVec; ++k) z[v][k] = 0;
             }
-            if (t + v * lanes < n) {
-                rr += p;
-                gr += q;
-            }
+            const bool in = t + v * lanes < n;
+            float q = 0;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) q += d[v][k] * w[v][k] * r[v][k];
+            rr += in ? squares8(r[v]) : 0;
+            gr += in ? q : 0;
         }
+        fetch(row + walkers);
+        double rsum, gsum;
+        rr = lanes_sum<64>(rr);
+        gr = lanes_sum<64>(gr);
         if constexpr (LANES != 0) {
-            rr = lanes_sum<LANES>(rr);
-            gr = lanes_sum<LANES>(gr);
+            rsum = rr;
+            gsum = gr;
         } else {  // two copies of the sums: the next row's do not wait for this row's readers
-            rr = lanes_sum<64>(rr);
-            gr = lanes_sum<64>(gr);
             if ((threadIdx.x & 63) == 0) {
                 wave_sum[turn][0][threadIdx.x >> 6] = rr;
                 wave_sum[turn][1][threadIdx.x >> 6] = gr;
             }
-            __syncthreads();
-            rr = gr = 0;
+            lds_barrier();  // the next row's loads stay in flight
+            rsum = gsum = 0;
             for (int k = 0; k < (int)(blockDim.x >> 6); ++k) {
-                rr += wave_sum[turn][0][k];
-                gr += wave_sum[turn][1][k];
+                rsum += wave_sum[turn][0][k];
+                gsum += wave_sum[turn][1][k];
             }
         }
-        const float rs = inverse_rms(rr, (float)a.width, a.eps), mean = rs * gr / (float)a.width;
+        const float rs = inverse_rms(rsum, a.inverse_width, a.eps), mean = rs * (float)(gsum * a.inverse_width);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = t + v * lanes;
-            const int64_t o = row * a.width + i * kVec;
             float dx[kVec];
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
                 const float norm = r[v][k] * rs;
-                dx[k] = rs * (d[v][k] * w[v][k] - norm * mean);
+                dx[k] = z[v][k] + rs * (d[v][k] * w[v][k] - norm * mean);
                 dw[v][k] += d[v][k] * norm;
             }
-            if (i < n && a.dx != nullptr) {
-                if (a.dresidual != nullptr) {
-                    float z[kVec];
-                    load8<DR>(a.dresidual, o, z);
-#pragma unroll
-                    for (int k = 0; k < kVec; ++k) dx[k] += z[k];
-                }
-                store8<DR>(a.dx, o, dx);
-            }
+            if (i < n && a.dx != nullptr) store8<DR>(a.dx, row * a.width + i * kVec, dx);
         }
     }
     if (a.partial == nullptr) return;
+    if constexpr (LANES != 0) {  // the waves' parts, in their order
+        if (wave > 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) share[wave - 1][(v * kVec + k) * 64 + t] = dw[v][k];
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) dw[v][k] += share[u][(v * kVec + k) * 64 + t];
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int i = t + v * lanes;
-        if (i < n) store8<GDN_F32>(a.partial, walker * a.width + i * kVec, dw[v]);
+        if (i < n) store8<GDN_F32>(a.partial, (int64_t)blockIdx.x * a.width + i * kVec, dw[v]);
     }
 }
 
-// 32 columns a workgroup, 32 slices of the partials, joined in LDS.
+// COLUMNS columns a workgroup, 1024 / COLUMNS slices of the partials, joined in LDS.
+template <int COLUMNS>
 __global__ __launch_bounds__(1024) void sum_partials_kernel(const float* partial, int n_partials, int width, float* out) {
-    __shared__ float part[32][33];
-    const int c = threadIdx.x % 32, slice = threadIdx.x / 32, col = blockIdx.x * 32 + c;
+    constexpr int kSlices = 1024 / COLUMNS;
+    __shared__ float part[kSlices][COLUMNS + 1];
+    const int c = threadIdx.x % COLUMNS, slice = threadIdx.x / COLUMNS, col = blockIdx.x * COLUMNS + c;
     float s = 0;
-    if (col < width)
-        for (int p = slice; p < n_partials; p += 32) s += partial[(int64_t)p * width + col];
+    if (col < width) {
+#pragma unroll 8
+        for (int p = slice; p < n_partials; p += kSlices) s += partial[(int64_t)p * width + col];
+    }
     part[slice][c] = s;
+    __syncthreads();
+    // eight slices' sums, then theirs
+    if (slice < kSlices / 8) {
+        s = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += part[8 * slice + k][c];
+    }
+    __syncthreads();
+    if (slice < kSlices / 8) part[slice][c] = s;
     __syncthreads();
     if (slice == 0 && col < width) {
         s = 0;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s += part[k][c];
+        for (int k = 0; k < kSlices / 8; ++k) s += part[k][c];
         out[col] = s;
     }
 }
@@ -220,34 +255,26 @@ struct NormPlan {
     int threads, grid;
 };
 
-int32_t walkers_of(const NormPlan& p) { return p.lanes != 0 ? p.grid * (p.threads / p.lanes) : p.grid; }
-
-// Rows of up to 256 channels take 16 lanes, up to 2048 a wave, longer ones a workgroup.
-NormPlan plan_rows(int64_t rows, int32_t width, int64_t most_rows) {
+// Rows of up to 256 channels take 16 lanes (forward), up to 2048 a wave, longer ones a workgroup, two vectors a lane from
+// 4097 channels on where there are rows to fill the chip with (4096 x 5120: 33.9 us, one vector 35.9; 2999 x 2560: 21.8
+// and 21.5; backward 41 and 53, 29 and 28).
+NormPlan plan_rows(int64_t rows, int32_t width, bool backward) {
     const int n = width / kVec;
     NormPlan p;
     if (n <= 256) {
-        p.lanes = n <= 32 ? 16 : 64;
+        p.lanes = n <= 32 && !backward ? 16 : 64;
         p.vectors = n <= p.lanes ? 1 : n <= 2 * p.lanes ? 2 : 4;
         p.threads = 256;
     } else {
         p.lanes = 0;
-        p.vectors = n <= 1024 ? 1 : 2;
+        p.vectors = n <= 512 || (n <= 1024 && rows < 256 && !backward) ? 1 : n <= 1024 || !backward ? 2 : 4;
         p.threads = (((n + p.vectors - 1) / p.vectors + 63) / 64) * 64;
     }
     const int per_wg = p.lanes != 0 ? p.threads / p.lanes : 1;
-    const int64_t walk = rows < most_rows ? rows : most_rows;
-    p.grid = (int)((walk + per_wg - 1) / per_wg);
-    return p;
-}
-
-NormPlan plan_backward(const gdn_norm_shape* sh) {
-    NormPlan p = plan_rows(sh->rows, sh->width, kMaxWalkers);
-    if (p.lanes == 16) {  // a wave a row: fewer partials
-        p = NormPlan{64, 1, 256, 0};
-        const int64_t walk = sh->rows < kMaxWalkers ? sh->rows : kMaxWalkers;
-        p.grid = (int)((walk + 3) / 4);
-    }
+    const int64_t grid = (rows + per_wg - 1) / per_wg;
+    // walkers enough to fill the chip, and partials of dweight (one a workgroup) of at most 4 MiB or two a CU
+    const int64_t most = !backward ? 0x7fffffff : std::max<int64_t>(512, std::min<int64_t>(2048, (1 << 20) / width));
+    p.grid = (int)std::min(grid, most);
     return p;
 }
 
@@ -261,7 +288,7 @@ hipError_t launch(const NormPlan& p, const NormArgs& a, hipStream_t stream) {
     };
     auto pick = [&](auto lanes) {
         if (p.vectors == 1) return go(std::integral_constant<int, 1>{}, lanes);
-        if constexpr (decltype(lanes)::value == 64)
+        if constexpr (decltype(lanes)::value == 64 || (BACK && decltype(lanes)::value == 0))
             if (p.vectors == 4) return go(std::integral_constant<int, 4>{}, lanes);
         return go(std::integral_constant<int, 2>{}, lanes);
     };
@@ -299,6 +326,7 @@ NormArgs args_of(const gdn_norm_shape* sh) {
     a.rows = sh->rows;
     a.x_stride = sh->x_stride;
     a.width = sh->width;
+    a.inverse_width = 1.0 / sh->width;
     a.weight_dtype = sh->weight_dtype;
     a.scale_stride = sh->scale_stride;
     a.eps = sh->eps;
@@ -309,7 +337,9 @@ NormArgs args_of(const gdn_norm_shape* sh) {
 }  // namespace
 
 hipError_t launch_sum_partials(const float* partial, int32_t n_partials, int32_t width, float* out, hipStream_t stream) {
-    hipLaunchKernelGGL(sum_partials_kernel, dim3((width + 31) / 32), dim3(1024), 0, stream, partial, n_partials, width, out);
+    // few columns: more slices (1024 partials of 128 columns: 11 us in 32 columns a workgroup)
+    if (width <= 1024) hipLaunchKernelGGL(sum_partials_kernel<8>, dim3((width + 7) / 8), dim3(1024), 0, stream, partial, n_partials, width, out);
+    else hipLaunchKernelGGL(sum_partials_kernel<32>, dim3((width + 31) / 32), dim3(1024), 0, stream, partial, n_partials, width, out);
     return hipGetLastError();
 }
 
@@ -341,13 +371,13 @@ int gdn_norm_forward(const gdn_norm_shape* shape, const void* x, const void* res
     a.out = out;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales);
-    const NormPlan p = plan_rows(shape->rows, shape->width, shape->rows);
+    const NormPlan p = plan_rows(shape->rows, shape->width, false);
     return launch<false>(shape, p, a, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 size_t gdn_norm_backward_workspace_bytes(const gdn_norm_shape* shape) {
     if (check_norm(shape) != GDN_OK) return 0;
-    return (size_t)walkers_of(plan_backward(shape)) * shape->width * sizeof(float);
+    return (size_t)plan_rows(shape->rows, shape->width, true).grid * shape->width * sizeof(float);
 }
 
 int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void* r, const void* weight,
@@ -365,7 +395,7 @@ int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void*
     if (dout == nullptr || r == nullptr || weight == nullptr) return GDN_ERR_NULL;
     if (!aligned_to(dout, 16) || !aligned_to(r, 16) || !aligned_to(weight, 16) || !aligned_to(dresidual, 16) || !aligned_to(dx, 16))
         return GDN_ERR_ALIGN;
-    const NormPlan p = plan_backward(shape);
+    const NormPlan p = plan_rows(shape->rows, shape->width, true);
     if (dweight != nullptr) {
         if (workspace == nullptr || workspace_bytes < gdn_norm_backward_workspace_bytes(shape)) return GDN_ERR_WORKSPACE;
         if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGN;
@@ -379,7 +409,7 @@ int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void*
     a.partial = dweight != nullptr ? static_cast<float*>(workspace) : nullptr;
     if (launch<true>(shape, p, a, st) != hipSuccess) return GDN_ERR_HIP;
     if (dweight == nullptr) return GDN_OK;
-    return launch_sum_partials(a.partial, walkers_of(p), shape->width, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    return launch_sum_partials(a.partial, p.grid, shape->width, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 }  // extern "C"

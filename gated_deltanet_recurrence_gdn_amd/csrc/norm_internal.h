@@ -17,30 +17,46 @@ constexpr int kVec = 8;  // channels of a lane
 inline bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 inline bool real_dtype(int32_t t) { return t == GDN_F32 || t == GDN_BF16 || t == GDN_F16; }
 
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+// Eight elements as they are in memory, so that a load ahead of its use takes no more registers than it has to.
+template <int DT>
+struct Raw8 {
+    u32x4 w[DT == GDN_F32 ? 2 : 1];
+};
 
 template <int DT>
-__device__ __forceinline__ void load8(const void* base, int64_t i, float (&x)[kVec]) {
+__device__ __forceinline__ Raw8<DT> load_raw8(const void* base, int64_t i) {
+    Raw8<DT> x;
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(base) + i * (DT == GDN_F32 ? 4 : 2));
+    x.w[0] = p[0];
+    if constexpr (DT == GDN_F32) x.w[1] = p[1];
+    return x;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& raw, float (&x)[kVec]) {
     if constexpr (DT == GDN_F32) {
-        const float* p = static_cast<const float*>(base) + i;
-        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+        const f32x4 a = __builtin_bit_cast(f32x4, raw.w[0]), b = __builtin_bit_cast(f32x4, raw.w[1]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             x[k] = a[k];
             x[4 + k] = b[k];
         }
     } else if constexpr (DT == GDN_BF16) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            x[2 * k] = bf16_lo(w[k]);
-            x[2 * k + 1] = bf16_hi(w[k]);
+            x[2 * k] = bf16_lo(raw.w[0][k]);
+            x[2 * k + 1] = bf16_hi(raw.w[0][k]);
         }
     } else {
-        const f16x8 h = *reinterpret_cast<const f16x8*>(static_cast<const _Float16*>(base) + i);
+        const f16x8 h = __builtin_bit_cast(f16x8, raw.w[0]);
 #pragma unroll
         for (int k = 0; k < kVec; ++k) x[k] = (float)h[k];
     }
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* base, int64_t i, float (&x)[kVec]) {
+    widen8<DT>(load_raw8<DT>(base, i), x);
 }
 
 // Rounds to the nearest, ties to even.
@@ -89,6 +105,14 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return x;
 }
 
+// A barrier for data exchanged through LDS stores: loads and stores to memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // The largest of 16 lanes' values.
 __device__ __forceinline__ uint32_t lanes16_max(uint32_t x) {
     auto step = [&](uint32_t y) { x = x > y ? x : y; };
@@ -130,8 +154,21 @@ __device__ __forceinline__ u32x2 codes8(const float (&y)[kVec], float down) {
     return u32x2{(uint32_t)lo, (uint32_t)hi};
 }
 
-// 1 / sqrt(sum / n + eps), each step rounded to the nearest.
-__device__ __forceinline__ float inverse_rms(float sum, float n, float eps) { return 1.0f / sqrtf(sum / n + eps); }
+// The sum of eight squares, in pairs.
+__device__ __forceinline__ float squares8(const float (&x)[kVec]) {
+    const float a = __builtin_fmaf(x[0], x[0], x[1] * x[1]), b = __builtin_fmaf(x[2], x[2], x[3] * x[3]);
+    const float c = __builtin_fmaf(x[4], x[4], x[5] * x[5]), d = __builtin_fmaf(x[6], x[6], x[7] * x[7]);
+    return (a + b) + (c + d);
+}
+
+// 1 / sqrt(sum / n + eps) rounded once, from 64 bits: an ulp here moves codes of the whole row over their borders
+// (4096 x 5120: 2.0e-4 of the codes' 2-norm with fp32 steps, 4e-5 so).
+__device__ __forceinline__ float inverse_rms(double sum, double inverse_n, float eps) {
+    const double m = __builtin_fma(sum, inverse_n, (double)eps);
+    const double y = __builtin_amdgcn_rsq(m);
+    const float r = (float)(y * __builtin_fma(-0.5 * m * y, y, 1.5));
+    return m == __builtin_inf() ? 0.0f : r;  // a sum past fp32's range
+}
 
 // out[c] = sum of partial[p][c] over p, in an order that depends on the sizes alone.
 hipError_t launch_sum_partials(const float* partial, int32_t n_partials, int32_t width, float* out, hipStream_t stream);
