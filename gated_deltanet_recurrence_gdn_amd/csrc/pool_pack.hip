@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kDeep = 8;                       // pieces of four states per thread and tile
 constexpr int kTile = kThreads * kDeep * 4;    // states
-constexpr int kGrid = 4096;                    // workgroups that walk the tiles
+constexpr int kGrid = 16384;                   // workgroups that walk the tiles (4096: 318 us for 303)
 
 struct PackArgs {
     const unsigned char* states_in;
@@ -76,15 +76,31 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
     return x;
 }
 
-// x / scale to the nearest integer, ties to even, decided exactly: `down` is 1 / scale to an ulp, so q is off by one
-// at most, and near a half x - q scale has no more than 24 bits.
-__device__ __forceinline__ int code_of(float x, float scale, float down) {
-    float q = __builtin_rintf(x * down);
-    const float rest = __builtin_fmaf(-q, scale, x), half = 0.5f * scale;
+// Correctly rounded x / 127 of a finite x >= 0 whose quotient is not subnormal: the quotient by a rounded reciprocal,
+// corrected by its exact remainder (all 2^23 mantissas checked).
+__device__ __forceinline__ float over127(float x) {
+    constexpr float kInverse = 1.0f / 127.0f;
+    const float q = x * kInverse;
+    return __builtin_fmaf(__builtin_fmaf(-127.0f, q, x), kInverse, q);
+}
+
+// x / scale to the nearest integer q, ties to even, as q + kMagic, whose low byte is q's.  `down` is 1 / scale to an ulp,
+// so x down is off by less than 2^-15; nearer than that to a half (*near), exact() decides.
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: fp32's step there is 1
+
+__device__ __forceinline__ float nearest(float x, float down, bool* near) {
+    const float f = __builtin_fmaf(x, down, kMagic), rest = __builtin_fmaf(x, down, kMagic - f);
+    *near |= __builtin_fabsf(rest) > 0.5f - 0x1p-15f;
+    return f;
+}
+
+// By the remainder x - q scale, which has no more than 24 bits near a half.
+__device__ __forceinline__ float exact(float f, float x, float scale) {
+    const float q = f - kMagic, rest = __builtin_fmaf(-q, scale, x), half = 0.5f * scale;
     const bool odd = ((int)q & 1) != 0;
-    if (rest > half || (rest == half && odd)) q += 1;
-    else if (rest < -half || (rest == -half && odd)) q -= 1;
-    return (int)q;
+    if (rest > half || (rest == half && odd)) return f + 1;
+    if (rest < -half || (rest == -half && odd)) return f - 1;
+    return f;
 }
 
 // The rows of pair `pair` and whether they are copied; the whole workgroup asks together.
@@ -132,14 +148,21 @@ __global__ __launch_bounds__(kThreads) void pool_pack_kernel(const PackArgs a) {
             }
             top = lanes_max<DK / 4>(top);
             const bool bad = top >= 0x7f800000u;
-            float scale = __builtin_bit_cast(float, top) / 127.0f;
-            scale = scale < 0x1p-126f ? 0x1p-126f : scale;
+            const float scale = __builtin_fmaxf(over127(__builtin_bit_cast(float, top)), 0x1p-126f);
             const float down = __builtin_amdgcn_rcpf(scale);
-            int q[4];
+            bool near = false;
+            float f[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = bad ? 0 : code_of(x[k][j], scale, down);
+            for (int j = 0; j < 4; ++j) f[j] = nearest(x[k][j], down, &near);
+            if (near)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = exact(f[j], x[k][j], scale);
+            uint32_t q = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q |= (__builtin_bit_cast(uint32_t, f[j]) & 255) << (8 * j);
+            if (bad) q = 0;
             if (o < left) {
-                *reinterpret_cast<uint32_t*>(codes + o) = (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 | (uint32_t)q[3] << 24;
+                *reinterpret_cast<uint32_t*>(codes + o) = q;
                 if (o % DK == 0) scales[o / DK] = bad ? __builtin_bit_cast(float, 0x7fc00000u) : scale;
             }
         }
