@@ -57,6 +57,18 @@ __device__ __forceinline__ float logistic(float z) {
     return __builtin_fmaf(q, __builtin_fmaf(-d, q, 1.0f), q);
 }
 
+// The same in 64 bits, for |z| up to 700: e^-z = 2^n e^r with |r| <= ln(2) / 2, whose series ends at r^13 / 13!.
+__device__ __forceinline__ double logistic_f64(double z) {
+    constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453, kLn2Rest = 2.3190468138462996e-17;
+    const double n = __builtin_rint(-z * kLog2e);
+    double r = __builtin_fma(-n, kLn2, -z);
+    r = __builtin_fma(-n, kLn2Rest, r);
+    double p = 1;
+#pragma unroll
+    for (int i = 13; i >= 1; --i) p = __builtin_fma(p * r, 1.0 / i, 1.0);
+    return 1.0 / (1.0 + __builtin_ldexp(p, (int)n));
+}
+
 // The sums of a head's lanes.  L lanes a head (2, 4, 8, 16 or 32), or any number through LDS (0).
 template <int L>
 __device__ __forceinline__ float head_sum(float x, float* part, int first, int head_lanes) {
@@ -86,17 +98,18 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     load8<DX>(a.x, row * a.x_stride + c, x);
     load8<DZ>(a.z, row * a.z_stride + c, z);
     load8(a.weight, i % head_lanes * kVec, a.weight_dtype, w);
-    const float s = head_sum<L>(squares8(x), part, (int)threadIdx.x - p % head_lanes, head_lanes);
-    const float rs = inverse_rms(s, a.inverse_size, a.eps);
+    const double root = inverse_rms(head_sum<L>(squares8(x), part, (int)threadIdx.x - p % head_lanes, head_lanes), a.inverse_size, a.eps);
+    const float rs = (float)root;
 #pragma unroll
     for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * (z[k] * logistic(z[k]));
     const int64_t o = row * (int64_t)a.vectors * kVec + i * (int64_t)kVec;
     if (live && a.out != nullptr) store8<DZ>(a.out, o, y);
     if (a.codes != nullptr) {
-        float down;
-        const uint32_t byte = scale_byte(lanes16_max(live ? top8(y) : 0), &down);
+        // fp32: s, the gate (6 ulps) and four products are rounded
+        u32x2 codes;
+        const int byte = quantise8(y, live, 16, [&](int k) { return (double)x[k] * root * (double)w[k] * ((double)z[k] * logistic_f64(z[k])); }, &codes);
         if (live) {
-            *reinterpret_cast<u32x2*>(a.codes + o) = codes8(y, down);
+            *reinterpret_cast<u32x2*>(a.codes + o) = codes;
             if ((i & 15) == 0) a.scales[row * a.scale_stride + (i >> 4)] = (uint8_t)byte;
         }
     }
@@ -135,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const Gat
         const int lead = (int)threadIdx.x - column;
         const float xx = head_sum<L>(squares8(x), part, lead, head_lanes);
         gx = head_sum<L>(gx, part, lead, head_lanes);
-        const float rs = inverse_rms(xx, a.inverse_size, a.eps), mean = rs * (float)(gx * a.inverse_size);
+        const float rs = (float)inverse_rms(xx, a.inverse_size, a.eps), mean = rs * (float)(gx * a.inverse_size);
         float dx[kVec], dz[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {

@@ -82,7 +82,8 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
     float sum = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8(r[v]) : 0;
-    const float rs = inverse_rms(row_sum<LANES>(sum, wave_sum), a.inverse_width, a.eps);
+    const double root = inverse_rms(row_sum<LANES>(sum, wave_sum), a.inverse_width, a.eps);
+    const float rs = (float)root;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int i = t + v * lanes;
@@ -94,10 +95,11 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
         if (live && a.residual_out != nullptr) store8<DR>(a.residual_out, o, r[v]);
         if (live && a.out != nullptr) store8<DX>(a.out, o, y);
         if (a.codes != nullptr) {
-            float down;
-            const uint32_t byte = scale_byte(lanes16_max(live ? top8(y) : 0), &down);
+            // fp32: s, w + w0 and two products are rounded, 2 ulps in all
+            u32x2 codes;
+            const int byte = quantise8(y, live, 4, [&](int k) { return (double)r[v][k] * root * ((double)w[v][k] + (double)a.weight_offset); }, &codes);
             if (live) {
-                *reinterpret_cast<u32x2*>(a.codes + o) = codes8(y, down);
+                *reinterpret_cast<u32x2*>(a.codes + o) = codes;
                 if ((t & 15) == 0) a.scales[row * a.scale_stride + (i >> 4)] = (uint8_t)byte;
             }
         }
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_k
                 gsum += wave_sum[turn][1][k];
             }
         }
-        const float rs = inverse_rms(rsum, a.inverse_width, a.eps), mean = rs * (float)(gsum * a.inverse_width);
+        const float rs = (float)inverse_rms(rsum, a.inverse_width, a.eps), mean = rs * (float)(gsum * a.inverse_width);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = t + v * lanes;

@@ -113,13 +113,30 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// A value of each lane of a 16-lane row for another lane of the row.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t x) {
+    return dpp_u32<CTRL>((uint32_t)x) | (uint64_t)dpp_u32<CTRL>((uint32_t)(x >> 32)) << 32;
+}
 // The largest of 16 lanes' values.
 __device__ __forceinline__ uint32_t lanes16_max(uint32_t x) {
     auto step = [&](uint32_t y) { x = x > y ? x : y; };
-    step(__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false));
-    step(__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false));
-    step(__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, false));
-    step(__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, false));
+    step(dpp_u32<0xB1>(x));
+    step(dpp_u32<0x4E>(x));
+    step(dpp_u32<0x141>(x));
+    step(dpp_u32<0x140>(x));
+    return x;
+}
+__device__ __forceinline__ uint64_t lanes16_max(uint64_t x) {
+    auto step = [&](uint64_t y) { x = x > y ? x : y; };
+    step(dpp_u64<0xB1>(x));
+    step(dpp_u64<0x4E>(x));
+    step(dpp_u64<0x141>(x));
+    step(dpp_u64<0x140>(x));
     return x;
 }
 
@@ -134,24 +151,66 @@ __device__ __forceinline__ uint32_t top8(const float (&y)[kVec]) {
     return t;
 }
 
-// Scale byte of a group whose largest magnitude has these bits (e + 127 for the smallest e >= -126 with
-// top 2^-e <= 448 = 1.75 * 2^8), and 2^-e; 255 and NaN for a group with a NaN or an infinity.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t top, float* down) {
-    int b = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
-    b = b < 1 ? 1 : b;
-    const bool bad = top >= 0x7f800000u;
-    *down = __builtin_bit_cast(float, bad ? 0x7fc00000u : (uint32_t)(254 - b) << 23);
-    return bad ? 255u : (uint32_t)b;
+// Scale byte of a group whose largest magnitude has these bits: e + 127 for the smallest e >= -126 with
+// top 2^-e <= 448 = 1.75 * 2^8; 255 for a group with a NaN or an infinity.
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+    const int b = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
+    return top >= 0x7f800000u ? 255 : b < 1 ? 1 : b;
 }
 
-// Eight values times 2^-e as e4m3 codes.  The products are exact but below 2^-126, far under half of
-// the smallest code, so each value is rounded once.
-__device__ __forceinline__ u32x2 codes8(const float (&y)[kVec], float down) {
-    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * down, y[1] * down, 0, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * down, y[3] * down, lo, true);
-    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * down, y[5] * down, 0, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * down, y[7] * down, hi, true);
-    return u32x2{(uint32_t)lo, (uint32_t)hi};
+// Whether an fp32 value that is off by a few ulps may lie on either side of a border whose mantissa ends so.
+__device__ __forceinline__ bool near_border(uint32_t bits, uint32_t mask, uint32_t border, uint32_t ulps) {
+    return ((bits - border + ulps) & mask) <= 2 * ulps;
+}
+
+// Eight channels of a lane as e4m3 codes, the group's scale from its 16 lanes (all of which take part; lanes that are
+// not live count as zeros).  Codes and scale are those of the 64-bit values exact(k): where an fp32 value is within
+// `ulps` of its code's or the scale's border, the 64-bit one decides (one value in 32000, one group in 250000 at 16 ulps).
+// Returns the scale byte.
+template <typename Exact>
+__device__ __forceinline__ int quantise8(const float (&y)[kVec], bool live, uint32_t ulps, Exact exact, u32x2* codes) {
+    const uint32_t top = lanes16_max(live ? top8(y) : 0);
+    int byte = scale_byte(top);
+    if (byte < 255 && near_border(top, 0x7fffffu, 0x600000u, ulps)) {  // the same in all 16 lanes
+        uint64_t t = 0;
+        if (live)
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                const uint64_t v = __builtin_bit_cast(uint64_t, __builtin_fabs(exact(k)));
+                t = t > v ? t : v;
+            }
+        const double most = __builtin_bit_cast(double, lanes16_max(t));
+        const double limit = __builtin_ldexp(448.0, byte - 127);
+        if (most > limit) ++byte;
+        else if (byte > 1 && most <= 0.5 * limit) --byte;
+    }
+    const float down = __builtin_bit_cast(float, byte == 255 ? 0x7fc00000u : (uint32_t)(254 - byte) << 23);
+    // the products are exact but below 2^-126, far under half of the smallest code
+    float c[kVec];
+    auto halfway = [&](int k) { return near_border(__builtin_bit_cast(uint32_t, c[k]), 0xfffffu, 0x80000u, ulps); };  // between codes
+    bool near = false;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        c[k] = y[k] * down;
+        near |= halfway(k);
+    }
+    if (near && live && byte < 255)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            if (!halfway(k)) continue;
+            const double v = exact(k) * down;
+            c[k] = (float)v;
+            const uint32_t bits = __builtin_bit_cast(uint32_t, c[k]);
+            // halfway as fp32 only: one step towards the value
+            if ((bits & 0xfffffu) == 0x80000u && (double)c[k] != v)
+                c[k] = __builtin_bit_cast(float, __builtin_fabs(v) > (double)__builtin_fabsf(c[k]) ? bits + 1 : bits - 1);
+        }
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], hi, true);
+    *codes = u32x2{(uint32_t)lo, (uint32_t)hi};
+    return byte;
 }
 
 // The sum of eight squares, in pairs.
@@ -161,13 +220,12 @@ __device__ __forceinline__ float squares8(const float (&x)[kVec]) {
     return (a + b) + (c + d);
 }
 
-// 1 / sqrt(sum / n + eps) rounded once, from 64 bits: an ulp here moves codes of the whole row over their borders
-// (4096 x 5120: 2.0e-4 of the codes' 2-norm with fp32 steps, 4e-5 so).
-__device__ __forceinline__ float inverse_rms(double sum, double inverse_n, float eps) {
+// 1 / sqrt(sum / n + eps) to 2^-48.  (Rounded at each step to fp32 it would move codes of whole rows over their borders:
+// 4096 x 5120, 2.0e-4 of the codes' 2-norm.)
+__device__ __forceinline__ double inverse_rms(double sum, double inverse_n, float eps) {
     const double m = __builtin_fma(sum, inverse_n, (double)eps);
     const double y = __builtin_amdgcn_rsq(m);
-    const float r = (float)(y * __builtin_fma(-0.5 * m * y, y, 1.5));
-    return m == __builtin_inf() ? 0.0f : r;  // a sum past fp32's range
+    return m == __builtin_inf() ? 0.0 : y * __builtin_fma(-0.5 * m * y, y, 1.5);  // infinite: an infinity in the row
 }
 
 // out[c] = sum of partial[p][c] over p, in an order that depends on the sizes alone.
