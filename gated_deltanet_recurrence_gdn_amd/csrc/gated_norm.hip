@@ -11,6 +11,7 @@
 // power of two, whose sums are lane exchanges; up to 240 lanes otherwise, whose
 // heads are summed through LDS.  No piece needs another, so both passes read
 // their inputs once and are bound by their bytes.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -20,6 +21,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kSlice = int64_t{1} << 23;  // workgroups of a forward launch, whose threads are counted in 32 bits
 constexpr int kPart = kThreads + 32;  // lanes past the last piece sum over a head's width too
 constexpr int kBackGrid = 1024;  // workgroups of a backward pass, each with its own partial of dweight
 
@@ -38,6 +40,7 @@ struct GatedArgs {
     double inverse_size; // 1 / d_v
     uint32_t pieces;     // of a row
     uint32_t total;      // of the call
+    uint64_t first;      // the launch's first piece (forward)
     int32_t lanes;       // of a piece
     int32_t per_wg;      // pieces of a workgroup
     int32_t vectors;     // of a row: h_v d_v / 8
@@ -86,9 +89,9 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     __shared__ float part[L == 0 ? kPart : 1];
     const int lanes = L == 0 ? a.lanes : L < 16 ? 16 : L, head_lanes = L == 0 ? a.head_lanes : L;
     const int in_wg = threadIdx.x / lanes, p = threadIdx.x % lanes;
-    const uint32_t at = blockIdx.x * (uint32_t)a.per_wg + in_wg;
+    const uint64_t at = a.first + blockIdx.x * (uint64_t)a.per_wg + in_wg;
     const bool mine = in_wg < a.per_wg && at < a.total;
-    const uint32_t piece = mine ? at : 0;
+    const uint32_t piece = mine ? (uint32_t)at : 0;
     const int64_t row = piece / a.pieces;
     const int i = (int)(piece % a.pieces) * lanes + p;
     const bool live = mine && i < a.vectors;
@@ -184,7 +187,7 @@ int check_gated(const gdn_gated_norm_shape* sh) {
 }
 
 // The pieces of a call; *grid workgroups of them, at most `most`.
-int plan_gated(const gdn_gated_norm_shape* sh, int64_t most, GatedArgs* a, int* grid) {
+int plan_gated(const gdn_gated_norm_shape* sh, int64_t most, GatedArgs* a, int64_t* grid) {
     const int head = sh->d_v / kVec;
     int lanes = head;  // a multiple of both 16 lanes and a head
     while (lanes % 16 != 0) lanes += head;
@@ -198,7 +201,7 @@ int plan_gated(const gdn_gated_norm_shape* sh, int64_t most, GatedArgs* a, int* 
     if (total > 0xffffffffLL) return GDN_ERR_SHAPE;
     a->total = (uint32_t)total;
     const int64_t wgs = (total + a->per_wg - 1) / a->per_wg;
-    *grid = (int)(wgs < most ? wgs : most);
+    *grid = wgs < most ? wgs : most;
     a->rows = sh->rows;
     a->x_stride = sh->x_stride;
     a->z_stride = sh->z_stride;
@@ -209,11 +212,12 @@ int plan_gated(const gdn_gated_norm_shape* sh, int64_t most, GatedArgs* a, int* 
 }
 
 template <bool BACK>
-hipError_t launch(const gdn_gated_norm_shape* sh, const GatedArgs& a, int grid, hipStream_t stream) {
+hipError_t launch(const gdn_gated_norm_shape* sh, const GatedArgs& a, int64_t wgs, hipStream_t stream) {
+    const dim3 grid((unsigned)wgs);
     auto go = [&](auto dx, auto dz, auto l) {
         constexpr int DX = decltype(dx)::value, DZ = decltype(dz)::value, L = decltype(l)::value;
-        if constexpr (BACK) hipLaunchKernelGGL((gated_norm_backward_kernel<DX, DZ, L>), dim3(grid), dim3(kThreads), 0, stream, a);
-        else hipLaunchKernelGGL((gated_norm_forward_kernel<DX, DZ, L>), dim3(grid), dim3(kThreads), 0, stream, a);
+        if constexpr (BACK) hipLaunchKernelGGL((gated_norm_backward_kernel<DX, DZ, L>), grid, dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL((gated_norm_forward_kernel<DX, DZ, L>), grid, dim3(kThreads), 0, stream, a);
         return hipGetLastError();
     };
     auto head = [&](auto dx, auto dz) {
@@ -251,7 +255,7 @@ int gdn_gated_norm_forward(const gdn_gated_norm_shape* shape, const void* x, con
     if (codes != nullptr && (shape->scale_stride % 4 != 0 || shape->scale_stride < (width + GDN_GROUP - 1) / GDN_GROUP))
         return GDN_ERR_SHAPE;
     GatedArgs a = {};
-    int grid = 0;
+    int64_t grid = 0;
     if ((rc = plan_gated(shape, 0x7fffffffLL, &a, &grid)) != GDN_OK) return rc;
     if (shape->rows == 0) return GDN_OK;
     if (x == nullptr || z == nullptr || weight == nullptr) return GDN_ERR_NULL;
@@ -265,12 +269,16 @@ int gdn_gated_norm_forward(const gdn_gated_norm_shape* shape, const void* x, con
     a.out = out;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales);
-    return launch<false>(shape, a, grid, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    for (int64_t wg = 0; wg < grid; wg += kSlice) {
+        a.first = (uint64_t)wg * a.per_wg;
+        if (launch<false>(shape, a, std::min(kSlice, grid - wg), static_cast<hipStream_t>(stream)) != hipSuccess) return GDN_ERR_HIP;
+    }
+    return GDN_OK;
 }
 
 size_t gdn_gated_norm_backward_workspace_bytes(const gdn_gated_norm_shape* shape) {
     GatedArgs a = {};
-    int grid = 0;
+    int64_t grid = 0;
     if (check_gated(shape) != GDN_OK || plan_gated(shape, kBackGrid, &a, &grid) != GDN_OK) return 0;
     return (size_t)grid * shape->d_v * sizeof(float);
 }
@@ -281,7 +289,7 @@ int gdn_gated_norm_backward(const gdn_gated_norm_shape* shape, const void* dout,
     int rc = check_gated(shape);
     if (rc != GDN_OK) return rc;
     GatedArgs a = {};
-    int grid = 0;
+    int64_t grid = 0;
     if ((rc = plan_gated(shape, kBackGrid, &a, &grid)) != GDN_OK) return rc;
     if (dx == nullptr && dz == nullptr && dweight == nullptr) return GDN_ERR_NULL;
     if (!aligned_to(dweight, 16)) return GDN_ERR_ALIGN;
@@ -306,7 +314,7 @@ int gdn_gated_norm_backward(const gdn_gated_norm_shape* shape, const void* dout,
     a.partial = dweight != nullptr ? static_cast<float*>(workspace) : nullptr;
     if (launch<true>(shape, a, grid, st) != hipSuccess) return GDN_ERR_HIP;
     if (dweight == nullptr) return GDN_OK;
-    return launch_sum_partials(a.partial, grid, shape->d_v, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    return launch_sum_partials(a.partial, (int32_t)grid, shape->d_v, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 }  // extern "C"

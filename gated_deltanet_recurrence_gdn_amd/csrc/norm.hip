@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxBackThreads = 512;
+constexpr int64_t kSlice = int64_t{1} << 21;  // rows of a forward launch, whose threads are counted in 32 bits
 
 struct NormArgs {
     const void* x;       // forward: x; backward: r
@@ -31,6 +32,7 @@ struct NormArgs {
     void* dx;
     float* partial;      // [workgroups][width]
     int64_t rows, x_stride;
+    int64_t first;       // the launch's first row (forward)
     double inverse_width;
     int32_t width, weight_dtype, scale_stride;
     float eps, weight_offset;
@@ -54,7 +56,7 @@ template <int DX, int DR, int V, int LANES>
 __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel(const NormArgs a) {
     __shared__ float wave_sum[kMaxThreads / 64];
     const int lanes = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % LANES : threadIdx.x;
-    const int64_t at = LANES ? (int64_t)blockIdx.x * (blockDim.x / (LANES ? LANES : 1)) + threadIdx.x / (LANES ? LANES : 1) : blockIdx.x;
+    const int64_t at = a.first + (LANES ? (int64_t)blockIdx.x * (blockDim.x / (LANES ? LANES : 1)) + threadIdx.x / (LANES ? LANES : 1) : blockIdx.x);
     const int64_t row = at < a.rows ? at : a.rows - 1;
     const int n = a.width / kVec;
     float r[V][kVec], w[V][kVec];
@@ -95,9 +97,9 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
         if (live && a.residual_out != nullptr) store8<DR>(a.residual_out, o, r[v]);
         if (live && a.out != nullptr) store8<DX>(a.out, o, y);
         if (a.codes != nullptr) {
-            // fp32: s, w + w0 and two products are rounded, 2 ulps in all
+            // fp32: s, w + w0 and two products are rounded, 4 ulps at most
             u32x2 codes;
-            const int byte = quantise8(y, live, 4, [&](int k) { return (double)r[v][k] * root * ((double)w[v][k] + (double)a.weight_offset); }, &codes);
+            const int byte = quantise8(y, live, 6, [&](int k) { return (double)r[v][k] * root * ((double)w[v][k] + (double)a.weight_offset); }, &codes);
             if (live) {
                 *reinterpret_cast<u32x2*>(a.codes + o) = codes;
                 if ((t & 15) == 0) a.scales[row * a.scale_stride + (i >> 4)] = (uint8_t)byte;
@@ -373,8 +375,11 @@ int gdn_norm_forward(const gdn_norm_shape* shape, const void* x, const void* res
     a.out = out;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales);
-    const NormPlan p = plan_rows(shape->rows, shape->width, false);
-    return launch<false>(shape, p, a, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    for (a.first = 0; a.first < shape->rows; a.first += kSlice) {
+        const NormPlan p = plan_rows(std::min(kSlice, shape->rows - a.first), shape->width, false);
+        if (launch<false>(shape, p, a, static_cast<hipStream_t>(stream)) != hipSuccess) return GDN_ERR_HIP;
+    }
+    return GDN_OK;
 }
 
 size_t gdn_norm_backward_workspace_bytes(const gdn_norm_shape* shape) {

@@ -149,7 +149,7 @@ int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_sca
         if (s < shape->inner || s % 16 != 0 || s > (int64_t{1} << 22)) return GDN_ERR_SHAPE;
     if (shape->w_scale_dtype != GDN_F32 && shape->w_scale_dtype != GDN_E8M0) return GDN_ERR_DTYPE;
     if (shape->out_dtype != GDN_BF16 && shape->out_dtype != GDN_F16) return GDN_ERR_DTYPE;
-    if (shape->a_scale_stride < groups || shape->a_scale_stride % 4 != 0) return GDN_ERR_SHAPE;
+    if (shape->a_scale_stride < groups || shape->a_scale_stride % 4 != 0 || shape->a_scale_stride > (1 << 22)) return GDN_ERR_SHAPE;
     if (shape->w_scale_stride < groups || (shape->w_scale_dtype == GDN_E8M0 && shape->w_scale_stride % 4 != 0)) return GDN_ERR_SHAPE;
     if (n_parts < 1 || n_parts > GDN_MAX_PARTS) return GDN_ERR_SHAPE;
     if (parts == nullptr) return GDN_ERR_NULL;
@@ -167,10 +167,10 @@ int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_sca
         if (columns % 4 == 0 && q.stride % 4 == 0 && aligned_to(q.data, 8)) p.part[i].wide = 1;
         if (columns % 8 == 0 && q.stride % 8 == 0 && aligned_to(q.data, 16)) p.part[i].wide = 2;
         columns += q.columns;
-        if (columns > 0x7fffffffLL - 1024) return GDN_ERR_SHAPE;
+        if (columns > (int64_t{1} << 27)) return GDN_ERR_SHAPE;
     }
-    // workgroups of the smallest tiles
-    if ((shape->tokens + 63) / 64 * ((columns + 63) / 64) > 0x7fffffffLL) return GDN_ERR_SHAPE;
+    // a launch's threads are counted in 32 bits; more results than any memory holds
+    if ((shape->tokens + 255) / 256 * ((columns + 255) / 256) > (int64_t{1} << 21)) return GDN_ERR_SHAPE;
     if (shape->tokens == 0) return GDN_OK;
     if (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr) return GDN_ERR_NULL;
     if (!aligned_to(a, 16) || !aligned_to(w, 16) || !aligned_to(a_scales, 4) || !aligned_to(w_scales, 4)) return GDN_ERR_ALIGN;

@@ -597,7 +597,7 @@ int gdn_scan_backward(const gdn_shape* shape, const int32_t* cu_seqlens, const v
 
 typedef struct gdn_norm_shape {
     int64_t rows;          /* tokens, 0 .. 2^31 - 1 */
-    int64_t x_stride;      /* elements from one row of x (backward: of r) to the next, a multiple of 8, at least width */
+    int64_t x_stride;      /* elements from one row of x (backward: of r) to the next, a multiple of 8, width .. 2^31 */
     int32_t width;         /* channels, a multiple of 8 up to GDN_MAX_WIDTH */
     int32_t dtype;         /* of x, out and dout: GDN_F32, GDN_BF16 or GDN_F16 */
     int32_t residual_dtype;/* of residual, residual_out, r, dresidual and dx */
@@ -616,8 +616,10 @@ typedef struct gdn_norm_shape {
  * and, or, to `codes` and `scales` (nullable, both or none).  Sums and products
  * are fp32.
  * residual, residual_out, out and codes are dense [rows][width]; residual_out may be
- * residual (no other output overlaps an input).  x, residual, residual_out, out and
- * weight are 16-byte aligned, codes 8-byte.
+ * residual, and out may be a dense x (no other output overlaps an input).  x, residual,
+ * residual_out, out and weight are 16-byte aligned, codes 8-byte, scales 4-byte.  A row
+ * of zeros with eps = 0 is NaN; a NaN or an infinity in a row leaves nothing finite of
+ * the channels that hold one and may reach its whole row, but no other.
  *
  * gdn_norm_backward: from dout [rows][width] (dtype) and r (residual_dtype; x itself, in
  * residual_dtype = dtype, where there was no residual)
@@ -638,7 +640,7 @@ int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void*
 
 typedef struct gdn_gated_norm_shape {
     int64_t rows;          /* tokens, 0 .. 2^31 - 1 */
-    int64_t x_stride;      /* elements from one row of x to the next, a multiple of 8, at least h_v d_v */
+    int64_t x_stride;      /* elements from one row of x to the next, a multiple of 8, h_v d_v .. 2^31 */
     int64_t z_stride;      /* of z, likewise */
     int32_t h_v;           /* value heads, >= 1, at most 2^20 */
     int32_t d_v;           /* value channels: a multiple of 16 up to 256 */
@@ -655,7 +657,9 @@ typedef struct gdn_gated_norm_shape {
  *     y = n w silu(z),   silu(z) = z / (1 + e^-z)
  * x is `out` of a verify, prefill or scan ([rows][h_v][d_v]), z the gate's projection,
  * weight [d_v].  y goes to `out` (nullable, z_dtype) and, or, to `codes` and `scales`
- * (nullable, both or none), [rows][h_v d_v] as the output projection reads them.
+ * (nullable, both or none), [rows][h_v d_v] as the output projection reads them.  out
+ * may be a dense z, or a dense x of its type.  A NaN or an infinity in x or z may reach its whole head,
+ * and makes its group's scale NaN, but no other head's `out`.
  *
  * gdn_gated_norm_backward: with s = 1 / sqrt(mean x^2 + eps), a = 1 / (1 + e^-z) and
  * g = dout w silu(z)
@@ -675,16 +679,16 @@ int gdn_gated_norm_backward(const gdn_gated_norm_shape* shape, const void* dout,
 typedef struct gdn_project_part {
     void* data;       /* aligned to its element size; 16 bytes for the widest stores */
     int64_t stride;   /* at least columns */
-    int32_t columns;  /* >= 1 */
+    int32_t columns;  /* >= 1; of all parts together N, at most 2^27 */
     int32_t reserved; /* 0 */
 } gdn_project_part;
 
 typedef struct gdn_project_shape {
-    int64_t tokens;       /* M >= 0, below 2^31 */
-    int64_t a_stride;     /* bytes from one row of a to the next, a multiple of 16, at least inner */
+    int64_t tokens;       /* M >= 0, below 2^31; ceil(M / 256) * ceil(N / 256) at most 2^21 */
+    int64_t a_stride;     /* bytes from one row of a to the next, a multiple of 16, inner .. 2^22 */
     int64_t w_stride;     /* of w, likewise */
     int32_t inner;        /* K, a multiple of 16, at least 16 */
-    int32_t a_scale_stride; /* bytes from one row of a_scales to the next, a multiple of 4, at least ceil(K / 128) */
+    int32_t a_scale_stride; /* bytes from one row of a_scales to the next, a multiple of 4, ceil(K / 128) .. 2^22 */
     int32_t w_scale_stride; /* GDN_E8M0: likewise; GDN_F32: elements, at least ceil(K / 128) */
     int32_t w_scale_dtype;  /* GDN_F32 or GDN_E8M0 */
     int32_t out_dtype;      /* GDN_BF16 or GDN_F16 */
@@ -698,7 +702,7 @@ typedef struct gdn_project_shape {
  * verify, the prefill and the gated norm take.  a [M][K] and w [N][K] are e4m3 codes
  * with the scales above (a: codes and scales of gdn_norm_forward or
  * gdn_gated_norm_forward), 16-byte aligned; a_scales and GDN_E8M0 scales are
- * 4-byte aligned.
+ * 4-byte aligned.  No output overlaps an input or another output.
  *
  * Groups are summed in fp32, in an order that depends on the shape alone, so results
  * repeat bit for bit; the matrix instruction adds the products within a group with

@@ -131,6 +131,9 @@ def project(parts=None, n_parts=None, a=FAKE, a_scales=FAKE, w=FAKE, w_scales=FA
     (dict(parts=[part(reserved=1)]), "GDN_ERR_SHAPE"), (dict(parts=[part(data=None)]), "GDN_ERR_NULL"),
     (dict(parts=[part(data=FAKE + 1)]), "GDN_ERR_ALIGN"),
     (dict(parts=[part(columns=1 << 30), part(columns=1 << 30)]), "GDN_ERR_SHAPE"),
+    (dict(parts=[part(columns=1 << 27), part(columns=1)]), "GDN_ERR_SHAPE"), (dict(a_scale_stride=1 << 23), "GDN_ERR_SHAPE"),
+    (dict(w_stride=(1 << 22) + 16), "GDN_ERR_SHAPE"), (dict(tokens=(1 << 31) - 1, parts=[part(columns=256)]), "GDN_ERR_SHAPE"),
+    (dict(tokens=1 << 20, parts=[part(columns=1 << 18)]), "GDN_ERR_SHAPE"),
 ])
 def test_project_refusals(kw, code):
     assert project(**kw) == E[code]
