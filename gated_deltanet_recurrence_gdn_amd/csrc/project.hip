@@ -115,20 +115,27 @@ hipError_t launch(const ProjectArgs& p, hipStream_t stream) {
         const hipError_t e = allow_max_lds<&project_rows_kernel<DT, E8M0, MT, NT>>();
         if (e != hipSuccess) return e;
         const int waves = std::min(p.groups, kMaxWaves);
-        const int64_t grid = ((int64_t)p.columns + 16 * NT - 1) / (16 * NT) * ((p.tokens + 16 * MT - 1) / (16 * MT));
+        const int64_t grid = ((int64_t)p.columns + 16 * NT - 1) / (16 * NT) * (((int64_t)p.tokens + 16 * MT - 1) / (16 * MT));
         hipLaunchKernelGGL((project_rows_kernel<DT, E8M0, MT, NT>), dim3((unsigned)grid), dim3(64 * waves), waves * kStage, stream, p);
         return hipGetLastError();
     };
     constexpr std::integral_constant<int, 1> one;
     constexpr std::integral_constant<int, 2> two;
     constexpr std::integral_constant<int, 4> four;
+    const int cus = device_cus();
+    if (cus <= 0) return hipErrorUnknown;
     // 64 columns a workgroup read a less often, 32 give more workgroups: 64 tokens x 16384 x 5120 take 23 and 29 us,
     // x 5120 x 6144 20 and 13
-    const bool wide = (p.columns + 63) / 64 >= device_cus();
+    const bool wide = (p.columns + 63) / 64 >= cus;
     if (p.tokens <= 16) return wide ? go(one, four) : go(one, two);
     if (p.tokens <= 32) return wide ? go(two, four) : go(two, two);
-    // from 65 tokens on a tile (128 tokens x 16384 x 5120: 32 us; rows for 64 tokens twice: 47)
     if (p.tokens <= 64) return wide ? go(four, four) : go(four, two);
+    // More tokens in blocks of 64 where these workgroups are few and their waves' shares of the groups, at about 2.1 us a
+    // group, end before a tile's steps would: 333 x 1039 x 1936 take 9 us and 14, 256 x 1024 x 8192 17 and 38, 128 x 5120
+    // x 6144 22 and 30; by tiles 128 x 16384 x 1024 9 and 15
+    const int64_t blocks = ((int64_t)p.columns + 31) / 32 * (((int64_t)p.tokens + 63) / 64);
+    const float us = 2.1f * (float)((blocks + cus - 1) / cus) * (float)((p.groups + kMaxWaves - 1) / kMaxWaves);
+    if (blocks <= 4 * cus && us < project_tiles_us(p)) return go(four, two);
     return launch_project_tiles(p, E8M0, DT, stream);
 }
 

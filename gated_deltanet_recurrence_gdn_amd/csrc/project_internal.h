@@ -40,6 +40,8 @@ struct ProjectArgs {
 
 // The product in tiles (project_tile.hip).
 hipError_t launch_project_tiles(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t stream);
+// About how long that takes.
+float project_tiles_us(const ProjectArgs& p);
 
 __device__ __forceinline__ f32x4 mfma_scaled(i32x8 w, i32x8 a, f32x4 c, int w_scale, int a_scale) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, w_scale, 0, a_scale);
@@ -54,20 +56,8 @@ __device__ __forceinline__ rsrc_t rsrc_of(const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
 }
 
-__device__ __forceinline__ i32x4 load_regs(rsrc_t from, uint32_t offset) {
-    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(from, offset, 0, 0));
-}
-
-__device__ __forceinline__ int load_word(rsrc_t from, uint32_t offset) {
-    return __builtin_amdgcn_raw_buffer_load_b32(from, offset, 0, 0);
-}
-
 __device__ __forceinline__ int load_byte(rsrc_t from, uint32_t lane_offset, int offset) {
     return __builtin_amdgcn_raw_buffer_load_b8(from, lane_offset, offset, 0);
-}
-
-__device__ __forceinline__ float load_float(rsrc_t from, int offset) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, 0, offset, 0));
 }
 
 // 16 bytes a lane into LDS, lane after lane from `to` on.

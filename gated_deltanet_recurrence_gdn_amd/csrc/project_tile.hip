@@ -223,26 +223,36 @@ hipError_t launch(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t st
     return e8m0 ? launch<GDN_F16, true, WM, WN, FN, DEEP>(p, stream) : launch<GDN_F16, false, WM, WN, FN, DEEP>(p, stream);
 }
 
-}  // namespace
-
 // The tile: the one whose rounds over the chip take least.  Microseconds a step of 128 channels, as measured with fp32
 // weight scales, times the rounds:
-//   256 x 256, one a CU                2.2    (4096 x 16384 x 5120: 346 us, 128 x 128 404; 1024 x 16384 x 5120: 90 and 114)
+//   256 x 256, one a CU                2.2    (4096 x 16384 x 5120: 338 us, 128 x 128 404; 1024 x 16384 x 5120: 89 and 114)
 //   128 x 128, two a CU                1.25, alone on a CU 1.0   (4096 x 5120 x 6144: 158 us, 256 x 256 184)
 //   128 x 128, one a CU, four steps    0.8    (512 x 5120 x 6144: 38 us, two a CU 47, 64 x 128 50)
 //   64 x 128, two a CU, three steps    1.0, alone on a CU 0.75   (128 x 16384 x 5120: 32 us, 128 x 128 38)
-hipError_t launch_project_tiles(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t stream) {
+struct Choice {
+    int tile;
+    float us;  // a step
+};
+
+Choice choose_tile(const ProjectArgs& p) {
     const int64_t cus = device_cus();
-    if (cus <= 0) return hipErrorUnknown;
     auto tiles = [&](int64_t tm, int64_t tn) { return (p.tokens + tm - 1) / tm * ((p.columns + tn - 1) / tn); };
     auto rounds = [&](int64_t n, int64_t slots) { return (float)((n + slots - 1) / slots); };
     const int64_t large = tiles(256, 256), middle = tiles(128, 128), small = tiles(64, 128);
-    const float cost[4] = {2.2f * rounds(large, cus), middle <= cus ? 1.0f : 1.25f * rounds(middle, 2 * cus), 0.8f * rounds(middle, cus),
-                           small <= cus ? 0.75f : rounds(small, 2 * cus)};
-    int best = 0;
+    const float us[4] = {2.2f * rounds(large, cus), middle <= cus ? 1.0f : 1.25f * rounds(middle, 2 * cus), 0.8f * rounds(middle, cus),
+                         small <= cus ? 0.75f : rounds(small, 2 * cus)};
+    Choice best = {0, us[0]};
     for (int i = 1; i < 4; ++i)
-        if (cost[i] < cost[best]) best = i;
-    switch (best) {
+        if (us[i] < best.us) best = Choice{i, us[i]};
+    return best;
+}
+
+}  // namespace
+
+float project_tiles_us(const ProjectArgs& p) { return choose_tile(p).us * (float)p.groups; }
+
+hipError_t launch_project_tiles(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t stream) {
+    switch (choose_tile(p).tile) {
         case 0: return launch<4, 2, 8, 2>(p, e8m0, dtype, stream);
         case 1: return launch<2, 2, 4, 2>(p, e8m0, dtype, stream);
         case 2: return launch<2, 2, 4, 4>(p, e8m0, dtype, stream);

@@ -47,7 +47,7 @@ def test_product(M, N, K, scales):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("M", [1, 16, 40, 300])
+@pytest.mark.parametrize("M", [1, 16, 40, 300, 2200])
 @pytest.mark.parametrize("parts", [[256, 256, 768], [777, 6, 6, 250], [1] * 8, [3, 129, 5], [128, 4, 124, 2]])
 def test_parts(M, parts, dtype):
     x = operands(M, M, sum(parts), 272)
@@ -56,7 +56,7 @@ def test_parts(M, parts, dtype):
     check(*x, outs)
 
 
-@pytest.mark.parametrize("M", [1, 22, 150])
+@pytest.mark.parametrize("M", [1, 22, 150, 8300])
 def test_rows_apart(M):
     """Operands and outputs that are slices of wider rows; what lies between is left as it was."""
     a, sa, w, sw = operands(3, M, 200, 640)
@@ -91,7 +91,7 @@ def test_what_is_behind_the_last_channel_is_not_read(M, scales):
     ref.near(outs[0][:, 1:], y, lost)
 
 
-@pytest.mark.parametrize("M", [1, 20, 140])
+@pytest.mark.parametrize("M", [1, 20, 140, 1700])
 @pytest.mark.parametrize("scales", ["f32", "e8m0"])
 def test_nan_scales_and_far_powers(M, scales):
     a, sa, w, sw = operands(2, M, 300, 512, scales)
@@ -121,7 +121,7 @@ def test_no_tokens():
     gb.gdn_project(a[:0], sa.view(torch.uint8)[:0].view(torch.float8_e8m0fnu), w, sw, out)
 
 
-@pytest.mark.parametrize("M", [4, 200])
+@pytest.mark.parametrize("M", [4, 200, 1000])
 def test_repeats_and_captured(M):
     x = operands(5, M, 520, 1040)
     outs, again = outputs(M, [512, 8], torch.bfloat16), outputs(M, [512, 8], torch.bfloat16)
@@ -151,10 +151,10 @@ def test_another_stream():
     check(*x, outs)
 
 
-# sizes that take each of the tiles: 256 x 256, 128 x 128 two and one a CU, 64 x 128; more than 64 groups
+# sizes that take each of the tiles: 256 x 256, 128 x 128 two and one a CU, 64 x 128; more than 64 groups; blocks of rows
 @pytest.mark.parametrize("scales", ["f32", "e8m0"])
 @pytest.mark.parametrize("M,parts,K", [(1000, [16000, 380], 272), (300, [16380], 400), (500, [5000, 100], 640), (70, [5100], 384),
-                                       (70, [300], 8400), (300, [16384], 8336), (1024, [16384], 8464), (3, [200], 8400), (60, [16400], 1168)])
+                                       (70, [300], 8400), (300, [16384], 8336), (2060, [2300], 272), (256, [1000], 8336), (4100, [60], 2064), (1024, [16384], 8464), (3, [200], 8400), (60, [16400], 1168)])
 def test_tiles(M, parts, K, scales):
     x = operands(M, M, sum(parts), K, scales)
     outs = outputs(M, parts, torch.bfloat16)
