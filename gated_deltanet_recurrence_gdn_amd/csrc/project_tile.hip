@@ -76,6 +76,9 @@ __device__ __forceinline__ void store_tile(const ProjectArgs& p, unsigned char* 
     }
 }
 
+// 4096 x 16384 x 5120 take 338 us with fp32 weight scales (2.03 PFLOP/s) and 312 with e8m0 ones; a library product of the
+// same operands without scales 225.  The matrix cores are busy half of the cycles, LDS reads a third; the e8m0 form takes
+// 249 without the loads, 221 without LDS reads too, and 249 with all of it on zeros, whose products draw less power.
 template <int DT, bool E8M0, int WM, int WN, int FN, int DEEP>
 __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const ProjectArgs p) {
     using T = Tile<WM, WN, FN, DEEP>;

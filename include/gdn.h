@@ -1,7 +1,10 @@
 /*
  * gdn.h -- C ABI of the Gated DeltaNet recurrent-state library for MI355X
  * (gfx950): speculative-draft verify over a chain or a tree, commit of the
- * accepted node, and chunked prefill.
+ * accepted node, chunked prefill, the training scan, the rows of the state
+ * pool (also in 8 bits), and what stands around the rule in a layer: the input
+ * norm, the gated norm of its outputs, both to 8 bits and with gradients, and
+ * projections in 8 bits.
  *
  * The recurrence, per (sequence, value head), with S the d_v x d_k state:
  *     S_t = alpha_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T
