@@ -49,8 +49,9 @@ struct GatedArgs {
     float eps;
 };
 
-// a = 1 / (1 + e^-z) to about an ulp.  -z log2(e) goes to the exponential in two parts; from z = -87 on, where
-// a is below 2^-126, it is held there.
+// a = 1 / (1 + e^-z) to about an ulp, for z from kLeast on, where a is still above 2^-126.  -z log2(e) goes to the
+// exponential in two parts.
+constexpr float kLeast = -86.0f;
 __device__ __forceinline__ float logistic(float z) {
     constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;  // log2(e)
     const float hi = -z * kHi, lo = __builtin_fmaf(-z, kHi, -hi) - z * kLo;
@@ -60,9 +61,10 @@ __device__ __forceinline__ float logistic(float z) {
     return __builtin_fmaf(q, __builtin_fmaf(-d, q, 1.0f), q);
 }
 
-// The same in 64 bits, for |z| up to 700: e^-z = 2^n e^r with |r| <= ln(2) / 2, whose series ends at r^13 / 13!.
+// The same in 64 bits (z a is nothing below z = -700, z above 700): e^-z = 2^n e^r with |r| <= ln(2) / 2, whose series ends at r^13 / 13!.
 __device__ __forceinline__ double logistic_f64(double z) {
     constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453, kLn2Rest = 2.3190468138462996e-17;
+    z = __builtin_fmax(__builtin_fmin(z, 700.0), -700.0);
     const double n = __builtin_rint(-z * kLog2e);
     double r = __builtin_fma(-n, kLn2, -z);
     r = __builtin_fma(-n, kLn2Rest, r);
@@ -70,6 +72,14 @@ __device__ __forceinline__ double logistic_f64(double z) {
 #pragma unroll
     for (int i = 13; i >= 1; --i) p = __builtin_fma(p * r, 1.0 / i, 1.0);
     return 1.0 / (1.0 + __builtin_ldexp(p, (int)n));
+}
+
+// Whether a lane's eight need the 64-bit form.
+__device__ __forceinline__ bool any_below(const float (&z)[kVec]) {
+    float least = z[0];
+#pragma unroll
+    for (int k = 1; k < kVec; ++k) least = __builtin_fminf(least, z[k]);
+    return least < kLeast;
 }
 
 // The sums of a head's lanes.  L lanes a head (2, 4, 8, 16 or 32), or any number through LDS (0).
@@ -82,6 +92,13 @@ __device__ __forceinline__ float head_sum(float x, float* part, int first, int h
     float s = 0;
     for (int k = 0; k < head_lanes; ++k) s += part[first + k];
     return s;
+}
+
+// Whether a lane asks: of the wave, or of the workgroup where sums go through LDS.
+template <int L>
+__device__ __forceinline__ bool any_of(bool ask) {
+    if constexpr (L != 0) return __any(ask);
+    else return __syncthreads_or(ask);
 }
 
 // Bytes bound it: 4096 tokens x 48 heads of 128, f16 to 8 bits, 28 us (4.5 TB/s); 16 tokens of fp32 3.4 us.
@@ -98,14 +115,23 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     const bool live = mine && i < a.vectors;
     // lanes without a vector read one all the same: whole heads, whose sums nothing uses
     const int64_t c = (i < a.vectors ? i : i % head_lanes) * kVec;
-    float x[kVec], z[kVec], w[kVec], y[kVec];
+    float x[kVec], z[kVec], w[kVec], y[kVec], gated[kVec];
     load8<DX>(a.x, row * a.x_stride + c, x);
     load8<DZ>(a.z, row * a.z_stride + c, z);
     load8(a.weight, i % head_lanes * kVec, a.weight_dtype, w);
-    const double root = inverse_rms(head_sum<L>(squares8(x), part, (int)threadIdx.x - p % head_lanes, head_lanes), a.inverse_size, a.eps);
+    const int lead = (int)threadIdx.x - p % head_lanes;
+    float sum = head_sum<L>(squares8(x), part, lead, head_lanes);
+    const float scale = range_scale(sum, a.eps);
+    if (any_of<L>(scale != 1.0f)) sum = head_sum<L>(squares8_of_scaled(x, scale), part, lead, head_lanes);
+    const double root = inverse_rms(sum, a.inverse_size, a.eps, scale) * scale;
     const float rs = (float)root;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * (z[k] * logistic(z[k]));
+    for (int k = 0; k < kVec; ++k) gated[k] = z[k] * logistic(z[k]);
+    if (any_below(z))
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) gated[k] = (float)(z[k] * logistic_f64(z[k]));
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * gated[k];
     const int64_t o = row * (int64_t)a.vectors * kVec + i * (int64_t)kVec;
     if (live && a.out != nullptr) store8<DZ>(a.out, o, y);
     if (a.codes != nullptr) {
@@ -146,15 +172,28 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const Gat
         load8<DZ>(a.dout, o, d);
         float gx = 0;
 #pragma unroll
+        for (int k = 0; k < kVec; ++k) gate[k] = logistic(z[k]);
+        if (any_below(z))
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) gate[k] = (float)logistic_f64(z[k]);
+#pragma unroll
         for (int k = 0; k < kVec; ++k) {
-            gate[k] = logistic(z[k]);
             g[k] = d[k] * w[k] * (z[k] * gate[k]);
             gx += g[k] * x[k];
         }
         const int lead = (int)threadIdx.x - column;
-        const float xx = head_sum<L>(squares8(x), part, lead, head_lanes);
+        float xx = head_sum<L>(squares8(x), part, lead, head_lanes);
         gx = head_sum<L>(gx, part, lead, head_lanes);
-        const float rs = (float)inverse_rms(xx, a.inverse_size, a.eps), mean = rs * (float)(gx * a.inverse_size);
+        const float scale = range_scale(xx, a.eps);
+        if (any_of<L>(scale != 1.0f)) {
+            xx = head_sum<L>(squares8_of_scaled(x, scale), part, lead, head_lanes);
+            gx = 0;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) gx += g[k] * (x[k] * scale);
+            gx = head_sum<L>(gx, part, lead, head_lanes);
+        }
+        const double root = inverse_rms(xx, a.inverse_size, a.eps, scale);
+        const float rs = (float)(root * scale), mean = (float)(root * gx * a.inverse_size);
         float dx[kVec], dz[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {

@@ -86,7 +86,16 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
     float sum = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8(r[v]) : 0;
-    const double root = inverse_rms(row_sum<LANES>(sum, wave_sum), a.inverse_width, a.eps);
+    double squares = row_sum<LANES>(sum, wave_sum);
+    const float c = range_scale(squares, a.eps);
+    if (LANES ? __any(c != 1.0f) : c != 1.0f) {  // the whole row's lanes
+        if constexpr (LANES == 0) __syncthreads();  // the first sum's readers are done
+        sum = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8_of_scaled(r[v], c) : 0;
+        squares = row_sum<LANES>(sum, wave_sum);
+    }
+    const double root = inverse_rms(squares, a.inverse_width, a.eps, c) * c;
     const float rs = (float)root;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -116,7 +125,7 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
 template <int DX, int DR, int V, int LANES>
 __global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_kernel(const NormArgs a) {
     constexpr int kWaves = LANES ? 4 : 1;  // walkers of a workgroup
-    __shared__ float wave_sum[2][2][kMaxBackThreads / 64];
+    __shared__ float wave_sum[3][2][kMaxBackThreads / 64];
     __shared__ float share[LANES ? 3 : 1][LANES ? V * 64 * kVec : 1];
     const int lanes = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % 64 : threadIdx.x;
     const int wave = LANES ? threadIdx.x / 64 : 0;
@@ -172,24 +181,42 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_k
         }
         fetch(row + walkers);
         double rsum, gsum;
-        rr = lanes_sum<64>(rr);
-        gr = lanes_sum<64>(gr);
-        if constexpr (LANES != 0) {
-            rsum = rr;
-            gsum = gr;
-        } else {  // two copies of the sums: the next row's do not wait for this row's readers
-            if ((threadIdx.x & 63) == 0) {
-                wave_sum[turn][0][threadIdx.x >> 6] = rr;
-                wave_sum[turn][1][threadIdx.x >> 6] = gr;
+        auto sum = [&](int copy) {
+            rr = lanes_sum<64>(rr);
+            gr = lanes_sum<64>(gr);
+            if constexpr (LANES != 0) {
+                rsum = rr;
+                gsum = gr;
+            } else {
+                if ((threadIdx.x & 63) == 0) {
+                    wave_sum[copy][0][threadIdx.x >> 6] = rr;
+                    wave_sum[copy][1][threadIdx.x >> 6] = gr;
+                }
+                lds_barrier();  // the next row's loads stay in flight
+                rsum = gsum = 0;
+                for (int k = 0; k < (int)(blockDim.x >> 6); ++k) {
+                    rsum += wave_sum[copy][0][k];
+                    gsum += wave_sum[copy][1][k];
+                }
             }
-            lds_barrier();  // the next row's loads stay in flight
-            rsum = gsum = 0;
-            for (int k = 0; k < (int)(blockDim.x >> 6); ++k) {
-                rsum += wave_sum[turn][0][k];
-                gsum += wave_sum[turn][1][k];
+        };
+        sum(turn);  // two copies in turn, and one for second sums: the next row's do not wait for this row's readers
+        const float scale = range_scale(rsum, a.eps);
+        if (scale != 1.0f) {  // the whole row's lanes
+            rr = gr = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool in = t + v * lanes < n;
+                float q = 0;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) q += d[v][k] * w[v][k] * (r[v][k] * scale);
+                rr += in ? squares8_of_scaled(r[v], scale) : 0;
+                gr += in ? q : 0;
             }
+            sum(2);
         }
-        const float rs = (float)inverse_rms(rsum, a.inverse_width, a.eps), mean = rs * (float)(gsum * a.inverse_width);
+        const double root = inverse_rms(rsum, a.inverse_width, a.eps, scale);
+        const float rs = (float)(root * scale), mean = (float)(root * gsum * a.inverse_width);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = t + v * lanes;

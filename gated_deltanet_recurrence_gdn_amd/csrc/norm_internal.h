@@ -222,10 +222,24 @@ __device__ __forceinline__ float squares8(const float (&x)[kVec]) {
 
 // 1 / sqrt(sum / n + eps) to 2^-48.  (Rounded at each step to fp32 it would move codes of whole rows over their borders:
 // 4096 x 5120, 2.0e-4 of the codes' 2-norm.)
-__device__ __forceinline__ double inverse_rms(double sum, double inverse_n, float eps) {
-    const double m = __builtin_fma(sum, inverse_n, (double)eps);
+// With c, of a row summed as c x: 1 / sqrt(sum / n + c^2 eps), c times too small for x.
+__device__ __forceinline__ double inverse_rms(double sum, double inverse_n, float eps, float c) {
+    const double m = __builtin_fma(sum, inverse_n, (double)eps * c * c);
     const double y = __builtin_amdgcn_rsq(m);
     return m == __builtin_inf() ? 0.0 : y * __builtin_fma(-0.5 * m * y, y, 1.5);  // infinite: an infinity in the row
+}
+
+// The power of two to sum a row times again, where its sum of squares has left fp32's range or is so small that parts of
+// it have (and eps does not hide them); 1 for other rows.
+__device__ __forceinline__ float range_scale(double sum, float eps) {
+    if (sum > 0x1p120) return 0x1p-80f;
+    return sum < 0x1p-100 && eps < 0x1p-90f ? 0x1p100f : 1.0f;
+}
+__device__ __forceinline__ float squares8_of_scaled(const float (&x)[kVec], float c) {
+    float y[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) y[k] = x[k] * c;
+    return squares8(y);
 }
 
 // out[c] = sum of partial[p][c] over p, in an order that depends on the sizes alone.

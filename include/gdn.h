@@ -622,7 +622,8 @@ typedef struct gdn_norm_shape {
  * residual, and out may be a dense x (no other output overlaps an input).  x, residual,
  * residual_out, out and weight are 16-byte aligned, codes 8-byte, scales 4-byte.  A row
  * of zeros with eps = 0 is NaN; a NaN or an infinity in a row leaves nothing finite of
- * the channels that hold one and may reach its whole row, but no other.
+ * the channels that hold one and may reach its whole row, but no other.  Other rows may be
+ * of any magnitude: one whose squares leave fp32's range is summed again, scaled.
  *
  * gdn_norm_backward: from dout [rows][width] (dtype) and r (residual_dtype; x itself, in
  * residual_dtype = dtype, where there was no residual)
