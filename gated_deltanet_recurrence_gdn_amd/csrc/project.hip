@@ -75,7 +75,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void project_rows_kernel(const Proj
         for (int t = 0; t < MT; ++t) av[t] = operand(16 * (NT + t));
 #pragma unroll
         for (int t = 0; t < MT; ++t) by[t] = scale[t];
-        const float now = sw;
+        int byte;
+        float now = sw;
+        if constexpr (E8M0) byte = __builtin_bit_cast(int, sw);
+        else now = split_scale(sw, &byte);
         wait_reads();
         if (g + waves < p.groups) stage(g + waves);
 #pragma unroll
@@ -83,9 +86,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void project_rows_kernel(const Proj
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 if constexpr (E8M0) {
-                    acc[s][t] = mfma_scaled(wv[s], av[t], acc[s][t], __builtin_bit_cast(int, now), by[t]);
+                    acc[s][t] = mfma_scaled(wv[s], av[t], acc[s][t], byte, by[t]);
                 } else {
-                    acc[s][t] += now * mfma_scaled(wv[s], av[t], f32x4{0, 0, 0, 0}, kOne, by[t]);
+                    acc[s][t] += now * mfma_scaled(wv[s], av[t], f32x4{0, 0, 0, 0}, byte, by[t]);
                 }
             }
     }

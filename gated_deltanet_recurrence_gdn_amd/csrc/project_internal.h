@@ -43,6 +43,15 @@ hipError_t launch_project_tiles(const ProjectArgs& p, bool e8m0, int32_t dtype, 
 // About how long that takes.
 float project_tiles_us(const ProjectArgs& p);
 
+// An fp32 weight scale's power of two goes into the instruction as an e8m0 one does, so that no group's sum leaves fp32's
+// range where its result does not; 1 to 2 is left for the sum (0 and subnormals: less, infinities and NaN: themselves).
+__device__ __forceinline__ float split_scale(float scale, int* byte) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, scale);
+    const int e = bits >> 23 & 255;
+    *byte = e == 255 ? kOne : e == 0 ? 1 : e;
+    return e == 255 ? scale : e == 0 ? scale * 0x1p126f : __builtin_bit_cast(float, (bits & 0x807fffffu) | (uint32_t)kOne << 23);
+}
+
 __device__ __forceinline__ f32x4 mfma_scaled(i32x8 w, i32x8 a, f32x4 c, int w_scale, int a_scale) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, w_scale, 0, a_scale);
 }

@@ -117,10 +117,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const Pro
     };
     // w's: 64 groups of the wave's block, one a lane
     const int64_t block = (int64_t)(min(n0 + wn * T::FN * 16, p.columns - 1) / GDN_GROUP) * p.w_scale_stride;
+    int powers;  // what of them goes into the instruction
+    float sws = 0;
     auto w_scales = [&](int g) {
         g = min(g + lane, p.groups - 1);
-        if constexpr (E8M0) return __builtin_bit_cast(float, (int)static_cast<const uint8_t*>(p.w_scales)[block + g]);
-        else return static_cast<const float*>(p.w_scales)[block + g];
+        if constexpr (E8M0) powers = static_cast<const uint8_t*>(p.w_scales)[block + g];
+        else sws = split_scale(static_cast<const float*>(p.w_scales)[block + g], &powers);
     };
 
     const unsigned char* at = lds;
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const Pro
 #pragma unroll
     for (int g = 0; g < T::DEEP; ++g)
         if (g == 0 || T::DEEP > 2) stage(g, g * T::STAGE);
-    float sws = w_scales(0);
+    w_scales(0);
     if constexpr (T::DEEP == 2) {
         wait_and_barrier<0>();
         stage(1, T::STAGE);
@@ -167,11 +169,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const Pro
     float sw = 0, sw_before = 0;
     int here = 0;  // this step's rows
     for (int first = 0; first < p.groups; first += 64) {
-        if (first > 0) sws = w_scales(first);
+        if (first > 0) w_scales(first);
         const int end = min(64, p.groups - first);
         for (int i = 0; i < end; ++i) {
             const int g = first + i;
-            sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sws), i));
+            const int power = __builtin_amdgcn_readlane(powers, i);
+            if constexpr (!E8M0) sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sws), i));
 #pragma unroll
             for (int s = 0; s < T::FN; ++s) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -188,10 +191,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const Pro
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if constexpr (E8M0) {
-                        acc[s][t] = mfma_scaled(wv[s % kAhead], av[t], acc[s][t], __builtin_bit_cast(int, sw), by[t]);
+                        acc[s][t] = mfma_scaled(wv[s % kAhead], av[t], acc[s][t], power, by[t]);
                     } else {
                         // the sums of 128 are scaled while the matrix cores form the next ones
-                        y[s & 1][t] = mfma_scaled(wv[s % kAhead], av[t], f32x4{0, 0, 0, 0}, kOne, by[t]);
+                        y[s & 1][t] = mfma_scaled(wv[s % kAhead], av[t], f32x4{0, 0, 0, 0}, power, by[t]);
                         acc[s == 0 ? T::FN - 1 : s - 1][t] += (s == 0 ? sw_before : sw) * y[(s & 1) ^ 1][t];
                     }
                     if (s == T::FN - 1) read_a(t);

@@ -712,7 +712,8 @@ typedef struct gdn_project_shape {
  * repeat bit for bit; the matrix instruction adds the products within a group with
  * about 17 bits below the largest (2e-5 of the 2-norm of y, of normal operands), which
  * is why y is bf16 or f16 and not fp32.  f16 outputs above 65504 become infinite.  A
- * scale of NaN, or a NaN code, makes NaN every y that it has part in.
+ * scale of NaN, or a NaN code, makes NaN every y that it has part in.  Scales may be of
+ * any magnitude: a group's sum is formed with both, so it overflows where y does.
  */
 int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_scales, const void* w,
                 const void* w_scales, const gdn_project_part* parts, int32_t n_parts, void* stream);

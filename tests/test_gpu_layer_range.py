@@ -106,3 +106,21 @@ def test_gates_at_the_ends(heads, d, dtype):
     ref.near(dx, want, lost)
     ref.near(dz, want_z, lost_z)
     ref.near(dw, want_w, lost_w)
+
+
+# rows, blocks of rows, tiles
+@pytest.mark.parametrize("M", [1, 20, 64, 200, 1700])
+@pytest.mark.parametrize("K", [272, 512])
+def test_projections_of_any_magnitude(M, K):
+    """Activations of 2^108 (2^-110) by fp32 weight scales of 1e-33 (1e33), scales of 0 and below 2^-126."""
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    N = 300
+    a, w = [(torch.randn(r, K, generator=g, device=DEV) * 60).clamp(-448, 448).to(torch.float8_e4m3fn) for r in (M, N)]
+    for power, size in ((235, 1e-33), (17, 1e33), (127, 1e-41), (127, 0.0), (240, 1e-41)):
+        sa = torch.full((M, 4 * (K // 512 + 1)), power, dtype=torch.uint8, device=DEV).view(torch.float8_e8m0fnu)
+        sw = torch.rand(3, ref.cut(K), generator=g, device=DEV) * size
+        sw[1] = -sw[1]
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+        gb.gdn_project(a, sa, w, sw, out)
+        y, lost = ref.project(a, sa, w, sw)
+        ref.near(out, y, lost)
