@@ -15,7 +15,11 @@
 namespace gdn {
 namespace {
 
-constexpr int kMaxWaves = 8;
+// Waves of a workgroup: eight of 64 columns; as many of 32 as LDS holds, which has few workgroups (22 x 5120 x 6144 11.2
+// us with eight, 10.5 with 16; 16 x 16384 x 5120 17.2 and 17.5 of 64 columns).
+constexpr int max_waves(int mt, int nt) {
+    return nt == 4 ? 8 : kMaxLdsBytes / (16 * (nt + mt) * GDN_GROUP) < 16 ? kMaxLdsBytes / (16 * (nt + mt) * GDN_GROUP) : 16;
+}
 
 // Few tokens: the weights are read once, at the memory's rate.  16 NT columns and 16 MT tokens a workgroup.  Its waves
 // take the groups in turn, each for itself: a group's rows come into the wave's own LDS in whole lines (loads straight
@@ -23,7 +27,7 @@ constexpr int kMaxWaves = 8;
 // 16384 x 5120 31 us so, 17 through LDS, 4.9 TB/s of weights), and the next group's are on their way during the
 // products.  The waves' sums are joined through LDS in their order.
 template <int DT, bool E8M0, int MT, int NT>
-__global__ __launch_bounds__(64 * kMaxWaves) void project_rows_kernel(const ProjectArgs p) {
+__global__ __launch_bounds__(64 * max_waves(MT, NT)) void project_rows_kernel(const ProjectArgs p) {
     extern __shared__ __align__(16) unsigned char rows_lds[];
     constexpr int kRows = 16 * (NT + MT), kStage = kRows * GDN_GROUP;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -114,10 +118,10 @@ template <int DT, bool E8M0>
 hipError_t launch(const ProjectArgs& p, hipStream_t stream) {
     auto go = [&](auto mt, auto nt) {
         constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, kStage = 16 * (NT + MT) * GDN_GROUP;
-        static_assert(kMaxWaves * kStage <= kMaxLdsBytes && NT * MT * 1024 <= kStage, "");
+        static_assert(max_waves(MT, NT) * kStage <= kMaxLdsBytes && NT * MT * 1024 <= kStage, "");
         const hipError_t e = allow_max_lds<&project_rows_kernel<DT, E8M0, MT, NT>>();
         if (e != hipSuccess) return e;
-        const int waves = std::min(p.groups, kMaxWaves);
+        const int waves = std::min(p.groups, max_waves(MT, NT));
         const int64_t grid = ((int64_t)p.columns + 16 * NT - 1) / (16 * NT) * (((int64_t)p.tokens + 16 * MT - 1) / (16 * MT));
         hipLaunchKernelGGL((project_rows_kernel<DT, E8M0, MT, NT>), dim3((unsigned)grid), dim3(64 * waves), waves * kStage, stream, p);
         return hipGetLastError();
@@ -133,12 +137,11 @@ hipError_t launch(const ProjectArgs& p, hipStream_t stream) {
     if (p.tokens <= 16) return wide ? go(one, four) : go(one, two);
     if (p.tokens <= 32) return wide ? go(two, four) : go(two, two);
     if (p.tokens <= 64) return wide ? go(four, four) : go(four, two);
-    // More tokens in blocks of 64 where these workgroups are few and their waves' shares of the groups, at about 2.1 us a
-    // group, end before a tile's steps would: 333 x 1039 x 1936 take 9 us and 14, 256 x 1024 x 8192 17 and 38, 128 x 5120
-    // x 6144 22 and 30; by tiles 128 x 16384 x 1024 9 and 15
+    // More tokens in blocks of 64 where their rounds over the chip, at about 0.26 us a group each, take less than a tile's
+    // step: 333 x 1039 x 1936 9 us and 14, 256 x 1024 x 8192 17 and 38, 128 x 5120 x 6144 22 and 30, 4096 x 96 x 5120 13 and
+    // 27; by tiles 256 x 5120 x 6144 31 and 35, 128 x 16384 x 1024 9 and 15
     const int64_t blocks = ((int64_t)p.columns + 31) / 32 * (((int64_t)p.tokens + 63) / 64);
-    const float us = 2.1f * (float)((blocks + cus - 1) / cus) * (float)((p.groups + kMaxWaves - 1) / kMaxWaves);
-    if (blocks <= 4 * cus && us < project_tiles_us(p)) return go(four, two);
+    if (blocks <= 4 * cus && 0.26f * (float)((blocks + cus - 1) / cus) < project_step_us(p)) return go(four, two);
     return launch_project_tiles(p, E8M0, DT, stream);
 }
 

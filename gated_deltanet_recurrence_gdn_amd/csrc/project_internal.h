@@ -40,8 +40,8 @@ struct ProjectArgs {
 
 // The product in tiles (project_tile.hip).
 hipError_t launch_project_tiles(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t stream);
-// About how long that takes.
-float project_tiles_us(const ProjectArgs& p);
+// About how long a group of it takes.
+float project_step_us(const ProjectArgs& p);
 
 // An fp32 weight scale's power of two goes into the instruction as an e8m0 one does, so that no group's sum leaves fp32's
 // range where its result does not; 1 to 2 is left for the sum (0 and subnormals: less, infinities and NaN: themselves).

@@ -255,7 +255,7 @@ Choice choose_tile(const ProjectArgs& p) {
 
 }  // namespace
 
-float project_tiles_us(const ProjectArgs& p) { return choose_tile(p).us * (float)p.groups; }
+float project_step_us(const ProjectArgs& p) { return choose_tile(p).us; }
 
 hipError_t launch_project_tiles(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t stream) {
     switch (choose_tile(p).tile) {

@@ -85,7 +85,7 @@ def test_gated_norm(rows, heads, d):
 
 
 @pytest.mark.parametrize("scales", ["f32", "e8m0"])
-@pytest.mark.parametrize("M", [1, 17, 33, 65, 200, 300])
+@pytest.mark.parametrize("M", [1, 17, 33, 65, 200, 300, 66000])
 @pytest.mark.parametrize("parts,K", [([5], 16), ([130, 7], 400), ([96, 40], 1040), ([1000, 24, 6], 272)])
 def test_project(parts, K, M, scales):
     g = Guarded()

@@ -109,7 +109,7 @@ def test_gates_at_the_ends(heads, d, dtype):
 
 
 # rows, blocks of rows, tiles
-@pytest.mark.parametrize("M", [1, 20, 64, 200, 1700])
+@pytest.mark.parametrize("M", [1, 20, 64, 200, 4000])
 @pytest.mark.parametrize("K", [272, 512])
 def test_projections_of_any_magnitude(M, K):
     """Activations of 2^108 (2^-110) by fp32 weight scales of 1e-33 (1e33), scales of 0 and below 2^-126."""
