@@ -141,8 +141,14 @@ __device__ __forceinline__ void store_narrow(const ProjectArgs& p, int64_t m, in
 // Columns n .. n + 3 of token m; `home` holds column n.
 template <int DT>
 __device__ __forceinline__ void store_four(const ProjectArgs& p, const Home& home, int64_t m, int n, f32x4 y) {
-    if (home.wide && n + 4 <= home.end) *reinterpret_cast<u32x2*>(home.data + m * home.stride + (n - home.begin)) = four<DT>(y);
-    else store_narrow<DT>(p, m, n, y);
+    if (n + 4 > home.end) return store_narrow<DT>(p, m, n, y);
+    uint16_t* at = home.data + m * home.stride + (n - home.begin);
+    if (home.wide) {
+        *reinterpret_cast<u32x2*>(at) = four<DT>(y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) at[j] = half_bits<DT>(y[j]);
+    }
 }
 
 }  // namespace gdn
