@@ -15,7 +15,9 @@ keep their storage, shapes and the stream must stay valid while it is used.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 
 import numpy as np
 import torch
@@ -756,7 +758,8 @@ def _at(t, name, device, dense=True):
 
 def _call(name, args, keep, prepare):
     if prepare:
-        typed = [a if isinstance(a, (ctypes.Array, type(ctypes.byref(_i32())))) else t(a) for a, t in zip(args, _SIGS[name])]
+        typed = [ctypes.c_char_p(a) if isinstance(a, bytes) else a if isinstance(a, (ctypes.Array, type(ctypes.byref(_i32())))) else t(a)
+                 for a, t in zip(args, _SIGS[name])]
         return PreparedCall(name, typed, (*keep, args))
     rc = getattr(_lib or lib(), name)(*args)
     if rc != 0:
@@ -956,9 +959,7 @@ def _rows_of(t, name, tail):
     d = len(size) - tail
     if d < 1:
         raise ValueError(f"{name} must have at least {tail + 1} dimensions, got shape {tuple(size)}")
-    row = size[d]
-    for k in range(d + 1, d + tail):
-        row *= size[k]
+    row = size[d] if tail == 1 else math.prod(size[d:])
     if t.is_contiguous():
         return (t.numel() // row if row else 0), row
     strides, want = t.stride(), 1
@@ -971,6 +972,14 @@ def _rows_of(t, name, tail):
     return size[0], strides[0] if size[0] > 1 else row
 
 
+def _columns_of(t, name, rows):
+    if isinstance(t, torch.Tensor):
+        size = t.shape
+        if len(size) == 2 and size[0] == rows:
+            return size[1]
+    _expect(t, name, (rows, _shape_of(t, name, 2)[1]))
+
+
 def _check_codes(codes, scales, rows, width):
     """The scales' stride in bytes of 8-bit outputs or operands [rows][width]."""
     if (codes is None) != (scales is None):
@@ -978,8 +987,9 @@ def _check_codes(codes, scales, rows, width):
     if codes is None:
         return 0
     _expect(codes, "codes", (rows, width), _E4M3)
-    groups, stride = -(-width // GDN_GROUP), _shape_of(scales, "scales", 2)[1]
-    _expect(scales, "scales", (rows, stride), _E8M0)
+    groups, stride = -(-width // GDN_GROUP), _columns_of(scales, "scales", rows)
+    if scales.dtype is not _E8M0:
+        _expect(scales, "scales", (rows, stride), _E8M0)
     if stride < groups or stride % 4:
         raise ValueError(f"scales must have a multiple of 4 columns, at least {groups}, got {stride}")
     return stride
@@ -1043,8 +1053,8 @@ def _gated_shape(x, z, weight, eps):
     rows, x_stride = _rows_of(x, "x", 2)
     shape = x.shape
     _expect(z, "z", shape)
-    _, z_stride = _rows_of(z, "z", 2)
-    Hv, dv = shape[-2:]
+    z_stride = _rows_of(z, "z", 2)[1]
+    Hv, dv = shape[-2], shape[-1]
     _expect(weight, "weight", (dv,))
     return GdnGatedNormShape(rows, x_stride, z_stride, Hv, dv, _code(x), _code(z), _code(weight), 0, eps)
 
@@ -1085,20 +1095,34 @@ def gdn_gated_norm_backward(dout, x, z, weight, dx=None, dz=None, dweight=None, 
     return _call("gdn_gated_norm_backward", args, (sh, dout, x, z, weight, dx, dz, dweight, workspace), prepare)
 
 
+def _codes_of(t, name):
+    """(rows, width, bytes from one row to the next) of an e4m3 operand."""
+    if isinstance(t, torch.Tensor) and t.dtype is _E4M3 and t.is_cuda and t.is_contiguous():
+        size = t.shape
+        if len(size) == 2:
+            rows, width = size
+            return rows, width, width  # the usual case
+    rows, width = _shape_of(t, name, 2)
+    _expect(t, name, (rows, width), _E4M3)
+    return rows, width, _rows_of(t, name, 1)[1]
+
+
+_PART = [struct.Struct("=" + "Qqii" * n) for n in range(GDN_MAX_PARTS + 1)]  # gdn_project_part
+
+
 def gdn_project(a, a_scales, w, w_scales, outs, *, stream=None, prepare: bool = False):
     """a [tokens][inner] times w [columns][inner] transposed, both e4m3, with the scales of groups of 128 (``a_scales``
     e8m0 [tokens][>= groups], a multiple of 4) and of blocks of 128 x 128 (``w_scales`` fp32 [column blocks][groups], or
     e8m0, padded alike); the columns go to ``outs``, a tensor or up to 8 of bf16 or f16: [tokens][...] each, whose rows may
     be apart where they are 2-D.  See include/gdn.h."""
-    M, K = _shape_of(a, "a", 2)
-    N = _shape_of(w, "w", 2)[0]
-    _expect(a, "a", (M, K), _E4M3)
-    _expect(w, "w", (N, K), _E4M3)
-    a_stride, w_stride = _rows_of(a, "a", 1)[1], _rows_of(w, "w", 1)[1]
+    M, K, a_stride = _codes_of(a, "a")
+    N, inner, w_stride = _codes_of(w, "w")
+    if inner != K:
+        _expect(w, "w", (N, K))
     groups = -(-K // GDN_GROUP)
-    a_pad, w_pad = _shape_of(a_scales, "a_scales", 2)[1], _shape_of(w_scales, "w_scales", 2)[1]
-    _expect(a_scales, "a_scales", (M, a_pad), _E8M0)
-    _expect(w_scales, "w_scales", (-(-N // GDN_GROUP), w_pad))
+    a_pad, w_pad = _columns_of(a_scales, "a_scales", M), _columns_of(w_scales, "w_scales", -(-N // GDN_GROUP))
+    if a_scales.dtype is not _E8M0:
+        _expect(a_scales, "a_scales", (M, a_pad), _E8M0)
     w_dtype = w_scales.dtype
     if a_pad < groups or a_pad % 4:
         raise ValueError(f"a_scales must have a multiple of 4 columns, at least {groups}, got {a_pad}")
@@ -1110,14 +1134,19 @@ def gdn_project(a, a_scales, w, w_scales, outs, *, stream=None, prepare: bool = 
         outs = (outs,)
     if not 1 <= len(outs) <= GDN_MAX_PARTS:
         raise ValueError(f"1 to {GDN_MAX_PARTS} outputs, got {len(outs)}")
-    parts, columns, dtype = [], 0, outs[0].dtype
+    strides, widths, dtype = [], [], getattr(outs[0], "dtype", None)
     for t in outs:
-        if not isinstance(t, torch.Tensor) or t.dim() < 2 or t.shape[0] != M or t.dtype is not dtype:
+        size = t.shape if isinstance(t, torch.Tensor) else ()
+        if len(size) < 2 or size[0] != M or t.dtype is not dtype:
             raise ValueError("outs must be tensors [tokens][...], a row for each token, of one dtype")
-        stride = _rows_of(t, "outs", t.dim() - 1)[1]
-        n = t.numel() // M if M else stride
-        parts.append((t.data_ptr(), stride, n, 0))
-        columns += n
+        if M and t.is_contiguous():
+            n = stride = t.numel() // M
+        else:
+            stride = _rows_of(t, "outs", len(size) - 1)[1]
+            n = t.numel() // M if M else stride
+        strides.append(stride)
+        widths.append(n)
+    columns = sum(widths)
     if columns != N:
         raise ValueError(f"the outputs have {columns} columns, the weights {N}")
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
@@ -1125,8 +1154,9 @@ def gdn_project(a, a_scales, w, w_scales, outs, *, stream=None, prepare: bool = 
     sh = GdnProjectShape(M, a_stride, w_stride, K, a_pad, w_pad, GDN_F32 if w_dtype is torch.float32 else GDN_E8M0,
                          GDN_BF16 if dtype is torch.bfloat16 else GDN_F16)
     device, handle = _site("gdn_project", stream)
-    for t in outs:
-        _at(t, "outs", device, False)
+    parts = []
+    for t, stride, n in zip(outs, strides, widths):
+        parts += _at(t, "outs", device, False), stride, n, 0
     args = (ctypes.byref(sh), _at(a, "a", device, False), _at(a_scales, "a_scales", device), _at(w, "w", device, False),
-            _at(w_scales, "w_scales", device), (GdnProjectPart * len(parts))(*parts), len(parts), handle)
+            _at(w_scales, "w_scales", device), _PART[len(outs)].pack(*parts), len(outs), handle)
     return _call("gdn_project", args, (sh, a, a_scales, w, w_scales, tuple(outs)), prepare)
