@@ -158,9 +158,15 @@ __device__ __forceinline__ int scale_byte(uint32_t top) {
     return top >= 0x7f800000u ? 255 : b < 1 ? 1 : b;
 }
 
-// Whether an fp32 value that is off by a few ulps may lie on either side of a border whose mantissa ends so.
-__device__ __forceinline__ bool near_border(uint32_t bits, uint32_t mask, uint32_t border, uint32_t ulps) {
-    return ((bits - border + ulps) & mask) <= 2 * ulps;
+// How far, of 2 * ulps, the mantissa of an fp32 value is above `ulps` below a border whose lowest BITS bits are so, in
+// steps of 2^(BITS - 32): up to border_width() where the value, off by `ulps` at most, may lie on either side.
+template <int BITS>
+__device__ __forceinline__ uint32_t above_border(uint32_t bits, uint32_t border, uint32_t ulps) {
+    return (bits - (border - ulps)) << (32 - BITS);
+}
+template <int BITS>
+__device__ __forceinline__ uint32_t border_width(uint32_t ulps) {
+    return (2 * ulps) << (32 - BITS);
 }
 
 // Eight channels of a lane as e4m3 codes, the group's scale from its 16 lanes (all of which take part; lanes that are
@@ -171,7 +177,7 @@ template <typename Exact>
 __device__ __forceinline__ int quantise8(const float (&y)[kVec], bool live, uint32_t ulps, Exact exact, u32x2* codes) {
     const uint32_t top = lanes16_max(live ? top8(y) : 0);
     int byte = scale_byte(top);
-    if (byte < 255 && near_border(top, 0x7fffffu, 0x600000u, ulps)) {  // the same in all 16 lanes
+    if (byte < 255 && above_border<23>(top, 0x600000u, ulps) <= border_width<23>(ulps)) {  // the same in all 16 lanes
         uint64_t t = 0;
         if (live)
 #pragma unroll
@@ -187,17 +193,18 @@ __device__ __forceinline__ int quantise8(const float (&y)[kVec], bool live, uint
     const float down = __builtin_bit_cast(float, byte == 255 ? 0x7fc00000u : (uint32_t)(254 - byte) << 23);
     // the products are exact but below 2^-126, far under half of the smallest code
     float c[kVec];
-    auto halfway = [&](int k) { return near_border(__builtin_bit_cast(uint32_t, c[k]), 0xfffffu, 0x80000u, ulps); };  // between codes
-    bool near = false;
+    auto halfway = [&](int k) { return above_border<20>(__builtin_bit_cast(uint32_t, c[k]), 0x80000u, ulps); };  // between codes
+    uint32_t least = 0xffffffffu;
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {
         c[k] = y[k] * down;
-        near |= halfway(k);
+        const uint32_t h = halfway(k);
+        least = least < h ? least : h;
     }
-    if (near && live && byte < 255)
+    if (least <= border_width<20>(ulps) && live && byte < 255)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
-            if (!halfway(k)) continue;
+            if (halfway(k) > border_width<20>(ulps)) continue;
             const double v = exact(k) * down;
             c[k] = (float)v;
             const uint32_t bits = __builtin_bit_cast(uint32_t, c[k]);
