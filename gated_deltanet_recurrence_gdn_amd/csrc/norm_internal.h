@@ -142,13 +142,10 @@ __device__ __forceinline__ uint64_t lanes16_max(uint64_t x) {
 
 // The largest magnitude of eight values as its bits: NaN above infinity above all others.
 __device__ __forceinline__ uint32_t top8(const float (&y)[kVec]) {
-    uint32_t t = 0;
+    float t = __builtin_fabsf(y[0]);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, y[k]) & 0x7fffffffu;
-        t = t > b ? t : b;
-    }
-    return t;
+    for (int k = 1; k < kVec; ++k) t = __builtin_elementwise_maximum(t, __builtin_fabsf(y[k]));  // NaN if one is
+    return __builtin_bit_cast(uint32_t, t);
 }
 
 // Scale byte of a group whose largest magnitude has these bits: e + 127 for the smallest e >= -126 with
