@@ -83,14 +83,14 @@ __device__ __forceinline__ bool any_below(const float (&z)[kVec]) {
 }
 
 // The sums of a head's lanes.  L lanes a head (2, 4, 8, 16 or 32), or any number through LDS (0).
-template <int L>
-__device__ __forceinline__ float head_sum(float x, float* part, int first, int head_lanes) {
+template <int L, typename T>
+__device__ __forceinline__ T head_sum(T x, double* part, int first, int head_lanes) {
     if constexpr (L != 0) return lanes_sum<L>(x);
     __syncthreads();  // an earlier sum's readers are done
     part[threadIdx.x] = x;
     __syncthreads();
-    float s = 0;
-    for (int k = 0; k < head_lanes; ++k) s += part[first + k];
+    T s = 0;
+    for (int k = 0; k < head_lanes; ++k) s += (T)part[first + k];
     return s;
 }
 
@@ -102,10 +102,10 @@ __device__ __forceinline__ bool any_of(bool ask) {
 }
 
 // Bytes bound it, vector operations come close (about 40 an element): 4096 tokens x 48 heads of 128 bf16 31 us (4.9 TB/s);
-// to 8 bits 27, of f16 29, 4.3 TB/s; 16 tokens of fp32 3.6 us.
+// to 8 bits 28, of f16 28, 4.5 TB/s; 16 tokens of fp32 3.6 us.
 template <int DX, int DZ, int L>
 __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const GatedArgs a) {
-    __shared__ float part[L == 0 ? kPart : 1];
+    __shared__ double part[L == 0 ? kPart : 1];
     const int lanes = L == 0 ? a.lanes : L < 16 ? 16 : L, head_lanes = L == 0 ? a.head_lanes : L;
     const int in_wg = threadIdx.x / lanes, p = threadIdx.x % lanes;
     const uint64_t at = a.first + blockIdx.x * (uint64_t)a.per_wg + in_wg;
@@ -121,9 +121,15 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     load8<DZ>(a.z, row * a.z_stride + c, z);
     load8(a.weight, i % head_lanes * kVec, a.weight_dtype, w);
     const int lead = (int)threadIdx.x - p % head_lanes;
-    float sum = head_sum<L>(squares8(x), part, lead, head_lanes);
-    const float scale = range_scale(sum, a.eps);
-    if (any_of<L>(scale != 1.0f)) sum = head_sum<L>(squares8_of_scaled(x, scale), part, lead, head_lanes);
+    double sum;
+    float scale = 1;
+    if (a.codes != nullptr) {
+        sum = head_sum<L>(squares8_f64(x), part, lead, head_lanes);
+    } else {
+        sum = head_sum<L>(squares8(x), part, lead, head_lanes);
+        scale = range_scale(sum, a.eps);
+        if (any_of<L>(scale != 1.0f)) sum = head_sum<L>(squares8_of_scaled(x, scale), part, lead, head_lanes);
+    }
     const double root = inverse_rms(sum, a.inverse_size, a.eps, scale) * scale;
     const float rs = (float)root;
 #pragma unroll
@@ -150,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
 // 252 MB (5.5 TB/s, part of it still cached from the forward pass), and 5 for the partials' sum.
 template <int DX, int DZ, int L>
 __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const GatedArgs a) {
-    __shared__ float part[L == 0 ? kPart : 1];
+    __shared__ double part[L == 0 ? kPart : 1];
     __shared__ float share[kThreads][kVec + 1];
     const int lanes = L == 0 ? a.lanes : L < 16 ? 16 : L, head_lanes = L == 0 ? a.head_lanes : L;
     const int in_wg = threadIdx.x / lanes, p = threadIdx.x % lanes, column = p % head_lanes;

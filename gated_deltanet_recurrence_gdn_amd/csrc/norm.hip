@@ -39,8 +39,8 @@ struct NormArgs {
 };
 
 // Sum over the LANES lanes of a row: part of a wave, or the workgroup (LANES = 0).
-template <int LANES>
-__device__ __forceinline__ double row_sum(float x, float* wave_sum) {
+template <int LANES, typename T>
+__device__ __forceinline__ double row_sum(T x, T* wave_sum) {
     if constexpr (LANES != 0) return lanes_sum<LANES>(x);
     x = lanes_sum<64>(x);
     const int waves = blockDim.x >> 6;
@@ -57,6 +57,7 @@ __device__ __forceinline__ double row_sum(float x, float* wave_sum) {
 template <int DX, int DR, int V, int LANES>
 __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel(const NormArgs a) {
     __shared__ float wave_sum[kMaxThreads / 64];
+    __shared__ double wave_sum_f64[kMaxThreads / 64];
     const int lanes = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % LANES : threadIdx.x;
     const int64_t at = a.first + (LANES ? (int64_t)blockIdx.x * (blockDim.x / (LANES ? LANES : 1)) + threadIdx.x / (LANES ? LANES : 1) : blockIdx.x);
     const int64_t row = at < a.rows ? at : a.rows - 1;
@@ -83,17 +84,26 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
         const int i = t + v * lanes;
         load8(a.weight, (i < n ? i : n - 1) * kVec, a.weight_dtype, w[v]);
     }
-    float sum = 0;
+    double squares;
+    float c = 1;
+    if (a.codes != nullptr) {
+        double sum = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8(r[v]) : 0;
-    double squares = row_sum<LANES>(sum, wave_sum);
-    const float c = range_scale(squares, a.eps);
-    if (LANES ? __any(c != 1.0f) : c != 1.0f) {  // the whole row's lanes
-        if constexpr (LANES == 0) __syncthreads();  // the first sum's readers are done
-        sum = 0;
+        for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8_f64(r[v]) : 0;
+        squares = row_sum<LANES>(sum, wave_sum_f64);
+    } else {
+        float sum = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8_of_scaled(r[v], c) : 0;
+        for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8(r[v]) : 0;
         squares = row_sum<LANES>(sum, wave_sum);
+        c = range_scale(squares, a.eps);
+        if (LANES ? __any(c != 1.0f) : c != 1.0f) {  // the whole row's lanes
+            if constexpr (LANES == 0) __syncthreads();  // the first sum's readers are done
+            sum = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum += t + v * lanes < n ? squares8_of_scaled(r[v], c) : 0;
+            squares = row_sum<LANES>(sum, wave_sum);
+        }
     }
     const double root = inverse_rms(squares, a.inverse_width, a.eps, c) * c;
     const float rs = (float)root;

@@ -122,6 +122,19 @@ template <int CTRL>
 __device__ __forceinline__ uint64_t dpp_u64(uint64_t x) {
     return dpp_u32<CTRL>((uint32_t)x) | (uint64_t)dpp_u32<CTRL>((uint32_t)(x >> 32)) << 32;
 }
+// lanes_sum in 64 bits.
+template <int L>
+__device__ __forceinline__ double lanes_sum(double x) {
+    auto with = [&](uint64_t other) { x += __builtin_bit_cast(double, other); };
+    with(dpp_u64<0xB1>(__builtin_bit_cast(uint64_t, x)));
+    if constexpr (L >= 4) with(dpp_u64<0x4E>(__builtin_bit_cast(uint64_t, x)));
+    if constexpr (L >= 8) with(dpp_u64<0x141>(__builtin_bit_cast(uint64_t, x)));
+    if constexpr (L >= 16) with(dpp_u64<0x140>(__builtin_bit_cast(uint64_t, x)));
+    if constexpr (L >= 32) x += __shfl_xor(x, 16);
+    if constexpr (L >= 64) x += __shfl_xor(x, 32);
+    return x;
+}
+
 // The largest of 16 lanes' values.
 __device__ __forceinline__ uint32_t lanes16_max(uint32_t x) {
     auto step = [&](uint32_t y) { x = x > y ? x : y; };
@@ -225,12 +238,23 @@ __device__ __forceinline__ float squares8(const float (&x)[kVec]) {
 }
 
 // 1 / sqrt(sum / n + eps) to 2^-48.  (Rounded at each step to fp32 it would move codes of whole rows over their borders:
-// 4096 x 5120, 2.0e-4 of the codes' 2-norm.)
+// 4096 x 5120, 2.0e-4 of the codes' 2-norm; from an fp32 sum of squares single codes, 3e-5.)
 // With c, of a row summed as c x: 1 / sqrt(sum / n + c^2 eps), c times too small for x.
 __device__ __forceinline__ double inverse_rms(double sum, double inverse_n, float eps, float c) {
     const double m = __builtin_fma(sum, inverse_n, (double)eps * c * c);
     const double y = __builtin_amdgcn_rsq(m);
     return m == __builtin_inf() ? 0.0 : y * __builtin_fma(-0.5 * m * y, y, 1.5);  // infinite: an infinity in the row
+}
+
+// In 64 bits, of any fp32 values: the sum behind codes, which are those of the 64-bit values.
+__device__ __forceinline__ double squares8_f64(const float (&x)[kVec]) {
+    double a = 0, b = 0;
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) {
+        a = __builtin_fma((double)x[k], (double)x[k], a);
+        b = __builtin_fma((double)x[k + 1], (double)x[k + 1], b);
+    }
+    return a + b;
 }
 
 // The power of two to sum a row times again, where its sum of squares has left fp32's range or is so small that parts of

@@ -617,7 +617,7 @@ typedef struct gdn_norm_shape {
  * The norm is of r as stored, so the backward pass needs nothing but r.  Without a
  * residual (NULL; residual_out is NULL then) r is x.  y goes to `out` (nullable, dtype)
  * and, or, to `codes` and `scales` (nullable, both or none).  Sums and products
- * are fp32.
+ * are fp32; codes and scales are those of the values in 64 bits.
  * residual, residual_out, out and codes are dense [rows][width]; residual_out may be
  * residual, and out may be a dense x (no other output overlaps an input).  x, residual,
  * residual_out, out and weight are 16-byte aligned, codes 8-byte, scales 4-byte.  A row

@@ -108,6 +108,26 @@ def test_gates_at_the_ends(heads, d, dtype):
     ref.near(dw, want_w, lost_w)
 
 
+# 2^-40: what float64 may lose here, far above it, and far below an fp32 step
+@pytest.mark.parametrize("rows,width", [(4096, 5120), (20000, 200), (3000, 1024), (5000, 2560), (500, 16000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_codes_of_the_norm_are_exact(rows, width, dtype):
+    x, w = normal(5, rows, width).to(T[dtype]), 1 + 0.1 * normal(1, width)
+    codes, scales = codes_for(rows, width)
+    gb.gdn_norm_forward(x, w, codes=codes, scales=scales, eps=1e-6)
+    ref.check_codes(ref.norm(x, w, 1e-6)[0], codes, scales, 2.0 ** -40)
+
+
+@pytest.mark.parametrize("heads,d", HEADS)
+@pytest.mark.parametrize("x,z", [("f32", "bf16"), ("f16", "f32"), ("bf16", "bf16")])
+def test_codes_of_the_gated_norm_are_exact(heads, d, x, z):
+    rows = 4000
+    x, z, w = normal(5, rows, heads, d).to(T[x]), (3 * normal(6, rows, heads, d)).to(T[z]), 1 + 0.1 * normal(1, d)
+    codes, scales = codes_for(rows, heads * d)
+    gb.gdn_gated_norm_forward(x, z, w, codes=codes, scales=scales, eps=1e-6)
+    ref.check_codes(ref.gated(x, z, w, 1e-6)[0].flatten(1), codes, scales, 2.0 ** -40)
+
+
 # rows, blocks of rows, tiles
 @pytest.mark.parametrize("M", [1, 20, 64, 200, 4000])
 @pytest.mark.parametrize("K", [272, 512])
