@@ -15,11 +15,10 @@
 namespace gdn {
 namespace {
 
-// Waves of a workgroup: eight of 64 columns; as many of 32 as LDS holds, which has few workgroups (22 x 5120 x 6144 11.2
-// us with eight, 10.5 with 16; 16 x 16384 x 5120 17.2 and 17.5 of 64 columns).
-constexpr int max_waves(int mt, int nt) {
-    return nt == 4 ? 8 : kMaxLdsBytes / (16 * (nt + mt) * GDN_GROUP) < 16 ? kMaxLdsBytes / (16 * (nt + mt) * GDN_GROUP) : 16;
-}
+// Waves of a workgroup: 16 of 32 columns and up to 32 tokens with fp32 scales, whose scaling keeps a wave longer from its
+// next loads (16 x 5120 x 6144 8.0 us, with eight 8.7; 22 x 5120 x 6144 8.8 and 9.1), else eight (the same with e8m0
+// scales 7.9 and 7.4, 8.7 and 8.2; blocks of 64 tokens: 100 x 2048 x 2048 13 waves 6.5, eight 6.2).
+constexpr int max_waves(bool e8m0, int mt, int nt) { return !e8m0 && mt <= 2 && nt == 2 ? 16 : 8; }
 
 // Few tokens: the weights are read once, at the memory's rate.  16 NT columns and 16 MT tokens a workgroup.  Its waves
 // take the groups in turn, each for itself: a group's rows come into the wave's own LDS in whole lines (loads straight
@@ -27,7 +26,7 @@ constexpr int max_waves(int mt, int nt) {
 // 16384 x 5120 31 us so, 17 through LDS, 4.9 TB/s of weights), and the next group's are on their way during the
 // products.  The waves' sums are joined through LDS in their order.
 template <int DT, bool E8M0, int MT, int NT>
-__global__ __launch_bounds__(64 * max_waves(MT, NT)) void project_rows_kernel(const ProjectArgs p) {
+__global__ __launch_bounds__(64 * max_waves(E8M0, MT, NT)) void project_rows_kernel(const ProjectArgs p) {
     extern __shared__ __align__(16) unsigned char rows_lds[];
     constexpr int kRows = 16 * (NT + MT), kStage = kRows * GDN_GROUP;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -118,10 +117,10 @@ template <int DT, bool E8M0>
 hipError_t launch(const ProjectArgs& p, hipStream_t stream) {
     auto go = [&](auto mt, auto nt) {
         constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, kStage = 16 * (NT + MT) * GDN_GROUP;
-        static_assert(max_waves(MT, NT) * kStage <= kMaxLdsBytes && NT * MT * 1024 <= kStage, "");
+        static_assert(max_waves(E8M0, MT, NT) * kStage <= kMaxLdsBytes && NT * MT * 1024 <= kStage, "");
         const hipError_t e = allow_max_lds<&project_rows_kernel<DT, E8M0, MT, NT>>();
         if (e != hipSuccess) return e;
-        const int waves = std::min(p.groups, max_waves(MT, NT));
+        const int waves = std::min(p.groups, max_waves(E8M0, MT, NT));
         const int64_t grid = ((int64_t)p.columns + 16 * NT - 1) / (16 * NT) * (((int64_t)p.tokens + 16 * MT - 1) / (16 * MT));
         hipLaunchKernelGGL((project_rows_kernel<DT, E8M0, MT, NT>), dim3((unsigned)grid), dim3(64 * waves), waves * kStage, stream, p);
         return hipGetLastError();
