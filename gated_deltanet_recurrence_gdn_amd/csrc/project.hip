@@ -41,13 +41,17 @@ __global__ __launch_bounds__(64 * max_waves(E8M0, MT, NT)) void project_rows_ker
     const rsrc_t rs = rsrc_of(p.a_scales + (int64_t)m0 * p.a_scale_stride, rows_a * p.a_scale_stride);
     const int64_t block = (int64_t)(n0 / GDN_GROUP) * p.w_scale_stride;
     const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;  // of row lane / 8 of the eight a load takes
-    const uint32_t oa = (lane >> 3) * as + chunk, ow = (lane >> 3) * ws + chunk, os = r * p.a_scale_stride;
+    const uint32_t oa = (lane >> 3) * as + chunk, ow = (lane >> 3) * ws + chunk;
+    // rows in the lanes' offset, which is checked against the buffer's end; only the group, inside a row, in the scalar one
+    uint32_t os[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) os[t] = (16 * t + r) * (uint32_t)p.a_scale_stride;
     unsigned char* own = rows_lds + wave * kStage;
     int scale[MT];
     float sw;
     auto stage = [&](int g) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) scale[t] = load_byte(rs, os, g + t * 16 * p.a_scale_stride);
+        for (int t = 0; t < MT; ++t) scale[t] = load_byte(rs, os[t], g);
         if constexpr (E8M0) sw = __builtin_bit_cast(float, (int)static_cast<const uint8_t*>(p.w_scales)[block + g]);
         else sw = static_cast<const float*>(p.w_scales)[block + g];
         const bool in_row = g * GDN_GROUP + chunk < p.inner;

@@ -65,6 +65,7 @@ __device__ __forceinline__ rsrc_t rsrc_of(const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
 }
 
+// `offset` is not part of the check against the end.
 __device__ __forceinline__ int load_byte(rsrc_t from, uint32_t lane_offset, int offset) {
     return __builtin_amdgcn_raw_buffer_load_b8(from, lane_offset, offset, 0);
 }
