@@ -49,14 +49,15 @@ struct GatedArgs {
     float eps;
 };
 
-// a = 1 / (1 + e^-z) to three ulps (exponential and reciprocal one each, two roundings), for z from kLeast on, where a is still above 2^-126.  -z log2(e) goes to the
-// exponential in two parts.
+// a = 1 / (1 + e^-z) to three ulps (exponential and reciprocal one each, two roundings), for z from kLeast on, where a is
+// still above 2^-126.  -z log2(e) goes to the exponential in two parts; the small one is below 2^-16 for z up to 128, and
+// bounded above that, where it leaves fp32's range (2.4e38) beside an exponential of 0.
 constexpr float kLeast = -86.0f;
 __device__ __forceinline__ float logistic(float z) {
     constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;  // log2(e)
     const float hi = -z * kHi, lo = __builtin_fmaf(-z, kHi, -hi) - z * kLo;
     const float p = __builtin_amdgcn_exp2f(hi);
-    const float d = 1.0f + __builtin_fmaf(p, lo * 0.693147180559945f, p);  // 2^lo = 1 + lo ln 2
+    const float d = 1.0f + __builtin_fmaf(p, __builtin_fminf(lo, 1.0f) * 0.693147180559945f, p);  // 2^lo = 1 + lo ln 2
     return __builtin_amdgcn_rcpf(d);
 }
 
