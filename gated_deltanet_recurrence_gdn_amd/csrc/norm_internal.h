@@ -168,26 +168,41 @@ __device__ __forceinline__ int scale_byte(uint32_t top) {
     return top >= 0x7f800000u ? 255 : b < 1 ? 1 : b;
 }
 
-// How far, of 2 * ulps, the mantissa of an fp32 value is above `ulps` below a border whose lowest BITS bits are so, in
-// steps of 2^(BITS - 32): up to border_width() where the value, off by `ulps` at most, may lie on either side.
-template <int BITS>
-__device__ __forceinline__ uint32_t above_border(uint32_t bits, uint32_t border, uint32_t ulps) {
-    return (bits - (border - ulps)) << (32 - BITS);
+// Whether a value, off by `ulps` steps of 2^-23 of it at most, may lie on either side of 448 times a power of two.
+__device__ __forceinline__ bool next_to_border(uint32_t bits, uint32_t ulps) {
+    return (bits - (0x600000u - ulps)) << 9 <= (2 * ulps) << 9;
 }
-template <int BITS>
-__device__ __forceinline__ uint32_t border_width(uint32_t ulps) {
-    return (2 * ulps) << (32 - BITS);
+
+// Eight values in e4m3, the nearest each, ties to even.
+__device__ __forceinline__ u32x2 e4m3x8(const float (&c)[kVec]) {
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], hi, true);
+    return u32x2{(uint32_t)lo, (uint32_t)hi};
+}
+
+// A 64-bit value in e4m3: by an fp32 value that is it, or the one with an odd last bit next to it, which lies on the
+// same side of every code and every half.
+__device__ __forceinline__ uint32_t e4m3_of(double v) {
+    float c = (float)v;
+    if ((double)c != v) {
+        uint32_t bits = __builtin_bit_cast(uint32_t, c);
+        if (__builtin_fabs((double)c) > __builtin_fabs(v)) --bits;
+        c = __builtin_bit_cast(float, bits | 1);
+    }
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, c, 0, false) & 255;
 }
 
 // Eight channels of a lane as e4m3 codes, the group's scale from its 16 lanes (all of which take part; lanes that are
-// not live count as zeros).  Codes and scale are those of the 64-bit values exact(k): where an fp32 value is within
-// `ulps` of its code's or the scale's border, the 64-bit one decides (one value in 32000, one group in 250000 at 16 ulps).
-// Returns the scale byte.
+// not live count as zeros).  Codes and scale are those of the 64-bit values exact(k), y being off by `ulps` steps of
+// 2^-23 of it at most: where the codes of the ends of y's range differ, or the scale may be another, the 64-bit value
+// decides (one value in 20000, one group in 250000 at 16 ulps).  Returns the scale byte.
 template <typename Exact>
 __device__ __forceinline__ int quantise8(const float (&y)[kVec], bool live, uint32_t ulps, Exact exact, u32x2* codes) {
     const uint32_t top = lanes16_max(live ? top8(y) : 0);
     int byte = scale_byte(top);
-    if (byte < 255 && above_border<23>(top, 0x600000u, ulps) <= border_width<23>(ulps)) {  // the same in all 16 lanes
+    if (byte < 255 && next_to_border(top, ulps)) {  // the same in all 16 lanes
         uint64_t t = 0;
         if (live)
 #pragma unroll
@@ -201,32 +216,24 @@ __device__ __forceinline__ int quantise8(const float (&y)[kVec], bool live, uint
         else if (byte > 1 && most <= 0.5 * limit) --byte;
     }
     const float down = __builtin_bit_cast(float, byte == 255 ? 0x7fc00000u : (uint32_t)(254 - byte) << 23);
-    // the products are exact but below 2^-126, far under half of the smallest code
-    float c[kVec];
-    auto halfway = [&](int k) { return above_border<20>(__builtin_bit_cast(uint32_t, c[k]), 0x80000u, ulps); };  // between codes
-    uint32_t least = 0xffffffffu;
+    // a step more for the product, which is off but for that below 2^-126 alone, far under half of the smallest code
+    const float slack = (float)(ulps + 1) * 0x1p-23f, less = down * (1 - slack), more = down * (1 + slack);
+    float below[kVec], above[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {
-        c[k] = y[k] * down;
-        const uint32_t h = halfway(k);
-        least = least < h ? least : h;
+        below[k] = y[k] * less;
+        above[k] = y[k] * more;
     }
-    if (least <= border_width<20>(ulps) && live && byte < 255)
+    u32x2 q = e4m3x8(below);
+    const u32x2 other = e4m3x8(above), differ = q ^ other;
+    if ((differ[0] | differ[1]) != 0 && live && byte < 255)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
-            if (halfway(k) > border_width<20>(ulps)) continue;
-            const double v = exact(k) * down;
-            c[k] = (float)v;
-            const uint32_t bits = __builtin_bit_cast(uint32_t, c[k]);
-            // halfway as fp32 only: one step towards the value
-            if ((bits & 0xfffffu) == 0x80000u && (double)c[k] != v)
-                c[k] = __builtin_bit_cast(float, __builtin_fabs(v) > (double)__builtin_fabsf(c[k]) ? bits + 1 : bits - 1);
+            const int at = 8 * (k & 3);
+            if ((differ[k / 4] >> at & 255) == 0) continue;
+            q[k / 4] = (q[k / 4] & ~(255u << at)) | e4m3_of(exact(k) * down) << at;
         }
-    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
-    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], hi, true);
-    *codes = u32x2{(uint32_t)lo, (uint32_t)hi};
+    *codes = q;
     return byte;
 }
 
