@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     const bool live = mine && i < a.vectors;
     // lanes without a vector read one all the same: whole heads, whose sums nothing uses
     const int64_t c = (i < a.vectors ? i : i % head_lanes) * kVec;
-    float x[kVec], z[kVec], w[kVec], y[kVec], gated[kVec];
+    float x[kVec], z[kVec], w[kVec], y[kVec];
     load8<DX>(a.x, row * a.x_stride + c, x);
     load8<DZ>(a.z, row * a.z_stride + c, z);
     load8(a.weight, i % head_lanes * kVec, a.weight_dtype, w);
@@ -133,19 +133,18 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     }
     const double root = inverse_rms(sum, a.inverse_size, a.eps, scale) * scale;
     const float rs = (float)root;
+    auto exact = [&](int k) { return (double)x[k] * root * (double)w[k] * ((double)z[k] * logistic_f64(z[k])); };
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) gated[k] = z[k] * logistic(z[k]);
-    if (any_below(z))
+    for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * (z[k] * logistic(z[k]));
+    if (any_below(z))  // the whole product: the weight may bring such a gate back into fp32's range
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) gated[k] = (float)(z[k] * logistic_f64(z[k]));
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * gated[k];
+        for (int k = 0; k < kVec; ++k) y[k] = (float)exact(k);
     const int64_t o = row * (int64_t)a.vectors * kVec + i * (int64_t)kVec;
     if (live && a.out != nullptr) store8<DZ>(a.out, o, y);
     if (a.codes != nullptr) {
         // fp32: s, the gate (6 ulps) and four products are rounded
         u32x2 codes;
-        const int byte = quantise8(y, live, 16, [&](int k) { return (double)x[k] * root * (double)w[k] * ((double)z[k] * logistic_f64(z[k])); }, &codes);
+        const int byte = quantise8(y, live, 16, exact, &codes);
         if (live) {
             *reinterpret_cast<u32x2*>(a.codes + o) = codes;
             if ((i & 15) == 0) a.scales[row * a.scale_stride + (i >> 4)] = (uint8_t)byte;

@@ -226,11 +226,13 @@ __device__ __forceinline__ int quantise8(const float (&y)[kVec], bool live, uint
     }
     u32x2 q = e4m3x8(below);
     const u32x2 other = e4m3x8(above), differ = q ^ other;
-    if ((differ[0] | differ[1]) != 0 && live && byte < 255)
+    // groups so small that values below 2^-126, of which fp32 has fewer bits, get codes (of 2^-10 on): all of them in 64 bits
+    const bool low = byte < 12 && top != 0;
+    if ((low || (differ[0] | differ[1]) != 0) && live && byte < 255)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
             const int at = 8 * (k & 3);
-            if ((differ[k / 4] >> at & 255) == 0) continue;
+            if (!low && (differ[k / 4] >> at & 255) == 0) continue;
             q[k / 4] = (q[k / 4] & ~(255u << at)) | e4m3_of(exact(k) * down) << at;
         }
     *codes = q;

@@ -54,3 +54,37 @@ def test_gated_norm_next_to_halves(heads, d):
     gb.gdn_gated_norm_forward(x, z, w, codes=codes, scales=scales, eps=0.0)
     y, _ = ref.gated(x, z, w, 0.0)
     ref.check_codes(y.reshape(rows, -1), codes, scales, EXACT)
+
+
+@pytest.mark.parametrize("width", [128, 200, 2048, 5120, 16384])
+def test_norm_below_fp32(width):
+    """Results below 2^-126, where fp32 has fewer bits."""
+    rows = 2000000 // width
+    x = normal(1, rows, width)
+    w = torch.ldexp(1 + 0.1 * normal(2, width), -118 - torch.arange(width, device=DEV) // 128 % 16)
+    codes, scales = codes_for(rows, width)
+    gb.gdn_norm_forward(x, w, codes=codes, scales=scales, eps=0.0)
+    ref.check_codes(ref.norm(x, w, 0.0)[0], codes, scales, EXACT)
+
+
+@pytest.mark.parametrize("heads,d", [(3, 16), (2, 64), (1, 48), (48, 128), (2, 96), (3, 256)])
+@pytest.mark.parametrize("weight", [0, 30])
+def test_gated_norm_below_fp32(heads, d, weight):
+    """Gates whose silu is about 2^-118 to 2^-140, by weights about 1 and 2^30."""
+    rows = 2000000 // (heads * d)
+    x, w = normal(d, rows, heads, d), torch.ldexp(1 + 0.1 * normal(1, d), torch.tensor(weight, device=DEV))
+    z = -(86 + 17 * torch.rand(rows, 1, 1, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)) + 0.5 * normal(4, rows, heads, d)
+    codes, scales = codes_for(rows, heads * d)
+    gb.gdn_gated_norm_forward(x, z, w, codes=codes, scales=scales, eps=0.0)
+    y, _ = ref.gated(x, z, w, 0.0)
+    ref.check_codes(y.reshape(rows, -1), codes, scales, EXACT)
+
+
+@pytest.mark.parametrize("width", [200, 2048, 5120])
+def test_zero_rows_beside_small_ones(width):
+    x, w = normal(1, 9, width), torch.full((width,), 2.0 ** -130, device=DEV)
+    x[::2] = 0
+    codes, scales = codes_for(9, width)
+    gb.gdn_norm_forward(x, w, codes=codes, scales=scales, eps=1e-6)
+    ref.check_codes(ref.norm(x, w, 1e-6)[0], codes, scales, EXACT)
+    assert not codes[::2].float().any()
