@@ -136,7 +136,8 @@ __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const Gate
     auto exact = [&](int k) { return (double)x[k] * root * (double)w[k] * ((double)z[k] * logistic_f64(z[k])); };
 #pragma unroll
     for (int k = 0; k < kVec; ++k) y[k] = x[k] * rs * w[k] * (z[k] * logistic(z[k]));
-    if (any_below(z))  // the whole product: the weight may bring such a gate back into fp32's range
+    // the whole product: the weight may bring such a gate back into fp32's range, an element of a tiny head its root
+    if (any_below(z) || root > kLargeRoot)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) y[k] = (float)exact(k);
     const int64_t o = row * (int64_t)a.vectors * kVec + i * (int64_t)kVec;
@@ -200,12 +201,13 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const Gat
             gx = head_sum<L>(gx, part, lead, head_lanes);
         }
         const double root = inverse_rms(xx, a.inverse_size, a.eps, scale);
-        const float rs = (float)(root * scale), mean = (float)(root * gx * a.inverse_size);
+        const float up = scale > 1 ? scale : 1;  // of a tiny head: its root may be above fp32's range
+        const float rs = (float)(root * (scale > 1 ? 1 : scale)), mean = (float)(root * gx * a.inverse_size);
         float dx[kVec], dz[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
-            const float n = x[k] * rs, dn = d[k] * n;
-            dx[k] = rs * (g[k] - n * mean);
+            const float n = x[k] * up * rs, dn = d[k] * n;
+            dx[k] = up * (rs * (g[k] - n * mean));
             dz[k] = dn * w[k] * gate[k] * (1 + z[k] * (1 - gate[k]));
             dw[k] += live ? dn * (z[k] * gate[k]) : 0;
         }

@@ -114,13 +114,17 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
         float y[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) y[k] = r[v][k] * rs * (w[v][k] + a.weight_offset);
+        auto exact = [&](int k) { return (double)r[v][k] * root * ((double)w[v][k] + (double)a.weight_offset); };
+        if (root > kLargeRoot)  // a tiny row: its elements bring the root back into fp32's range
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) y[k] = (float)exact(k);
         const int64_t o = row * a.width + i * kVec;
         if (live && a.residual_out != nullptr) store8<DR>(a.residual_out, o, r[v]);
         if (live && a.out != nullptr) store8<DX>(a.out, o, y);
         if (a.codes != nullptr) {
             // fp32: s, w + w0 and two products are rounded, 4 ulps at most
             u32x2 codes;
-            const int byte = quantise8(y, live, 6, [&](int k) { return (double)r[v][k] * root * ((double)w[v][k] + (double)a.weight_offset); }, &codes);
+            const int byte = quantise8(y, live, 6, exact, &codes);
             if (live) {
                 *reinterpret_cast<u32x2*>(a.codes + o) = codes;
                 if ((t & 15) == 0) a.scales[row * a.scale_stride + (i >> 4)] = (uint8_t)byte;
@@ -226,15 +230,16 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_k
             sum(2);
         }
         const double root = inverse_rms(rsum, a.inverse_width, a.eps, scale);
-        const float rs = (float)(root * scale), mean = (float)(root * gsum * a.inverse_width);
+        const float up = scale > 1 ? scale : 1;  // of a tiny row: its root may be above fp32's range
+        const float rs = (float)(root * (scale > 1 ? 1 : scale)), mean = (float)(root * gsum * a.inverse_width);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = t + v * lanes;
             float dx[kVec];
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
-                const float norm = r[v][k] * rs;
-                dx[k] = z[v][k] + rs * (d[v][k] * w[v][k] - norm * mean);
+                const float norm = r[v][k] * up * rs;
+                dx[k] = z[v][k] + up * (rs * (d[v][k] * w[v][k] - norm * mean));
                 dw[v][k] += d[v][k] * norm;
             }
             if (i < n && a.dx != nullptr) store8<DR>(a.dx, row * a.width + i * kVec, dx);
