@@ -2,7 +2,8 @@
 // read back (gdn_pool_unpack) (gfx950).
 //
 //     scale = max(max_k |S_k| / 127, 2^-126),  code_k = rint(S_k / scale),  value = code_k scale
-// for each value channel (a row of d_k states).
+// for each value channel (a row of d_k states).  127 scales are an fp32 value: the scale of the largest one's channel is
+// rounded down.
 //
 // Bound by HBM: 4 (or 2) bytes a state on one side, 1 + 4 / d_k on the other.  A
 // lane holds four consecutive states (16 bytes of fp32 in, 4 bytes of codes out), a
@@ -85,6 +86,9 @@ __device__ __forceinline__ float over127(float x) {
     return __builtin_fmaf(__builtin_fmaf(-127.0f, q, x), kInverse, q);
 }
 
+// The largest scale: 127 times the next one, to which the largest value's quotient rounds, is infinite.
+constexpr float kMostScale = 0x1.020406p+121f;
+
 // x / scale to the nearest integer q, ties to even, as q + kMagic, whose low byte is q's.  `down` is 1 / scale to an ulp,
 // so x down is off by less than 2^-15; nearer than that to a half (*near), exact() decides.
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: fp32's step there is 1
@@ -149,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void pool_pack_kernel(const PackArgs a) {
             }
             top = lanes_max<DK / 4>(top);
             const bool bad = top >= 0x7f800000u;
-            const float scale = __builtin_fmaxf(over127(__builtin_bit_cast(float, top)), 0x1p-126f);
+            const float scale = __builtin_fminf(__builtin_fmaxf(over127(__builtin_bit_cast(float, top)), 0x1p-126f), kMostScale);
             const float down = __builtin_amdgcn_rcpf(scale);
             bool near = false;
             float f[4];

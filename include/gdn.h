@@ -369,6 +369,7 @@ int gdn_pool_compact(const gdn_pool* pools, int32_t n_pools, const int32_t* tabl
  * of a state pool holds n = row_bytes / (element size * d_k) value channels of
  * d_k states each (n = h_v d_v); channel c of a packed row is
  *     scale[c] = max(max_k |S[c][k]| / 127, 2^-126)       fp32, rounded to nearest
+ *                (rounded down for a largest magnitude of FLT_MAX, whose channel would read back as infinite)
  *     code[c][k] = S[c][k] / scale[c] to the nearest integer, ties to even  int8
  * and stands for code * scale.  Uniform steps: a value is off by at most half a
  * scale, amax / 254.  A channel that holds a NaN or an infinity is packed as
