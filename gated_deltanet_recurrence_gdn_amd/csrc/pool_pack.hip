@@ -99,12 +99,13 @@ __device__ __forceinline__ float nearest(float x, float down, bool* near) {
     return f;
 }
 
-// By the remainder x - q scale, which has no more than 24 bits near a half.
+// By the remainder x - q scale, which has no more than 24 bits near a half.  Twice of it is compared: half of a scale
+// below 2^-125 need not be an fp32 value.
 __device__ __forceinline__ float exact(float f, float x, float scale) {
-    const float q = f - kMagic, rest = __builtin_fmaf(-q, scale, x), half = 0.5f * scale;
+    const float q = f - kMagic, twice = 2 * __builtin_fmaf(-q, scale, x);
     const bool odd = ((int)q & 1) != 0;
-    if (rest > half || (rest == half && odd)) return f + 1;
-    if (rest < -half || (rest == -half && odd)) return f - 1;
+    if (twice > scale || (twice == scale && odd)) return f + 1;
+    if (twice < -scale || (twice == -scale && odd)) return f - 1;
     return f;
 }
 

@@ -46,3 +46,24 @@ def test_largest_values(dk, dtype):
     over = (127 * want).isinf()
     assert torch.equal(torch.where(over, torch.nextafter(want, torch.zeros_like(want)), want), scales)
     assert int(over.sum()) == (2 if dtype is torch.float32 else 0)
+
+
+def test_halves_of_the_smallest_scales():
+    """Scales from 2^-126 to 2^-125 with an odd last bit, whose half is no fp32 value: states beside each half of a step."""
+    dv, dk = 64, 128
+    unit = torch.tensor(-149, device=DEV)
+    # the scales in steps of 2^-149, and largest values whose quotient by 127 is the scale
+    mantissa = 2 ** 23 + 2 * torch.randint(0, 2 ** 21, (4 * dv,), generator=torch.Generator().manual_seed(7)).to(DEV) + 1
+    tops = torch.ldexp((127 * mantissa).double(), unit).float()
+    kept = torch.ldexp((tops.double() / 127).float().double(), -unit) == mantissa
+    mantissa, tops = mantissa[kept][:dv], tops[kept][:dv]
+    x = torch.zeros(1, 2, 1, dv, dk, device=DEV)
+    k = torch.arange(dk, device=DEV) - 64
+    for row, side in enumerate((0, 1)):  # the steps of 2^-149 below and above the half
+        steps = ((2 * k + 1) * mantissa[:, None]) // 2 + side
+        x[0, row, 0] = torch.ldexp(steps.double(), unit).float()
+    x[..., 0] = tops
+    codes, scales, back = round_trip(x)
+    want_c, want_s = ref.pack(x)
+    assert torch.equal(scales, want_s) and torch.all((scales.view(torch.int32) & 1) == 1)
+    assert torch.equal(codes, want_c)
