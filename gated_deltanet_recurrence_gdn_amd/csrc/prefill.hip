@@ -733,7 +733,7 @@ __device__ __forceinline__ void dma_slot(const DmaCtx& d) {
         }
     } else if constexpr (i0 < CB::NFRAG + CB::NVI) {
         constexpr int n0 = (i0 - CB::NFRAG) / NSL;  // this wave's V load index
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(d.vw, (lds_void*)(d.dst + 1024 * i0), 16, d.vv, n0 * d.vstep, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(d.vw, (lds_void*)(d.dst + 1024 * i0), 16, d.vv + n0 * d.vstep, 0, 0, 0);
     } else {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(d.gw, (lds_void*)d.gdst, 4, d.vg, 0, 0, 0);
     }

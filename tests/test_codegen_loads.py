@@ -30,3 +30,28 @@ def test_rows_of_scales_are_in_the_checked_offset(disassembly):  # noqa: F811
         for i in range(0, len(loads), tiles):
             step = loads[i:i + tiles]
             assert len({scalar for _, scalar in step}) == 1 and len({rows for rows, _ in step}) == tiles, (name, step)
+
+
+def test_value_rows_of_a_prefill_are_in_the_checked_offset(disassembly):  # noqa: F811
+    """The scan's rows of v end at the sequence's last token: the loads of a chunk's rows, those before its gates' load
+    from the same buffer, have no scalar offset."""
+    kernels, loads = {}, None
+    for line in disassembly.split("\n"):
+        m = re.match(r"^[0-9a-f]+ <(\S+)>:", line)
+        if m:
+            loads = kernels.setdefault(m.group(1), []) if "prefill_scan_kernel" in m.group(1) else None
+        elif loads is not None:
+            m = re.match(r"\s*(buffer_load_dword\S*) v\d+, (s\[\d+:\d+\]), (\S+) offen.* lds", line)
+            if m:
+                loads.append(m.groups())
+    assert kernels
+    for name, loads in kernels.items():
+        gates = [i for i, x in enumerate(loads) if x[0] == "buffer_load_dword"]
+        assert gates, name
+        for i in gates:
+            rows = loads[i - 1][1]
+            j = i - 1
+            while j >= 0 and loads[j][:2] == ("buffer_load_dwordx4", rows):
+                assert loads[j][2] == "0", (name, loads[j])
+                j -= 1
+            assert i - 1 - j >= 2, name
