@@ -14,10 +14,6 @@ using namespace gdn;
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool valid_dtype(int32_t d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_F16; }
-
 // Checks shared by verify (chain and tree): sizes, dtypes, pointers.
 int check_verify(const gdn_shape* sh, const void* q, const void* k, const void* v, const float* alpha,
                  const float* beta, const float* state, const int32_t* state_slot, const void* out,

@@ -103,7 +103,7 @@ __device__ __forceinline__ bool any_of(bool ask) {
 }
 
 // Bytes bound it, vector operations come close (about 40 an element): 4096 tokens x 48 heads of 128 bf16 31 us (4.9 TB/s);
-// to 8 bits 28, of f16 28, 4.5 TB/s; 16 tokens of fp32 3.6 us.
+// to 8 bits 29, of f16 29, 4.3 TB/s; 16 tokens of fp32 3.6 us.
 template <int DX, int DZ, int L>
 __global__ __launch_bounds__(kThreads) void gated_norm_forward_kernel(const GatedArgs a) {
     __shared__ double part[L == 0 ? kPart : 1];
@@ -232,7 +232,7 @@ int check_gated(const gdn_gated_norm_shape* sh) {
     const int64_t width = (int64_t)sh->h_v * sh->d_v;
     for (int64_t s : {sh->x_stride, sh->z_stride})
         if (s < width || s % kVec != 0 || s > (int64_t{1} << 31)) return GDN_ERR_SHAPE;
-    if (!real_dtype(sh->x_dtype) || !real_dtype(sh->z_dtype) || !real_dtype(sh->weight_dtype)) return GDN_ERR_DTYPE;
+    if (!valid_dtype(sh->x_dtype) || !valid_dtype(sh->z_dtype) || !valid_dtype(sh->weight_dtype)) return GDN_ERR_DTYPE;
     if (!(sh->eps >= 0) || !(sh->eps < INFINITY)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
@@ -311,8 +311,8 @@ int gdn_gated_norm_forward(const gdn_gated_norm_shape* shape, const void* x, con
     if (shape->rows == 0) return GDN_OK;
     if (x == nullptr || z == nullptr || weight == nullptr) return GDN_ERR_NULL;
     if ((codes == nullptr) != (scales == nullptr) || (out == nullptr && codes == nullptr)) return GDN_ERR_NULL;
-    if (!aligned_to(x, 16) || !aligned_to(z, 16) || !aligned_to(weight, 16) || !aligned_to(out, 16) || !aligned_to(codes, 8) ||
-        !aligned_to(scales, 4))
+    if (!aligned(x, 16) || !aligned(z, 16) || !aligned(weight, 16) || !aligned(out, 16) || !aligned(codes, 8) ||
+        !aligned(scales, 4))
         return GDN_ERR_ALIGN;
     a.x = x;
     a.z = z;
@@ -343,7 +343,7 @@ int gdn_gated_norm_backward(const gdn_gated_norm_shape* shape, const void* dout,
     int64_t grid = 0;
     if ((rc = plan_gated(shape, kBackGrid, &a, &grid)) != GDN_OK) return rc;
     if (dx == nullptr && dz == nullptr && dweight == nullptr) return GDN_ERR_NULL;
-    if (!aligned_to(dweight, 16)) return GDN_ERR_ALIGN;
+    if (!aligned(dweight, 16)) return GDN_ERR_ALIGN;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (shape->rows == 0) {
         if (dweight == nullptr) return GDN_OK;
@@ -351,10 +351,10 @@ int gdn_gated_norm_backward(const gdn_gated_norm_shape* shape, const void* dout,
     }
     if (dout == nullptr || x == nullptr || z == nullptr || weight == nullptr) return GDN_ERR_NULL;
     for (const void* p : {dout, x, z, weight, static_cast<const void*>(dx), static_cast<const void*>(dz)})
-        if (!aligned_to(p, 16)) return GDN_ERR_ALIGN;
+        if (!aligned(p, 16)) return GDN_ERR_ALIGN;
     if (dweight != nullptr) {
         if (workspace == nullptr || workspace_bytes < gdn_gated_norm_backward_workspace_bytes(shape)) return GDN_ERR_WORKSPACE;
-        if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGN;
+        if (!aligned(workspace, 16)) return GDN_ERR_ALIGN;
     }
     a.x = x;
     a.z = z;

@@ -19,6 +19,10 @@ constexpr int kMaxLdsBytes = 160 * 1024;  // LDS of one gfx950 compute unit, all
 constexpr int kDefaultLdsBytes = 64 * 1024;  // dynamic LDS a launch may use without the attribute below
 constexpr int kMaxDevices = 64;
 
+// What the host checks share.
+inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline bool valid_dtype(int32_t d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_F16; }
+
 // Allows launches of kernel K (a __global__ function) to take up to
 // kMaxLdsBytes of dynamic LDS on the current device.  The attribute is set once
 // per kernel and device; concurrent first calls may both set it (the call is

@@ -135,7 +135,7 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
 
 // A walker (a wave, or the workgroup) takes every walkers-th row and sums its part of dweight in registers; the next
 // row's loads are under way while a row is worked on.  Bytes bound it: 2999 x 2560, bf16 with an fp32 residual, 20 us (107 MB,
-// part of it still cached), and 4 for the partials' sum; 4096 x 5120 41 us (4.1 TB/s), without the loads ahead 53.
+// part of it still cached), and 4 for the partials' sum; 4096 x 5120 40 us (4.2 TB/s), without the loads ahead 53.
 template <int DX, int DR, int V, int LANES>
 __global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_kernel(const NormArgs a) {
     constexpr int kWaves = LANES ? 4 : 1;  // walkers of a workgroup
@@ -365,7 +365,7 @@ int check_norm(const gdn_norm_shape* sh) {
     if (sh->rows < 0 || sh->rows > 0x7fffffffLL) return GDN_ERR_SHAPE;
     if (sh->width < kVec || sh->width > GDN_MAX_WIDTH || sh->width % kVec != 0) return GDN_ERR_SHAPE;
     if (sh->x_stride < sh->width || sh->x_stride % kVec != 0 || sh->x_stride > (int64_t{1} << 31)) return GDN_ERR_SHAPE;
-    if (!real_dtype(sh->dtype) || !real_dtype(sh->residual_dtype) || !real_dtype(sh->weight_dtype)) return GDN_ERR_DTYPE;
+    if (!valid_dtype(sh->dtype) || !valid_dtype(sh->residual_dtype) || !valid_dtype(sh->weight_dtype)) return GDN_ERR_DTYPE;
     if (!(sh->eps >= 0) || !(sh->eps < INFINITY) || !(fabsf(sh->weight_offset) < INFINITY)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
@@ -409,8 +409,8 @@ int gdn_norm_forward(const gdn_norm_shape* shape, const void* x, const void* res
     if ((codes == nullptr) != (scales == nullptr)) return GDN_ERR_NULL;
     if (out == nullptr && codes == nullptr && residual_out == nullptr) return GDN_ERR_NULL;
     if (residual == nullptr && residual_out != nullptr) return GDN_ERR_NULL;
-    if (!aligned_to(x, 16) || !aligned_to(residual, 16) || !aligned_to(weight, 16) || !aligned_to(residual_out, 16) ||
-        !aligned_to(out, 16) || !aligned_to(codes, 8) || !aligned_to(scales, 4))
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+        !aligned(out, 16) || !aligned(codes, 8) || !aligned(scales, 4))
         return GDN_ERR_ALIGN;
     NormArgs a = args_of(shape);
     a.x = x;
@@ -438,19 +438,19 @@ int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void*
     const int rc = check_norm(shape);
     if (rc != GDN_OK) return rc;
     if (dx == nullptr && dweight == nullptr) return GDN_ERR_NULL;
-    if (!aligned_to(dweight, 16)) return GDN_ERR_ALIGN;
+    if (!aligned(dweight, 16)) return GDN_ERR_ALIGN;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (shape->rows == 0) {
         if (dweight == nullptr) return GDN_OK;
         return launch_sum_partials(nullptr, 0, shape->width, dweight, st) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
     }
     if (dout == nullptr || r == nullptr || weight == nullptr) return GDN_ERR_NULL;
-    if (!aligned_to(dout, 16) || !aligned_to(r, 16) || !aligned_to(weight, 16) || !aligned_to(dresidual, 16) || !aligned_to(dx, 16))
+    if (!aligned(dout, 16) || !aligned(r, 16) || !aligned(weight, 16) || !aligned(dresidual, 16) || !aligned(dx, 16))
         return GDN_ERR_ALIGN;
     const NormPlan p = plan_rows(shape->rows, shape->width, true);
     if (dweight != nullptr) {
         if (workspace == nullptr || workspace_bytes < gdn_norm_backward_workspace_bytes(shape)) return GDN_ERR_WORKSPACE;
-        if (!aligned_to(workspace, 16)) return GDN_ERR_ALIGN;
+        if (!aligned(workspace, 16)) return GDN_ERR_ALIGN;
     }
     NormArgs a = args_of(shape);
     a.x = r;

@@ -14,9 +14,6 @@ namespace gdn {
 
 constexpr int kVec = 8;  // channels of a lane
 
-inline bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-inline bool real_dtype(int32_t t) { return t == GDN_F32 || t == GDN_BF16 || t == GDN_F16; }
-
 // Eight elements as they are in memory, so that a load ahead of its use takes no more registers than it has to.
 template <int DT>
 struct Raw8 {

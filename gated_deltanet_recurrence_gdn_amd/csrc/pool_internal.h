@@ -18,8 +18,6 @@ __device__ bool pair_stands(const Args& a, int i, int s, int d) {
     return __syncthreads_or(bad) == 0;
 }
 
-inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 // One past the last byte of a pool.
 inline const unsigned char* pool_end(const gdn_pool& p) {
     return static_cast<const unsigned char*>(p.data) + (int64_t)(p.n_layers - 1) * p.layer_bytes + (int64_t)p.n_slots * p.row_bytes;

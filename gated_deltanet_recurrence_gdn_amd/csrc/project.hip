@@ -17,7 +17,7 @@ namespace {
 
 // Waves of a workgroup: 16 of 32 columns and up to 32 tokens with fp32 scales, whose scaling keeps a wave longer from its
 // next loads (16 x 5120 x 6144 8.0 us, with eight 8.7; 22 x 5120 x 6144 8.8 and 9.1), else eight (the same with e8m0
-// scales 7.9 and 7.4, 8.7 and 8.2; blocks of 64 tokens: 100 x 2048 x 2048 13 waves 6.5, eight 6.2).
+// scales 7.9 and 7.4, 8.7 and 8.2; blocks of 64 tokens: 100 x 2048 x 2048 13 waves 6.5, eight 6.0).
 constexpr int max_waves(bool e8m0, int mt, int nt) { return !e8m0 && mt <= 2 && nt == 2 ? 16 : 8; }
 
 // Few tokens: the weights are read once, at the memory's rate.  16 NT columns and 16 MT tokens a workgroup.  Its waves
@@ -115,8 +115,6 @@ __global__ __launch_bounds__(64 * max_waves(E8M0, MT, NT)) void project_rows_ker
     }
 }
 
-bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 template <int DT, bool E8M0>
 hipError_t launch(const ProjectArgs& p, hipStream_t stream) {
     auto go = [&](auto mt, auto nt) {
@@ -175,13 +173,13 @@ int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_sca
         const gdn_project_part& q = parts[i];
         if (q.columns < 1 || q.stride < q.columns || q.stride > (int64_t{1} << 40) || q.reserved != 0) return GDN_ERR_SHAPE;
         if (shape->tokens > 0 && q.data == nullptr) return GDN_ERR_NULL;
-        if (!aligned_to(q.data, 2)) return GDN_ERR_ALIGN;
+        if (!aligned(q.data, 2)) return GDN_ERR_ALIGN;
         p.part[i].data = q.data;
         p.part[i].stride = q.stride;
         p.part[i].begin = (int32_t)columns;
         p.part[i].wide = 0;
-        if (columns % 4 == 0 && q.stride % 4 == 0 && aligned_to(q.data, 8)) p.part[i].wide = 1;
-        if (columns % 8 == 0 && q.stride % 8 == 0 && aligned_to(q.data, 16)) p.part[i].wide = 2;
+        if (columns % 4 == 0 && q.stride % 4 == 0 && aligned(q.data, 8)) p.part[i].wide = 1;
+        if (columns % 8 == 0 && q.stride % 8 == 0 && aligned(q.data, 16)) p.part[i].wide = 2;
         columns += q.columns;
         if (columns > (int64_t{1} << 27)) return GDN_ERR_SHAPE;
     }
@@ -189,7 +187,7 @@ int gdn_project(const gdn_project_shape* shape, const void* a, const void* a_sca
     if ((shape->tokens + 255) / 256 * ((columns + 255) / 256) > (int64_t{1} << 21)) return GDN_ERR_SHAPE;
     if (shape->tokens == 0) return GDN_OK;
     if (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr) return GDN_ERR_NULL;
-    if (!aligned_to(a, 16) || !aligned_to(w, 16) || !aligned_to(a_scales, 4) || !aligned_to(w_scales, 4)) return GDN_ERR_ALIGN;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scales, 4) || !aligned(w_scales, 4)) return GDN_ERR_ALIGN;
     p.a = static_cast<const uint8_t*>(a);
     p.a_scales = static_cast<const uint8_t*>(a_scales);
     p.w = static_cast<const uint8_t*>(w);

@@ -76,9 +76,10 @@ __device__ __forceinline__ void store_tile(const ProjectArgs& p, unsigned char* 
     }
 }
 
-// 4096 x 16384 x 5120 take 338 us with fp32 weight scales (2.03 PFLOP/s) and 312 with e8m0 ones; a library product of the
-// same operands without scales 225.  The matrix cores are busy half of the cycles, LDS reads a third; the e8m0 form takes
-// 249 without the loads, 221 without LDS reads too, and 249 with all of it on zeros, whose products draw less power.
+// 4096 x 16384 x 5120 take 335 us with fp32 weight scales (2.05 PFLOP/s) and 312 with e8m0 ones; a library product of the
+// same operands without scales 225.  The matrix cores are busy 45 and 50% of the cycles, LDS 37 and 41%, nearly half of
+// that in bank conflicts; the e8m0 form takes 249 without the loads, 221 without LDS reads too, and 249 with all of it on
+// zeros.
 template <int DT, bool E8M0, int WM, int WN, int FN, int DEEP>
 __global__ __launch_bounds__(64 * WM * WN, 2) void project_tile_kernel(const ProjectArgs p) {
     using T = Tile<WM, WN, FN, DEEP>;
@@ -230,7 +231,7 @@ hipError_t launch(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t st
 }
 
 // The tile: the one whose rounds over the chip take least.  Microseconds a step of 128 channels, as measured with fp32
-// weight scales, times the rounds:
+// weight scales (e8m0 ones take the same tile, at up to a tenth less), times the rounds:
 //   256 x 256, one a CU                2.2    (4096 x 16384 x 5120: 338 us, 128 x 128 404; 1024 x 16384 x 5120: 89 and 114)
 //   128 x 128, two a CU                1.25, alone on a CU 1.0   (4096 x 5120 x 6144: 158 us, 256 x 256 184)
 //   128 x 128, one a CU, four steps    0.8    (512 x 5120 x 6144: 38 us, two a CU 47, 64 x 128 50)

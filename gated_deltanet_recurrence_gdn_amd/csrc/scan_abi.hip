@@ -10,8 +10,6 @@
 namespace gdn {
 namespace {
 
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 int64_t chunks_of(int64_t tokens) { return (tokens + kScanChunk - 1) / kScanChunk; }
 
 // The shape and the packed sequences' offsets; *units is the number of chunks.

@@ -369,7 +369,7 @@ int gdn_pool_compact(const gdn_pool* pools, int32_t n_pools, const int32_t* tabl
  * of a state pool holds n = row_bytes / (element size * d_k) value channels of
  * d_k states each (n = h_v d_v); channel c of a packed row is
  *     scale[c] = max(max_k |S[c][k]| / 127, 2^-126)       fp32, rounded to nearest
- *                (rounded down for a largest magnitude of FLT_MAX, whose channel would read back as infinite)
+ *                (down where 127 of it would be infinite: a channel of FLT_MAX)
  *     code[c][k] = S[c][k] / scale[c] to the nearest integer, ties to even  int8
  * and stands for code * scale.  Uniform steps: a value is off by at most half a
  * scale, amax / 254.  A channel that holds a NaN or an infinity is packed as
@@ -592,7 +592,9 @@ int gdn_scan_backward(const gdn_shape* shape, const int32_t* cu_seqlens, const v
  * e4m3 is the OCP format: values up to 448, steps of 2^-3 of the power of two below
  * a value, 2^-9 at the least.  The codes a norm writes are y 2^-e to the nearest, ties to even, with the
  * smallest e from -126 on that leaves no |y| 2^-e of the group above 448.  A group
- * with a NaN or an infinity has scale byte 255 and codes NaN.
+ * with a NaN or an infinity has scale byte 255 and codes NaN.  Codes and scales are those of
+ * y in 64 bits, but where a product of y's first factors (the normed value, in the gated norm
+ * with the weight) is below 2^-126 or overflows in fp32 and the next factor makes up for it.
  */
 #define GDN_GROUP 128       /* channels that share a scale */
 #define GDN_MAX_PARTS 8     /* outputs of one gdn_project call */
@@ -617,21 +619,23 @@ typedef struct gdn_norm_shape {
  *     y = r / sqrt(mean_k r_k^2 + eps) * (w + w0)
  * The norm is of r as stored, so the backward pass needs nothing but r.  Without a
  * residual (NULL; residual_out is NULL then) r is x.  y goes to `out` (nullable, dtype)
- * and, or, to `codes` and `scales` (nullable, both or none).  Sums and products
- * are fp32; codes and scales are those of the values in 64 bits.
+ * and, or, to `codes` and `scales` (nullable, both or none).  Sums and products of `out`
+ * are fp32.
  * residual, residual_out, out and codes are dense [rows][width]; residual_out may be
  * residual, and out may be a dense x (no other output overlaps an input).  x, residual,
  * residual_out, out and weight are 16-byte aligned, codes 8-byte, scales 4-byte.  A row
  * of zeros with eps = 0 is NaN; a NaN or an infinity in a row leaves nothing finite of
  * the channels that hold one and may reach its whole row, but no other.  Other rows may be
- * of any magnitude: one whose squares leave fp32's range is summed again, scaled.
+ * of any magnitude, subnormal ones with eps = 0 included: one whose squares leave fp32's
+ * range is summed again, scaled.
  *
  * gdn_norm_backward: from dout [rows][width] (dtype) and r (residual_dtype; x itself, in
  * residual_dtype = dtype, where there was no residual)
  *     g = dout (w + w0),  s = 1 / sqrt(mean r^2 + eps)
  *     dx = dresidual + s g - r s^3 mean_k g_k r_k,   dweight = sum_rows dout r s
  * dx (residual_dtype; the gradient of x and of residual alike) may be dresidual
- * (nullable: zeros).  dweight is fp32 [width]; its sums are taken in a fixed order
+ * (nullable: zeros).  Sums and products are fp32, dout (w + w0) r among them: where they
+ * overflow, dx need not be finite.  dweight is fp32 [width]; its sums are taken in a fixed order
  * and repeat bit for bit.  With no rows it is zero.  dx and dweight are nullable.
  * `workspace`: gdn_norm_backward_workspace_bytes(shape) bytes, 16-byte aligned;
  * calls that share one are ordered on one stream.
@@ -644,7 +648,7 @@ int gdn_norm_backward(const gdn_norm_shape* shape, const void* dout, const void*
                       void* stream);
 
 typedef struct gdn_gated_norm_shape {
-    int64_t rows;          /* tokens, 0 .. 2^31 - 1 */
+    int64_t rows;          /* tokens, 0 .. 2^31 - 1; rows * ceil(h_v d_v / lcm(d_v, 128)) below 2^32 */
     int64_t x_stride;      /* elements from one row of x to the next, a multiple of 8, h_v d_v .. 2^31 */
     int64_t z_stride;      /* of z, likewise */
     int32_t h_v;           /* value heads, >= 1, at most 2^20 */
@@ -664,14 +668,15 @@ typedef struct gdn_gated_norm_shape {
  * weight [d_v].  y goes to `out` (nullable, z_dtype) and, or, to `codes` and `scales`
  * (nullable, both or none), [rows][h_v d_v] as the output projection reads them.  out
  * may be a dense z, or a dense x of its type.  A NaN or an infinity in x or z may reach its whole head,
- * and makes its group's scale NaN, but no other head's `out`.
+ * and makes its group's scale NaN, but no other head's `out`.  Heads and gates may be of any
+ * finite magnitude, as the norm's rows.
  *
  * gdn_gated_norm_backward: with s = 1 / sqrt(mean x^2 + eps), a = 1 / (1 + e^-z) and
  * g = dout w silu(z)
  *     dx = s g - x s^3 mean_j g_j x_j,   dz = dout n w a (1 + z (1 - a)),
  *     dweight = sum over rows and heads of dout n silu(z)   (fp32 [d_v])
- * dx, dz and dweight are nullable.  Alignment, the sums' order and the workspace are
- * those of gdn_norm_backward; dz may be dout or z, dx may be x (the same rows, dense).
+ * dx, dz and dweight are nullable.  Alignment, the sums' order, what may overflow (g x) and
+ * the workspace are those of gdn_norm_backward; dz may be dout or z, dx may be x (the same rows, dense).
  */
 int gdn_gated_norm_forward(const gdn_gated_norm_shape* shape, const void* x, const void* z, const void* weight,
                            void* out, void* codes, void* scales, void* stream);
@@ -711,8 +716,8 @@ typedef struct gdn_project_shape {
  *
  * Groups are summed in fp32, in an order that depends on the shape alone, so results
  * repeat bit for bit; the matrix instruction adds the products within a group with
- * about 17 bits below the largest (2e-5 of the 2-norm of y, of normal operands), which
- * is why y is bf16 or f16 and not fp32.  f16 outputs above 65504 become infinite.  A
+ * about 17 bits below the largest (1.5e-5 of the 2-norm of y for normal operands, 2.3e-5
+ * for a layer's), which is why y is bf16 or f16 and not fp32.  f16 outputs above 65504 become infinite.  A
  * scale of NaN, or a NaN code, makes NaN every y that it has part in.  Scales may be of
  * any magnitude: a group's sum is formed with both, so it overflows where y does.
  */
