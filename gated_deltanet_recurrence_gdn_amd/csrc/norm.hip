@@ -106,18 +106,16 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxThreads) void norm_forward_kernel
         }
     }
     const double root = inverse_rms(squares, a.inverse_width, a.eps, c) * c;
-    const float rs = (float)root;
+    const float up = root > kLargeRoot ? 0x1p100f : 1.0f;  // of a tiny row
+    const float rs = (float)(root > kLargeRoot ? root * 0x1p-100 : root);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int i = t + v * lanes;
         const bool live = i < n && at < a.rows;
         float y[kVec];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) y[k] = r[v][k] * rs * (w[v][k] + a.weight_offset);
+        for (int k = 0; k < kVec; ++k) y[k] = r[v][k] * up * rs * (w[v][k] + a.weight_offset);
         auto exact = [&](int k) { return (double)r[v][k] * root * ((double)w[v][k] + (double)a.weight_offset); };
-        if (root > kLargeRoot)  // a tiny row: its elements bring the root back into fp32's range
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) y[k] = (float)exact(k);
         const int64_t o = row * a.width + i * kVec;
         if (live && a.residual_out != nullptr) store8<DR>(a.residual_out, o, r[v]);
         if (live && a.out != nullptr) store8<DX>(a.out, o, y);

@@ -252,8 +252,8 @@ __device__ __forceinline__ double inverse_rms(double sum, double inverse_n, floa
     return m == __builtin_inf() ? 0.0 : y * __builtin_fma(-0.5 * m * y, y, 1.5);  // infinite: an infinity in the row
 }
 
-// Inverse roots above this (rows whose root mean square is below 2^-100) are multiplied in 64 bits: from 2^128 on they
-// are above fp32's range, where their products with the row's elements are not.
+// From 2^128 on an inverse root is above fp32's range, where its products with the row's elements are not.  Rows whose
+// root is above this (their root mean square is below 2^-100) are scaled by 2^100 first, or multiplied in 64 bits.
 constexpr double kLargeRoot = 0x1p100;
 
 // In 64 bits, of any fp32 values: the sum behind codes, which are those of the 64-bit values.
