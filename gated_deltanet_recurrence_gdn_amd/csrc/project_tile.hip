@@ -232,7 +232,7 @@ hipError_t launch(const ProjectArgs& p, bool e8m0, int32_t dtype, hipStream_t st
 
 // The tile: the one whose rounds over the chip take least.  Microseconds a step of 128 channels, as measured with fp32
 // weight scales (e8m0 ones take the same tile, at up to a tenth less), times the rounds:
-//   256 x 256, one a CU                2.2    (4096 x 16384 x 5120: 338 us, 128 x 128 404; 1024 x 16384 x 5120: 89 and 114)
+//   256 x 256, one a CU                2.2    (4096 x 16384 x 5120: 335 us, 128 x 128 404; 1024 x 16384 x 5120: 89 and 114)
 //   128 x 128, two a CU                1.25, alone on a CU 1.0   (4096 x 5120 x 6144: 158 us, 256 x 256 184)
 //   128 x 128, one a CU, four steps    0.8    (512 x 5120 x 6144: 38 us, two a CU 47, 64 x 128 50)
 //   64 x 128, two a CU, three steps    1.0, alone on a CU 0.75   (128 x 16384 x 5120: 32 us, 128 x 128 38)
