@@ -75,7 +75,17 @@ __device__ __forceinline__ double logistic_f64(double z) {
     return 1.0 / (1.0 + __builtin_ldexp(p, (int)n));
 }
 
-// Whether a lane's eight need the 64-bit form.
+// The same below kLeast, where a is e^z, for a product with x: its power of two goes to x, which may bring the product
+// back into fp32's range, but for 2^-30, with which 1 - a is 1.
+__device__ __forceinline__ float closed_logistic(float z, float* x) {
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;  // log2(e)
+    z = __builtin_fmaxf(z, -700.0f);  // nothing times any x from here on
+    const float n = __builtin_rintf(z * kHi);
+    *x = __builtin_ldexpf(*x, (int)n + 30);
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kHi, -n) + z * kLo) * 0x1p-30f;
+}
+
+// Whether a lane's eight need another form.
 __device__ __forceinline__ bool any_below(const float (&z)[kVec]) {
     float least = z[0];
 #pragma unroll
@@ -183,7 +193,8 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const Gat
         for (int k = 0; k < kVec; ++k) gate[k] = logistic(z[k]);
         if (any_below(z))
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) gate[k] = (float)logistic_f64(z[k]);
+            for (int k = 0; k < kVec; ++k)
+                if (z[k] < kLeast) gate[k] = closed_logistic(z[k], &d[k]);
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
             g[k] = d[k] * w[k] * (z[k] * gate[k]);

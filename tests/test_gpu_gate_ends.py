@@ -53,3 +53,28 @@ def test_infinite_gates(heads, d):
     assert out[0, 0, 5] == y[0, 0, 5] and out[0, 0, 5].isinf()
     fine = z.isfinite()
     ref.near(out[fine], y[fine], y[fine].abs() * ref.GATED)
+
+
+@pytest.mark.parametrize("heads,d", [(3, 16), (2, 64), (1, 48), (5, 128), (2, 96), (3, 256)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_of_closed_gates(heads, d, dtype):
+    """Gates below e^-86, which have few bits in fp32 or none, and gradients of 2^80, which bring them back."""
+    rows = 40
+    x, w = normal(d, rows, heads, d).to(T[dtype]), 1 + 0.1 * normal(1, d)
+    z = -(60 + 70 * torch.rand(rows, heads, d, generator=torch.Generator(device=DEV).manual_seed(d), device=DEV)).to(T[dtype])
+    dout = torch.ldexp(normal(4, rows, heads, d), torch.tensor(80, device=DEV)).to(T[dtype])
+    dx, dz, dw = like(x), like(z), torch.empty(d, device=DEV)
+    gb.gdn_gated_norm_backward(dout, x, z, w, dx, dz, dw, eps=EPS)
+    want, lost, want_z, lost_z, want_w, lost_w = ref.gated_gradients(dout, x, z, w, EPS)
+    ref.near(dx, want, lost)
+    # 1 - a is 1 in fp32 here, so 1 + z (1 - a) is rounded once
+    ref.near(dz, want_z, want_z.abs() * (ref.HEAD + ref.GATE + 8 * ref.U))
+    ref.near(dw, want_w, lost_w)
+    for b in range(rows):  # rows whose gates are all closed: as near in their own size
+        one = [t[b:b + 1].clone() for t in (dout, x, z)]
+        one[2] = one[2].clamp(max=-90)
+        dx, dz = like(one[1]), like(one[2])
+        gb.gdn_gated_norm_backward(*one, w, dx, dz, eps=EPS)
+        want, lost, want_z, _, _, _ = ref.gated_gradients(*one, w, EPS)
+        ref.near(dx, want, lost)
+        ref.near(dz, want_z, want_z.abs() * (ref.HEAD + ref.GATE + 8 * ref.U))
