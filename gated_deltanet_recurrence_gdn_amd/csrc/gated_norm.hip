@@ -203,17 +203,17 @@ __global__ __launch_bounds__(kThreads) void gated_norm_backward_kernel(const Gat
         const int lead = (int)threadIdx.x - column;
         float xx = head_sum<L>(squares8(x), part, lead, head_lanes);
         gx = head_sum<L>(gx, part, lead, head_lanes);
-        const float scale = range_scale(xx, a.eps);
-        if (any_of<L>(scale != 1.0f)) {
+        const float scale = range_scale(xx, a.eps), g_scale = sum_scale(gx);
+        if (any_of<L>(scale != 1.0f || g_scale != 1.0f)) {
             xx = head_sum<L>(squares8_of_scaled(x, scale), part, lead, head_lanes);
             gx = 0;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) gx += g[k] * (x[k] * scale);
+            for (int k = 0; k < kVec; ++k) gx += g[k] * g_scale * (x[k] * scale);
             gx = head_sum<L>(gx, part, lead, head_lanes);
         }
         const double root = inverse_rms(xx, a.inverse_size, a.eps, scale);
         const float up = scale > 1 ? scale : 1;  // of a tiny head: its root may be above fp32's range
-        const float rs = (float)(root * (scale > 1 ? 1 : scale)), mean = (float)(root * gx * a.inverse_size);
+        const float rs = (float)(root * (scale > 1 ? 1 : scale)), mean = (float)(root * gx * a.inverse_size * (g_scale == 1 ? 1.0 : 0x1p80));
         float dx[kVec], dz[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {

@@ -213,15 +213,15 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_k
             }
         };
         sum(turn);  // two copies in turn, and one for second sums: the next row's do not wait for this row's readers
-        const float scale = range_scale(rsum, a.eps);
-        if (scale != 1.0f) {  // the whole row's lanes
+        const float scale = range_scale(rsum, a.eps), g_scale = sum_scale(gsum);
+        if (scale != 1.0f || g_scale != 1.0f) {  // the whole row's lanes
             rr = gr = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const bool in = t + v * lanes < n;
                 float q = 0;
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) q += d[v][k] * w[v][k] * (r[v][k] * scale);
+                for (int k = 0; k < kVec; ++k) q += d[v][k] * w[v][k] * g_scale * (r[v][k] * scale);
                 rr += in ? squares8_of_scaled(r[v], scale) : 0;
                 gr += in ? q : 0;
             }
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(LANES ? 256 : kMaxBackThreads) void norm_backward_k
         }
         const double root = inverse_rms(rsum, a.inverse_width, a.eps, scale);
         const float up = scale > 1 ? scale : 1;  // of a tiny row: its root may be above fp32's range
-        const float rs = (float)(root * (scale > 1 ? 1 : scale)), mean = (float)(root * gsum * a.inverse_width);
+        const float rs = (float)(root * (scale > 1 ? 1 : scale)), mean = (float)(root * gsum * a.inverse_width * (g_scale == 1 ? 1.0 : 0x1p80));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = t + v * lanes;

@@ -273,6 +273,8 @@ __device__ __forceinline__ float range_scale(double sum, float eps) {
     if (sum > 0x1p120) return 0x1p-80f;
     return sum < 0x1p-100 && eps < 0x1p-90f ? 0x1p100f : 1.0f;
 }
+// What dout w r is scaled by, besides, where its sum has left fp32's range: with this and the scale of r no term does.
+__device__ __forceinline__ float sum_scale(double sum) { return __builtin_fabs(sum) <= 0x1p127 ? 1.0f : 0x1p-80f; }
 __device__ __forceinline__ float squares8_of_scaled(const float (&x)[kVec], float c) {
     float y[kVec];
 #pragma unroll

@@ -634,8 +634,8 @@ typedef struct gdn_norm_shape {
  *     g = dout (w + w0),  s = 1 / sqrt(mean r^2 + eps)
  *     dx = dresidual + s g - r s^3 mean_k g_k r_k,   dweight = sum_rows dout r s
  * dx (residual_dtype; the gradient of x and of residual alike) may be dresidual
- * (nullable: zeros).  Sums and products are fp32, dout (w + w0) r among them: where they
- * overflow, dx need not be finite.  dweight is fp32 [width]; its sums are taken in a fixed order
+ * (nullable: zeros).  Sums and products are fp32; a sum of g r that leaves its range is formed
+ * again, scaled.  dweight is fp32 [width]; its sums are taken in a fixed order
  * and repeat bit for bit.  With no rows it is zero.  dx and dweight are nullable.
  * `workspace`: gdn_norm_backward_workspace_bytes(shape) bytes, 16-byte aligned;
  * calls that share one are ordered on one stream.
@@ -675,8 +675,8 @@ typedef struct gdn_gated_norm_shape {
  * g = dout w silu(z)
  *     dx = s g - x s^3 mean_j g_j x_j,   dz = dout n w a (1 + z (1 - a)),
  *     dweight = sum over rows and heads of dout n silu(z)   (fp32 [d_v])
- * dx, dz and dweight are nullable.  Alignment, the sums' order, what may overflow (g x) and
- * the workspace are those of gdn_norm_backward; dz may be dout or z, dx may be x (the same rows, dense).
+ * dx, dz and dweight are nullable.  Alignment, the sums and the workspace are
+ * those of gdn_norm_backward; dz may be dout or z, dx may be x (the same rows, dense).
  */
 int gdn_gated_norm_forward(const gdn_gated_norm_shape* shape, const void* x, const void* z, const void* weight,
                            void* out, void* codes, void* scales, void* stream);
